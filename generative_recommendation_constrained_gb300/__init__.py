@@ -14,7 +14,9 @@ from ._lib import (DTYPES, LIB_PATH, ZG_BF16, ZG_F16, ZG_F32, ZG_FMT_DENSE, ZG_F
                    zg_decode_static, zg_decode_trace, zg_decode_workspace_size, zg_index_build,
                    zg_index_export, zg_index_info_get, zg_index_load, zg_index_save, zg_index_stats,
                    zg_plan_describe, zg_plan_force, zg_plan_load, zg_plan_save, zg_plan_set_fusion,
-                   zg_plan_set_full_projection, zg_plan_set_order, zg_tune, zg_version)
+                   zg_plan_set_full_projection, zg_plan_set_order, zg_tune, zg_version, KV_FORMATS, ZG_KV_E4M3,
+                   ZG_KV_INT8, make_kv_cache, make_norm_rope, make_rows, zg_kv_append, zg_kv_attention,
+                   zg_kv_attention_workspace_size, zg_kv_read, zg_qk_norm_rope)
 
 __all__ = [
     "DTYPES", "LIB_PATH", "ZG_BF16", "ZG_F16", "ZG_F32", "ZG_FMT_DENSE", "ZG_FMT_SPARSE",
@@ -28,4 +30,6 @@ __all__ = [
     "zg_index_export", "zg_index_info_get", "zg_index_load", "zg_index_save", "zg_index_stats",
     "zg_plan_describe", "zg_plan_force", "zg_plan_load", "zg_plan_save", "zg_plan_set_fusion",
     "zg_plan_set_full_projection", "zg_plan_set_order", "zg_tune", "zg_version",
+    "KV_FORMATS", "ZG_KV_E4M3", "ZG_KV_INT8", "make_kv_cache", "make_norm_rope", "make_rows", "zg_kv_append",
+    "zg_kv_attention", "zg_kv_attention_workspace_size", "zg_kv_read", "zg_qk_norm_rope",
 ]

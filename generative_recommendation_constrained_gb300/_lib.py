@@ -80,6 +80,28 @@ class zg_trace(C.Structure):
                 ("ms_fused", C.c_float), ("ms_total", C.c_float)]
 
 
+ZG_KV_E4M3, ZG_KV_INT8 = 0, 1
+KV_FORMATS = {"e4m3": ZG_KV_E4M3, "int8": ZG_KV_INT8}
+
+
+class zg_rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("dtype", C.c_int32), ("reserved", C.c_int32),
+                ("stride_b", C.c_int64), ("stride_t", C.c_int64), ("stride_h", C.c_int64)]
+
+
+class zg_kv_cache(C.Structure):
+    _fields_ = [("format", C.c_int32), ("n_blocks", C.c_int32), ("heads", C.c_int32),
+                ("block_tokens", C.c_int32), ("dim", C.c_int32), ("reserved", C.c_int32),
+                ("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p)]
+
+
+class zg_norm_rope(C.Structure):
+    _fields_ = [("norm", C.c_int32), ("eps", C.c_float), ("q_gain", C.c_void_p), ("k_gain", C.c_void_p),
+                ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("theta", C.c_double),
+                ("freq", C.POINTER(C.c_double))]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() (nvcc, sm_103a)")
@@ -108,6 +130,12 @@ def _load():
         "zg_check_device_status": [vp],
         "zg_plan_save": [vp, C.c_char_p],
         "zg_plan_load": [C.c_char_p, P(vp)],
+        "zg_qk_norm_rope": [P(zg_norm_rope)] + [P(zg_rows)] * 4 + [vp] + [i32] * 5 + [vp],
+        "zg_kv_append": [P(zg_kv_cache), P(zg_norm_rope)] + [P(zg_rows)] * 4 + [i32, vp, i32, vp, vp, i32, i32, vp],
+        "zg_kv_read": [P(zg_kv_cache), vp, i32, vp, vp, i32, i32, P(zg_rows), P(zg_rows), vp],
+        "zg_kv_attention_workspace_size": [P(zg_kv_cache), i32, i32, i32, i32, P(sz)],
+        "zg_kv_attention": [P(zg_kv_cache), vp, i32, vp, vp, P(zg_rows), P(zg_rows), vp, i32, i32, i32, C.c_float,
+                            i32, vp, sz, vp],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -377,3 +405,56 @@ def zg_plan_set_fusion(plan: Plan, cluster_ctas):
     if cluster_ctas is True:
         cluster_ctas = 8
     _check(lib.zg_plan_set_fusion(plan, int(cluster_ctas)))
+
+
+def make_rows(data, dtype: int, stride_b: int, stride_t: int, stride_h: int) -> zg_rows:
+    """zg_rows from a device pointer (or tensor) and element strides."""
+    return zg_rows(_ptr(data), dtype, 0, stride_b, stride_t, stride_h)
+
+
+def make_kv_cache(fmt: int, n_blocks: int, heads: int, block_tokens: int, dim: int, k_codes, v_codes, k_scale,
+                  v_scale) -> zg_kv_cache:
+    return zg_kv_cache(fmt, n_blocks, heads, block_tokens, dim, 0, _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
+                       _ptr(v_scale))
+
+
+def make_norm_rope(norm: bool, eps: float, q_gain, k_gain, rot_dim: int, interleaved: bool, theta: float,
+                   freq=None) -> zg_norm_rope:
+    """freq: radians a position of each pair (host sequence), or None for theta^(-2i/rot_dim)."""
+    s = zg_norm_rope(int(norm), eps, _ptr(q_gain), _ptr(k_gain), rot_dim, int(interleaved), theta, None)
+    if freq is not None:
+        if len(freq) != rot_dim // 2:
+            raise ValueError("freq must have rot_dim / 2 entries")
+        s._freq = (C.c_double * len(freq))(*[float(f) for f in freq])      # kept alive with the struct
+        s.freq = C.cast(s._freq, C.POINTER(C.c_double))
+    return s
+
+
+def zg_qk_norm_rope(nr: zg_norm_rope, q, k, q_out, k_out, positions, B: int, T: int, Hq: int, Hk: int, dim: int,
+                    stream: int = 0):
+    """q, k, q_out, k_out: zg_rows or None."""
+    _check(lib.zg_qk_norm_rope(nr, q, k, q_out, k_out, _ptr(positions), B, T, Hq, Hk, dim, stream or None))
+
+
+def zg_kv_append(cache: zg_kv_cache, nr, k, v, q, q_out, Hq: int, table, max_blocks: int, start, n_new, B: int,
+                 T: int, stream: int = 0):
+    """k, v, q, q_out: zg_rows (q and q_out may be None)."""
+    _check(lib.zg_kv_append(cache, nr, k, v, q, q_out, Hq, _ptr(table), max_blocks, _ptr(start), _ptr(n_new), B, T,
+                            stream or None))
+
+
+def zg_kv_read(cache: zg_kv_cache, table, max_blocks: int, start, n, B: int, T: int, k_out, v_out, stream: int = 0):
+    _check(lib.zg_kv_read(cache, _ptr(table), max_blocks, _ptr(start), _ptr(n), B, T, k_out, v_out, stream or None))
+
+
+def zg_kv_attention_workspace_size(cache: zg_kv_cache, max_blocks: int, B: int, R: int, Hq: int) -> int:
+    n = C.c_size_t(0)
+    _check(lib.zg_kv_attention_workspace_size(cache, max_blocks, B, R, Hq, C.byref(n)))
+    return n.value
+
+
+def zg_kv_attention(cache: zg_kv_cache, table, max_blocks: int, length, n_rows, q, out, lse, B: int, R: int,
+                    Hq: int, scale: float, causal: bool, workspace, ws_bytes: int, stream: int = 0):
+    """q, out: zg_rows."""
+    _check(lib.zg_kv_attention(cache, _ptr(table), max_blocks, _ptr(length), _ptr(n_rows), q, out, _ptr(lse), B, R,
+                               Hq, scale, int(causal), _ptr(workspace), ws_bytes, stream or None))

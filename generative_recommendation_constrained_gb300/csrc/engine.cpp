@@ -235,6 +235,8 @@ std::mutex g_status_mu;
 uint32_t* g_status_ptr[64] = {};
 unsigned long long g_status_ctx[64] = {};
 
+}  // namespace
+
 zg_status get_status_ptr(uint32_t** p) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -251,6 +253,8 @@ zg_status get_status_ptr(uint32_t** p) {
   *p = g_status_ptr[dev];
   return ZG_OK;
 }
+
+namespace {
 
 // Everything one decode needs, resolved once.
 struct Run {
@@ -1123,6 +1127,8 @@ zg_status zg_check_device_status(void* stream) {
   if (v & kStatusTimeout) msg += " tensor-core wait expired;";
   if (v & kStatusTmem) msg += " tensor-memory allocation failed;";
   if (v & kStatusSelect) msg += " select found fewer candidates than its cut;";
+  if (v & kStatusCache) msg += " history cache block or length out of range;";
+  if (v & kStatusNonFinite) msg += " NaN or infinity written to a history cache;";
   return fail(ZG_ERR_DEVICE_STATUS, msg);
 }
 

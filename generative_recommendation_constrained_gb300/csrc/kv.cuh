@@ -1,0 +1,236 @@
+// Device helpers of the history cache: rows of activations in three types,
+// the 8-bit codes, and the norm and rotation of one head.
+#pragma once
+
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "zg_internal.h"
+
+namespace zg {
+
+// zg_rows as a kernel argument.
+template <typename T>
+struct Rows {
+  T* data;
+  int64_t sb, st, sh;
+  __device__ __forceinline__ T* at(int b, int t, int h) const { return data + b * sb + t * st + h * sh; }
+};
+
+template <typename T>
+inline Rows<T> rows_of(const zg_rows* r) {
+  Rows<T> o = {};
+  if (r) o = {static_cast<T*>(r->data), r->stride_b, r->stride_t, r->stride_h};
+  return o;
+}
+
+// Four neighbouring elements, widened to or rounded from float.
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+}
+__device__ __forceinline__ void load4(const __half* p, float* v) {
+  const uint2 x = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
+  const uint2 x = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__half* p, const float* v) {
+  const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// Two e4m3 codes (low byte first) as halves; every e4m3 value is one exactly.
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t two) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
+  return d;
+}
+
+// Four codes to four halves, exactly: (code 0, code 1), (code 2, code 3).
+// int8: the code with its sign bit flipped is code + 128 = the low mantissa
+// bits of the half 1024 + that; subtracting 1152 leaves the code.
+template <bool INT8>
+__device__ __forceinline__ void codes_half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (INT8) {
+    w ^= 0x80808080u;
+    lo = __byte_perm(w, 0x64646464u, 0x4140);
+    hi = __byte_perm(w, 0x64646464u, 0x4342);
+    const uint32_t off = 0x64806480u;
+    *reinterpret_cast<__half2*>(&lo) =
+        __hsub2(*reinterpret_cast<__half2*>(&lo), *reinterpret_cast<const __half2*>(&off));
+    *reinterpret_cast<__half2*>(&hi) =
+        __hsub2(*reinterpret_cast<__half2*>(&hi), *reinterpret_cast<const __half2*>(&off));
+  } else {
+    lo = e4m3x2_half2(w & 0xFFFFu);
+    hi = e4m3x2_half2(w >> 16);
+  }
+}
+
+template <bool INT8>
+__device__ __forceinline__ void codes_float4(uint32_t w, float* v) {
+  uint32_t lo, hi;
+  codes_half4<INT8>(w, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+
+// Four values times `inv` to codes: to nearest even, within +-Q.
+template <bool INT8>
+__device__ __forceinline__ uint32_t float4_codes(const float* v, float inv) {
+  if constexpr (INT8) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = __float2int_rn(fminf(fmaxf(v[i] * inv, -127.f), 127.f));
+      w |= ((uint32_t)q & 0xFFu) << (8 * i);
+    }
+    return w;
+  } else {
+    uint16_t a, b;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(v[1] * inv), "f"(v[0] * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(v[3] * inv), "f"(v[2] * inv));
+    return (uint32_t)a | ((uint32_t)b << 16);
+  }
+}
+
+// Lanes of a head's row: eight elements a lane, groups of a power of two
+// (a head of 96 leaves four of its sixteen lanes idle).
+template <int D>
+struct HeadLanes {
+  static constexpr int kUsed = D / 8;
+  static constexpr int kGroup = D == 96 ? 16 : D / 8;
+};
+
+// zg_norm_rope as a kernel argument: pair i turns by turns[i] * 2^-64 of a
+// full turn a position.  Products with the position wrap modulo 2^64, which
+// takes the turns modulo 1 exactly, whatever the position.
+struct NormRopeArgs {
+  int32_t norm, rot, inter;
+  float eps;
+  const float *q_gain, *k_gain;
+  uint64_t turns[64];
+};
+
+// What one lane holds of a head: elements e0..e0+3 and e1..e1+3.  Rotated
+// lanes hold four whole pairs: (e0 + i, e1 + i), or interleaved neighbours.
+struct LaneMap {
+  int e0, e1;
+  bool used, rotated;
+};
+
+template <int D>
+__device__ __forceinline__ LaneMap lane_map(const NormRopeArgs& a, int l) {
+  LaneMap m;
+  m.used = l < HeadLanes<D>::kUsed;
+  m.rotated = m.used && 8 * l < a.rot;
+  if (a.inter || !m.rotated) {
+    m.e0 = 8 * l;
+    m.e1 = 8 * l + 4;
+  } else {
+    m.e0 = 4 * l;
+    m.e1 = 4 * l + a.rot / 2;
+  }
+  return m;
+}
+
+__device__ __forceinline__ void lane_angles(const NormRopeArgs& a, const LaneMap& m, int l, int pos, float* cs,
+                                            float* sn) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+    if (m.rotated) {
+      const uint64_t t = (uint64_t)(int64_t)pos * a.turns[4 * l + i];
+      sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+    }
+  }
+}
+
+// x[0..3] = elements e0.., x[4..7] = elements e1.. of one head, in place.
+// Every lane of the warp takes part (group sums by shuffles).
+template <int D>
+__device__ __forceinline__ void norm_rotate(const NormRopeArgs& a, const LaneMap& m, const float* gain, float* x,
+                                            const float* cs, const float* sn) {
+  if (a.norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int o = HeadLanes<D>::kGroup / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    const float inv = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * gain[i];
+  }
+  if (m.rotated) {
+    if (a.inter) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float u = x[2 * i], v = x[2 * i + 1];
+        x[2 * i] = u * cs[i] - v * sn[i];
+        x[2 * i + 1] = u * sn[i] + v * cs[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float u = x[i], v = x[4 + i];
+        x[i] = u * cs[i] - v * sn[i];
+        x[4 + i] = u * sn[i] + v * cs[i];
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void lane_gain(const float* gain, const LaneMap& m, float* g) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = 1.f;
+  if (gain && m.used) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      g[i] = gain[m.e0 + i];
+      g[4 + i] = gain[m.e1 + i];
+    }
+  }
+}
+
+// Run-time head size and type as template arguments: f(Dim<D>{}), f(Elem<T>{}).
+template <int D>
+using Dim = std::integral_constant<int, D>;
+template <typename T>
+struct Elem {
+  using type = T;
+};
+
+template <typename F>
+void for_dim(int dim, F&& f) {
+  switch (dim) {
+    case 32: f(Dim<32>{}); break;
+    case 64: f(Dim<64>{}); break;
+    case 96: f(Dim<96>{}); break;
+    default: f(Dim<128>{}); break;
+  }
+}
+
+// host checks shared by the entry points (kv_cache.cu)
+zg_status bad_arg(const char* call, const std::string& what);
+zg_status check_rows(const zg_rows* r, const char* name, int dtype, const char* call);
+zg_status check_cache(const zg_kv_cache* c, const int32_t* table, int32_t max_blocks, const char* call);
+
+}  // namespace zg

@@ -1,0 +1,502 @@
+// The history cache's writes: per-head norm and rotation, quantised writes,
+// reads.  All are bound by memory; each input element is loaded once and each
+// output written once, with 32-bit arithmetic between.
+//
+//   norm     y = x / sqrt(mean(x^2) + eps) * gain over a head
+//   rotation (a, b) -> (a cos - b sin, a sin + b cos) by position * frequency
+//   code     rne(y / scale), scale = max |y| of a (block, head) / Q
+//
+// A lane holds eight elements of a head as two vectors of four that make four
+// whole rotation pairs, so the rotation needs no exchange between lanes and
+// the norm one short shuffle sum.
+#include <cfloat>
+#include <cmath>
+#include <string>
+
+#include "kv.cuh"
+
+namespace zg {
+namespace {
+
+// ---------------------------------------------------------- norm + rotation
+
+template <typename T>
+struct RotateArgs {
+  Rows<T> q, k, qo, ko;
+  const int32_t* pos;
+  int32_t B, T_, Hq, Hk, chunk, nchunk;  // heads a group of lanes walks; such chunks a token
+  NormRopeArgs nr;
+};
+
+// One group of lanes a (token, chunk of heads): the angles are computed once
+// for the chunk.  Heads 0..Hq-1 are the queries, Hq..Hq+Hk-1 the keys.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_norm_rope(const __grid_constant__ RotateArgs<T> a) {
+  constexpr int GS = HeadLanes<D>::kGroup;
+  const int l = threadIdx.x % GS;
+  const int64_t g = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS;
+  const int64_t token = g / a.nchunk;
+  const bool live = token < (int64_t)a.B * a.T_;
+  const int b = live ? (int)(token / a.T_) : 0, t = live ? (int)(token % a.T_) : 0;
+  const int h0 = (int)(g % a.nchunk) * a.chunk;
+  const LaneMap m = lane_map<D>(a.nr, l);
+  float cs[4], sn[4], gq[8], gk[8];
+  lane_angles(a.nr, m, l, live && a.nr.rot ? a.pos[token] : 0, cs, sn);
+  lane_gain(a.nr.q_gain, m, gq);
+  lane_gain(a.nr.k_gain, m, gk);
+  for (int i = 0; i < a.chunk; ++i) {
+    const int h = h0 + i;
+    const bool on = live && m.used && h < a.Hq + a.Hk;
+    const bool isq = h < a.Hq;
+    float x[8] = {};
+    if (on) {
+      const T* p = isq ? a.q.at(b, t, h) : a.k.at(b, t, h - a.Hq);
+      load4(p + m.e0, x);
+      load4(p + m.e1, x + 4);
+    }
+    norm_rotate<D>(a.nr, m, isq ? gq : gk, x, cs, sn);
+    if (on) {
+      T* p = isq ? a.qo.at(b, t, h) : a.ko.at(b, t, h - a.Hq);
+      store4(p + m.e0, x);
+      store4(p + m.e1, x + 4);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- append
+
+struct CacheView {
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  int32_t n_blocks, heads, bt, max_blocks;
+  const int32_t* table;
+  uint32_t* status;
+};
+
+template <typename T>
+struct AppendArgs {
+  CacheView c;
+  Rows<T> k, v, q, qo;
+  const int32_t *start, *n_new;
+  int32_t B, T_, Hq, jmax;      // jmax: blocks that T_ tokens may touch
+  int32_t kv_ctas, chunk, nchunk;
+  int32_t has_nr;
+  NormRopeArgs nr;
+};
+
+constexpr int kPasses = 8;  // rows a lane group keeps in registers
+
+// One CTA a (block, side, head) that is written: the rows stay in registers
+// between the maximum and the codes.  CTAs past kv_ctas turn the queries.
+template <typename T, int D, bool INT8>
+__global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ AppendArgs<T> a) {
+  constexpr int GS = HeadLanes<D>::kGroup;
+  constexpr float Q = INT8 ? 127.f : 448.f;
+  __shared__ float red[8];
+  const int l = threadIdx.x % GS, grp = threadIdx.x / GS, rpp = blockDim.x / GS;
+  const LaneMap m = lane_map<D>(a.nr, l);
+
+  if (blockIdx.x >= a.kv_ctas) {
+    const int64_t g = (int64_t)(blockIdx.x - a.kv_ctas) * rpp + grp;
+    const int64_t token = g / a.nchunk;
+    const bool live = token < (int64_t)a.B * a.T_;
+    const int b = live ? (int)(token / a.T_) : 0, t = live ? (int)(token % a.T_) : 0;
+    const int h0 = (int)(g % a.nchunk) * a.chunk;
+    float cs[4], sn[4], gq[8];
+    lane_angles(a.nr, m, l, live ? a.start[b] + t : 0, cs, sn);
+    lane_gain(a.nr.q_gain, m, gq);
+    for (int i = 0; i < a.chunk; ++i) {
+      const int h = h0 + i;
+      const bool on = live && m.used && h < a.Hq;
+      float x[8] = {};
+      if (on) {
+        load4(a.q.at(b, t, h) + m.e0, x);
+        load4(a.q.at(b, t, h) + m.e1, x + 4);
+      }
+      norm_rotate<D>(a.nr, m, gq, x, cs, sn);
+      if (on) {
+        store4(a.qo.at(b, t, h) + m.e0, x);
+        store4(a.qo.at(b, t, h) + m.e1, x + 4);
+      }
+    }
+    return;
+  }
+
+  int it = blockIdx.x;
+  const int h = it % a.c.heads;
+  it /= a.c.heads;
+  const int side = it & 1;
+  it >>= 1;
+  const int j = it % a.jmax, b = it / a.jmax;
+  const int start = a.start[b];
+  const int n = a.n_new ? a.n_new[b] : a.T_;
+  if (start < 0 || n < 0 || n > a.T_ || (int64_t)start + n > (int64_t)a.c.max_blocks * a.c.bt) {
+    if (threadIdx.x == 0) atomicOr(a.c.status, kStatusCache);
+    return;
+  }
+  const int bj = start / a.c.bt + j;
+  const int lo = j ? 0 : start - bj * a.c.bt;
+  const int64_t left = (int64_t)start + n - (int64_t)bj * a.c.bt;
+  const int hi = left < a.c.bt ? (int)left : a.c.bt;
+  if (n == 0 || hi <= lo) return;
+  const int blk = a.c.table[(int64_t)b * a.c.max_blocks + bj];
+  if (blk < 0 || blk >= a.c.n_blocks) {
+    if (threadIdx.x == 0) atomicOr(a.c.status, kStatusCache);
+    return;
+  }
+  const int64_t bh = (int64_t)blk * a.c.heads + h;
+  float* scale = (side ? a.c.vs : a.c.ks) + bh;
+  uint8_t* codes = (side ? a.c.vc : a.c.kc) + bh * a.c.bt * D;
+  const Rows<T>& src = side ? a.v : a.k;
+  const bool turn = !side && a.has_nr;
+  float gk[8];
+  lane_gain(turn ? a.nr.k_gain : nullptr, m, gk);
+
+  float x[kPasses][8];
+  float top = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int r = lo + p * rpp + grp;
+    const bool on = m.used && r < hi;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[p][i] = 0.f;
+    if (on) {
+      const T* s = src.at(b, bj * a.c.bt + r - start, h);
+      load4(s + m.e0, x[p]);
+      load4(s + m.e1, x[p] + 4);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int r = lo + p * rpp + grp;
+    if (lo + p * rpp < hi) {  // uniform over the CTA
+      if (turn) {
+        float cs[4], sn[4];
+        lane_angles(a.nr, m, l, bj * a.c.bt + r, cs, sn);
+        norm_rotate<D>(a.nr, m, gk, x[p], cs, sn);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = fabsf(x[p][i]);
+        if (y <= FLT_MAX) {
+          top = fmaxf(top, m.used && r < hi ? y : 0.f);
+        } else {  // NaN -> 0; an infinity saturates
+          bad |= m.used && r < hi;
+          x[p][i] = isnan(x[p][i]) ? 0.f : copysignf(FLT_MAX, x[p][i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  if (blockDim.x > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+    __syncthreads();
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) top = fmaxf(top, red[w]);
+  }
+  const float s0 = lo ? *scale : 0.f;
+  float s1 = fmaxf(s0, __fdiv_rn(top, Q));
+  if (s1 < FLT_MIN) s1 = 0.f;  // 1 / s1 stays finite
+  const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
+  __syncthreads();  // every thread has read the old scale
+  if (threadIdx.x == 0) *scale = s1;
+  if (bad) atomicOr(a.c.status, kStatusNonFinite);
+  if (s1 > s0 && m.used) {
+    for (int r = grp; r < lo; r += rpp) {  // rows held already: the scale has grown
+      uint32_t* w0 = reinterpret_cast<uint32_t*>(codes + r * D + m.e0);
+      uint32_t* w1 = reinterpret_cast<uint32_t*>(codes + r * D + m.e1);
+      float y[8];
+      codes_float4<INT8>(*w0, y);
+      codes_float4<INT8>(*w1, y + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= s0;
+      *w0 = float4_codes<INT8>(y, inv);
+      *w1 = float4_codes<INT8>(y + 4, inv);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int r = lo + p * rpp + grp;
+    if (m.used && r < hi) {
+      *reinterpret_cast<uint32_t*>(codes + r * D + m.e0) = float4_codes<INT8>(x[p], inv);
+      *reinterpret_cast<uint32_t*>(codes + r * D + m.e1) = float4_codes<INT8>(x[p] + 4, inv);
+    }
+  }
+}
+
+// --------------------------------------------------------------------- read
+
+template <typename T>
+struct ReadArgs {
+  CacheView c;
+  Rows<T> ko, vo;
+  const int32_t *start, *n;
+  int32_t B, T_, sides, side0;
+};
+
+// One group of lanes a (token, side, head), eight codes a lane.
+template <typename T, int D, bool INT8>
+__global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ ReadArgs<T> a) {
+  constexpr int GS = HeadLanes<D>::kGroup;
+  const int l = threadIdx.x % GS;
+  int64_t g = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS;
+  const int h = (int)(g % a.c.heads);
+  g /= a.c.heads;
+  const int side = a.side0 + (int)(g % a.sides);
+  g /= a.sides;
+  if (g >= (int64_t)a.B * a.T_ || l >= HeadLanes<D>::kUsed) return;
+  const int t = (int)(g % a.T_), b = (int)(g / a.T_);
+  const int n = a.n ? a.n[b] : a.T_;
+  const int start = a.start[b];
+  float x[8] = {};
+  if (t < n) {
+    const int64_t p = (int64_t)start + t;
+    int blk = -1;
+    if (start >= 0 && p < (int64_t)a.c.max_blocks * a.c.bt)
+      blk = a.c.table[(int64_t)b * a.c.max_blocks + p / a.c.bt];
+    if (blk < 0 || blk >= a.c.n_blocks) {
+      if (l == 0) atomicOr(a.c.status, kStatusCache);
+    } else {
+      const int64_t bh = (int64_t)blk * a.c.heads + h;
+      const float s = (side ? a.c.vs : a.c.ks)[bh];
+      const uint8_t* codes = (side ? a.c.vc : a.c.kc) + (bh * a.c.bt + p % a.c.bt) * D + 8 * l;
+      const uint2 w = *reinterpret_cast<const uint2*>(codes);
+      codes_float4<INT8>(w.x, x);
+      codes_float4<INT8>(w.y, x + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= s;
+    }
+  }
+  T* o = (side ? a.vo : a.ko).at(b, t, h) + 8 * l;
+  store4(o, x);
+  store4(o + 4, x + 4);
+}
+
+// ---------------------------------------------------------------- host side
+
+bool dim_ok(int d) { return d == 32 || d == 64 || d == 96 || d == 128; }
+
+// zg_norm_rope (NULL: neither norm nor rotation) as a kernel argument.
+zg_status nr_args(const zg_norm_rope* nr, int dim, const char* call, NormRopeArgs* o) {
+  *o = {};
+  if (!nr) return ZG_OK;
+  if (nr->rot_dim < 0 || nr->rot_dim > dim || nr->rot_dim % 8)
+    return bad_arg(call, "rot_dim must be a multiple of 8 in [0, dim]");
+  if (nr->norm && !(nr->eps >= 0.f && std::isfinite(nr->eps))) return bad_arg(call, "eps must be finite and >= 0");
+  if ((reinterpret_cast<uintptr_t>(nr->q_gain) | reinterpret_cast<uintptr_t>(nr->k_gain)) % 4)
+    return bad_arg(call, "gains must be aligned to 4 bytes");
+  if (nr->rot_dim && !nr->freq && !(nr->theta >= 1.0 && std::isfinite(nr->theta)))
+    return bad_arg(call, "theta must be finite and >= 1 (or freq given)");
+  o->norm = nr->norm != 0;
+  o->rot = nr->rot_dim;
+  o->inter = nr->interleaved != 0;
+  o->eps = nr->eps;
+  o->q_gain = nr->q_gain;
+  o->k_gain = nr->k_gain;
+  for (int i = 0; i < nr->rot_dim / 2; ++i) {
+    const double f = nr->freq ? nr->freq[i] : std::pow(nr->theta, -2.0 * i / nr->rot_dim);
+    if (!(f >= 0.0 && f <= 4.0)) return bad_arg(call, "freq must be in [0, 4]");
+    o->turns[i] = (uint64_t)(f / 6.283185307179586476925 * 18446744073709551616.0);
+  }
+  return ZG_OK;
+}
+
+CacheView view(const zg_kv_cache* c, const int32_t* table, int32_t max_blocks, uint32_t* status) {
+  return {static_cast<uint8_t*>(c->k_codes), static_cast<uint8_t*>(c->v_codes), c->k_scale, c->v_scale,
+          c->n_blocks, c->heads, c->block_tokens, max_blocks, table, status};
+}
+
+template <typename F>
+void for_type(int dtype, F&& f) {
+  if (dtype == ZG_F32) f(Elem<float>{});
+  else if (dtype == ZG_BF16) f(Elem<__nv_bfloat16>{});
+  else f(Elem<__half>{});
+}
+
+int group_lanes(int dim) { return dim == 96 ? 16 : dim / 8; }
+
+// Heads a lane group walks: all of a token's when there are tokens enough for
+// every SM, fewer when there are not.
+int head_chunk(int64_t tokens, int heads, int lanes) {
+  const int64_t room = (int64_t)sm_count() * 1024;  // threads that keep the memory busy
+  const int64_t all = tokens * heads * lanes;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(heads, all / room));
+}
+
+zg_status after_launch(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ZG_OK : cuda_fail(e, what);
+}
+
+}  // namespace
+
+zg_status bad_arg(const char* call, const std::string& what) {
+  return fail(ZG_ERR_INVALID_ARG, std::string(call) + ": " + what);
+}
+
+zg_status check_rows(const zg_rows* r, const char* name, int dtype, const char* call) {
+  if (!r || !r->data) return bad_arg(call, std::string(name) + " is NULL");
+  if (r->dtype != ZG_F32 && r->dtype != ZG_BF16 && r->dtype != ZG_F16)
+    return bad_arg(call, std::string(name) + ".dtype must be ZG_F32, ZG_BF16 or ZG_F16");
+  if (dtype >= 0 && r->dtype != dtype) return bad_arg(call, std::string(name) + " must have the type of the other rows");
+  if (r->stride_b < 0 || r->stride_t < 0 || r->stride_h < 0 || (r->stride_b | r->stride_t | r->stride_h) % 4)
+    return bad_arg(call, std::string(name) + " strides must be non-negative multiples of 4");
+  if (reinterpret_cast<uintptr_t>(r->data) % (r->dtype == ZG_F32 ? 16 : 8))
+    return bad_arg(call, std::string(name) + ".data must be aligned to 4 elements");
+  return ZG_OK;
+}
+
+zg_status check_cache(const zg_kv_cache* c, const int32_t* table, int32_t max_blocks, const char* call) {
+  if (!c) return bad_arg(call, "cache is NULL");
+  if (c->format != ZG_KV_E4M3 && c->format != ZG_KV_INT8)
+    return bad_arg(call, "cache.format must be ZG_KV_E4M3 or ZG_KV_INT8");
+  if (c->n_blocks < 1 || c->heads < 1 || c->heads > 1024)
+    return bad_arg(call, "cache needs n_blocks >= 1 and heads in [1, 1024]");
+  const int t = c->block_tokens;
+  if (t != 16 && t != 32 && t != 64 && t != 128)
+    return bad_arg(call, "cache.block_tokens must be 16, 32, 64 or 128");
+  if (!dim_ok(c->dim)) return fail(ZG_ERR_UNSUPPORTED, std::string(call) + ": cache.dim must be 32, 64, 96 or 128");
+  if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale) return bad_arg(call, "cache pointer is NULL");
+  if ((reinterpret_cast<uintptr_t>(c->k_codes) | reinterpret_cast<uintptr_t>(c->v_codes)) % 16)
+    return bad_arg(call, "cache codes must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale)) % 4)
+    return bad_arg(call, "cache scales must be 4-byte aligned");
+  if (!table || reinterpret_cast<uintptr_t>(table) % 4) return bad_arg(call, "table is NULL or not 4-byte aligned");
+  if (max_blocks < 1 || (int64_t)max_blocks * c->block_tokens > 0x7FFFFFFF)
+    return bad_arg(call, "max_blocks must be >= 1 with max_blocks * block_tokens below 2^31");
+  return ZG_OK;
+}
+
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" {
+
+zg_status zg_qk_norm_rope(const zg_norm_rope* nr, const zg_rows* q, const zg_rows* k, const zg_rows* q_out,
+                          const zg_rows* k_out, const int32_t* positions, int32_t B, int32_t T, int32_t Hq,
+                          int32_t Hk, int32_t dim, void* stream) try {
+  const char* call = "zg_qk_norm_rope";
+  zg_status st;
+  if (!nr) return bad_arg(call, "norm_rope is NULL");
+  if (!dim_ok(dim)) return fail(ZG_ERR_UNSUPPORTED, "zg_qk_norm_rope: dim must be 32, 64, 96 or 128");
+  if (B < 0 || T < 0) return bad_arg(call, "B and T must be >= 0");
+  if (Hq < 0 || Hk < 0 || Hq > 1024 || Hk > 1024) return bad_arg(call, "Hq and Hk must be in [0, 1024]");
+  if ((!q) != (Hq == 0) || (!k) != (Hk == 0))
+    return bad_arg(call, "q and k are NULL exactly when their head count is 0");
+  if (Hq + Hk == 0) return bad_arg(call, "neither q nor k given");
+  const int dt = q ? q->dtype : k->dtype;
+  if (q && ((st = check_rows(q, "q", dt, call)) != ZG_OK || (st = check_rows(q_out, "q_out", dt, call)) != ZG_OK))
+    return st;
+  if (k && ((st = check_rows(k, "k", dt, call)) != ZG_OK || (st = check_rows(k_out, "k_out", dt, call)) != ZG_OK))
+    return st;
+  NormRopeArgs na;
+  if ((st = nr_args(nr, dim, call, &na)) != ZG_OK) return st;
+  if (na.rot && !positions) return bad_arg(call, "positions is NULL");
+  const int64_t tokens = (int64_t)B * T;
+  if (tokens == 0) return ZG_OK;
+  const int lanes = group_lanes(dim), heads = Hq + Hk;
+  const int chunk = head_chunk(tokens, heads, lanes), nchunk = (heads + chunk - 1) / chunk;
+  const int64_t ctas = (tokens * nchunk * lanes + 255) / 256;
+  if (ctas > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_qk_norm_rope: more than 2^31 CTAs");
+  for_type(dt, [&](auto e) {
+    using E = typename decltype(e)::type;
+    const RotateArgs<E> a = {rows_of<E>(q), rows_of<E>(k), rows_of<E>(q_out), rows_of<E>(k_out), positions,
+                             B, T, Hq, Hk, chunk, nchunk, na};
+    for_dim(dim, [&](auto dv) {
+      k_norm_rope<E, decltype(dv)::value><<<(unsigned)ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    });
+  });
+  return after_launch("norm and rotation launch");
+} catch (...) {
+  return ZG_ERR_OUT_OF_MEMORY;
+}
+
+zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const zg_rows* k, const zg_rows* v,
+                       const zg_rows* q, const zg_rows* q_out, int32_t Hq, const int32_t* table, int32_t max_blocks,
+                       const int32_t* start, const int32_t* n_new, int32_t B, int32_t T, void* stream) try {
+  const char* call = "zg_kv_append";
+  zg_status st;
+  if ((st = check_cache(cache, table, max_blocks, call)) != ZG_OK) return st;
+  if (B < 0 || T < 0) return bad_arg(call, "B and T must be >= 0");
+  if ((st = check_rows(k, "k", -1, call)) != ZG_OK || (st = check_rows(v, "v", k->dtype, call)) != ZG_OK) return st;
+  if (Hq < 0 || Hq > 1024 || (!q) != (Hq == 0))
+    return bad_arg(call, "Hq must be in [0, 1024], and 0 exactly when q is NULL");
+  if (q) {
+    if (!nr) return bad_arg(call, "q given without a norm_rope");
+    if ((st = check_rows(q, "q", k->dtype, call)) != ZG_OK ||
+        (st = check_rows(q_out, "q_out", k->dtype, call)) != ZG_OK)
+      return st;
+  }
+  if (!start) return bad_arg(call, "start is NULL");
+  NormRopeArgs na;
+  if ((st = nr_args(nr, cache->dim, call, &na)) != ZG_OK) return st;
+  if (B == 0 || T == 0) return ZG_OK;
+  const int bt = cache->block_tokens, lanes = group_lanes(cache->dim);
+  const int64_t jmax = ((int64_t)T + bt - 2) / bt + 1;
+  // eight rows a lane group at most: groups for min(T, bt) rows, whole warps
+  int groups = 1;
+  while (groups * kPasses < std::min(T, bt)) groups *= 2;
+  const int threads = std::max(32, groups * lanes);
+  const int64_t kv = (int64_t)B * jmax * 2 * cache->heads;
+  const int64_t tokens = (int64_t)B * T;
+  const int chunk = Hq ? head_chunk(tokens, Hq, lanes) : 1, nchunk = Hq ? (Hq + chunk - 1) / chunk : 0;
+  const int64_t qc = (tokens * nchunk * lanes + threads - 1) / threads;
+  if (kv + qc > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^31 CTAs");
+  uint32_t* status = nullptr;
+  if ((st = get_status_ptr(&status)) != ZG_OK) return st;
+  for_type(k->dtype, [&](auto e) {
+    using E = typename decltype(e)::type;
+    const AppendArgs<E> a = {view(cache, table, max_blocks, status), rows_of<E>(k), rows_of<E>(v), rows_of<E>(q),
+                             rows_of<E>(q_out), start, n_new, B, T, Hq, (int32_t)jmax, (int32_t)kv, chunk, nchunk,
+                             nr != nullptr, na};
+    for_dim(cache->dim, [&](auto dv) {
+      constexpr int D = decltype(dv)::value;
+      if (cache->format == ZG_KV_INT8)
+        k_kv_append<E, D, true><<<(unsigned)(kv + qc), threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      else
+        k_kv_append<E, D, false><<<(unsigned)(kv + qc), threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    });
+  });
+  return after_launch("cache append launch");
+} catch (...) {
+  return ZG_ERR_OUT_OF_MEMORY;
+}
+
+zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks, const int32_t* start,
+                     const int32_t* n, int32_t B, int32_t T, const zg_rows* k_out, const zg_rows* v_out,
+                     void* stream) try {
+  const char* call = "zg_kv_read";
+  zg_status st;
+  if ((st = check_cache(cache, table, max_blocks, call)) != ZG_OK) return st;
+  if (B < 0 || T < 0) return bad_arg(call, "B and T must be >= 0");
+  if (!k_out && !v_out) return bad_arg(call, "neither k_out nor v_out given");
+  const int dt = k_out ? k_out->dtype : v_out->dtype;
+  if (k_out && (st = check_rows(k_out, "k_out", dt, call)) != ZG_OK) return st;
+  if (v_out && (st = check_rows(v_out, "v_out", dt, call)) != ZG_OK) return st;
+  if (!start) return bad_arg(call, "start is NULL");
+  if (B == 0 || T == 0) return ZG_OK;
+  const int sides = (k_out ? 1 : 0) + (v_out ? 1 : 0);
+  const int64_t ctas = ((int64_t)B * T * sides * cache->heads * group_lanes(cache->dim) + 255) / 256;
+  if (ctas > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_read: more than 2^31 CTAs");
+  uint32_t* status = nullptr;
+  if ((st = get_status_ptr(&status)) != ZG_OK) return st;
+  for_type(dt, [&](auto e) {
+    using E = typename decltype(e)::type;
+    const ReadArgs<E> a = {view(cache, table, max_blocks, status), rows_of<E>(k_out), rows_of<E>(v_out), start, n,
+                           B, T, sides, k_out ? 0 : 1};
+    for_dim(cache->dim, [&](auto dv) {
+      constexpr int D = decltype(dv)::value;
+      if (cache->format == ZG_KV_INT8)
+        k_kv_read<E, D, true><<<(unsigned)ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      else
+        k_kv_read<E, D, false><<<(unsigned)ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    });
+  });
+  return after_launch("cache read launch");
+} catch (...) {
+  return ZG_ERR_OUT_OF_MEMORY;
+}
+
+}  // extern "C"

@@ -23,6 +23,8 @@ constexpr uint32_t kStatusToken = 2u;
 constexpr uint32_t kStatusTimeout = 4u;
 constexpr uint32_t kStatusTmem = 8u;
 constexpr uint32_t kStatusSelect = 16u;  // a select found fewer candidates than its own cut guarantees
+constexpr uint32_t kStatusCache = 32u;      // history cache: block number or length out of range
+constexpr uint32_t kStatusNonFinite = 64u;  // history cache: a NaN or an infinity written
 
 // Host-side metadata of one step table.
 struct StepMeta {
@@ -170,6 +172,7 @@ constexpr int kMaxPrefetch = 24;
 cudaError_t launch_decode_cluster(const StepLaunch* steps, int s0, int L, int G, const PrefetchRegion* pf, int npf,
                                   cudaStream_t st);
 cudaError_t status_word(uint32_t** dev_ptr);   // per-device status word address
+zg_status get_status_ptr(uint32_t** p);        // the same, cached per device and context (engine.cpp)
 // One step of the light decoder (deco.cu): the new positions' rows through
 // every layer, keys and values stored, hidden vectors of the beams entering
 // step s into H.

@@ -69,3 +69,169 @@ class Decoder:
             stream = torch.cuda.current_stream().cuda_stream
         return Z.zg_decode_trace(self.idx, self.plan, self.dm.struct, u, self.B, self.beam, self.K,
                                  self.out_sids, self.out_scores, self.ws, self.ws_bytes, stream)
+
+
+_ROW_TYPES = {torch.float32: Z.ZG_F32, torch.bfloat16: Z.ZG_BF16, torch.float16: Z.ZG_F16}
+_CODE_TYPES = {torch.float8_e4m3fn: Z.ZG_KV_E4M3, torch.int8: Z.ZG_KV_INT8}
+
+
+def _rows(x: torch.Tensor | None):
+    """zg_rows of a [B, T, heads, dim] tensor whose last dimension is contiguous."""
+    if x is None:
+        return None
+    dt = _ROW_TYPES.get(x.dtype)
+    if dt is None:
+        raise ValueError(f"rows must be float32, bfloat16 or float16, not {x.dtype}")
+    sb, st, sh, se = x.stride()
+    if se != 1:
+        raise ValueError("the last dimension of the rows must be contiguous")
+    return Z.zg_rows(x.data_ptr(), dt, 0, sb, st, sh)
+
+
+def _stream(stream):
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream
+
+
+def _int32(x: torch.Tensor | None, shape, name: str):
+    if x is not None and (x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+
+
+class NormRope:
+    """Norm and rotation of query and key heads (zg_norm_rope).  gains: float32 [dim] device tensors or None;
+    norm False leaves the norm out, rot_dim 0 the rotation; freq: radians a position of each pair instead of
+    theta^(-2i / rot_dim)."""
+
+    def __init__(self, dim: int, q_gain=None, k_gain=None, eps: float = 1e-6, rot_dim: int | None = None,
+                 theta: float = 10000.0, interleaved: bool = False, norm: bool = True, freq=None):
+        for g in (q_gain, k_gain):
+            if g is not None and (g.dtype != torch.float32 or tuple(g.shape) != (dim,) or not g.is_contiguous()):
+                raise ValueError("gains must be contiguous float32 tensors of shape [dim]")
+        self.dim, self.q_gain, self.k_gain = dim, q_gain, k_gain
+        self.struct = Z.make_norm_rope(norm, eps, q_gain, k_gain, dim if rot_dim is None else rot_dim, interleaved,
+                                       theta, freq)
+
+    def __call__(self, q, k, positions, q_out=None, k_out=None, stream: int | None = None):
+        """Rows q [B, T, Hq, dim] and k [B, T, Hk, dim] (either may be None) at int32 positions [B, T]; outputs
+        default to new tensors and may be the inputs themselves."""
+        x = q if q is not None else k
+        B, T = x.shape[:2]
+        _int32(positions, (B, T), "positions")
+        for i in (q, k):
+            if i is not None and (i.shape[:2] != x.shape[:2] or i.shape[3] != self.dim):
+                raise ValueError("q and k must be [B, T, heads, dim]")
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        for i, o in ((q, q_out), (k, k_out)):
+            if i is not None and o.shape != i.shape:
+                raise ValueError("an output must have its input's shape")
+        Z.zg_qk_norm_rope(self.struct, _rows(q), _rows(k), _rows(q_out) if q is not None else None,
+                          _rows(k_out) if k is not None else None, positions, B, T,
+                          0 if q is None else q.shape[2], 0 if k is None else k.shape[2], self.dim, _stream(stream))
+        return q_out, k_out
+
+
+class KVCache:
+    """A cache of keys and values in 8 bits (zg_kv_cache): codes [n_blocks, heads, block_tokens, dim] and a scale a
+    (block, head) and side.  Block tables [B, max_blocks], lengths and counts [B] are int32 device tensors that the
+    caller keeps; entries past a request's tokens are not read."""
+
+    def __init__(self, n_blocks: int, block_tokens: int, heads: int, dim: int, fmt: str = "e4m3", device="cuda"):
+        dt = torch.float8_e4m3fn if Z.KV_FORMATS[fmt] == Z.ZG_KV_E4M3 else torch.int8
+        codes = [torch.empty((n_blocks, heads, block_tokens, dim), dtype=dt, device=device) for _ in range(2)]
+        scales = [torch.empty((n_blocks, heads), dtype=torch.float32, device=device) for _ in range(2)]
+        self._set(*codes, *scales)
+
+    @classmethod
+    def over(cls, k_codes, v_codes, k_scale, v_scale) -> "KVCache":
+        """A cache in tensors that the caller holds."""
+        self = cls.__new__(cls)
+        self._set(k_codes, v_codes, k_scale, v_scale)
+        return self
+
+    def _set(self, k_codes, v_codes, k_scale, v_scale):
+        if k_codes.dtype not in _CODE_TYPES or k_codes.dim() != 4:
+            raise ValueError("codes must be float8_e4m3fn or int8 [n_blocks, heads, block_tokens, dim]")
+        for x, like in ((v_codes, k_codes), (k_scale, None), (v_scale, None)):
+            if like is not None and (x.dtype != like.dtype or x.shape != like.shape):
+                raise ValueError("k_codes and v_codes must be alike")
+            if like is None and (x.dtype != torch.float32 or x.shape != k_codes.shape[:2]):
+                raise ValueError("scales must be float32 [n_blocks, heads]")
+        if not all(x.is_contiguous() for x in (k_codes, v_codes, k_scale, v_scale)):
+            raise ValueError("codes and scales must be contiguous")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.n_blocks, self.heads, self.block_tokens, self.dim = k_codes.shape
+        self.struct = Z.make_kv_cache(_CODE_TYPES[k_codes.dtype], self.n_blocks, self.heads, self.block_tokens,
+                                      self.dim, k_codes, v_codes, k_scale, v_scale)
+
+    def append(self, k, v, table, start, n_new=None, q=None, q_out=None, norm_rope: NormRope | None = None,
+               stream: int | None = None):
+        """Writes k, v [B, T, heads, dim] behind the start[b] tokens that each request holds (n_new[b] of the T
+        rows, all when None); norm_rope turns the keys on the way, and q [B, T, Hq, dim] into q_out, which is
+        returned."""
+        B, T = k.shape[:2]
+        if k.shape != v.shape or k.shape[2] != self.heads or k.shape[3] != self.dim:
+            raise ValueError("k and v must be [B, T, heads, dim] of the cache")
+        if table.dim() != 2:
+            raise ValueError("table must be [B, max_blocks]")
+        if norm_rope is not None and norm_rope.dim != self.dim:
+            raise ValueError("norm_rope and the cache differ in dim")
+        _int32(table, (B, table.shape[1]), "table")
+        _int32(start, (B,), "start")
+        _int32(n_new, (B,), "n_new")
+        if q is not None:
+            if q.shape[:2] != k.shape[:2] or q.shape[3] != self.dim:
+                raise ValueError("q must be [B, T, Hq, dim]")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            elif q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+        Z.zg_kv_append(self.struct, norm_rope.struct if norm_rope is not None else None, _rows(k), _rows(v), _rows(q),
+                       _rows(q_out) if q is not None else None, 0 if q is None else q.shape[2], table,
+                       table.shape[1], start, n_new, B, T, _stream(stream))
+        return q_out
+
+    def read(self, table, start, n=None, k_out=None, v_out=None, stream: int | None = None):
+        """Tokens start[b] .. start[b] + n[b] - 1 back into k_out, v_out [B, T, heads, dim] (either may be None);
+        rows from n[b] on become zero."""
+        x = k_out if k_out is not None else v_out
+        B, T = x.shape[:2]
+        for o in (k_out, v_out):
+            if o is not None and tuple(o.shape) != (B, T, self.heads, self.dim):
+                raise ValueError("outputs must be [B, T, heads, dim] of the cache")
+        _int32(table, (B, table.shape[1]), "table")
+        _int32(start, (B,), "start")
+        _int32(n, (B,), "n")
+        Z.zg_kv_read(self.struct, table, table.shape[1], start, n, B, T, _rows(k_out), _rows(v_out), _stream(stream))
+        return k_out, v_out
+
+
+class CacheAttention:
+    """Workspace and outputs for repeated zg_kv_attention calls with fixed shapes: B requests of R query rows and Hq
+    heads over `cache` through tables of max_blocks blocks."""
+
+    def __init__(self, cache: KVCache, B: int, R: int, Hq: int, max_blocks: int, causal: bool = False,
+                 scale: float | None = None, dtype=torch.bfloat16, lse: bool = False):
+        device = cache.k_codes.device
+        self.cache, self.B, self.R, self.Hq, self.max_blocks = cache, B, R, Hq, max_blocks
+        self.causal, self.scale = causal, cache.dim ** -0.5 if scale is None else scale
+        self.ws_bytes = Z.zg_kv_attention_workspace_size(cache.struct, max_blocks, B, R, Hq)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.out = torch.empty((B, R, Hq, cache.dim), dtype=dtype, device=device)
+        self.lse = torch.empty((B, R, Hq), dtype=torch.float32, device=device) if lse else None
+        self._out_rows = _rows(self.out)
+
+    def __call__(self, q, table, length, n_rows=None, stream: int | None = None):
+        """q [B, R, Hq, dim] over the first length[b] tokens of each request; returns (out, lse or None), this
+        object's own buffers."""
+        if tuple(q.shape) != tuple(self.out.shape):
+            raise ValueError("q must be [B, R, Hq, dim]")
+        _int32(table, (self.B, self.max_blocks), "table")
+        _int32(length, (self.B,), "length")
+        _int32(n_rows, (self.B,), "n_rows")
+        Z.zg_kv_attention(self.cache.struct, table, self.max_blocks, length, n_rows, _rows(q), self._out_rows,
+                          self.lse, self.B, self.R, self.Hq, self.scale, self.causal, self.ws, self.ws_bytes,
+                          _stream(stream))
+        return self.out, self.lse

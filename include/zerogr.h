@@ -401,6 +401,127 @@ ZG_API zg_status zg_decode_static(const zg_index* idx, const zg_plan* plan, cons
  * cannot read the header). */
 ZG_API size_t zg_static_scratch_bytes(void);
 
+/* -------------------------------------------------------- history cache ---
+ * The hidden vector of a request (zg_decode's u) comes from a model over the
+ * user's history.  These calls are the memory side of that model: queries
+ * and keys normalised per head and rotated by position, keys and values held
+ * in 8 bits in blocks of tokens, and attention over such a cache for single
+ * tokens, for a decode's beams (many query rows, one history) and for causal
+ * chunks.  No counterpart in the pages; they serve the model the pages take
+ * as given ([Pipeline] stage 1).
+ *
+ * All calls only launch kernels on `stream` (capturable in a CUDA graph),
+ * allocate no device memory and return ZG_ERR_INVALID_ARG /
+ * ZG_ERR_UNSUPPORTED before any launch for arguments outside what each
+ * states.  Sizes of 0 (B, T, R) are valid and do nothing.  What only the
+ * device knows is checked there: a block number outside the cache, or a
+ * length outside the table, is recorded for zg_check_device_status and the
+ * access left out. */
+
+/* Activation rows: element i of head h of token t of request b at
+ * data[b*stride_b + t*stride_t + h*stride_h + i].  Strides count elements,
+ * are non-negative multiples of 4 and may be anything else (q, k and v may
+ * share one buffer); data is aligned to 4 elements. */
+typedef struct {
+  void* data;
+  int32_t dtype; /* zg_dtype */
+  int32_t reserved;
+  int64_t stride_b, stride_t, stride_h;
+} zg_rows;
+
+typedef enum { ZG_KV_E4M3 = 0, ZG_KV_INT8 = 1 } zg_kv_format;
+
+/* A cache of keys and values in blocks of block_tokens tokens.  Codes are
+ * [n_blocks][heads][block_tokens][dim] bytes (e4m3 or two's complement), one
+ * float32 scale a (block, head) and side: value = code * scale.  A request's
+ * token p is row p % block_tokens of block table[b][p / block_tokens].
+ * dim: 32, 64, 96 or 128; block_tokens: 16, 32, 64 or 128; codes 16-byte
+ * aligned.  Device memory, caller-owned; needs no initialisation. */
+typedef struct {
+  int32_t format, n_blocks, heads, block_tokens, dim, reserved;
+  void* k_codes;
+  void* v_codes;
+  float* k_scale;
+  float* v_scale;
+} zg_kv_cache;
+
+/* Norm and rotation of query and key heads:
+ *   norm != 0: x / sqrt(mean(x^2) + eps) * gain (q_gain / k_gain device
+ *              float32 [dim], NULL: no gain), the mean over the head;
+ *   rot_dim > 0 (a multiple of 8, at most dim): elements of pair i (i and
+ *              i + rot_dim/2, or 2i and 2i + 1 when interleaved) turned by
+ *              position * f_i, f_i = freq[i] (host [rot_dim/2], radians a
+ *              position, in [0, 4]) or theta^(-2i/rot_dim), theta >= 1, when
+ *              freq is NULL.  The turn is taken modulo 1 in 64-bit fixed
+ *              point: its error at position p is below p * 2^-52 turns. */
+typedef struct {
+  int32_t norm;
+  float eps;
+  const float* q_gain;
+  const float* k_gain;
+  int32_t rot_dim, interleaved;
+  double theta;
+  const double* freq;
+} zg_norm_rope;
+
+/* q_out = norm_rope(q), k_out = norm_rope(k), one pass: read once, 32-bit
+ * arithmetic, rounded once.  q: [B][T][Hq] heads, k: [B][T][Hk]; either may
+ * be NULL with its count 0.  Outputs have their input's type and may be the
+ * input itself (same data and strides), but not overlap it otherwise.
+ * positions: device int32 [B][T] (negative ones turn backwards); may be NULL
+ * without a rotation. */
+ZG_API zg_status zg_qk_norm_rope(const zg_norm_rope* nr, const zg_rows* q, const zg_rows* k,
+                                 const zg_rows* q_out, const zg_rows* k_out, const int32_t* positions,
+                                 int32_t B, int32_t T, int32_t Hq, int32_t Hk, int32_t dim, void* stream);
+
+/* Writes up to T tokens of every request behind the start[b] tokens that it
+ * holds: token t becomes token start[b] + t, t < n_new[b] (n_new NULL: T).
+ *   scale of a (block, head) = max(its scale if the block already holds rows
+ *     of this request, largest |x| written to it / Q), Q = 448 (e4m3) or 127
+ *     (int8); below 2^-126 it is held as 0;
+ *   code = x * (1 / scale), rounded to nearest even, within +-Q; the rows
+ *     that the block already holds are coded again if the scale has grown.
+ * A NaN is stored as 0 and an infinity as +-Q of the block's finite values;
+ * either is recorded for zg_check_device_status, so no NaN enters a cache.
+ * nr (may be NULL) is applied to the keys on the way, at positions start[b]
+ * + t and before the rounding to 8 bits, and to q (may be NULL) into q_out
+ * (all T rows of it).  k, v: [B][T][heads], q: [B][T][Hq], one type.  table:
+ * device int32 [B][max_blocks]; start, n_new: device int32 [B].  Blocks
+ * written by one call must belong to one request each. */
+ZG_API zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const zg_rows* k,
+                              const zg_rows* v, const zg_rows* q, const zg_rows* q_out, int32_t Hq,
+                              const int32_t* table, int32_t max_blocks, const int32_t* start,
+                              const int32_t* n_new, int32_t B, int32_t T, void* stream);
+
+/* Reads tokens start[b] .. start[b] + n[b] - 1 (n NULL: T) back as code *
+ * scale into k_out, v_out [B][T][heads] (either may be NULL); rows from n[b]
+ * on are zero. */
+ZG_API zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,
+                            const int32_t* start, const int32_t* n, int32_t B, int32_t T, const zg_rows* k_out,
+                            const zg_rows* v_out, void* stream);
+
+/* Attention of R query rows a request over its first length[b] cached
+ * tokens: out = softmax(scale * q k^T) v, Hq query heads over cache->heads
+ * key heads (query head j reads key head j / (Hq / heads)).  scale > 0.
+ *   n_rows: device int32 [B], the request's rows (NULL: R); rows from
+ *     n_rows[b] on are outputs of a row that sees nothing.
+ *   causal: row r sees the first length[b] - (n_rows[b] - 1 - r) tokens (the
+ *     rows are the history's last tokens), otherwise all length[b].
+ *   out: q's type (ZG_BF16 or ZG_F16); lse (may be NULL): device float32
+ *     [B][R][Hq], log sum exp(scale * q k).  A row that sees nothing gives
+ *     zeros and -inf.  Outputs over parts of a history merge by their lse.
+ * Query and probability enter the products as half values (a query row
+ * scaled by a power of two first; both relative 2^-11), codes exactly; sums,
+ * maxima and outputs are 32-bit.  Cached e4m3 codes within length must not
+ * be NaN; nothing behind it is used.  Hq a multiple of heads, at most 1024;
+ * B * R * Hq below 2^31. */
+ZG_API zg_status zg_kv_attention_workspace_size(const zg_kv_cache* cache, int32_t max_blocks, int32_t B,
+                                                int32_t R, int32_t Hq, size_t* bytes);
+ZG_API zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,
+                                 const int32_t* length, const int32_t* n_rows, const zg_rows* q,
+                                 const zg_rows* out, float* lse, int32_t B, int32_t R, int32_t Hq, float scale,
+                                 int32_t causal, void* workspace, size_t ws_bytes, void* stream);
+
 /* Test and diagnosis hook, no counterpart in the paper: the number of polls
  * after which a pipeline wait (an mbarrier) of the tensor-core full
  * projection gives up, records bit 2 in the device status word and ends the
@@ -422,9 +543,11 @@ ZG_API void zg_debug_inject_build_failure(int32_t point, int32_t after);
 
 /* Synchronises `stream`, then reports and clears the device status word that
  * kernels set instead of trapping (bit 0: row out of range, bit 1: token out
- * of range, bit 2: a bounded wait in the tensor-core kernel expired, bit 3:
+ * of range, bit 2: a bounded wait in a tensor-core kernel expired, bit 3:
  * tensor-memory allocation failed, bit 4: a select found fewer candidates
- * than its own cut guarantees).  Non-zero -> ZG_ERR_DEVICE_STATUS. */
+ * than its own cut guarantees, bit 5: a history cache's block number or length
+ * out of range, bit 6: a NaN or an infinity written to a history cache).
+ * Non-zero -> ZG_ERR_DEVICE_STATUS. */
 ZG_API zg_status zg_check_device_status(void* stream);
 
 ZG_API const char* zg_last_error(void);

@@ -1,0 +1,580 @@
+"""The history cache on the GPU against its definition in 64 bits: norm and
+rotation, the quantised write, the read back, attention.  The cases are the
+places where such kernels go wrong: lengths of zero and one, blocks that end
+inside a tile, rows that see nothing, NaN behind a history, strides, heads of
+every supported size, offsets past 32 bits, other streams, captured graphs."""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+QMAX = {"e4m3": 448.0, "int8": 127.0}
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}    # half a step, relative
+
+
+@pytest.fixture(scope="module")
+def zg():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import generative_recommendation_constrained_gb300 as zg
+    return zg
+
+
+@pytest.fixture(scope="module")
+def dev(zg):
+    from generative_recommendation_constrained_gb300 import device
+    return device
+
+
+def ok(zg):
+    torch.cuda.synchronize()
+    zg.zg_check_device_status(0)
+
+
+def randn(shape, dtype, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (scale * torch.randn(shape, generator=g, device="cuda")).to(dtype)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------- norm, rotation
+
+def turned(x, gain, pos, rot, theta, inter, norm, eps=1e-6, freq=None):
+    """The definition in 64 bits, and the size of the pair each element comes from (its error's scale)."""
+    y = x.double().cpu().numpy()
+    if norm:
+        y = y / np.sqrt((y ** 2).mean(-1, keepdims=True) + eps)
+        if gain is not None:
+            y = y * gain.double().cpu().numpy()
+    size = np.abs(y)
+    if rot:
+        f = np.array(freq) if freq is not None else theta ** (-2.0 * np.arange(rot // 2) / rot)
+        a = (pos.cpu().numpy().astype(np.float64)[..., None] * f)[:, :, None]
+        i = np.arange(rot // 2)
+        ia, ib = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+        u, v = y[..., ia].copy(), y[..., ib].copy()
+        y[..., ia], y[..., ib] = u * np.cos(a) - v * np.sin(a), u * np.sin(a) + v * np.cos(a)
+        size[..., ia] = size[..., ib] = np.hypot(u, v)
+    return y, size
+
+
+def near_turned(got, want, size, far=0):
+    # 32-bit arithmetic: at most 32 roundings of the pair's size on the way (sum of squares, root, gain, sine and
+    # cosine with their argument's rounding, two products), positions cost p * 2^-52 turns; then one rounding
+    err = np.abs(got.double().cpu().numpy() - want)
+    bound = U[got.dtype] * np.abs(want) * 1.001 + (32 * 2.0 ** -24 + far * 2.0 ** -49) * size
+    if got.dtype == torch.float16:
+        bound = bound + 2.0 ** -25
+    assert (err <= bound).all(), float((err - bound).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("dim, rot, inter", [(32, 32, False), (64, 64, True), (64, 24, False), (96, 96, False),
+                                             (96, 40, True), (128, 128, False), (128, 64, True), (128, 8, False),
+                                             (64, 0, False)])
+def test_norm_rope(zg, dev, dtype, dim, rot, inter):
+    for B, T, Hq, Hk, far in ((1, 1, 1, 1, 3), (3, 1, 8, 2, 9_000_000), (2, 37, 5, 3, 200_000), (1, 2100, 4, 4, 10)):
+        x = randn((B, T, Hq + Hk, dim), dtype, 7 * B + T)
+        q, k = x[:, :, :Hq], x[:, :, Hq:]
+        gq, gk = randn((dim,), torch.float32, 1), randn((dim,), torch.float32, 2)
+        pos = (ints([[far * (b + 1)] for b in range(B)]) + torch.arange(T, device="cuda", dtype=torch.int32)[None]).contiguous()
+        nr = dev.NormRope(dim, gq, gk, rot_dim=rot, theta=500000.0, interleaved=inter)
+        qo, ko = nr(q, k, pos)
+        ok(zg)
+        for got, src, g in ((qo, q, gq), (ko, k, gk)):
+            near_turned(got, *turned(src, g, pos, rot, 500000.0, inter, True), far=far * B + T)
+
+
+def test_norm_rope_forms(zg, dev):
+    """In place, one side only, without gains, without the norm, given frequencies, negative positions."""
+    q = randn((2, 5, 3, 64), torch.float32, 3)
+    pos = ints([[-7, -1, 0, 1, 2 ** 31 - 1], [5, 5, 5, 5, -2 ** 31]])
+    freq = [1.0 / (i + 1) for i in range(16)]
+    want = turned(q, None, pos, 32, 0, True, False, freq=freq)
+    nr = dev.NormRope(64, rot_dim=32, interleaved=True, norm=False, freq=freq)
+    out, none = nr(q, None, pos, q_out=q)
+    ok(zg)
+    assert out is q and none is None
+    near_turned(q, *want, far=2 ** 31)
+    k = randn((2, 5, 3, 64), torch.bfloat16, 4)
+    none, ko = dev.NormRope(64, rot_dim=0)(None, k, pos)
+    ok(zg)
+    near_turned(ko, *turned(k, None, pos, 0, 0, False, True))
+    z = torch.zeros((1, 1, 2, 96), device="cuda")
+    assert not dev.NormRope(96)(z, z, ints([[4]]))[0].any()
+    ok(zg)
+
+
+def test_norm_rope_refuses_shapes(dev):
+    nr = dev.NormRope(64)
+    q = torch.zeros((1, 2, 2, 64), device="cuda")
+    for bad in (ints([[1]]), ints([[1, 2]]).long(), ints([[1, 0, 2, 0]])[:, ::2]):
+        with pytest.raises(ValueError):
+            nr(q, None, bad)
+    with pytest.raises(ValueError):
+        nr(q.transpose(2, 3).contiguous().transpose(2, 3), None, ints([[1, 2]]))
+    with pytest.raises(ValueError):
+        nr(q, q[:, :1], ints([[1, 2]]))
+    with pytest.raises(ValueError):
+        dev.NormRope(64, q_gain=torch.ones(32, device="cuda"))
+
+
+# ------------------------------------------------------------------ write, read
+
+def half_step(code, fmt):
+    """Half the distance between neighbouring codes around |code| (64-bit array)."""
+    if fmt == "int8":
+        return np.full_like(code, 0.5)
+    e = np.floor(np.log2(np.maximum(np.abs(code), 2.0 ** -6)))
+    return 2.0 ** (e - 4)
+
+
+def place(table, start, bt, T):
+    p = start.cpu().numpy()[:, None] + np.arange(T)[None]
+    return np.take_along_axis(table.cpu().numpy(), np.minimum(p // bt, table.shape[1] - 1), 1), p % bt
+
+
+def new_cache(dev, fmt, n, bt, heads, dim):
+    c = dev.KVCache(n, bt, heads, dim, fmt)
+    for x in (c.k_codes, c.v_codes):
+        x.view(torch.uint8).fill_(0x7F)      # e4m3: NaN
+    c.k_scale.fill_(math.nan)
+    c.v_scale.fill_(math.nan)
+    return c
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("dim, heads, bt", [(32, 3, 16), (64, 1, 32), (96, 2, 64), (128, 2, 128), (128, 4, 64), (64, 2, 16)])
+def test_append_codes(zg, dev, fmt, dtype, dim, heads, bt):
+    """Chunks of every kind of length, one behind the other: scales and codes against their definition."""
+    B, width = 3, 8
+    n_blocks = B * width + 1
+    order = torch.randperm(n_blocks, generator=torch.Generator().manual_seed(5)).to(torch.int32).cuda()
+    table = order[:B * width].view(B, width).contiguous()
+    c = new_cache(dev, fmt, n_blocks, bt, heads, dim)
+    start = ints([0, 0, 0])
+    top = {}                                            # (side, block) -> largest |x| so far, by head
+    for step, (T, news) in enumerate([(1, [1, 1, 0]), (bt + 3, [bt + 3, 2, 1]), (5, [5, 0, 5]), (bt, [bt, bt - 1, bt]),
+                                      (2 * bt + 1, [1, 2 * bt + 1, 17 % (2 * bt)])]):
+        x = randn((B, T, 2 * heads + 1, dim), dtype, 20 + step, scale=0.1 * 3.0 ** step)
+        k, v = x[:, :, :heads], x[:, :, heads:2 * heads]
+        new = ints(news)
+        before = [t.view(torch.uint8).clone() for t in (c.k_codes, c.v_codes)]
+        c.append(k, v, table, start, new)
+        ok(zg)
+        blk, row = place(table, start, bt, T)
+        for side, (src, codes, scales, old) in enumerate(((k, c.k_codes, c.k_scale, before[0]), (v, c.v_codes, c.v_scale, before[1]))):
+            xs = src.double().cpu().numpy()
+            code, s = codes.float().double().cpu().numpy(), scales.double().cpu().numpy()
+            touched = set()
+            for b in range(B):
+                for t in range(news[b]):
+                    kb = (side, int(blk[b, t]))
+                    if row[b, t] == 0:
+                        top[kb] = 0
+                    top[kb] = np.maximum(top.get(kb, 0), np.abs(xs[b, t]).max(-1))
+                    touched.add(kb[1])
+                for t in range(news[b]):
+                    i = int(blk[b, t])
+                    # the scale: the quotient of the largest value and Q, rounded once
+                    assert np.array_equal(s[i], (top[(side, i)].astype(np.float32) / np.float32(QMAX[fmt])).astype(np.float64))
+                    # the code: the nearest to x / s; the product with 1 / s costs two roundings in 32 bits
+                    got = code[i, :, row[b, t]]
+                    y = xs[b, t] / s[i][:, None]
+                    assert (np.abs(got - y) <= half_step(got, fmt) * 1.0001 + np.abs(y) * 2.0 ** -22).all()
+            for i in range(n_blocks):      # nothing else has changed
+                if i not in touched:
+                    assert torch.equal(codes.view(torch.uint8)[i], old[i])
+        start = start + new
+    # what was coded again on the way is within the roundings it went through: half a step of each code it had,
+    # which no later scale makes finer
+    n = int(start.max())
+    ko = torch.empty((B, n, heads, dim), device="cuda")
+    c.read(table, ints([0] * B), start, k_out=ko)
+    ok(zg)
+    assert torch.isfinite(ko).all()
+    for b in range(B):
+        assert not ko[b, int(start[b]):].any()
+
+
+def test_append_recodes_held_rows(zg, dev):
+    """A growing scale: earlier rows keep their values to half a step of the new scale (int8)."""
+    c = new_cache(dev, "int8", 2, 32, 2, 64)
+    table = ints([[1]])
+    x = randn((1, 30, 2, 64), torch.float32, 9)
+    x[:, 20:] *= 50
+    for a, n in ((0, 7), (7, 1), (8, 12), (20, 1), (21, 9)):
+        c.append(x[:, a:a + n], x[:, a:a + n], table, ints([a]))
+    ok(zg)
+    got = torch.empty_like(x)
+    c.read(table, ints([0]), None, k_out=got)
+    ok(zg)
+    s = c.k_scale[1].double()[None, None, :, None]
+    # at most five roundings of at most half the final step each
+    assert ((got.double() - x.double()).abs() <= 5 * 0.5 * s * 1.001).all()
+    last = (got[:, 21:].double() - x[:, 21:].double()).abs()
+    assert (last <= 0.5 * s * 1.001).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_append_special_values(zg, dev, fmt):
+    c = new_cache(dev, fmt, 2, 16, 1, 64)
+    x = torch.zeros((1, 2, 1, 64), device="cuda")
+    table = ints([[0]])
+    c.append(x, x, table, ints([0]))                     # all zero: scale 0, codes 0
+    ok(zg)
+    assert float(c.k_scale[0]) == 0 and not c.k_codes.view(torch.uint8)[0, :, :2].any()
+    x[0, 0, 0, :4] = torch.tensor([1e-42, -1e-39, 0, 1e-40])      # below the smallest scale: held as zero
+    c.append(x, x, table, ints([0]))
+    ok(zg)
+    assert float(c.v_scale[0]) == 0 and not c.v_codes[0, :, :2].float().any()     # a zero may have a sign
+    x[0, 1, 0, :4] = torch.tensor([math.nan, math.inf, -math.inf, 2.0])
+    c.append(x, x, table, ints([0]))
+    torch.cuda.synchronize()
+    with pytest.raises(zg.ZgError, match="NaN or infinity"):
+        zg.zg_check_device_status(0)
+    got = torch.empty_like(x)
+    c.read(table, ints([0]), None, k_out=got)
+    ok(zg)
+    assert got[0, 1, 0, :4].tolist() == [0.0, 2.0, -2.0, 2.0]
+    big = torch.full((1, 1, 1, 64), 3.0e38, device="cuda")
+    c.append(big, big, table, ints([0]))
+    ok(zg)
+    c.read(table, ints([0]), None, v_out=big)
+    ok(zg)
+    assert (big / 3.0e38 - 1).abs().max() < 1e-6
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_append_turns_keys_and_queries(zg, dev, fmt):
+    """The fused write equals the turn in 64 bits to half a code's step, and turns q as the stand-alone call does."""
+    B, T, Hq, Hk, D, bt = 2, 41, 6, 2, 96, 32
+    x = randn((B, T, Hq + 2 * Hk, D), torch.bfloat16, 31)
+    q, k, v = x[:, :, :Hq], x[:, :, Hq:Hq + Hk], x[:, :, Hq + Hk:]
+    g = randn((D,), torch.float32, 1)
+    nr = dev.NormRope(D, g, g, rot_dim=48)
+    c = new_cache(dev, fmt, 9, bt, Hk, D)
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4).contiguous()
+    start = ints([19, 0])
+    c.append(k[:, :19].contiguous(), v[:, :19].contiguous(), table, ints([0, 0]), ints([19, 0]))   # rows held before
+    q_out = c.append(k, v, table, start, q=q, norm_rope=nr)
+    pos = (start[:, None] + torch.arange(T, device="cuda", dtype=torch.int32)).contiguous()
+    alone, _ = nr(q, None, pos)
+    ok(zg)
+    assert torch.equal(q_out, alone)
+    want, size = turned(k, g, pos, 48, 10000.0, False, True)
+    blk, row = place(table, start, bt, T)
+    code, s = c.k_codes.float().double().cpu().numpy(), c.k_scale.double().cpu().numpy()
+    for b in range(B):
+        for t in range(T):
+            got, sc = code[blk[b, t], :, row[b, t]], s[blk[b, t]][:, None]
+            err = np.abs(got * sc - want[b, t])
+            assert (err <= half_step(got, fmt) * sc * 1.0001 + 40 * 2.0 ** -24 * size[b, t]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_read(zg, dev, dtype):
+    for fmt, dim in (("e4m3", 96), ("int8", 32)):
+        c = new_cache(dev, fmt, 6, 16, 3, dim)
+        x = randn((2, 40, 3, dim), torch.float32, 4)
+        table = ints([[5, 0, 3], [1, 4, 2]])
+        c.append(x, x * 2, table, ints([0, 0]))
+        buf = torch.full((2, 50, 8, dim), 9.0, dtype=dtype, device="cuda")
+        start, n = ints([3, 39]), ints([37, 1])
+        c.read(table, start, n, k_out=buf[:, :, 1:4], v_out=buf[:, :, 5:])
+        ok(zg)
+        blk, row = place(table, start, 16, 50)
+        for out, codes, scales in ((buf[:, :, 1:4], c.k_codes, c.k_scale), (buf[:, :, 5:], c.v_codes, c.v_scale)):
+            cd, sc = codes.float().double().cpu().numpy(), scales.double().cpu().numpy()
+            for b in range(2):
+                m = int(n[b])
+                want = cd[blk[b, :m], :, row[b, :m]] * sc[blk[b, :m]][..., None]
+                err = np.abs(out[b, :m].double().cpu().numpy() - want)
+                # the product is rounded to 32 bits, then to the output's type
+                assert (err <= (U[dtype] + 2.0 ** -24) * 1.001 * np.abs(want) + 2.0 ** -25).all()
+                assert not out[b, m:].any()
+        assert (buf[:, :, 0] == 9).all() and (buf[:, :, 4] == 9).all()
+
+
+def test_bad_tables_are_reported(zg, dev):
+    """Blocks and lengths outside the cache: left out, recorded, and the next call is sound."""
+    c = new_cache(dev, "e4m3", 4, 16, 2, 64)
+    x = randn((1, 20, 2, 64), torch.bfloat16, 1)
+    q = randn((1, 1, 2, 64), torch.bfloat16, 2)
+    good = ints([[2, 1]])
+    attn = dev.CacheAttention(c, 1, 1, 2, 2)
+    c.append(x, x, good, ints([0]))
+    ok(zg)
+    kept = c.k_codes.view(torch.uint8).clone()
+    buf = torch.empty_like(x)
+    for f in (lambda: c.append(x, x, ints([[4, -1]]), ints([0])), lambda: c.append(x, x, good, ints([-1])),
+              lambda: c.append(x, x, good, ints([13])), lambda: c.append(x, x, good, ints([0]), ints([21])),
+              lambda: c.append(x, x, good, ints([0]), ints([-1])), lambda: c.read(good, ints([14]), None, k_out=buf),
+              lambda: c.read(ints([[0, 77]]), ints([0]), None, k_out=buf), lambda: c.read(good, ints([-2]), None, v_out=buf),
+              lambda: attn(q, ints([[2, 4]]), ints([20])), lambda: attn(q, good, ints([33])),
+              lambda: attn(q, good, ints([-1])), lambda: attn(q, good, ints([20]), ints([2]))):
+        f()
+        torch.cuda.synchronize()
+        with pytest.raises(zg.ZgError, match="out of range"):
+            zg.zg_check_device_status(0)
+        assert torch.equal(c.k_codes.view(torch.uint8), kept)
+    check_attention(zg, dev, c, q, good, ints([20]), None, False)
+
+
+# -------------------------------------------------------------------- attention
+
+def fill(c, seed):
+    """Codes and scales of any size within the format, NaN codes never among them."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for codes, scales in ((c.k_codes, c.k_scale), (c.v_codes, c.v_scale)):
+        m = 127 if codes.dtype == torch.int8 else 448
+        x = (torch.randn(codes.shape, generator=g, device="cuda") * (m / 4)).clamp(-m, m)
+        codes.copy_(x.round().to(codes.dtype) if codes.dtype == torch.int8 else x.to(codes.dtype))
+        scales.copy_(4.0 / m * torch.exp(1.5 * torch.randn(scales.shape, generator=g, device="cuda")))
+
+
+def behind(c, table, length):
+    """NaN codes behind every request's last token."""
+    if c.k_codes.dtype == torch.int8:
+        return
+    bt = c.block_tokens
+    for b, n in enumerate(length.tolist()):
+        if n % bt:
+            for x in (c.k_codes, c.v_codes):
+                x.view(torch.uint8)[int(table[b, n // bt]), :, n % bt:] = 0x7F
+
+
+def want_attention(c, q, table, length, rows, causal, scale):
+    """The definition in 64 bits: outputs, log-sum-exps, and the bounds of what 32-bit sums and half operands cost."""
+    B, R, Hq, D = q.shape
+    G, bt = Hq // c.heads, c.block_tokens
+    out = torch.zeros((B, R, Hq, D), dtype=torch.float64)
+    lse = torch.full((B, R, Hq), -math.inf, dtype=torch.float64)
+    tol, ltol = torch.zeros_like(out), torch.zeros_like(lse)
+    for b in range(B):
+        n, nr = int(length[b]), R if rows is None else int(rows[b])
+        if not n:
+            continue
+        blk = table[b, :-(-n // bt)].long()
+        k, v = ((x[blk].float().double() * s[blk].double()[..., None, None]).permute(1, 0, 2, 3).reshape(c.heads, -1, D)[:, :n].cpu()
+                for x, s in ((c.k_codes, c.k_scale), (c.v_codes, c.v_scale)))
+        for r in range(nr):
+            see = n - (nr - 1 - r) if causal else n
+            if see <= 0:
+                continue
+            qq = q[b, r].double().cpu().view(c.heads, G, 1, D)
+            z = (qq * k[:, None, :see]).sum(-1) * scale
+            # scores: D products and sums in 32 bits, q rounded to a half (relative 2^-11) unless it is one already
+            dz = ((qq.abs() * k[:, None, :see].abs()).sum(-1) * scale).amax(-1) * ((D + 8) * 2.0 ** -24)
+            p = torch.softmax(z, -1)
+            out[b, r] = (p @ v[:, :see]).reshape(Hq, D)
+            lse[b, r] = torch.logsumexp(z, -1).reshape(Hq)
+            mass = (p @ v[:, :see].abs()).reshape(Hq, D)
+            # probabilities: a half (2^-11), the scores' error twice (p and the sum), the exponential and the
+            # running sums in 32 bits
+            tol[b, r] = mass * (2.0 ** -11 + 2 * dz.reshape(Hq)[:, None] + 2.0 ** -18)
+            # a probability below 2^-14 of its row's reference is a subnormal half: absolute error 2^-25 each
+            big = v[:, :see].abs().amax((1, 2)).repeat_interleave(G)[:, None]
+            tol[b, r] += big * 2.0 ** -25 * (see / torch.exp(torch.logsumexp(z, -1) - z.amax(-1))).reshape(Hq)[:, None]
+            ltol[b, r] = dz.reshape(Hq) + 2.0 ** -18 + lse[b, r].abs() * 2.0 ** -22
+    return out, lse, tol, ltol
+
+
+def check_attention(zg, dev, c, q, table, length, rows, causal, scale=None, out=None):
+    B, R, Hq, D = q.shape
+    a = dev.CacheAttention(c, B, R, Hq, table.shape[1], causal=causal, scale=scale, dtype=q.dtype, lse=True)
+    a.out.fill_(math.nan)
+    a.lse.fill_(math.nan)
+    a.ws.fill_(0xFF)                                   # contents of a workspace are not defined
+    got, lse = a(q, table, length, rows)
+    ok(zg)
+    want, wlse, tol, ltol = want_attention(c, q, table, length, rows, causal, a.scale)
+    got, lse = got.double().cpu(), lse.double().cpu()
+    err = (got - want).abs()
+    bound = tol + U[q.dtype] * 1.001 * (want.abs() + tol) + (2.0 ** -25 if q.dtype == torch.float16 else 0)
+    assert torch.isfinite(got).all()
+    assert (err <= bound).all(), (float((err / bound.clamp(min=1e-30)).max()), (err > bound).nonzero()[:4].tolist())
+    assert torch.equal(lse == -math.inf, wlse == -math.inf)
+    seen = wlse > -math.inf
+    assert ((lse - wlse).abs()[seen] <= ltol[seen]).all(), float((lse - wlse).abs()[seen].max())
+    return a
+
+
+def build(dev, fmt, B, heads, dim, bt, lengths, width, seed):
+    c = dev.KVCache(B * width + 2, bt, heads, dim, fmt)
+    fill(c, seed)
+    order = torch.randperm(B * width + 2, generator=torch.Generator().manual_seed(seed)).to(torch.int32).cuda()
+    table = order[:B * width].view(B, width).contiguous()
+    length = ints(lengths)
+    behind(c, table, length)
+    used = (length + bt - 1) // bt
+    table = torch.where(torch.arange(width, device="cuda")[None] < used[:, None], table, ints([-5])[None])
+    return c, table.contiguous(), length
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+@pytest.mark.parametrize("bt", [16, 32, 64, 128])
+def test_attention_one_token(zg, dev, fmt, dim, bt):
+    """Every kind of length for one token a request, shared heads or not, both types."""
+    lengths = [0, 1, bt - 1, bt, bt + 1, 5 * bt + 7, 700]
+    width = -(-700 // bt) + 1
+    for heads, G, dtype in ((2, 1, torch.bfloat16), (1, 3, torch.float16), (2, 8, torch.bfloat16), (1, 20, torch.float16)):
+        c, table, length = build(dev, fmt, len(lengths), heads, dim, bt, lengths, width, 3 + G)
+        q = randn((len(lengths), 1, heads * G, dim), dtype, 5, scale=2.0)
+        check_attention(zg, dev, c, q, table, length, None, False)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dim, heads, G, bt", [(64, 2, 1, 16), (128, 1, 1, 64), (96, 2, 2, 32), (32, 1, 4, 128), (128, 2, 4, 16), (64, 1, 3, 128)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_many_rows(zg, dev, fmt, dim, heads, G, bt, causal):
+    """Beams and causal chunks: rows that see nothing, fewer rows than R, lengths around tiles."""
+    for R, lengths, rows in ((9, [0, 5, 64, 200], [9, 9, 1, 0]), (65, [1, 64, 129, 300], [65, 64, 65, 7]),
+                             (150, [40, 128, 257, 500], None)):
+        c, table, length = build(dev, fmt, 4, heads, dim, bt, lengths, -(-500 // bt), R)
+        q = randn((4, R, heads * G, dim), torch.bfloat16 if R != 65 else torch.float16, R, scale=2.0)
+        check_attention(zg, dev, c, q, table, length, ints(rows) if rows else None, causal)
+
+
+def test_attention_long(zg, dev):
+    """Long histories: the keys split over many parts, lengths that leave most parts empty."""
+    c, table, length = build(dev, "e4m3", 3, 1, 64, 64, [20011, 3, 9000], 320, 8)
+    q = randn((3, 1, 2, 64), torch.bfloat16, 1, scale=3.0)
+    check_attention(zg, dev, c, q, table, length, None, False)
+    q = randn((3, 33, 2, 64), torch.float16, 1)
+    check_attention(zg, dev, c, q, table, length, ints([33, 5, 1]), True)
+
+
+def test_attention_extremes(zg, dev):
+    """Scores and scales over many orders: the running maximum and reference scale move on every tile."""
+    for fmt in ("e4m3", "int8"):
+        c, table, length = build(dev, fmt, 2, 1, 64, 16, [333, 200], 24, 4)
+        ramp = torch.exp2(torch.arange(24, device="cuda").float() * 1.7 - 20)
+        for b in range(2):
+            used = table[b][table[b] >= 0].long()
+            c.v_scale[used, 0] = ramp[:len(used)] if b == 0 else ramp[:len(used)].flip(0)
+        c.v_scale[table[1, 2].long()] = 0
+        q = randn((2, 3, 4, 64), torch.bfloat16, 6, scale=30.0)
+        q[0, 1] = 0                                              # uniform weights
+        q[1, 2] *= 1e4
+        check_attention(zg, dev, c, q, table, length, None, False, scale=0.02)
+        check_attention(zg, dev, c, (q * 1e30).to(torch.bfloat16), table, length, None, True, scale=1e-32)
+        q = randn((2, 140, 4, 64), torch.bfloat16, 6, scale=30.0)
+        check_attention(zg, dev, c, q, table, length, None, False, scale=0.02)
+
+
+def test_attention_strides_and_streams(zg, dev):
+    """q inside a packed buffer, outputs into a wider one, on a stream that is not the current one."""
+    c, table, length = build(dev, "int8", 2, 2, 64, 32, [100, 77], 5, 2)
+    for R in (1, 70):
+        x = randn((2, R, 8, 64), torch.bfloat16, 11)
+        want = dev.CacheAttention(c, 2, R, 4, 5)(x[:, :, 2:6].contiguous(), table, length)[0].clone()
+        wide = torch.zeros((2, R, 9, 68), dtype=torch.bfloat16, device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        ws = torch.empty(zg.zg_kv_attention_workspace_size(c.struct, 5, 2, R, 4), dtype=torch.uint8, device="cuda")
+        q = x[:, :, 2:6]
+        o = wide[:, :, 5:]
+        zg.zg_kv_attention(c.struct, table, 5, length, None, zg.make_rows(q, zg.ZG_BF16, *q.stride()[:3]),
+                           zg.make_rows(o, zg.ZG_BF16, *o.stride()[:3]), None, 2, R, 4, 0.125, False, ws, ws.numel(),
+                           s.cuda_stream)
+        s.synchronize()
+        ok(zg)
+        assert torch.equal(o[..., :64], want) and not wide[:, :, :5].any() and not wide[..., 64:].any()
+
+
+def test_attention_in_a_graph(zg, dev):
+    """Write, then attend, captured once and replayed on new data."""
+    c = new_cache(dev, "e4m3", 8, 16, 2, 64)
+    table = ints([[3, 1], [0, 6]])
+    x = randn((2, 3, 8, 64), torch.bfloat16, 2)
+    start, length = ints([0, 0]), ints([3, 3])
+    nr = dev.NormRope(64)
+    attn = dev.CacheAttention(c, 2, 3, 4, 2, causal=True)
+    q = torch.empty((2, 3, 4, 64), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        c.append(x[:, :, 4:6], x[:, :, 6:], table, start, q=x[:, :, :4], q_out=q, norm_rope=nr)
+        attn(q, table, length)
+
+    step()
+    ok(zg)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    x.copy_(randn((2, 3, 8, 64), torch.bfloat16, 3))
+    start.copy_(ints([3, 3]))
+    length.copy_(ints([6, 6]))
+    g.replay()
+    ok(zg)
+    got = attn.out.clone()
+    step()
+    ok(zg)
+    assert torch.equal(got, attn.out)
+    check_attention(zg, dev, c, q, table, ints([3, 3]), None, True)
+
+
+def test_attention_repeats(zg, dev):
+    """The same call gives the same bits."""
+    c, table, length = build(dev, "e4m3", 5, 2, 128, 64, [5000, 0, 1, 4097, 300], 90, 12)
+    for R in (1, 200):
+        q = randn((5, R, 4, 128), torch.bfloat16, 3)
+        a = dev.CacheAttention(c, 5, R, 4, 90, lse=True)
+        o, l = (t.clone() for t in a(q, table, length))
+        for _ in range(3):
+            o2, l2 = a(q, table, length)
+            assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+def test_parts_merge_by_lse(zg, dev):
+    """Two halves of a history, each with its own table, merged by their log-sum-exps."""
+    c, table, length = build(dev, "int8", 1, 1, 64, 16, [160], 10, 3)
+    q = randn((1, 40, 2, 64), torch.float16, 3)
+    whole = check_attention(zg, dev, c, q, table, length, None, False)
+    o1, l1 = (t.clone() for t in dev.CacheAttention(c, 1, 40, 2, 4, dtype=q.dtype, lse=True)(q, table[:, :4].contiguous(), ints([64])))
+    o2, l2 = dev.CacheAttention(c, 1, 40, 2, 6, dtype=q.dtype, lse=True)(q, table[:, 4:].contiguous(), ints([96]))
+    w = torch.softmax(torch.stack([l1, l2]), 0)[..., None]
+    merged = w[0] * o1.float() + w[1] * o2.float()
+    # three results, each within half a step of its type and 2^-10 of the values' size
+    assert (merged - whole.out.float()).abs().max() <= 3 * 2.0 ** -10 * float((o1.abs().max() + o2.abs().max()))
+
+
+def test_cache_past_32_bits(zg, dev):
+    """A pool whose codes pass 4 GiB a side: blocks at its end."""
+    heads, bt, dim, n = 8, 128, 128, 33000
+    assert n * heads * bt * dim > 2 ** 32
+    c = dev.KVCache(n, bt, heads, dim, "int8")
+    table = ints([[n - 1, 0, n - 2], [n - 3, n - 4, 1]])
+    for b in table.flatten().tolist():
+        for x in (c.k_codes, c.v_codes):
+            x[b].fill_(0)
+    x = randn((2, 300, heads, dim), torch.bfloat16, 2)
+    c.append(x, x, table, ints([0, 0]))
+    out = torch.empty_like(x)
+    c.read(table, ints([0, 0]), None, k_out=out)
+    ok(zg)
+    assert ((out.float() - x.float()).abs() <= x.float().abs() * 2.0 ** -8 + 6.0 / 254 * 1.01).all()
+    check_attention(zg, dev, c, randn((2, 1, 8, dim), torch.bfloat16, 5), table, ints([300, 257]), None, False)
+    check_attention(zg, dev, c, randn((2, 20, 8, dim), torch.bfloat16, 5), table, ints([300, 257]), None, False)
+
+
+def test_wrappers_refuse_shapes(dev):
+    c = dev.KVCache(4, 16, 2, 64)
+    x = torch.zeros((1, 2, 2, 64), device="cuda", dtype=torch.bfloat16)
+    t, s = ints([[0, 1]]), ints([0])
+    for f in (lambda: c.append(x, x[:, :1], t, s), lambda: c.append(x, x, t.long(), s), lambda: c.append(x, x, t, ints([0, 0])),
+              lambda: c.append(x.double(), x, t, s), lambda: c.read(t, s, None, x[:, :, :1]),
+              lambda: dev.CacheAttention(c, 1, 1, 2, 2)(x, t, s), lambda: dev.CacheAttention(c, 1, 2, 2, 3)(x, t, s),
+              lambda: dev.KVCache.over(c.k_codes, c.v_codes, c.k_scale, c.v_scale[:2])):
+        with pytest.raises(ValueError):
+            f()

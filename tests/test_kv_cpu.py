@@ -1,0 +1,166 @@
+"""Refusals and sizes of the history-cache calls, without a GPU: every argument
+check comes before any CUDA call, so the pointers here are never followed."""
+import ctypes as C
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def zg():
+    import __graft_entry__
+    __graft_entry__.build()
+    import generative_recommendation_constrained_gb300 as zg
+    return zg
+
+
+P = 1 << 20      # an aligned address that nothing follows
+
+
+def cache(zg, **kw):
+    a = dict(fmt=zg.ZG_KV_E4M3, n_blocks=8, heads=2, block_tokens=16, dim=64, k_codes=P, v_codes=P, k_scale=P, v_scale=P)
+    a.update(kw)
+    return zg.make_kv_cache(**a)
+
+
+def rows(zg, data=P, dtype=None, sb=256, st=128, sh=64):
+    return zg.make_rows(data, zg.ZG_BF16 if dtype is None else dtype, sb, st, sh)
+
+
+def nrope(zg, **kw):
+    a = dict(norm=True, eps=1e-6, q_gain=None, k_gain=None, rot_dim=64, interleaved=False, theta=1e4)
+    a.update(kw)
+    return zg.make_norm_rope(**a)
+
+
+def refused(zg, status, words, f, *a, **kw):
+    with pytest.raises(zg.ZgError) as e:
+        f(*a, **kw)
+    assert e.value.status == status and words in str(e.value), str(e.value)
+
+
+BAD_CACHE = [(dict(fmt=2), 1, "format"), (dict(n_blocks=0), 1, "n_blocks"), (dict(heads=0), 1, "heads"),
+             (dict(heads=1025), 1, "heads"), (dict(block_tokens=24), 1, "block_tokens"), (dict(dim=80), 4, "dim"),
+             (dict(dim=256), 4, "dim"), (dict(k_codes=None), 1, "NULL"), (dict(v_scale=None), 1, "NULL"),
+             (dict(v_codes=P + 8), 1, "16-byte"), (dict(k_scale=P + 2), 1, "4-byte")]
+
+
+@pytest.mark.parametrize("kw, status, words", BAD_CACHE)
+def test_bad_caches(zg, kw, status, words):
+    c, r = cache(zg, **kw), rows(zg)
+    refused(zg, status, words, zg.zg_kv_append, c, None, r, r, None, None, 0, P, 4, P, None, 1, 1)
+    refused(zg, status, words, zg.zg_kv_read, c, P, 4, P, None, 1, 1, r, r)
+    refused(zg, status, words, zg.zg_kv_attention, c, P, 4, P, None, r, r, None, 1, 1, 2, 1.0, False, P, 1 << 30)
+    refused(zg, status, words, zg.zg_kv_attention_workspace_size, c, 4, 1, 1, 2)
+
+
+@pytest.mark.parametrize("kw, words", [(dict(data=None), "NULL"), (dict(dtype=3), "dtype"), (dict(sb=-4), "strides"),
+                                       (dict(st=130), "strides"), (dict(sh=2), "strides"), (dict(data=P + 4), "aligned"),
+                                       (dict(data=P + 8, dtype=0), "aligned")])
+def test_bad_rows(zg, kw, words):
+    r, good, c, n = rows(zg, **kw), rows(zg), cache(zg), nrope(zg)
+    refused(zg, 1, words, zg.zg_qk_norm_rope, n, r, None, good, None, P, 1, 1, 2, 0, 64)
+    refused(zg, 1, words, zg.zg_kv_append, c, None, r, good, None, None, 0, P, 4, P, None, 1, 1)
+    refused(zg, 1, words, zg.zg_kv_read, c, P, 4, P, None, 1, 1, r, None)
+    refused(zg, 1, words, zg.zg_kv_attention, c, P, 4, P, None, r, good, None, 1, 1, 2, 1.0, False, P, 1 << 30)
+
+
+@pytest.mark.parametrize("kw, words", [(dict(rot_dim=-8), "rot_dim"), (dict(rot_dim=72), "rot_dim"),
+                                       (dict(rot_dim=12), "rot_dim"), (dict(eps=-1.0), "eps"),
+                                       (dict(eps=float("nan")), "eps"), (dict(theta=0.5), "theta"),
+                                       (dict(theta=float("inf")), "theta"), (dict(q_gain=P + 2), "gains"),
+                                       (dict(rot_dim=8, freq=[1.0, 0.1, -0.1, 0.0]), "freq"),
+                                       (dict(rot_dim=8, freq=[1.0, 4.1, 0.1, 0.0]), "freq"),
+                                       (dict(rot_dim=8, freq=[1.0, float("nan"), 0.1, 0.0]), "freq")])
+def test_bad_norm_ropes(zg, kw, words):
+    n, r, c = nrope(zg, **kw), rows(zg), cache(zg)
+    refused(zg, 1, words, zg.zg_qk_norm_rope, n, r, r, r, r, P, 1, 1, 2, 2, 64)
+    refused(zg, 1, words, zg.zg_kv_append, c, n, r, r, None, None, 0, P, 4, P, None, 1, 1)
+
+
+def test_norm_rope_refusals(zg):
+    n, r = nrope(zg), rows(zg)
+    f = zg.zg_qk_norm_rope
+    refused(zg, 1, "norm_rope", f, None, r, r, r, r, P, 1, 1, 2, 2, 64)
+    refused(zg, 4, "dim", f, n, r, r, r, r, P, 1, 1, 2, 2, 48)
+    refused(zg, 1, "B and T", f, n, r, r, r, r, P, -1, 1, 2, 2, 64)
+    refused(zg, 1, "Hq and Hk", f, n, r, r, r, r, P, 1, 1, 2000, 2, 64)
+    refused(zg, 1, "exactly when", f, n, r, None, r, None, P, 1, 1, 2, 2, 64)
+    refused(zg, 1, "neither", f, n, None, None, None, None, P, 1, 1, 0, 0, 64)
+    refused(zg, 1, "type of the other", f, n, r, rows(zg, dtype=zg.ZG_F16), r, r, P, 1, 1, 2, 2, 64)
+    refused(zg, 1, "q_out", f, n, r, r, None, r, P, 1, 1, 2, 2, 64)
+    refused(zg, 1, "positions", f, n, r, r, r, r, None, 1, 1, 2, 2, 64)
+    f(n, r, r, r, r, P, 0, 5, 2, 2, 64)          # nothing to do: no launch
+    f(n, r, r, r, r, P, 5, 0, 2, 2, 64)
+
+
+def test_append_refusals(zg):
+    c, n, r = cache(zg), nrope(zg), rows(zg)
+    f = zg.zg_kv_append
+    refused(zg, 1, "cache is NULL", f, None, n, r, r, None, None, 0, P, 4, P, None, 1, 1)
+    refused(zg, 1, "table", f, c, n, r, r, None, None, 0, None, 4, P, None, 1, 1)
+    refused(zg, 1, "max_blocks", f, c, n, r, r, None, None, 0, P, 0, P, None, 1, 1)
+    refused(zg, 1, "max_blocks", f, c, n, r, r, None, None, 0, P, 1 << 27, P, None, 1, 1)
+    refused(zg, 1, "start", f, c, n, r, r, None, None, 0, P, 4, None, None, 1, 1)
+    refused(zg, 1, "B and T", f, c, n, r, r, None, None, 0, P, 4, P, None, 1, -1)
+    refused(zg, 1, "v must", f, c, n, r, rows(zg, dtype=zg.ZG_F16), None, None, 0, P, 4, P, None, 1, 1)
+    refused(zg, 1, "Hq", f, c, n, r, r, r, r, 0, P, 4, P, None, 1, 1)
+    refused(zg, 1, "Hq", f, c, n, r, r, None, None, 2, P, 4, P, None, 1, 1)
+    refused(zg, 1, "without a norm_rope", f, c, None, r, r, r, r, 2, P, 4, P, None, 1, 1)
+    refused(zg, 1, "q_out", f, c, n, r, r, r, None, 2, P, 4, P, None, 1, 1)
+    refused(zg, 4, "CTAs", f, c, n, r, r, None, None, 0, P, 4, P, None, 1 << 30, 16)
+    f(c, n, r, r, None, None, 0, P, 4, P, None, 0, 1)
+    f(c, n, r, r, None, None, 0, P, 4, P, None, 1, 0)
+
+
+def test_read_refusals(zg):
+    c, r = cache(zg), rows(zg)
+    refused(zg, 1, "neither", zg.zg_kv_read, c, P, 4, P, None, 1, 1, None, None)
+    refused(zg, 1, "start", zg.zg_kv_read, c, P, 4, None, None, 1, 1, r, r)
+    refused(zg, 1, "table", zg.zg_kv_read, c, None, 4, P, None, 1, 1, r, r)
+    zg.zg_kv_read(c, P, 4, P, None, 0, 1, r, None)
+
+
+def test_attention_refusals(zg):
+    c, r = cache(zg), rows(zg)
+    f = zg.zg_kv_attention
+    ok = dict(cache=c, table=P, max_blocks=4, length=P, n_rows=None, q=r, out=r, lse=None, B=1, R=1, Hq=2, scale=1.0,
+              causal=False, workspace=P, ws_bytes=1 << 30)
+
+    def no(status, words, **kw):
+        refused(zg, status, words, f, **{**ok, **kw})
+
+    no(1, "Hq", Hq=3)
+    no(1, "Hq", Hq=0)
+    no(1, "Hq", Hq=1026)
+    no(1, "2^31", B=1 << 20, R=1 << 11)
+    no(1, "B and R", R=-1)
+    no(4, "ZG_BF16 or ZG_F16", q=rows(zg, dtype=zg.ZG_F32), out=rows(zg, dtype=zg.ZG_F32))
+    no(1, "out must", out=rows(zg, dtype=zg.ZG_F16))
+    no(1, "length", length=None)
+    no(1, "table", table=None)
+    no(1, "scale", scale=0.0)
+    no(1, "scale", scale=float("nan"))
+    no(1, "lse", lse=P + 2)
+    long = dict(max_blocks=4096)
+    assert zg.zg_kv_attention_workspace_size(c, 4096, 1, 1, 2) > 0
+    no(1, "workspace", workspace=None, **long)
+    no(1, "workspace", workspace=P + 64, **long)
+    no(1, "workspace", ws_bytes=16, **long)
+    f(**{**ok, "B": 0})
+    f(**{**ok, "R": 0})
+    from generative_recommendation_constrained_gb300._lib import lib
+    assert lib.zg_kv_attention_workspace_size(c, 4, 1, 1, 2, None) == 1
+
+
+def test_workspace_covers_smaller_calls(zg):
+    """A workspace sized for a batch serves no less than the same batch needs: equal sizes, equal answers."""
+    c = cache(zg)
+    assert zg.zg_kv_attention_workspace_size(c, 64, 0, 4, 2) == 0
+    a = zg.zg_kv_attention_workspace_size(c, 4096, 2, 3, 4)
+    assert a == zg.zg_kv_attention_workspace_size(c, 4096, 2, 3, 4) and isinstance(a, int)
+
+
+def test_binding_structs_match_the_header(zg):
+    """Sizes of the argument structs as the C compiler lays them out."""
+    from generative_recommendation_constrained_gb300 import _lib
+    assert C.sizeof(_lib.zg_rows) == 40 and C.sizeof(_lib.zg_kv_cache) == 56 and C.sizeof(_lib.zg_norm_rope) == 48
