@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzerogr.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["index_build.cpp", "engine.cpp", "kernels.cu", "kernels_tc.cu", "naive.cu", "decode_static.cu", "deco.cu",
-           "kv_cache.cu", "kv_attention.cu"]
+           "kv_cache.cu", "kv_attention.cu", "kv_attention_tc.cu"]
 
 
 def _nvcc() -> str:

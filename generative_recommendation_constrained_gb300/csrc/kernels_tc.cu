@@ -520,6 +520,8 @@ cudaError_t launch_full_tc(const void* hi, const void* lo, const void* W, float*
                 : launch_tc_t<false, false>(mh, ml, mw, mz, M, V, d, ldz, bf16, epi, status, st);
 }
 
+uint32_t wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
 void set_wait_limit(uint32_t polls) { g_wait_limit.store(polls ? polls : kSpinLimit, std::memory_order_relaxed); }
 
 }  // namespace zg

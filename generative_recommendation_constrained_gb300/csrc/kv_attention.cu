@@ -1,78 +1,30 @@
 // Attention over a history cache held in 8 bits.
 //
-//   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j - m)
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j)
 //
-// in one pass over the cache with a running maximum m (in log2 units, so that
-// p is one exp2).  Codes enter the products exactly as halves; a key block's
-// scale multiplies its scores, a value block's scale its probabilities,
-// relative to a running reference scale that is folded back at the end.  The
-// reference maximum and scale move only when a tile exceeds them by 2^8 and
-// 2^4, so that accumulators are rescaled rarely; a probability then stays
-// below 2^12, well inside a half.
+// in one pass over the cache.  Codes enter the products exactly as halves.  A
+// key block's scale multiplies its scores; a value block's scale s enters the
+// exponent: with z the score in log2 units,
+//
+//   w_j = exp2(z_j + log2 s_j - m),  out = sum_j w_j code_j / sum_j w_j / s_j
+//
+// so one running reference m a row, the largest z + log2 s, keeps the weights
+// inside a half whatever the scales are, and a scale costs nothing an
+// element.  The reference moves only when a tile exceeds it by 2^8, so that
+// accumulators are rescaled rarely; a weight stays below 2^8.
 #include <cmath>
 #include <string>
 
-#include "kv.cuh"
+#include "kv_attn.cuh"
 
 namespace zg {
 namespace {
-
-struct AttnArgs {
-  const uint8_t *kc, *vc;
-  const float *ks, *vs;
-  const int32_t *table, *length, *n_rows;
-  uint32_t* status;
-  float* lse;
-  float* part;  // [item][split][16][D] outputs, then [item][split][16][2] (max, sum)
-  int32_t n_blocks, heads, bt, max_blocks;
-  int32_t B, R, Hq, G, mt, splits, causal;
-  float scale;  // scale * log2(e)
-};
-
-// The requests' lengths and rows, held inside what the tables can hold.
-struct Seen {
-  int len, rows;
-};
-__device__ __forceinline__ Seen seen_of(const AttnArgs& a, int b, bool report) {
-  Seen s = {a.length[b], a.n_rows ? a.n_rows[b] : a.R};
-  const int most = a.max_blocks * a.bt;
-  if (s.len < 0 || s.len > most || s.rows < 0 || s.rows > a.R) {
-    if (report) atomicOr(a.status, kStatusCache);
-    s.len = min(max(s.len, 0), most);
-    s.rows = min(max(s.rows, 0), a.R);
-  }
-  return s;
-}
-
-// Tokens that query row r sees.
-__device__ __forceinline__ int visible(const AttnArgs& a, const Seen& s, int r) {
-  if (r >= s.rows) return 0;
-  return a.causal ? max(0, s.len - (s.rows - 1 - r)) : s.len;
-}
 
 __device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The power of two that brings a row's largest |q| to [1, 2), as an exponent.
-__device__ __forceinline__ int row_exponent(float top) {
-  if (!(top > 0.f) || !(top <= 3.0e38f)) return 0;
-  const int e = (int)((__float_as_uint(top) >> 23) & 0xFF) - 127;
-  return max(e, -120);
 }
 
 template <typename T>
@@ -156,7 +108,7 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
   for (int j = 0; j < D / 8; ++j)
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
-  float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0.f;
+  float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
   for (int t = t0 + warp; t < t1; t += 4) {
     const int key0 = t * 16;
@@ -168,7 +120,7 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
     const int64_t bh = (int64_t)blk * a.heads + h;
     const uint8_t* kp = a.kc + (bh * a.bt + key0 % a.bt) * D;
     const uint8_t* vp = a.vc + (bh * a.bt + key0 % a.bt) * D;
-    const float ks = a.ks[bh], vs = a.vs[bh];
+    const float ks = a.ks[bh], lv = scale_log2(a.vs[bh]), iv = exp2_fast(-lv);
     uint2 kw[2][U];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -203,7 +155,7 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int key = key0 + n * 8 + 2 * c + (k & 1);
-        z[n][k] = key < vis[k >> 1] ? z[n][k] * (fz[k >> 1] * ks) : -INFINITY;
+        z[n][k] = key < vis[k >> 1] ? fmaf(z[n][k], fz[k >> 1] * ks, lv) : -INFINITY;
         tm[k >> 1] = fmaxf(tm[k >> 1], z[n][k]);
       }
 #pragma unroll
@@ -225,15 +177,6 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
         }
       }
     }
-    if (vs > 16.f * vref) {  // uniform over the warp
-      const float f = vref / vs;
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[j][k] *= f;
-      vref = vs;
-    }
-    const float vr = vref > 0.f ? vs / vref : 0.f;
     uint32_t pa[4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -241,8 +184,8 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const float p0 = exp2_fast(z[n][2 * e] - mu), p1 = exp2_fast(z[n][2 * e + 1] - mu);
-        l[e] += p0 + p1;
-        pa[2 * n + e] = pack_half2(p0 * vr, p1 * vr);
+        l[e] = fmaf(p0 + p1, iv, l[e]);
+        pa[2 * n + e] = pack_half2(p0, p1);
       }
     }
 #pragma unroll
@@ -268,8 +211,8 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
     }
 #pragma unroll
     for (int j = 0; j < D / 8; ++j) {
-      sm_o[warp][g + 8 * e][2 * c * (D / 8) + j] = o[j][2 * e] * vref;
-      sm_o[warp][g + 8 * e][(2 * c + 1) * (D / 8) + j] = o[j][2 * e + 1] * vref;
+      sm_o[warp][g + 8 * e][2 * c * (D / 8) + j] = o[j][2 * e];
+      sm_o[warp][g + 8 * e][(2 * c + 1) * (D / 8) + j] = o[j][2 * e + 1];
     }
   }
   __syncthreads();
@@ -319,17 +262,17 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
   const int64_t br = w / a.Hq;
   const int r = (int)(br % a.R), b = (int)(br / a.R);
   const int i = r * a.G + qh % a.G;
-  const int64_t item = ((int64_t)b * a.heads + qh / a.G) * a.mt + i / 16;
-  const float* ml = a.part + (int64_t)a.B * a.heads * a.mt * a.splits * 16 * D;
-  const int64_t p0 = item * a.splits * 16 + i % 16;
+  const int64_t item = ((int64_t)b * a.heads + qh / a.G) * a.mt + i / a.tile;
+  const float* ml = a.part + (int64_t)a.B * a.heads * a.mt * a.splits * a.tile * D;
+  const int64_t p0 = item * a.splits * a.tile + i % a.tile;
   float top = -INFINITY;
-  for (int sp = lane; sp < a.splits; sp += 32) top = fmaxf(top, ml[(p0 + (int64_t)sp * 16) * 2]);
+  for (int sp = lane; sp < a.splits; sp += 32) top = fmaxf(top, ml[(p0 + (int64_t)sp * a.tile) * 2]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   float sum = 0.f, x[D / 32] = {};
   if (top != -INFINITY) {
     for (int sp = 0; sp < a.splits; ++sp) {
-      const int64_t pi = p0 + (int64_t)sp * 16;
+      const int64_t pi = p0 + (int64_t)sp * a.tile;
       const float f = exp2_fast(ml[pi * 2] - top);
       sum = fmaf(f, ml[pi * 2 + 1], sum);
 #pragma unroll
@@ -347,21 +290,29 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
 // ---------------------------------------------------------------- host side
 
 struct AttnPlan {
-  int mt, splits;
+  bool tc;
+  int tile, mt, splits;
   int64_t items;
   size_t bytes;
 };
 
-// Items for every SM several times over; a part of the keys holds 256 at least.
+constexpr int kFewRows = 32;  // query rows a key head up to which k_attn_few is the faster
+
+// Few rows: items for every SM several times over, 256 keys a part at least.
+// Many rows: parts only where items leave SMs idle, 512 keys each at least.
 AttnPlan attn_plan(const zg_kv_cache* c, int max_blocks, int B, int R, int Hq) {
   AttnPlan p;
   const int64_t M = (int64_t)R * (Hq / c->heads);
-  p.mt = (int)((M + 15) / 16);
+  p.tc = M > kFewRows;
+  p.tile = p.tc ? attn_tc_tile(M) : 16;
+  p.mt = (int)((M + p.tile - 1) / p.tile);
   p.items = (int64_t)B * c->heads * p.mt;
-  const int64_t most = std::max<int64_t>(1, (int64_t)max_blocks * c->block_tokens / 256);
-  const int64_t want = p.items ? ((int64_t)sm_count() * 8 + p.items - 1) / p.items : 1;
+  const int64_t keys = (int64_t)max_blocks * c->block_tokens;
+  const int64_t most = std::max<int64_t>(1, keys / (p.tc ? 512 : 256));
+  int64_t want = 1;
+  if (p.items) want = p.tc ? sm_count() / p.items : ((int64_t)sm_count() * 8 + p.items - 1) / p.items;
   p.splits = (int)std::max<int64_t>(1, std::min(want, most));
-  p.bytes = p.splits > 1 ? (size_t)p.items * p.splits * 16 * (c->dim + 2) * 4 : 0;
+  p.bytes = p.splits > 1 ? (size_t)p.items * p.splits * p.tile * (c->dim + 2) * 4 : 0;
   return p;
 }
 
@@ -433,6 +384,7 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   a.R = R;
   a.Hq = Hq;
   a.G = Hq / cache->heads;
+  a.tile = p.tile;
   a.mt = p.mt;
   a.splits = p.splits;
   a.causal = causal != 0;
@@ -441,12 +393,18 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   auto launch = [&](auto ev, auto dv, auto iv) {
     using E = typename decltype(ev)::type;
     constexpr int D = decltype(dv)::value;
-    k_attn_few<E, D, decltype(iv)::value><<<(unsigned)(p.items * p.splits), kFewThreads, 0, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
+    if (!p.tc)
+      k_attn_few<E, D, decltype(iv)::value>
+          <<<(unsigned)(p.items * p.splits), kFewThreads, 0, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
     if (p.splits > 1) {
       const int64_t warps = (int64_t)B * R * Hq;
       k_attn_join<E, D><<<(unsigned)((warps + 7) / 8), 256, 0, sm>>>(a, rows_of<E>(out));
     }
   };
+  if (p.tc) {
+    const cudaError_t e = launch_attn_tc(a, q, out, cache->dim, cache->format == ZG_KV_INT8, p.items * p.splits, sm);
+    if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
+  }
   for_dim(cache->dim, [&](auto dv) {
     auto typed = [&](auto ev) {
       if (cache->format == ZG_KV_INT8) launch(ev, dv, std::true_type{});

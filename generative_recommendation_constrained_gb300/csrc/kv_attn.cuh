@@ -1,0 +1,77 @@
+// What the attention kernels over a history cache share.
+#pragma once
+
+#include "kv.cuh"
+
+namespace zg {
+
+struct AttnArgs {
+  const uint8_t *kc, *vc;
+  const float *ks, *vs;
+  const int32_t *table, *length, *n_rows;
+  uint32_t* status;
+  float* lse;
+  float* part;  // [item][split][tile][D] outputs, then [item][split][tile][2] (max, sum)
+  int32_t n_blocks, heads, bt, max_blocks;
+  int32_t B, R, Hq, G, splits, causal;
+  int32_t tile, mt;  // query rows an item (power of two), such items a (request, key head)
+  float scale;  // scale * log2(e)
+};
+
+// The requests' lengths and rows, held inside what the tables can hold.
+struct Seen {
+  int len, rows;
+};
+__device__ __forceinline__ Seen seen_of(const AttnArgs& a, int b, bool report) {
+  Seen s = {a.length[b], a.n_rows ? a.n_rows[b] : a.R};
+  const int most = a.max_blocks * a.bt;
+  if (s.len < 0 || s.len > most || s.rows < 0 || s.rows > a.R) {
+    if (report) atomicOr(a.status, kStatusCache);
+    s.len = min(max(s.len, 0), most);
+    s.rows = min(max(s.rows, 0), a.R);
+  }
+  return s;
+}
+
+// Tokens that query row r sees.
+__device__ __forceinline__ int visible(const AttnArgs& a, const Seen& s, int r) {
+  if (r >= s.rows) return 0;
+  return a.causal ? max(0, s.len - (s.rows - 1 - r)) : s.len;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// log2 of a value block's scale; a scale of 0 (all its codes are 0) stands at
+// the floor, so that its keys still count in the row's sum.
+__device__ __forceinline__ float scale_log2(float vs) { return vs > 0x1p-100f ? log2_fast(vs) : -100.f; }
+
+// The power of two that brings a row's largest |q| to [1, 2), as an exponent.
+__device__ __forceinline__ int row_exponent(float top) {
+  if (!(top > 0.f) || !(top <= 3.0e38f)) return 0;
+  const int e = (int)((__float_as_uint(top) >> 23) & 0xFF) - 127;
+  return max(e, -120);
+}
+
+
+// Many query rows: the products on the tensor cores' tcgen05 path
+// (kv_attention_tc.cu).  Query rows of an item, and its launch.
+int attn_tc_tile(int64_t rows);
+cudaError_t launch_attn_tc(const AttnArgs& a, const zg_rows* q, const zg_rows* out, int dim, bool int8,
+                           int64_t items, cudaStream_t st);
+
+}  // namespace zg

@@ -195,6 +195,7 @@ cudaError_t launch_full_tc(const void* hi, const void* lo, const void* W, float*
 // polls of an mbarrier before a pipeline wait of the tensor-core kernel gives
 // up (0: the default); the drain waits before exit always use the default
 void set_wait_limit(uint32_t polls);
+uint32_t wait_limit();
 // Unique id of the calling thread's current CUDA context (the driver's
 // cuCtxGetId; a context created after cudaDeviceReset gets a new id).  Device
 // addresses of __device__ variables are cached per context under this id.

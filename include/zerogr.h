@@ -524,7 +524,8 @@ ZG_API zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table,
 
 /* Test and diagnosis hook, no counterpart in the paper: the number of polls
  * after which a pipeline wait (an mbarrier) of the tensor-core full
- * projection gives up, records bit 2 in the device status word and ends the
+ * projection or of the cached attention gives up, records bit 2 in the device
+ * status word and ends the
  * kernel early (its copies and tensor-core operations drained, tensor memory
  * freed).  0 restores the default (2^26 polls, about a second).  Applies to
  * launches issued after the call, process-wide.  A limit too small for the

@@ -473,6 +473,25 @@ def test_attention_extremes(zg, dev):
         check_attention(zg, dev, c, q, table, length, None, False, scale=0.02)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_attention_scale_of_unseen_blocks(zg, dev, fmt):
+    """A value scale of a block that a causal row does not see leaves the row's precision alone; nor does a large
+    scale that a row sees with no weight."""
+    for R in (10, 90):
+        c, table, length = build(dev, fmt, 1, 1, 64, 16, [96], 6, 9)
+        for j, x in enumerate((1.0, 2.0 ** 30, 2.0 ** -30, 1.0, 2.0 ** 60, 2.0 ** 90)):
+            c.v_scale[table[0, j].long()] = x
+        q = randn((1, R, 2, 64), torch.bfloat16, 6, scale=2.0)
+        check_attention(zg, dev, c, q, table, length, None, True)
+        # keys of the large blocks far below the others: their weight times their values is nothing
+        blk = table[0].long()
+        c.v_scale[blk] = torch.tensor([[1.0], [4.0], [1.0], [2.0 ** 18], [1.0], [2.0 ** 20]], device="cuda")
+        for j in (3, 5):
+            c.k_codes.view(torch.uint8)[blk[j]] = c.k_codes.view(torch.uint8)[blk[j], :, :1].clone()
+        q = (-40 * torch.sign(c.k_codes[blk[3], 0, 0].float() + c.k_codes[blk[5], 0, 0].float())).expand(1, R, 2, 64).to(torch.bfloat16).contiguous()
+        check_attention(zg, dev, c, q, table, length, None, False)
+
+
 def test_attention_strides_and_streams(zg, dev):
     """q inside a packed buffer, outputs into a wider one, on a stream that is not the current one."""
     c, table, length = build(dev, "int8", 2, 2, 64, 32, [100, 77], 5, 2)
@@ -578,3 +597,19 @@ def test_wrappers_refuse_shapes(dev):
               lambda: dev.KVCache.over(c.k_codes, c.v_codes, c.k_scale, c.v_scale[:2])):
         with pytest.raises(ValueError):
             f()
+
+
+def test_expired_wait_is_reported(zg, dev):
+    """A pipeline wait that runs out ends the many-rows kernel early with a status; the next call is sound."""
+    c, table, length = build(dev, "e4m3", 2, 1, 64, 64, [700, 300], 11, 3)
+    q = randn((2, 200, 1, 64), torch.bfloat16, 3)
+    attn = dev.CacheAttention(c, 2, 200, 1, 11)
+    zg.zg_debug_set_wait_limit(1)
+    try:
+        attn(q, table, length)
+        torch.cuda.synchronize()
+        with pytest.raises(zg.ZgError, match="wait expired"):
+            zg.zg_check_device_status(0)
+    finally:
+        zg.zg_debug_set_wait_limit(0)
+    check_attention(zg, dev, c, q, table, length, None, False)
