@@ -3,8 +3,10 @@
 //
 // One CTA takes up to two tiles of 128 query rows (of one request and key
 // head) through 64 keys at a time:
-//   warps 8-11  widen the 8-bit codes of keys and values to halves, exactly,
-//               from global memory into two 128-byte-swizzled shared buffers;
+//   warp 13     brings the codes of 64 keys a step into a ring of four by bulk
+//               copies, 16 keys (always inside one block) a copy;
+//   warps 8-11  widen the codes of keys and values to halves, exactly, into
+//               two 128-byte-swizzled shared buffers;
 //   warp 12     issues S = Q K^T and O += P V (tcgen05, one thread): S and O
 //               live in tensor memory, P is read from there;
 //   warps 0-7   one thread a row: scores out of tensor memory, running
@@ -25,15 +27,17 @@ namespace {
 
 constexpr int kNK = 64;             // keys a step
 constexpr int kSoftWarps = 8, kWidenWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + kWidenWarps + 1);
-constexpr uint32_t kSpin = 1u << 20;  // polls of a wait at most; of the one before exit always
+constexpr int kThreads = 32 * (kSoftWarps + kWidenWarps + 2);
+constexpr int kRing = 4;            // steps of codes in flight
+constexpr uint32_t kSpin = 1u << 20;  // polls of a wait at most; of those before exit always
 
 template <int D>
 struct TcShape {
   static constexpr int kSub = (D + 63) / 64;          // 64-dim subtiles (128-byte rows)
   static constexpr int kQ = kSub * 128 * 128;         // bytes of one query tile
   static constexpr int kKV = kSub * kNK * 128;        // bytes of one widened key or value buffer
-  static constexpr size_t kSmem = 2 * kQ + 4 * kKV + 1024;
+  static constexpr int kRaw = 2 * kNK * D;            // codes of one step, keys then values
+  static constexpr size_t kSmem = 2 * kQ + 4 * kKV + kRing * kRaw + 1024;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -45,16 +49,25 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t n) {
 __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Bounded wait for the phase of the given parity; false on expiry.
+// Bounded wait for the phase of the given parity; false on expiry.  A poll
+// suspends the thread for up to a microsecond or so; under a limit of a few
+// polls (the debug hook's) it does not, so that the wait does run out.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
   const uint32_t a = smem_u32(bar);
   for (uint32_t it = 0; it < limit; ++it) {
     uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(a), "r"(parity)
-        : "memory");
+    if (limit > 64)
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+          : "=r"(done)
+          : "r"(a), "r"(parity)
+          : "memory");
+    else
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+          : "=r"(done)
+          : "r"(a), "r"(parity)
+          : "memory");
     if (done) return true;
   }
   return false;
@@ -62,6 +75,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_
 // The same for a whole warp: one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
   return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, limit));
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 
 // K-major operand, 128-byte swizzle: rows of 128 bytes, groups of 8 rows 1024 bytes apart.
@@ -113,6 +133,17 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr) : "memory");
+}
 // 64 columns.
 __device__ __forceinline__ void tmem_load64(uint32_t addr, uint32_t* r) {
   uint32_t* r2 = r + 32;
@@ -132,6 +163,14 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// `bytes` from global into shared memory, counted on `bar`; both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(to)),
+               "l"(from), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -154,15 +193,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sq = smem;                       // two query tiles
   uint8_t* sk = sq + 2 * Sh::kQ;            // two key buffers
   uint8_t* sv = sk + 2 * Sh::kKV;           // two value buffers
-  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], drained;
+  uint8_t* raw = sv + 2 * Sh::kKV;          // the ring of codes
+  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], drained, raw_full[kRing], raw_empty[kRing];
   // [query tile][step parity]: one phase of each is never passed before all its waits are over, because step t + 2
   // of a kind starts only after the warps that wait for step t have done their part of it
   __shared__ uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
-  // of 16 keys each, a ring of four steps: key scale, log2 of the value scale, and 2^-that
-  __shared__ float s_ks[4][4], s_lv[4][4], s_iv[4][4];
+  // of 16 keys each, a ring of eight steps (the codes of step t + 8 come only after the softmax of step t): key
+  // scale, log2 of the value scale, and 2^-that
+  __shared__ float s_ks[8][4], s_lv[8][4], s_iv[8][4];
   __shared__ uint32_t tmem_base;
   __shared__ int s_vmax;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   int it = blockIdx.x;
   const int split = it % a.splits;
@@ -188,6 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     bar_init(&drained, 1);
+    for (int i = 0; i < kRing; ++i) {
+      bar_init(&raw_full[i], 1);
+      bar_init(&raw_empty[i], kWidenWarps);
+    }
     s_vmax = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -249,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int steps_all = (s_vmax + kNK - 1) / kNK;
   const int per = (steps_all + a.splits - 1) / a.splits;
   const int t0 = min(steps_all, split * per);
-  const int steps = min(steps_all, t0 + per) - t0;
+  const int steps = __shfl_sync(0xFFFFFFFFu, min(steps_all, t0 + per) - t0, 0);  // uniform, for the compiler too
 
   auto give_up = [&]() { atomicOr(a.status, kStatusTimeout); };
 
@@ -258,38 +303,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int C16 = D / 16;                // 16-byte pieces of a code row
     constexpr int N = kNK * C16 / 128;         // pieces a thread and side
     const int tid = threadIdx.x - 32 * kSoftWarps;
-    const int64_t hb = (int64_t)a.bt * D;
-    uint4 kw[N], vw[N];
-    float sck = 0.f, scv = 0.f;                // threads 0-3: scales of their 16 keys
-    auto block_of = [&](int key) -> int {      // -1: behind the history, or outside the cache (recorded)
-      if (key >= s.len) return -1;
-      const int blk = a.table[(int64_t)b * a.max_blocks + key / a.bt];
-      if (blk < 0 || blk >= a.n_blocks) {
-        atomicOr(a.status, kStatusCache);
-        return -1;
-      }
-      return blk;
-    };
-    auto fetch = [&](int t) {
-      const int key0 = (t0 + t) * kNK;
+    auto widen = [&](uint8_t* buf, const uint8_t* codes, int held) {
+      uint4 w[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int idx = tid + 128 * i, r = idx / C16, c = idx % C16;
-        const int blk = block_of(key0 + r);
-        kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
-        if (blk >= 0) {
-          const int64_t at = ((int64_t)blk * a.heads + h) * hb + (int64_t)((key0 + r) % a.bt) * D + 16 * c;
-          kw[i] = *reinterpret_cast<const uint4*>(a.kc + at);
-          vw[i] = *reinterpret_cast<const uint4*>(a.vc + at);
-        }
+      for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4*>(codes + (tid + 128 * i) * 16);
+      if (held < kNK) {  // behind the history: not defined, may be NaN
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if ((tid + 128 * i) / C16 >= held) w[i] = make_uint4(0, 0, 0, 0);
       }
-      if (tid < kNK / 16) {
-        const int blk = block_of(key0 + 16 * tid);
-        sck = blk < 0 ? 0.f : a.ks[(int64_t)blk * a.heads + h];
-        scv = blk < 0 ? 0.f : a.vs[(int64_t)blk * a.heads + h];
-      }
-    };
-    auto put = [&](uint8_t* buf, const uint4* w) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int idx = tid + 128 * i, r = idx / C16, c = idx % C16;
@@ -305,33 +327,187 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4*>(p + (((j + (swap ? 1 : 0)) ^ (r & 7)) << 4)) = swap ? hi : lo;
         *reinterpret_cast<uint4*>(p + (((j + (swap ? 0 : 1)) ^ (r & 7)) << 4)) = swap ? lo : hi;
       }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
     };
-    if (steps > 0) fetch(0);
     for (int t = 0; t < steps; ++t) {
-      const int buf = t & 1;
-      if (t >= 2 && !warp_wait(&k_empty[buf], ((t >> 1) - 1) & 1, spin)) {
+      const int buf = t & 1, slot = t % kRing;
+      const int held = s.len - (t0 + t) * kNK;
+      const uint8_t* codes = raw + slot * Sh::kRaw;
+      if (!warp_wait(&raw_full[slot], (t / kRing) & 1, spin) ||
+          (t >= 2 && !warp_wait(&k_empty[buf], ((t >> 1) - 1) & 1, spin))) {
         if (lane == 0) give_up();
         break;
       }
-      if (tid < kNK / 16) {
-        s_ks[t & 3][tid] = sck;
-        s_lv[t & 3][tid] = scale_log2(scv);
-        s_iv[t & 3][tid] = exp2_fast(-scale_log2(scv));
-      }
-      put(sk + buf * Sh::kKV, kw);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
+      widen(sk + buf * Sh::kKV, codes, held);
       if (lane == 0) bar_arrive(&k_full[buf]);
       if (t >= 2 && !warp_wait(&v_empty[buf], ((t >> 1) - 1) & 1, spin)) {
         if (lane == 0) give_up();
         break;
       }
-      put(sv + buf * Sh::kKV, vw);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) bar_arrive(&v_full[buf]);
-      if (t + 1 < steps) fetch(t + 1);
+      widen(sv + buf * Sh::kKV, codes + kNK * D, held);
+      if (lane == 0) {
+        bar_arrive(&v_full[buf]);
+        bar_arrive(&raw_empty[slot]);
+      }
     }
+  } else if (warp == 13) {
+    // ---------------------------------------------------------------- codes
+    // Lane g of four brings keys 16 g .. 16 g + 15 of a step.  Block numbers are read two steps and scales one step
+    // ahead of their use.
+    const int g = lane & 3;
+    auto block_of = [&](int t) -> int {  // -1: behind the history, or outside the cache (recorded)
+      const int key = (t0 + t) * kNK + 16 * g;
+      if (t >= steps || key >= s.len) return -1;
+      const int blk = a.table[(int64_t)b * a.max_blocks + key / a.bt];
+      if (blk >= 0 && blk < a.n_blocks) return blk;
+      if (lane < 4) atomicOr(a.status, kStatusCache);
+      return -1;
+    };
+    int blk = block_of(0), blk1 = block_of(1);
+    float ks = blk < 0 ? 0.f : a.ks[(int64_t)blk * a.heads + h], vs = blk < 0 ? 0.f : a.vs[(int64_t)blk * a.heads + h];
+    int issued = 0;
+    for (int t = 0; t < steps; ++t) {
+      const int blk2 = block_of(t + 2);
+      const float ks1 = blk1 < 0 ? 0.f : a.ks[(int64_t)blk1 * a.heads + h];
+      const float vs1 = blk1 < 0 ? 0.f : a.vs[(int64_t)blk1 * a.heads + h];
+      const int slot = t % kRing;
+      if (t >= kRing && !warp_wait(&raw_empty[slot], ((t / kRing) - 1) & 1, spin)) {
+        if (lane == 0) give_up();
+        break;
+      }
+      if (lane < 4) {
+        s_ks[t & 7][g] = ks;
+        s_lv[t & 7][g] = scale_log2(vs);
+        s_iv[t & 7][g] = exp2_fast(-scale_log2(vs));
+      }
+      const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, lane < 4 && blk >= 0));
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&raw_full[slot])),
+                     "r"(n * 2u * 16u * (uint32_t)D)
+                     : "memory");
+      __syncwarp();
+      if (lane < 4 && blk >= 0) {
+        const int row = ((t0 + t) * kNK + 16 * g) % a.bt;
+        const int64_t at = (((int64_t)blk * a.heads + h) * a.bt + row) * D;
+        uint8_t* to = raw + slot * Sh::kRaw + 16 * g * D;
+        bulk_load(to, a.kc + at, 16 * D, &raw_full[slot]);
+        bulk_load(to + kNK * D, a.vc + at, 16 * D, &raw_full[slot]);
+      }
+      issued = t + 1;
+      blk = blk1, ks = ks1, vs = vs1, blk1 = blk2;
+    }
+    // every copy has landed before the CTA may end
+    for (int t = max(0, issued - kRing); t < issued; ++t)
+      if (!warp_wait(&raw_full[t % kRing], (t / kRing) & 1, kSpin) && lane == 0) give_up();
+  } else if (warp == 12) {
+    // ------------------------------------------------------------- products
+    // The whole warp walks the loop and one elected thread issues, so that descriptors stay in uniform registers
+    // (from one diverged thread an instruction took some 100 cycles to issue: 3,900 a step, 1,000 of them work).
+    if (steps > 0) {
+      const uint32_t id_s = (1u << 4) | ((uint32_t)(kNK >> 3) << 17) | ((128u >> 4) << 24);
+      const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+      const uint64_t q0 = desc_k(smem_u32(sq)), k0 = desc_k(smem_u32(sk)), v0 = desc_mn(smem_u32(sv), kNK * 128);
+      bool good = true;
+      for (int t = 0; t <= steps && good; ++t) {
+        if (t < steps) {
+          const uint32_t par = t & 1, ph = (t >> 1) & 1;
+          const uint64_t kd = k0 + par * (Sh::kKV >> 4);
+          good = warp_wait(&k_full[par], ph, spin);
+          for (int i = 0; i < tiles && good; ++i) {
+            // the scores go where step t - 2 had its probabilities
+            if (t >= 2) good = warp_wait(&o_done[i][par], ph ^ 1, spin);
+            if (!good) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + (uint32_t)(i * 128 + par * kNK);
+            const uint64_t qd = q0 + i * (Sh::kQ >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss(d, qd + (k / 4) * (128 * 128 >> 4) + (k % 4) * 2, kd + (k / 4) * (kNK * 128 >> 4) + (k % 4) * 2,
+                       id_s, k > 0);
+              commit(&s_full[i][par]);
+              if (i == tiles - 1) commit(&k_empty[par]);
+            }
+            __syncwarp();
+          }
+        }
+        if (t > 0 && good) {
+          const int u = t - 1;
+          const uint32_t par = u & 1, ph = (u >> 1) & 1;
+          const uint64_t vd = v0 + par * (Sh::kKV >> 4);
+          good = warp_wait(&v_full[par], ph, spin);
+          for (int i = 0; i < tiles && good; ++i) {
+            good = warp_wait(&p_full[i][par], ph, spin);
+            if (!good) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t p = tmem + (uint32_t)(i * 128 + par * kNK), o = t_o + (uint32_t)(i * 128);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kNK / 16; ++k) mma_ts(o, p + k * 8, vd + k * (2048 >> 4), id_o, (u > 0 || k > 0) ? 1u : 0u);
+              commit(&o_done[i][par]);
+              if (i == tiles - 1) commit(&v_empty[par]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (!good && lane == 0) give_up();
+      if (elect_one()) commit(&drained);
+      __syncwarp();
+      if (!warp_wait(&drained, 0, kSpin) && lane == 0) give_up();
+    }
+  } else if (warp == 13) {
+    // ---------------------------------------------------------------- codes
+    // Lane g of four brings keys 16 g .. 16 g + 15 of a step.  Block numbers are read two steps and scales one step
+    // ahead of their use.
+    const int g = lane & 3;
+    auto block_of = [&](int t) -> int {  // -1: behind the history, or outside the cache (recorded)
+      const int key = (t0 + t) * kNK + 16 * g;
+      if (t >= steps || key >= s.len) return -1;
+      const int blk = a.table[(int64_t)b * a.max_blocks + key / a.bt];
+      if (blk >= 0 && blk < a.n_blocks) return blk;
+      if (lane < 4) atomicOr(a.status, kStatusCache);
+      return -1;
+    };
+    int blk = block_of(0), blk1 = block_of(1);
+    float ks = blk < 0 ? 0.f : a.ks[(int64_t)blk * a.heads + h], vs = blk < 0 ? 0.f : a.vs[(int64_t)blk * a.heads + h];
+    int issued = 0;
+    for (int t = 0; t < steps; ++t) {
+      const int blk2 = block_of(t + 2);
+      const float ks1 = blk1 < 0 ? 0.f : a.ks[(int64_t)blk1 * a.heads + h];
+      const float vs1 = blk1 < 0 ? 0.f : a.vs[(int64_t)blk1 * a.heads + h];
+      const int slot = t % kRing;
+      if (t >= kRing && !warp_wait(&raw_empty[slot], ((t / kRing) - 1) & 1, spin)) {
+        if (lane == 0) give_up();
+        break;
+      }
+      if (lane < 4) {
+        s_ks[t & 7][g] = ks;
+        s_lv[t & 7][g] = scale_log2(vs);
+        s_iv[t & 7][g] = exp2_fast(-scale_log2(vs));
+      }
+      const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, lane < 4 && blk >= 0));
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&raw_full[slot])),
+                     "r"(n * 2u * 16u * (uint32_t)D)
+                     : "memory");
+      __syncwarp();
+      if (lane < 4 && blk >= 0) {
+        const int row = ((t0 + t) * kNK + 16 * g) % a.bt;
+        const int64_t at = (((int64_t)blk * a.heads + h) * a.bt + row) * D;
+        uint8_t* to = raw + slot * Sh::kRaw + 16 * g * D;
+        bulk_load(to, a.kc + at, 16 * D, &raw_full[slot]);
+        bulk_load(to + kNK * D, a.vc + at, 16 * D, &raw_full[slot]);
+      }
+      issued = t + 1;
+      blk = blk1, ks = ks1, vs = vs1, blk1 = blk2;
+    }
+    // every copy has landed before the CTA may end
+    for (int t = max(0, issued - kRing); t < issued; ++t)
+      if (!warp_wait(&raw_full[t % kRing], (t / kRing) & 1, kSpin) && lane == 0) give_up();
   } else if (warp == 12) {
     // ------------------------------------------------------------- products
     if (lane == 0 && steps > 0) {
@@ -405,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float f[4], lv[4], tm = -INFINITY;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        f[g] = fmaxf(fz * s_ks[t & 3][g], 1e-37f);  // a scale of 0 must not meet an infinite score
-        lv[g] = s_lv[t & 3][g];
+        f[g] = fmaxf(fz * s_ks[t & 7][g], 1e-37f);  // a scale of 0 must not meet an infinite score
+        lv[g] = s_lv[t & 7][g];
         float gm = z[16 * g];
 #pragma unroll
         for (int j = 1; j < 16; ++j) gm = fmaxf(gm, z[16 * g + j]);
@@ -425,12 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-          for (int d = 0; d < D; d += 32) {
-            uint32_t r[32];
-            tmem_load(o_at + d, r);
+          for (int d = 0; d < D; d += 16) {  // few at a time: the scores stay in registers
+            uint32_t r[16];
+            tmem_load16(o_at + d, r);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al);
-            tmem_store(o_at + d, r);
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al);
+            tmem_store16(o_at + d, r);
           }
           tmem_store_wait();
         }
@@ -447,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum += p0 + p1;
           pr[8 * g + j / 2] = pack_half2(p0, p1);
         }
-        l = fmaf(sum, s_iv[t & 3][g], l);
+        l = fmaf(sum, s_iv[t & 7][g], l);
       }
       tmem_store(s_at, pr);
       tmem_store_wait();
