@@ -27,32 +27,89 @@ __device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, uint32_t 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T>
-__device__ __forceinline__ void store2(T* p, float a, float b);
-template <>
-__device__ __forceinline__ void store2<__half>(__half* p, float a, float b) {
-  *reinterpret_cast<__half2*>(p) = __floats2half2_rn(a, b);
-}
-template <>
-__device__ __forceinline__ void store2<__nv_bfloat16>(__nv_bfloat16* p, float a, float b) {
-  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+// Transposes an 8 x 8 matrix of halves held one row a group of four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 constexpr int kFewThreads = 128;
 
-// Few query rows: one CTA an item (request, key head, 16 rows, part of the
-// keys); a row is (token, query head of the group).  Each warp walks its own
-// 16-key tiles straight from global memory into matrix fragments: the order
-// of the dims inside a product is free, so a lane reads neighbouring bytes.
-template <typename T, int D, bool INT8>
+// What one lane holds of 16 keys and values: of keys g and g + 8 (lane = 4 g +
+// c) the dims of `dim_of`, of values 2c, 2c + 1, 2c + 8, 2c + 9 the dims g * D/8
+// and on.  The order of the dims inside a product is free, so that a lane
+// reads neighbouring bytes and a warp whole rows.
+template <int D>
+struct Tile16 {
+  static constexpr int KW = D / 16, VW = D / 32;  // words of a key, of a value
+  uint32_t k[2][KW], v[4][VW];
+  float ks, vs;
+  static __device__ __forceinline__ int dim_of(int w, int c) {
+    return w < D / 64 * 4 ? w / 4 * 64 + 16 * c + 4 * (w % 4) : D / 64 * 64 + 8 * c + 4 * (w - D / 64 * 4);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < KW; ++i) k[0][i] = k[1][i] = 0;
+#pragma unroll
+    for (int i = 0; i < VW; ++i) v[0][i] = v[1][i] = v[2][i] = v[3][i] = 0;
+    ks = vs = 0.f;
+  }
+  __device__ __forceinline__ void load(const uint8_t* kp, const uint8_t* vp, int g, int c) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const uint8_t* p = kp + (n * 8 + g) * D;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) *reinterpret_cast<uint4*>(&k[n][4 * i]) = ldg16(p + 64 * i + 16 * c);
+      if constexpr (D % 64 != 0) *reinterpret_cast<uint2*>(&k[n][D / 64 * 4]) = ldg8(p + D / 64 * 64 + 8 * c);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint8_t* p = vp + (2 * c + (j & 1) + (j >> 1) * 8) * D + g * (D / 8);
+      if constexpr (D == 128) {
+        *reinterpret_cast<uint4*>(v[j]) = ldg16(p);
+      } else if constexpr (D == 64) {
+        *reinterpret_cast<uint2*>(v[j]) = ldg8(p);
+      } else {
+#pragma unroll
+        for (int u = 0; u < VW; ++u) v[j][u] = ldg4(p + 4 * u);
+      }
+    }
+  }
+  // each code is read once: past L1
+  static __device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+    uint4 x;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+    return x;
+  }
+  static __device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+    uint2 x;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
+    return x;
+  }
+  static __device__ __forceinline__ uint32_t ldg4(const uint8_t* p) {
+    uint32_t x;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(x) : "l"(p));
+    return x;
+  }
+};
+
+// Few query rows: one CTA an item (request, key head, 8 NT rows) and part of
+// the keys; a row is (token, query head of the group).  Each warp walks its own
+// 16-key tiles straight from global memory into matrix fragments, the next
+// tile's loads in flight under this one's products.  Keys and dims are the
+// long side of the products (S^T = K Q^T, O^T = V^T P^T), so that eight rows
+// fill an instruction that sixteen keys or dims by eight rows make.
+template <typename T, int D, bool INT8, int NT>
 __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant__ AttnArgs a, const Rows<T> q,
                                                           const Rows<T> out) {
-  constexpr int U = D / 32;  // 8-byte units of a key row a lane reads; words of a value row
-  __shared__ float sm_m[4][16], sm_l[4][16];
-  __shared__ float sm_o[4][16][D + 2];
+  using Tl = Tile16<D>;
+  constexpr int KW = Tl::KW, VW = Tl::VW, NR = 8 * NT;
+  __shared__ float sm_m[4][NR], sm_l[4][NR];
+  __shared__ float sm_o[4][NR][D + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   int it = blockIdx.x;
-  const int split = it % a.splits;
+  const int part = it % a.splits;
   it /= a.splits;
   const int item = it;
   const int m = it % a.mt;
@@ -60,191 +117,207 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
   const int h = it % a.heads, b = it / a.heads;
   const Seen s = seen_of(a, b, threadIdx.x == 0);
   const int M = a.R * a.G;
+  // later rows see no less: the item sees what its last row does, or its request's last
+  const int last = min(min(m * NR + NR, M) - 1, s.rows * a.G - 1);
+  const int vmax = last < m * NR ? 0 : visible(a, s, last / a.G);
+  const int parts = parts_of(a, vmax);
+  if (part >= parts) return;  // the join does not look for it
+  const int t0 = part * (a.chunk / 16) + warp, t1 = min((vmax + 15) / 16, (part + 1) * (a.chunk / 16));
 
-  int vis[2], row[2], qh[2];
-  uint32_t qa[2 * U][4];
-  float fz[2];
+  auto block_of = [&](int t) -> int {
+    if (t >= t1) return -1;
+    const int blk = a.table[(int64_t)b * a.max_blocks + t * 16 / a.bt];
+    if (blk >= 0 && blk < a.n_blocks) return blk;
+    if (lane == 0) atomicOr(a.status, kStatusCache);
+    return -1;
+  };
+  auto fetch = [&](Tl& x, int t, int blk) {
+    if (blk < 0) return x.zero();
+    const int64_t bh = (int64_t)blk * a.heads + h, at = (bh * a.bt + t * 16 % a.bt) * D;
+    x.load(a.kc + at, a.vc + at, g, c);
+    x.ks = a.ks[bh];
+    x.vs = a.vs[bh];
+  };
+  Tl cur, nxt;
+  int blk = block_of(t0), blk1 = block_of(t0 + 4);
+  fetch(cur, t0, blk);
+
+  // the rows: lane (g, c) the dims of its words of row g; then the sight and the scale of rows 2c, 2c + 1
+  uint32_t qb[NT][KW][2];
+  int vis[NT][2];
+  float fz[NT][2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = m * 16 + g + 8 * e;
-    row[e] = i / a.G;
-    qh[e] = h * a.G + i % a.G;
-    vis[e] = i < M ? visible(a, s, row[e]) : 0;
-    float x[U][8];
-    float top = 0.f;
+  for (int n = 0; n < NT; ++n) {
+    const int i = m * NR + n * 8 + g;
+    const int row = i / a.G;
+    const int sees = i < M ? visible(a, s, row) : 0;
+    float x[KW][4], top = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int w = 0; w < KW; ++w) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[u][k] = 0.f;
-      if (vis[e] > 0) {
-        load4(q.at(b, row[e], qh[e]) + u * 32 + c * 8, x[u]);
-        load4(q.at(b, row[e], qh[e]) + u * 32 + c * 8 + 4, x[u] + 4);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[u][k]));
+      for (int k = 0; k < 4; ++k) x[w][k] = 0.f;
+      if (sees > 0) load4(q.at(b, row, h * a.G + i % a.G) + Tl::dim_of(w, c), x[w]);
     }
+#pragma unroll
+    for (int w = 0; w < KW; ++w)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(x[w][k]));
     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     const int ex = row_exponent(top);
-    const float dn = __uint_as_float((uint32_t)(127 - ex) << 23);
-    fz[e] = a.scale * __uint_as_float((uint32_t)(127 + ex) << 23);
+    const float dn = __uint_as_float((uint32_t)(127 - ex) << 23), up = a.scale * __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        qa[2 * u + k][e] = pack_half2(x[u][4 * k] * dn, x[u][4 * k + 1] * dn);
-        qa[2 * u + k][2 + e] = pack_half2(x[u][4 * k + 2] * dn, x[u][4 * k + 3] * dn);
-      }
-  }
-  int vmax = max(vis[0], vis[1]);
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) vmax = max(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, o));
-  const int tiles = (vmax + 15) / 16;
-  const int per = (tiles + a.splits - 1) / a.splits;
-  const int t0 = split * per, t1 = min(tiles, t0 + per);
-
-  float o[D / 8][4];
-#pragma unroll
-  for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
-  float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  for (int t = t0 + warp; t < t1; t += 4) {
-    const int key0 = t * 16;
-    const int blk = a.table[(int64_t)b * a.max_blocks + key0 / a.bt];
-    if (blk < 0 || blk >= a.n_blocks) {
-      if (lane == 0) atomicOr(a.status, kStatusCache);
-      continue;
+    for (int w = 0; w < KW; ++w) {
+      qb[n][w][0] = pack_half2(x[w][0] * dn, x[w][1] * dn);
+      qb[n][w][1] = pack_half2(x[w][2] * dn, x[w][3] * dn);
     }
-    const int64_t bh = (int64_t)blk * a.heads + h;
-    const uint8_t* kp = a.kc + (bh * a.bt + key0 % a.bt) * D;
-    const uint8_t* vp = a.vc + (bh * a.bt + key0 % a.bt) * D;
-    const float ks = a.ks[bh], lv = scale_log2(a.vs[bh]), iv = exp2_fast(-lv);
-    uint2 kw[2][U];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int u = 0; u < U; ++u) kw[n][u] = *reinterpret_cast<const uint2*>(kp + (n * 8 + g) * D + u * 32 + c * 8);
-    uint32_t vw[4][U];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int key = 2 * c + (k & 1) + (k >> 1) * 8;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        vw[k][u] = *reinterpret_cast<const uint32_t*>(vp + key * D + g * (D / 8) + 4 * u);
-      if (key0 + key >= s.len) {  // behind the history: not defined, may be NaN
-#pragma unroll
-        for (int u = 0; u < U; ++u) vw[k][u] = 0;
-      }
-    }
-    float z[2][4] = {};
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint32_t b0, b1;
-        codes_half4<INT8>(kw[n][u].x, b0, b1);
-        mma_16816(z[n], qa[2 * u], b0, b1);
-        codes_half4<INT8>(kw[n][u].y, b0, b1);
-        mma_16816(z[n], qa[2 * u + 1], b0, b1);
-      }
-    float tm[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = key0 + n * 8 + 2 * c + (k & 1);
-        z[n][k] = key < vis[k >> 1] ? fmaf(z[n][k], fz[k >> 1] * ks, lv) : -INFINITY;
-        tm[k >> 1] = fmaxf(tm[k >> 1], z[n][k]);
-      }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xFFFFFFFFu, tm[e], 1));
-      tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xFFFFFFFFu, tm[e], 2));
+      vis[n][e] = __shfl_sync(0xFFFFFFFFu, sees, (2 * c + e) * 4);
+      fz[n][e] = __shfl_sync(0xFFFFFFFFu, up, (2 * c + e) * 4);
     }
-    if (__any_sync(0xFFFFFFFFu, tm[0] > mx[0] + 8.f || tm[1] > mx[1] + 8.f)) {
+  }
+
+  float o[NT][D / 16][4], mx[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    mx[n][0] = mx[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
+  }
+
+  for (int t = t0; t < t1; t += 4) {
+    const int blk2 = block_of(t + 8);
+    if (t + 4 < t1) fetch(nxt, t + 4, blk1);
+    const int key0 = t * 16;
+    float z[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[n][k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      uint32_t ka[4];
+      codes_half4<INT8>(cur.k[0][w], ka[0], ka[2]);
+      codes_half4<INT8>(cur.k[1][w], ka[1], ka[3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_16816(z[n], ka, qb[n][w][0], qb[n][w][1]);
+    }
+    const float ks = cur.ks, lv = scale_log2(cur.vs), iv = exp2_fast(-lv);
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float tm[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float nm = fmaxf(mx[e], tm[e]);
-        const float f = mx[e] == -INFINITY ? 0.f : exp2_fast(mx[e] - nm);
-        mx[e] = nm;
-        l[e] *= f;
+        const float f = fz[n][e] * ks;
+        z[n][e] = key0 + g < vis[n][e] ? fmaf(z[n][e], f, lv) : -INFINITY;
+        z[n][2 + e] = key0 + g + 8 < vis[n][e] ? fmaf(z[n][2 + e], f, lv) : -INFINITY;
+        tm[e] = fmaxf(z[n][e], z[n][2 + e]);
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          o[j][2 * e] *= f;
-          o[j][2 * e + 1] *= f;
+        for (int x = 4; x < 32; x <<= 1) tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xFFFFFFFFu, tm[e], x));
+      }
+      if (__any_sync(0xFFFFFFFFu, tm[0] > mx[n][0] + 8.f || tm[1] > mx[n][1] + 8.f)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float nm = fmaxf(mx[n][e], tm[e]);
+          const float f = mx[n][e] == -INFINITY ? 0.f : exp2_fast(mx[n][e] - nm);
+          mx[n][e] = nm;
+          l[n][e] *= f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            o[n][j][e] *= f;
+            o[n][j][2 + e] *= f;
+          }
         }
       }
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mu = mx[n][e] == -INFINITY ? 0.f : mx[n][e];
+        p[e] = exp2_fast(z[n][e] - mu);
+        p[2 + e] = exp2_fast(z[n][2 + e] - mu);
+        l[n][e] = fmaf(p[e] + p[2 + e], iv, l[n][e]);
+      }
+      pb[n][0] = transpose8(pack_half2(p[0], p[1]));  // (key, rows) -> (row, keys)
+      pb[n][1] = transpose8(pack_half2(p[2], p[3]));
     }
-    uint32_t pa[4];
+    if (key0 + 16 > s.len) {  // behind the history: not defined, may be NaN
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float mu = mx[e] == -INFINITY ? 0.f : mx[e];
+      for (int j = 0; j < 4; ++j)
+        if (key0 + 2 * c + (j & 1) + (j >> 1) * 8 >= s.len)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float p0 = exp2_fast(z[n][2 * e] - mu), p1 = exp2_fast(z[n][2 * e + 1] - mu);
-        l[e] = fmaf(p0 + p1, iv, l[e]);
-        pa[2 * n + e] = pack_half2(p0, p1);
+          for (int u = 0; u < VW; ++u) cur.v[j][u] = 0;
+    }
+#pragma unroll
+    for (int u = 0; u < VW; ++u) {
+      uint32_t x[4], y[4];  // of four dims: keys 2c, 2c + 1, and 8 on
+      codes_half4<INT8>(__byte_perm(cur.v[0][u], cur.v[1][u], 0x5140), x[0], x[1]);
+      codes_half4<INT8>(__byte_perm(cur.v[0][u], cur.v[1][u], 0x7362), x[2], x[3]);
+      codes_half4<INT8>(__byte_perm(cur.v[2][u], cur.v[3][u], 0x5140), y[0], y[1]);
+      codes_half4<INT8>(__byte_perm(cur.v[2][u], cur.v[3][u], 0x7362), y[2], y[3]);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t va[4] = {x[2 * v], x[2 * v + 1], y[2 * v], y[2 * v + 1]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_16816(o[n][2 * u + v], va, pb[n][0], pb[n][1]);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t b0[4], b1[4];  // four dims: (key 2c, key 2c + 1), and 8 keys on
-      codes_half4<INT8>(__byte_perm(vw[0][u], vw[1][u], 0x5140), b0[0], b0[1]);
-      codes_half4<INT8>(__byte_perm(vw[0][u], vw[1][u], 0x7362), b0[2], b0[3]);
-      codes_half4<INT8>(__byte_perm(vw[2][u], vw[3][u], 0x5140), b1[0], b1[1]);
-      codes_half4<INT8>(__byte_perm(vw[2][u], vw[3][u], 0x7362), b1[2], b1[3]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mma_16816(o[4 * u + k], pa, b0[k], b1[k]);
-    }
+    cur = nxt;
+    blk1 = blk2;
   }
 
-  // join the warps: column j of accumulator tile jj is dim (2c + j) * D/8 + jj
+  // join the warps: accumulator tile j, element (e, row g or g + 8) is row 2c + e, dim g * D/8 + 2 j (+ 1)
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
-    l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
-    if (c == 0) {
-      sm_m[warp][g + 8 * e] = mx[e];
-      sm_l[warp][g + 8 * e] = l[e];
-    }
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-      sm_o[warp][g + 8 * e][2 * c * (D / 8) + j] = o[j][2 * e];
-      sm_o[warp][g + 8 * e][(2 * c + 1) * (D / 8) + j] = o[j][2 * e + 1];
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], x);
+      const int r = n * 8 + 2 * c + e;
+      if (g == 0) {
+        sm_m[warp][r] = mx[n][e];
+        sm_l[warp][r] = l[n][e];
+      }
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+        *reinterpret_cast<float2*>(&sm_o[warp][r][g * (D / 8) + 2 * j]) = make_float2(o[n][j][e], o[n][j][2 + e]);
     }
-  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * (D / 2); i += kFewThreads) {
-    const int r = i / (D / 2), d = 2 * (i % (D / 2));
-    const int ri = m * 16 + r;
+  for (int i = threadIdx.x; i < NR * (D / 4); i += kFewThreads) {
+    const int r = i / (D / 4), d = 4 * (i % (D / 4));
+    const int ri = m * NR + r;
     if (ri >= M) continue;
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < 4; ++w) top = fmaxf(top, sm_m[w][r]);
-    float sum = 0.f, x0 = 0.f, x1 = 0.f;
+    float sum = 0.f, x[4] = {};
     if (top != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float f = exp2_fast(sm_m[w][r] - top);
         sum = fmaf(f, sm_l[w][r], sum);
-        x0 = fmaf(f, sm_o[w][r][d], x0);
-        x1 = fmaf(f, sm_o[w][r][d + 1], x1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = fmaf(f, sm_o[w][r][d + k], x[k]);
       }
     }
-    if (a.splits > 1) {
-      const int64_t pi = ((int64_t)item * a.splits + split) * 16 + r;
-      *reinterpret_cast<float2*>(a.part + pi * D + d) = make_float2(x0, x1);
+    if (parts > 1) {
+      const int64_t pi = ((int64_t)item * a.splits + part) * NR + r;
+      store4(a.part + pi * D + d, x);
       if (d == 0) {
-        float* ml = a.part + (int64_t)a.B * a.heads * a.mt * a.splits * 16 * D + pi * 2;
+        float* ml = a.part + (int64_t)a.B * a.heads * a.mt * a.splits * NR * D + pi * 2;
         ml[0] = top;
         ml[1] = sum;
       }
     } else {
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       const int tr = ri / a.G, th = h * a.G + ri % a.G;
-      store2(out.at(b, tr, th) + d, x0 * inv, x1 * inv);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] *= inv;
+      store4(out.at(b, tr, th) + d, x);
       if (a.lse && d == 0)
         a.lse[((int64_t)b * a.R + tr) * a.Hq + th] =
             top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
@@ -252,37 +325,50 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
   }
 }
 
-// Joins the parts of the keys: one warp a (request, row, query head).
+// Joins the parts of the keys: one warp a (request, row, query head).  Items
+// of one part have their outputs already.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnArgs a, const Rows<T> out) {
+  constexpr int kLanes = D / 4;  // lanes that hold four dims
   const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (w >= (int64_t)a.B * a.R * a.Hq) return;
   const int qh = (int)(w % a.Hq);
   const int64_t br = w / a.Hq;
   const int r = (int)(br % a.R), b = (int)(br / a.R);
-  const int i = r * a.G + qh % a.G;
-  const int64_t item = ((int64_t)b * a.heads + qh / a.G) * a.mt + i / a.tile;
+  const int i = r * a.G + qh % a.G, m = i / a.tile;
+  const Seen s = seen_of(a, b, false);
+  const int last = min(min((m + 1) * a.tile, a.R * a.G) - 1, s.rows * a.G - 1);
+  const int parts = parts_of(a, last < m * a.tile ? 0 : visible(a, s, last / a.G));
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (parts <= 1) return;
+  const int64_t item = ((int64_t)b * a.heads + qh / a.G) * a.mt + m;
   const float* ml = a.part + (int64_t)a.B * a.heads * a.mt * a.splits * a.tile * D;
   const int64_t p0 = item * a.splits * a.tile + i % a.tile;
   float top = -INFINITY;
-  for (int sp = lane; sp < a.splits; sp += 32) top = fmaxf(top, ml[(p0 + (int64_t)sp * a.tile) * 2]);
+  for (int sp = lane; sp < parts; sp += 32) top = fmaxf(top, ml[(p0 + (int64_t)sp * a.tile) * 2]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  float sum = 0.f, x[D / 32] = {};
-  if (top != -INFINITY) {
-    for (int sp = 0; sp < a.splits; ++sp) {
+  float sum = 0.f, x[4] = {};
+  if (top != -INFINITY && lane < kLanes) {
+#pragma unroll 4
+    for (int sp = 0; sp < parts; ++sp) {
       const int64_t pi = p0 + (int64_t)sp * a.tile;
-      const float f = exp2_fast(ml[pi * 2] - top);
-      sum = fmaf(f, ml[pi * 2 + 1], sum);
+      const float2 e = *reinterpret_cast<const float2*>(ml + pi * 2);
+      float y[4];
+      load4(a.part + pi * D + 4 * lane, y);
+      const float f = exp2_fast(e.x - top);
+      sum = fmaf(f, e.y, sum);
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) x[k] = fmaf(f, a.part[pi * D + lane + 32 * k], x[k]);
+      for (int k = 0; k < 4; ++k) x[k] = fmaf(f, y[k], x[k]);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  T* p = out.at(b, r, qh);
+  if (lane < kLanes) {
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) p[lane + 32 * k] = (T)(x[k] * inv);
+    for (int k = 0; k < 4; ++k) x[k] *= inv;
+    store4(out.at(b, r, qh) + 4 * lane, x);
+  }
   if (a.lse && lane == 0)
     a.lse[w] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
 }
@@ -291,27 +377,30 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
 
 struct AttnPlan {
   bool tc;
-  int tile, mt, splits;
+  int tile, mt, splits, chunk;
   int64_t items;
   size_t bytes;
 };
 
 constexpr int kFewRows = 32;  // query rows a key head up to which k_attn_few is the faster
 
-// Few rows: items for every SM several times over, 256 keys a part at least.
-// Many rows: parts only where items leave SMs idle, 512 keys each at least.
+// Keys go to CTAs in parts of `chunk`, as many as a history has; the longest
+// may have `splits`.  Few rows: about 1,200 CTAs (three resident on each of 152
+// SMs, two to three rounds) where that leaves a part 64 keys, one tile a warp;
+// many rows: parts only where items leave SMs idle, 512 keys each at least.
 AttnPlan attn_plan(const zg_kv_cache* c, int max_blocks, int B, int R, int Hq) {
   AttnPlan p;
   const int64_t M = (int64_t)R * (Hq / c->heads);
   p.tc = M > kFewRows;
-  p.tile = p.tc ? attn_tc_tile(M) : 16;
+  p.tile = p.tc ? attn_tc_tile(M) : M > 8 ? 16 : 8;
   p.mt = (int)((M + p.tile - 1) / p.tile);
   p.items = (int64_t)B * c->heads * p.mt;
   const int64_t keys = (int64_t)max_blocks * c->block_tokens;
-  const int64_t most = std::max<int64_t>(1, keys / (p.tc ? 512 : 256));
-  int64_t want = 1;
-  if (p.items) want = p.tc ? sm_count() / p.items : ((int64_t)sm_count() * 8 + p.items - 1) / p.items;
-  p.splits = (int)std::max<int64_t>(1, std::min(want, most));
+  const int64_t room = p.tc ? sm_count() : (int64_t)sm_count() * 8, least = p.tc ? 512 : 64;
+  const int64_t parts = std::max<int64_t>(1, p.items ? room / p.items : 1);
+  const int64_t chunk = std::max(least, ((keys + parts - 1) / parts + least - 1) / least * least);
+  p.chunk = (int)std::min<int64_t>(chunk, 1 << 30);
+  p.splits = (int)((keys + p.chunk - 1) / p.chunk);
   p.bytes = p.splits > 1 ? (size_t)p.items * p.splits * p.tile * (c->dim + 2) * 4 : 0;
   return p;
 }
@@ -387,18 +476,30 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   a.tile = p.tile;
   a.mt = p.mt;
   a.splits = p.splits;
+  a.chunk = p.chunk;
   a.causal = causal != 0;
   a.scale = scale * 1.4426950408889634f;
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
   auto launch = [&](auto ev, auto dv, auto iv) {
     using E = typename decltype(ev)::type;
     constexpr int D = decltype(dv)::value;
-    if (!p.tc)
-      k_attn_few<E, D, decltype(iv)::value>
-          <<<(unsigned)(p.items * p.splits), kFewThreads, 0, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
+    if (!p.tc) {
+      const unsigned ctas = (unsigned)(p.items * p.splits);
+      if (p.tile == 8) k_attn_few<E, D, decltype(iv)::value, 1><<<ctas, kFewThreads, 0, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
+      else k_attn_few<E, D, decltype(iv)::value, 2><<<ctas, kFewThreads, 0, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
+    }
     if (p.splits > 1) {
-      const int64_t warps = (int64_t)B * R * Hq;
-      k_attn_join<E, D><<<(unsigned)((warps + 7) / 8), 256, 0, sm>>>(a, rows_of<E>(out));
+      // may start while the parts are still made; it waits for them before it reads
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(((int64_t)B * R * Hq + 7) / 8));
+      cfg.blockDim = dim3(256);
+      cfg.stream = sm;
+      cudaLaunchAttribute attr = {};
+      attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr.val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      cudaLaunchKernelEx(&cfg, k_attn_join<E, D>, a, rows_of<E>(out));
     }
   };
   if (p.tc) {

@@ -283,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // later rows see no less: the item sees what its last row does, or its request's last
   const int last = min((m * a.tile + mine - 1) / a.G, s.rows - 1);
   const int vmax = last < m * a.tile / a.G ? 0 : visible(a, s, last);
-  const int steps_all = (vmax + kNK - 1) / kNK;
-  const int per = (steps_all + a.splits - 1) / a.splits;
-  const int t0 = min(steps_all, split * per);
-  const int steps = __shfl_sync(0xFFFFFFFFu, min(steps_all, t0 + per) - t0, 0);  // uniform, for the compiler too
+  const int parts = parts_of(a, vmax);
+  if (split >= parts) return;  // the join does not look for it
+  const int t0 = split * (a.chunk / kNK), t1 = min((vmax + kNK - 1) / kNK, t0 + a.chunk / kNK);
+  const int steps = __shfl_sync(0xFFFFFFFFu, t1 - t0, 0);  // uniform, for the compiler too
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRaw; ++i) {
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j) o[j] = 0;
           }
           const float* x = reinterpret_cast<const float*>(o);
-          if (a.splits > 1) {
+          if (parts > 1) {
             if (live)
 #pragma unroll
               for (int j = 0; j < 32; j += 4)
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              pack2<T>(x[j + 4] * inv, x[j + 5] * inv), pack2<T>(x[j + 6] * inv, x[j + 7] * inv));
           }
         }
-        if (a.splits == 1) {  // whole rows out, as the queries came in
+        if (parts == 1) {  // whole rows out, as the queries came in
           const int64_t out_row = b * out.sb + row * out.st + qh * out.sh;
           const uint32_t mine_of = __ballot_sync(0xFFFFFFFFu, live);
           __syncwarp();
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tile + (e / 64) * (128 * 128) + rr * 128 + ((((e % 64) / 8) ^ (rr & 7)) << 4) + (e & 4) * 2);
           }
         }
-        if (live && a.splits > 1) {
+        if (live && parts > 1) {
           float* ml = a.part + (int64_t)a.B * a.heads * a.mt * a.splits * a.tile * D + pi * 2;
           ml[0] = l > 0.f ? mx : -INFINITY;
           ml[1] = l;

@@ -15,6 +15,7 @@ struct AttnArgs {
   int32_t n_blocks, heads, bt, max_blocks;
   int32_t B, R, Hq, G, splits, causal;
   int32_t tile, mt;  // query rows an item (power of two), such items a (request, key head)
+  int32_t chunk;     // keys of a part, a multiple of 64
   float scale;  // scale * log2(e)
 };
 
@@ -59,6 +60,9 @@ __device__ __forceinline__ float log2_fast(float x) {
 // log2 of a value block's scale; a scale of 0 (all its codes are 0) stands at
 // the floor, so that its keys still count in the row's sum.
 __device__ __forceinline__ float scale_log2(float vs) { return vs > 0x1p-100f ? log2_fast(vs) : -100.f; }
+
+// Parts that the keys of an item are in.
+__device__ __forceinline__ int parts_of(const AttnArgs& a, int keys) { return max(1, (keys + a.chunk - 1) / a.chunk); }
 
 // The power of two that brings a row's largest |q| to [1, 2), as an exponent.
 __device__ __forceinline__ int row_exponent(float top) {
