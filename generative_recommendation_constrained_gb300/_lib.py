@@ -130,12 +130,12 @@ def _load():
         "zg_check_device_status": [vp],
         "zg_plan_save": [vp, C.c_char_p],
         "zg_plan_load": [C.c_char_p, P(vp)],
-        "zg_qk_norm_rope": [P(zg_norm_rope)] + [P(zg_rows)] * 4 + [vp] + [i32] * 5 + [vp],
-        "zg_kv_append": [P(zg_kv_cache), P(zg_norm_rope)] + [P(zg_rows)] * 4 + [i32, vp, i32, vp, vp, i32, i32, vp],
-        "zg_kv_read": [P(zg_kv_cache), vp, i32, vp, vp, i32, i32, P(zg_rows), P(zg_rows), vp],
-        "zg_kv_attention_workspace_size": [P(zg_kv_cache), i32, i32, i32, i32, P(sz)],
-        "zg_kv_attention": [P(zg_kv_cache), vp, i32, vp, vp, P(zg_rows), P(zg_rows), vp, i32, i32, i32, C.c_float,
-                            i32, vp, sz, vp],
+        # structs by address (c_void_p): a ctypes struct (through _ref) or its bytes
+        "zg_qk_norm_rope": [vp] * 6 + [i32] * 5 + [vp],
+        "zg_kv_append": [vp] * 6 + [i32, vp, i32, vp, vp, i32, i32, vp],
+        "zg_kv_read": [vp, vp, i32, vp, vp, i32, i32, vp, vp, vp],
+        "zg_kv_attention_workspace_size": [vp, i32, i32, i32, i32, P(sz)],
+        "zg_kv_attention": [vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, C.c_float, i32, vp, sz, vp],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -430,31 +430,46 @@ def make_norm_rope(norm: bool, eps: float, q_gain, k_gain, rot_dim: int, interle
     return s
 
 
+def _ref(x):
+    """A struct argument: NULL, a ctypes struct, or the struct's bytes."""
+    return x if x is None or isinstance(x, bytes) else C.byref(x)
+
+
 def zg_qk_norm_rope(nr: zg_norm_rope, q, k, q_out, k_out, positions, B: int, T: int, Hq: int, Hk: int, dim: int,
                     stream: int = 0):
-    """q, k, q_out, k_out: zg_rows or None."""
-    _check(lib.zg_qk_norm_rope(nr, q, k, q_out, k_out, _ptr(positions), B, T, Hq, Hk, dim, stream or None))
+    """q, k, q_out, k_out: zg_rows (or their bytes) or None."""
+    st = lib.zg_qk_norm_rope(_ref(nr), _ref(q), _ref(k), _ref(q_out), _ref(k_out), _ptr(positions), B, T, Hq, Hk, dim,
+                             stream)
+    if st:
+        _check(st)
 
 
 def zg_kv_append(cache: zg_kv_cache, nr, k, v, q, q_out, Hq: int, table, max_blocks: int, start, n_new, B: int,
                  T: int, stream: int = 0):
-    """k, v, q, q_out: zg_rows (q and q_out may be None)."""
-    _check(lib.zg_kv_append(cache, nr, k, v, q, q_out, Hq, _ptr(table), max_blocks, _ptr(start), _ptr(n_new), B, T,
-                            stream or None))
+    """k, v, q, q_out: zg_rows or their bytes (q and q_out may be None)."""
+    st = lib.zg_kv_append(_ref(cache), _ref(nr), _ref(k), _ref(v), _ref(q), _ref(q_out), Hq, _ptr(table), max_blocks,
+                          _ptr(start), _ptr(n_new), B, T, stream)
+    if st:
+        _check(st)
 
 
 def zg_kv_read(cache: zg_kv_cache, table, max_blocks: int, start, n, B: int, T: int, k_out, v_out, stream: int = 0):
-    _check(lib.zg_kv_read(cache, _ptr(table), max_blocks, _ptr(start), _ptr(n), B, T, k_out, v_out, stream or None))
+    st = lib.zg_kv_read(_ref(cache), _ptr(table), max_blocks, _ptr(start), _ptr(n), B, T, _ref(k_out), _ref(v_out),
+                        stream)
+    if st:
+        _check(st)
 
 
 def zg_kv_attention_workspace_size(cache: zg_kv_cache, max_blocks: int, B: int, R: int, Hq: int) -> int:
     n = C.c_size_t(0)
-    _check(lib.zg_kv_attention_workspace_size(cache, max_blocks, B, R, Hq, C.byref(n)))
+    _check(lib.zg_kv_attention_workspace_size(_ref(cache), max_blocks, B, R, Hq, C.byref(n)))
     return n.value
 
 
 def zg_kv_attention(cache: zg_kv_cache, table, max_blocks: int, length, n_rows, q, out, lse, B: int, R: int,
                     Hq: int, scale: float, causal: bool, workspace, ws_bytes: int, stream: int = 0):
-    """q, out: zg_rows."""
-    _check(lib.zg_kv_attention(cache, _ptr(table), max_blocks, _ptr(length), _ptr(n_rows), q, out, _ptr(lse), B, R,
-                               Hq, scale, int(causal), _ptr(workspace), ws_bytes, stream or None))
+    """q, out: zg_rows or their bytes."""
+    st = lib.zg_kv_attention(_ref(cache), _ptr(table), max_blocks, _ptr(length), _ptr(n_rows), _ref(q), _ref(out),
+                             _ptr(lse), B, R, Hq, scale, causal, _ptr(workspace), ws_bytes, stream)
+    if st:
+        _check(st)

@@ -94,10 +94,30 @@ struct Tile16 {
   }
 };
 
-// Few query rows: one CTA an item (request, key head, 8 NT rows) and part of
-// the keys; a row is (token, query head of the group).  Each warp walks its own
-// 16-key tiles straight from global memory into matrix fragments, the next
-// tile's loads in flight under this one's products.  Keys and dims are the
+// Keys go to the CTAs of k_attn_few by the unit of 64 (a tile a warp), all
+// items (request, key head, 8 NT rows) in a row and the same share for each
+// CTA, however the histories' lengths differ: an item may lie in several CTAs
+// (the join adds their parts up), and a CTA may hold the end of one item,
+// whole ones and the beginning of another.
+constexpr int kUnit = 64;
+__device__ __forceinline__ int item_keys(const AttnArgs& a, const Seen& s, int m, int nr) {
+  // later rows see no less: the item sees what its last row does, or its request's last
+  const int last = min(min(m * nr + nr, a.R * a.G) - 1, s.rows * a.G - 1);
+  return last < m * nr ? 0 : visible(a, s, last / a.G);
+}
+// A row of items that see nothing takes one unit too: somebody has to write its outputs.
+__device__ __forceinline__ int item_units(const AttnArgs& a, const Seen& s, int m, int nr) {
+  return max(1, (item_keys(a, s, m, nr) + kUnit - 1) / kUnit);
+}
+__device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, int nr) {
+  int n = 0;
+  for (int m = 0; m < a.mt; ++m) n += item_units(a, s, m, nr);
+  return n * a.heads;
+}
+
+// Few query rows: a row is (token, query head of the group).  Each warp walks
+// its own 16-key tiles straight from global memory into matrix fragments, the
+// next tile's loads in flight under this one's products.  Keys and dims are the
 // long side of the products (S^T = K Q^T, O^T = V^T P^T), so that eight rows
 // fill an instruction that sixteen keys or dims by eight rows make.
 template <typename T, int D, bool INT8, int NT>
@@ -107,220 +127,278 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
   constexpr int KW = Tl::KW, VW = Tl::VW, NR = 8 * NT;
   __shared__ float sm_m[4][NR], sm_l[4][NR];
   __shared__ float sm_o[4][NR][D + 2];
+  __shared__ int sm_sum[4], sm_b, sm_first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  int it = blockIdx.x;
-  const int part = it % a.splits;
-  it /= a.splits;
-  const int item = it;
-  const int m = it % a.mt;
-  it /= a.mt;
-  const int h = it % a.heads, b = it / a.heads;
-  const Seen s = seen_of(a, b, threadIdx.x == 0);
   const int M = a.R * a.G;
-  // later rows see no less: the item sees what its last row does, or its request's last
-  const int last = min(min(m * NR + NR, M) - 1, s.rows * a.G - 1);
-  const int vmax = last < m * NR ? 0 : visible(a, s, last / a.G);
-  const int parts = parts_of(a, vmax);
-  if (part >= parts) return;  // the join does not look for it
-  const int t0 = part * (a.chunk / 16) + warp, t1 = min((vmax + 15) / 16, (part + 1) * (a.chunk / 16));
 
-  auto block_of = [&](int t) -> int {
-    if (t >= t1) return -1;
-    const int blk = a.table[(int64_t)b * a.max_blocks + t * 16 / a.bt];
-    if (blk >= 0 && blk < a.n_blocks) return blk;
-    if (lane == 0) atomicOr(a.status, kStatusCache);
-    return -1;
-  };
-  auto fetch = [&](Tl& x, int t, int blk) {
-    if (blk < 0) return x.zero();
-    const int64_t bh = (int64_t)blk * a.heads + h, at = (bh * a.bt + t * 16 % a.bt) * D;
-    x.load(a.kc + at, a.vc + at, g, c);
-    x.ks = a.ks[bh];
-    x.vs = a.vs[bh];
-  };
-  Tl cur, nxt;
-  int blk = block_of(t0), blk1 = block_of(t0 + 4);
-  fetch(cur, t0, blk);
-
-  // the rows: lane (g, c) the dims of its words of row g; then the sight and the scale of rows 2c, 2c + 1
-  uint32_t qb[NT][KW][2];
-  int vis[NT][2];
-  float fz[NT][2];
+  // every request's units, their sum, and the request in which this CTA's share begins
+  int total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    const int begin = pass ? (int)((int64_t)blockIdx.x * ((total + gridDim.x - 1) / gridDim.x)) : 0;
+    int before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kFewThreads) {
+      const int b = b0 + threadIdx.x;
+      int n = 0;
+      if (b < a.B) n = request_units(a, seen_of(a, b, pass == 0 && blockIdx.x == 0), NR);
+      int x = n;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int i = m * NR + n * 8 + g;
-    const int row = i / a.G;
-    const int sees = i < M ? visible(a, s, row) : 0;
-    float x[KW][4], top = 0.f;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[w][k] = 0.f;
-      if (sees > 0) load4(q.at(b, row, h * a.G + i % a.G) + Tl::dim_of(w, c), x[w]);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) sm_sum[warp] = x;
+      __syncthreads();
+      int all = 0;
+      for (int w = 0; w < 4; ++w) {
+        if (w < warp) x += sm_sum[w];
+        all += sm_sum[w];
+      }
+      const int first = before + x - n;
+      if (pass) {
+        if (b < a.B && first <= begin && begin < first + n) {
+          sm_b = b;
+          sm_first = first;
+        }
+        if (blockIdx.x == 0 && b < a.B && a.prefix) {
+          a.prefix[b] = first;
+          if (b == a.B - 1) a.prefix[a.B] = first + n;
+        }
+      }
+      before += all;
+      __syncthreads();
     }
-#pragma unroll
-    for (int w = 0; w < KW; ++w)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(x[w][k]));
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const int ex = row_exponent(top);
-    const float dn = __uint_as_float((uint32_t)(127 - ex) << 23), up = a.scale * __uint_as_float((uint32_t)(127 + ex) << 23);
-#pragma unroll
-    for (int w = 0; w < KW; ++w) {
-      qb[n][w][0] = pack_half2(x[w][0] * dn, x[w][1] * dn);
-      qb[n][w][1] = pack_half2(x[w][2] * dn, x[w][3] * dn);
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      vis[n][e] = __shfl_sync(0xFFFFFFFFu, sees, (2 * c + e) * 4);
-      fz[n][e] = __shfl_sync(0xFFFFFFFFu, up, (2 * c + e) * 4);
-    }
+    total = before;
+  }
+  const int share = (total + gridDim.x - 1) / gridDim.x;
+  int u = blockIdx.x * share;
+  const int u_end = min(total, u + share);
+  if (u >= u_end) return;
+  int b = sm_b, first = sm_first;  // `first`: units before request b, then before the item
+  Seen s = seen_of(a, b, false);
+  // the item: (head, rows), units one row of items after the other
+  int h = 0, m = 0, units = item_units(a, s, 0, NR);
+  while (first + units <= u) {
+    first += units;
+    if (++m == a.mt) m = 0, ++h;
+    units = item_units(a, s, m, NR);
   }
 
-  float o[NT][D / 16][4], mx[NT][2], l[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    mx[n][0] = mx[n][1] = -INFINITY;
-    l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
-  }
+  while (u < u_end) {
+    const int vmax = item_keys(a, s, m, NR);
+    const int v_end = min(u_end, first + units);  // units [u, v_end) of this item are ours
+    const int t0 = (u - first) * (kUnit / 16) + warp, t1 = min((vmax + 15) / 16, (v_end - first) * (kUnit / 16));
+    const bool whole = u == first && v_end == first + units;
+    const int slot = 2 * blockIdx.x + (u > (int)blockIdx.x * share ? 1 : 0);
 
-  for (int t = t0; t < t1; t += 4) {
-    const int blk2 = block_of(t + 8);
-    if (t + 4 < t1) fetch(nxt, t + 4, blk1);
-    const int key0 = t * 16;
-    float z[NT][4];
+    auto block_of = [&](int t) -> int {
+      if (t >= t1) return -1;
+      const int blk = a.table[(int64_t)b * a.max_blocks + t * 16 / a.bt];
+      if (blk >= 0 && blk < a.n_blocks) return blk;
+      if (lane == 0) atomicOr(a.status, kStatusCache);
+      return -1;
+    };
+    auto fetch = [&](Tl& x, int t, int blk) {
+      if (blk < 0) return x.zero();
+      const int64_t bh = (int64_t)blk * a.heads + h, at = (bh * a.bt + t * 16 % a.bt) * D;
+      x.load(a.kc + at, a.vc + at, g, c);
+      x.ks = a.ks[bh];
+      x.vs = a.vs[bh];
+    };
+    Tl cur, nxt;
+    int blk = block_of(t0), blk1 = block_of(t0 + 4);
+    fetch(cur, t0, blk);
+
+    // the rows: lane (g, c) the dims of its words of row g; then the sight and the scale of rows 2c, 2c + 1
+    uint32_t qb[NT][KW][2];
+    int vis[NT][2];
+    float fz[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int i = m * NR + n * 8 + g;
+      const int row = i / a.G;
+      const int sees = i < M ? visible(a, s, row) : 0;
+      float x[KW][4], top = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[w][k] = 0.f;
+        if (sees > 0) load4(q.at(b, row, h * a.G + i % a.G) + Tl::dim_of(w, c), x[w]);
+      }
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(x[w][k]));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const int ex = row_exponent(top);
+      const float dn = __uint_as_float((uint32_t)(127 - ex) << 23), up = a.scale * __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        qb[n][w][0] = pack_half2(x[w][0] * dn, x[w][1] * dn);
+        qb[n][w][1] = pack_half2(x[w][2] * dn, x[w][3] * dn);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        vis[n][e] = __shfl_sync(0xFFFFFFFFu, sees, (2 * c + e) * 4);
+        fz[n][e] = __shfl_sync(0xFFFFFFFFu, up, (2 * c + e) * 4);
+      }
+    }
+
+    float o[NT][D / 16][4], mx[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      mx[n][0] = mx[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
+    }
+
+    for (int t = t0; t < t1; t += 4) {
+      const int blk2 = block_of(t + 8);
+      if (t + 4 < t1) fetch(nxt, t + 4, blk1);
+      const int key0 = t * 16;
+      float z[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[n][k] = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        uint32_t ka[4];
+        codes_half4<INT8>(cur.k[0][w], ka[0], ka[2]);
+        codes_half4<INT8>(cur.k[1][w], ka[1], ka[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_16816(z[n], ka, qb[n][w][0], qb[n][w][1]);
+      }
+      const float ks = cur.ks, lv = scale_log2(cur.vs), iv = exp2_fast(-lv);
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float tm[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = fz[n][e] * ks;
+          z[n][e] = key0 + g < vis[n][e] ? fmaf(z[n][e], f, lv) : -INFINITY;
+          z[n][2 + e] = key0 + g + 8 < vis[n][e] ? fmaf(z[n][2 + e], f, lv) : -INFINITY;
+          tm[e] = fmaxf(z[n][e], z[n][2 + e]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xFFFFFFFFu, tm[e], x));
+        }
+        if (__any_sync(0xFFFFFFFFu, tm[0] > mx[n][0] + 8.f || tm[1] > mx[n][1] + 8.f)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float nm = fmaxf(mx[n][e], tm[e]);
+            const float f = mx[n][e] == -INFINITY ? 0.f : exp2_fast(mx[n][e] - nm);
+            mx[n][e] = nm;
+            l[n][e] *= f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              o[n][j][e] *= f;
+              o[n][j][2 + e] *= f;
+            }
+          }
+        }
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mu = mx[n][e] == -INFINITY ? 0.f : mx[n][e];
+          p[e] = exp2_fast(z[n][e] - mu);
+          p[2 + e] = exp2_fast(z[n][2 + e] - mu);
+          l[n][e] = fmaf(p[e] + p[2 + e], iv, l[n][e]);
+        }
+        pb[n][0] = transpose8(pack_half2(p[0], p[1]));  // (key, rows) -> (row, keys)
+        pb[n][1] = transpose8(pack_half2(p[2], p[3]));
+      }
+      if (key0 + 16 > s.len) {  // behind the history: not defined, may be NaN
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (key0 + 2 * c + (j & 1) + (j >> 1) * 8 >= s.len)
+#pragma unroll
+            for (int u = 0; u < VW; ++u) cur.v[j][u] = 0;
+      }
+#pragma unroll
+      for (int u = 0; u < VW; ++u) {
+        uint32_t x[4], y[4];  // of four dims: keys 2c, 2c + 1, and 8 on
+        codes_half4<INT8>(__byte_perm(cur.v[0][u], cur.v[1][u], 0x5140), x[0], x[1]);
+        codes_half4<INT8>(__byte_perm(cur.v[0][u], cur.v[1][u], 0x7362), x[2], x[3]);
+        codes_half4<INT8>(__byte_perm(cur.v[2][u], cur.v[3][u], 0x5140), y[0], y[1]);
+        codes_half4<INT8>(__byte_perm(cur.v[2][u], cur.v[3][u], 0x7362), y[2], y[3]);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t va[4] = {x[2 * v], x[2 * v + 1], y[2 * v], y[2 * v + 1]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_16816(o[n][2 * u + v], va, pb[n][0], pb[n][1]);
+        }
+      }
+      cur = nxt;
+      blk1 = blk2;
+    }
+
+    // join the warps: accumulator tile j, element (e, row g or g + 8) is row 2c + e, dim g * D/8 + 2 j (+ 1)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) z[n][k] = 0.f;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) {
-      uint32_t ka[4];
-      codes_half4<INT8>(cur.k[0][w], ka[0], ka[2]);
-      codes_half4<INT8>(cur.k[1][w], ka[1], ka[3]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mma_16816(z[n], ka, qb[n][w][0], qb[n][w][1]);
-    }
-    const float ks = cur.ks, lv = scale_log2(cur.vs), iv = exp2_fast(-lv);
-    uint32_t pb[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float tm[2];
-#pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float f = fz[n][e] * ks;
-        z[n][e] = key0 + g < vis[n][e] ? fmaf(z[n][e], f, lv) : -INFINITY;
-        z[n][2 + e] = key0 + g + 8 < vis[n][e] ? fmaf(z[n][2 + e], f, lv) : -INFINITY;
-        tm[e] = fmaxf(z[n][e], z[n][2 + e]);
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xFFFFFFFFu, tm[e], x));
+        for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], x);
+        const int r = n * 8 + 2 * c + e;
+        if (g == 0) {
+          sm_m[warp][r] = mx[n][e];
+          sm_l[warp][r] = l[n][e];
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+          *reinterpret_cast<float2*>(&sm_o[warp][r][g * (D / 8) + 2 * j]) = make_float2(o[n][j][e], o[n][j][2 + e]);
       }
-      if (__any_sync(0xFFFFFFFFu, tm[0] > mx[n][0] + 8.f || tm[1] > mx[n][1] + 8.f)) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < NR * (D / 4); i += kFewThreads) {
+      const int r = i / (D / 4), d = 4 * (i % (D / 4));
+      const int ri = m * NR + r;
+      if (ri >= M) continue;
+      float top = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float nm = fmaxf(mx[n][e], tm[e]);
-          const float f = mx[n][e] == -INFINITY ? 0.f : exp2_fast(mx[n][e] - nm);
-          mx[n][e] = nm;
-          l[n][e] *= f;
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, sm_m[w][r]);
+      float sum = 0.f, x[4] = {};
+      if (top != -INFINITY) {
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            o[n][j][e] *= f;
-            o[n][j][2 + e] *= f;
-          }
+        for (int w = 0; w < 4; ++w) {
+          const float f = exp2_fast(sm_m[w][r] - top);
+          sum = fmaf(f, sm_l[w][r], sum);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = fmaf(f, sm_o[w][r][d + k], x[k]);
         }
       }
-      float p[4];
+      if (!whole) {
+        const int64_t pi = (int64_t)slot * NR + r;
+        store4(a.part + pi * D + d, x);
+        if (d == 0) {
+          float* ml = a.part + a.slots * NR * D + pi * 2;
+          ml[0] = top;
+          ml[1] = sum;
+        }
+      } else {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int tr = ri / a.G, th = h * a.G + ri % a.G;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mu = mx[n][e] == -INFINITY ? 0.f : mx[n][e];
-        p[e] = exp2_fast(z[n][e] - mu);
-        p[2 + e] = exp2_fast(z[n][2 + e] - mu);
-        l[n][e] = fmaf(p[e] + p[2 + e], iv, l[n][e]);
-      }
-      pb[n][0] = transpose8(pack_half2(p[0], p[1]));  // (key, rows) -> (row, keys)
-      pb[n][1] = transpose8(pack_half2(p[2], p[3]));
-    }
-    if (key0 + 16 > s.len) {  // behind the history: not defined, may be NaN
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (key0 + 2 * c + (j & 1) + (j >> 1) * 8 >= s.len)
-#pragma unroll
-          for (int u = 0; u < VW; ++u) cur.v[j][u] = 0;
-    }
-#pragma unroll
-    for (int u = 0; u < VW; ++u) {
-      uint32_t x[4], y[4];  // of four dims: keys 2c, 2c + 1, and 8 on
-      codes_half4<INT8>(__byte_perm(cur.v[0][u], cur.v[1][u], 0x5140), x[0], x[1]);
-      codes_half4<INT8>(__byte_perm(cur.v[0][u], cur.v[1][u], 0x7362), x[2], x[3]);
-      codes_half4<INT8>(__byte_perm(cur.v[2][u], cur.v[3][u], 0x5140), y[0], y[1]);
-      codes_half4<INT8>(__byte_perm(cur.v[2][u], cur.v[3][u], 0x7362), y[2], y[3]);
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint32_t va[4] = {x[2 * v], x[2 * v + 1], y[2 * v], y[2 * v + 1]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma_16816(o[n][2 * u + v], va, pb[n][0], pb[n][1]);
+        for (int k = 0; k < 4; ++k) x[k] *= inv;
+        store4(out.at(b, tr, th) + d, x);
+        if (a.lse && d == 0)
+          a.lse[((int64_t)b * a.R + tr) * a.Hq + th] =
+              top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
       }
     }
-    cur = nxt;
-    blk1 = blk2;
-  }
-
-  // join the warps: accumulator tile j, element (e, row g or g + 8) is row 2c + e, dim g * D/8 + 2 j (+ 1)
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], x);
-      const int r = n * 8 + 2 * c + e;
-      if (g == 0) {
-        sm_m[warp][r] = mx[n][e];
-        sm_l[warp][r] = l[n][e];
+    __syncthreads();  // the joined warps' buffers are free again
+    u = v_end;
+    if (u < u_end) {
+      first += units;
+      if (++m == a.mt) m = 0, ++h;
+      if (h == a.heads) {
+        h = 0;
+        s = seen_of(a, ++b, false);
       }
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-        *reinterpret_cast<float2*>(&sm_o[warp][r][g * (D / 8) + 2 * j]) = make_float2(o[n][j][e], o[n][j][2 + e]);
-    }
-  __syncthreads();
-  for (int i = threadIdx.x; i < NR * (D / 4); i += kFewThreads) {
-    const int r = i / (D / 4), d = 4 * (i % (D / 4));
-    const int ri = m * NR + r;
-    if (ri >= M) continue;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, sm_m[w][r]);
-    float sum = 0.f, x[4] = {};
-    if (top != -INFINITY) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = exp2_fast(sm_m[w][r] - top);
-        sum = fmaf(f, sm_l[w][r], sum);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = fmaf(f, sm_o[w][r][d + k], x[k]);
-      }
-    }
-    if (parts > 1) {
-      const int64_t pi = ((int64_t)item * a.splits + part) * NR + r;
-      store4(a.part + pi * D + d, x);
-      if (d == 0) {
-        float* ml = a.part + (int64_t)a.B * a.heads * a.mt * a.splits * NR * D + pi * 2;
-        ml[0] = top;
-        ml[1] = sum;
-      }
-    } else {
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const int tr = ri / a.G, th = h * a.G + ri % a.G;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] *= inv;
-      store4(out.at(b, tr, th) + d, x);
-      if (a.lse && d == 0)
-        a.lse[((int64_t)b * a.R + tr) * a.Hq + th] =
-            top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+      units = item_units(a, s, m, NR);
     }
   }
 }
@@ -338,22 +416,38 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
   const int r = (int)(br % a.R), b = (int)(br / a.R);
   const int i = r * a.G + qh % a.G, m = i / a.tile;
   const Seen s = seen_of(a, b, false);
-  const int last = min(min((m + 1) * a.tile, a.R * a.G) - 1, s.rows * a.G - 1);
-  const int parts = parts_of(a, last < m * a.tile ? 0 : visible(a, s, last / a.G));
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int parts, cta = 0, later = 0;  // few rows: the first CTA that has some of the item, and whether it has other items first
+  int64_t slot0 = 0, step = 1;
+  if (a.prefix) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int h = qh / a.G, share = (a.prefix[a.B] + a.ctas - 1) / a.ctas;
+    int i0 = a.prefix[b] + request_units(a, s, a.tile) / a.heads * h, units = 0;
+    for (int j = 0; j <= m; ++j) {
+      i0 += units;
+      units = item_units(a, s, j, a.tile);
+    }
+    cta = i0 / share;
+    later = i0 > cta * share;
+    parts = (i0 + units - 1) / share - cta + 1;
+    slot0 = 2 * cta, step = 2;
+  } else {
+    const int last = min(min((m + 1) * a.tile, a.R * a.G) - 1, s.rows * a.G - 1);
+    parts = parts_of(a, last < m * a.tile ? 0 : visible(a, s, last / a.G));
+    slot0 = (((int64_t)b * a.heads + qh / a.G) * a.mt + m) * a.splits;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   if (parts <= 1) return;
-  const int64_t item = ((int64_t)b * a.heads + qh / a.G) * a.mt + m;
-  const float* ml = a.part + (int64_t)a.B * a.heads * a.mt * a.splits * a.tile * D;
-  const int64_t p0 = item * a.splits * a.tile + i % a.tile;
+  const float* ml = a.part + a.slots * a.tile * D;
+  auto row_of = [&](int sp) -> int64_t { return (slot0 + sp * step + (sp == 0 ? later : 0)) * a.tile + i % a.tile; };
   float top = -INFINITY;
-  for (int sp = lane; sp < parts; sp += 32) top = fmaxf(top, ml[(p0 + (int64_t)sp * a.tile) * 2]);
+  for (int sp = lane; sp < parts; sp += 32) top = fmaxf(top, ml[row_of(sp) * 2]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   float sum = 0.f, x[4] = {};
   if (top != -INFINITY && lane < kLanes) {
 #pragma unroll 4
     for (int sp = 0; sp < parts; ++sp) {
-      const int64_t pi = p0 + (int64_t)sp * a.tile;
+      const int64_t pi = row_of(sp);
       const float2 e = *reinterpret_cast<const float2*>(ml + pi * 2);
       float y[4];
       load4(a.part + pi * D + 4 * lane, y);
@@ -377,31 +471,36 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
 
 struct AttnPlan {
   bool tc;
-  int tile, mt, splits, chunk;
-  int64_t items;
+  int tile, mt, splits, chunk, ctas;
+  int64_t items, slots;
   size_t bytes;
 };
 
 constexpr int kFewRows = 32;  // query rows a key head up to which k_attn_few is the faster
 
-// Keys go to CTAs in parts of `chunk`, as many as a history has; the longest
-// may have `splits`.  Few rows: about 1,200 CTAs (three resident on each of 152
-// SMs, two to three rounds) where that leaves a part 64 keys, one tile a warp;
-// many rows: parts only where items leave SMs idle, 512 keys each at least.
+// Few rows: as many CTAs as are resident, or one for each unit that the
+// histories may have.  Many rows: one CTA an item, its keys in parts only where
+// items leave SMs idle, 512 keys each at least; the longest history may have
+// `splits`.
 AttnPlan attn_plan(const zg_kv_cache* c, int max_blocks, int B, int R, int Hq) {
-  AttnPlan p;
+  AttnPlan p = {};
   const int64_t M = (int64_t)R * (Hq / c->heads);
   p.tc = M > kFewRows;
   p.tile = p.tc ? attn_tc_tile(M) : M > 8 ? 16 : 8;
   p.mt = (int)((M + p.tile - 1) / p.tile);
   p.items = (int64_t)B * c->heads * p.mt;
   const int64_t keys = (int64_t)max_blocks * c->block_tokens;
-  const int64_t room = p.tc ? sm_count() : (int64_t)sm_count() * 8, least = p.tc ? 512 : 64;
-  const int64_t parts = std::max<int64_t>(1, p.items ? room / p.items : 1);
-  const int64_t chunk = std::max(least, ((keys + parts - 1) / parts + least - 1) / least * least);
-  p.chunk = (int)std::min<int64_t>(chunk, 1 << 30);
-  p.splits = (int)((keys + p.chunk - 1) / p.chunk);
-  p.bytes = p.splits > 1 ? (size_t)p.items * p.splits * p.tile * (c->dim + 2) * 4 : 0;
+  if (p.tc) {
+    const int64_t parts = std::max<int64_t>(1, p.items ? sm_count() / p.items : 1);
+    p.chunk = (int)std::min<int64_t>(std::max<int64_t>(512, ((keys + parts - 1) / parts + 511) / 512 * 512), 1 << 30);
+    p.splits = (int)((keys + p.chunk - 1) / p.chunk);
+    p.slots = p.splits > 1 ? p.items * p.splits : 0;
+  } else {
+    const int resident = p.tile == 16 && c->dim == 128 ? 2 : c->dim > 64 ? 3 : 4;
+    p.ctas = (int)std::min<int64_t>((int64_t)sm_count() * resident, p.items * ((keys + 63) / 64));
+    p.slots = p.ctas > 1 && keys > 64 ? 2 * (int64_t)p.ctas : 0;
+  }
+  p.bytes = p.slots ? ((size_t)p.slots * p.tile * (c->dim + 2) + B + 1) * 4 : 0;
   return p;
 }
 
@@ -451,7 +550,8 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   const AttnPlan p = attn_plan(cache, max_blocks, B, R, Hq);
   if (p.bytes && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < p.bytes))
     return bad_arg(call, "workspace must hold zg_kv_attention_workspace_size bytes, 256-byte aligned");
-  if (p.items * p.splits > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_attention: more than 2^31 CTAs");
+  if (p.items * std::max<int64_t>(p.tc ? p.splits : ((int64_t)max_blocks * cache->block_tokens + 63) / 64, 1) > 0x7FFFFFFF)
+    return fail(ZG_ERR_UNSUPPORTED, "zg_kv_attention: more than 2^31 units of work (B * Hq * keys of a table / 64)");
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
   AttnArgs a = {};
@@ -476,6 +576,9 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   a.tile = p.tile;
   a.mt = p.mt;
   a.splits = p.splits;
+  a.ctas = p.ctas;
+  a.slots = p.slots;
+  if (!p.tc && p.slots) a.prefix = static_cast<int32_t*>(workspace) + (size_t)p.slots * p.tile * (cache->dim + 2);
   a.chunk = p.chunk;
   a.causal = causal != 0;
   a.scale = scale * 1.4426950408889634f;
@@ -484,11 +587,11 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
     using E = typename decltype(ev)::type;
     constexpr int D = decltype(dv)::value;
     if (!p.tc) {
-      const unsigned ctas = (unsigned)(p.items * p.splits);
+      const unsigned ctas = (unsigned)p.ctas;
       if (p.tile == 8) k_attn_few<E, D, decltype(iv)::value, 1><<<ctas, kFewThreads, 0, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
       else k_attn_few<E, D, decltype(iv)::value, 2><<<ctas, kFewThreads, 0, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
     }
-    if (p.splits > 1) {
+    if (p.slots) {
       // may start while the parts are still made; it waits for them before it reads
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3((unsigned)(((int64_t)B * R * Hq + 7) / 8));

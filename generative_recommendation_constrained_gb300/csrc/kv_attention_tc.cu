@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (live && parts > 1) {
-          float* ml = a.part + (int64_t)a.B * a.heads * a.mt * a.splits * a.tile * D + pi * 2;
+          float* ml = a.part + a.slots * a.tile * D + pi * 2;
           ml[0] = l > 0.f ? mx : -INFINITY;
           ml[1] = l;
         } else if (live && a.lse) {

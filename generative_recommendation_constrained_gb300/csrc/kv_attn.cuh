@@ -11,9 +11,11 @@ struct AttnArgs {
   const int32_t *table, *length, *n_rows;
   uint32_t* status;
   float* lse;
-  float* part;  // [item][split][tile][D] outputs, then [item][split][tile][2] (max, sum)
+  float* part;      // [slot][tile][D] outputs, then [slot][tile][2] (max, sum)
+  int64_t slots;    // many rows: item * splits + part; few rows: two a CTA
+  int32_t* prefix;  // few rows: [B + 1] units before each request
   int32_t n_blocks, heads, bt, max_blocks;
-  int32_t B, R, Hq, G, splits, causal;
+  int32_t B, R, Hq, G, splits, ctas, causal;
   int32_t tile, mt;  // query rows an item (power of two), such items a (request, key head)
   int32_t chunk;     // keys of a part, a multiple of 64
   float scale;  // scale * log2(e)

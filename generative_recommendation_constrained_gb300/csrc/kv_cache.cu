@@ -28,6 +28,8 @@ struct RotateArgs {
   NormRopeArgs nr;
 };
 
+constexpr int kBatch = 4;  // heads whose loads a lane group has in flight
+
 // One group of lanes a (token, chunk of heads): the angles are computed once
 // for the chunk.  Heads 0..Hq-1 are the queries, Hq..Hq+Hk-1 the keys.
 template <typename T, int D>
@@ -44,21 +46,29 @@ __global__ void __launch_bounds__(256) k_norm_rope(const __grid_constant__ Rotat
   lane_angles(a.nr, m, l, live && a.nr.rot ? a.pos[token] : 0, cs, sn);
   lane_gain(a.nr.q_gain, m, gq);
   lane_gain(a.nr.k_gain, m, gk);
-  for (int i = 0; i < a.chunk; ++i) {
-    const int h = h0 + i;
-    const bool on = live && m.used && h < a.Hq + a.Hk;
-    const bool isq = h < a.Hq;
-    float x[8] = {};
-    if (on) {
-      const T* p = isq ? a.q.at(b, t, h) : a.k.at(b, t, h - a.Hq);
-      load4(p + m.e0, x);
-      load4(p + m.e1, x + 4);
+  const int n = live && m.used ? min(a.chunk, a.Hq + a.Hk - h0) : 0;
+  for (int i0 = 0; i0 < a.chunk; i0 += kBatch) {
+    float x[kBatch][8];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i0 + i;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
+      if (i0 + i < n) {
+        const T* p = h < a.Hq ? a.q.at(b, t, h) : a.k.at(b, t, h - a.Hq);
+        load4(p + m.e0, x[i]);
+        load4(p + m.e1, x[i] + 4);
+      }
     }
-    norm_rotate<D>(a.nr, m, isq ? gq : gk, x, cs, sn);
-    if (on) {
-      T* p = isq ? a.qo.at(b, t, h) : a.ko.at(b, t, h - a.Hq);
-      store4(p + m.e0, x);
-      store4(p + m.e1, x + 4);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i0 + i;
+      norm_rotate<D>(a.nr, m, h < a.Hq ? gq : gk, x[i], cs, sn);
+      if (i0 + i < n) {
+        T* p = h < a.Hq ? a.qo.at(b, t, h) : a.ko.at(b, t, h - a.Hq);
+        store4(p + m.e0, x[i]);
+        store4(p + m.e1, x[i] + 4);
+      }
     }
   }
 }
@@ -79,20 +89,36 @@ struct AppendArgs {
   Rows<T> k, v, q, qo;
   const int32_t *start, *n_new;
   int32_t B, T_, Hq, jmax;      // jmax: blocks that T_ tokens may touch
-  int32_t kv_ctas, chunk, nchunk;
+  int32_t pieces, kv_ctas, chunk, nchunk;
   int32_t has_nr;
   NormRopeArgs nr;
 };
 
 constexpr int kPasses = 8;  // rows a lane group keeps in registers
 
-// One CTA a (block, side, head) that is written: the rows stay in registers
-// between the maximum and the codes.  CTAs past kv_ctas turn the queries.
+// Four elements from global to shared memory, asynchronously.
+template <typename T>
+__device__ __forceinline__ void copy4_async(T* to, const T* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+               "n"(4 * sizeof(T))
+               : "memory");
+}
+
+// What a CTA writes at a time: one side and head of one block.
+struct Piece {
+  int b, h, side, bj, blk, lo, hi, start;  // rows lo..hi-1 of the block; hi <= lo: none
+};
+
+// Persistent CTAs, one piece after the other: the rows of the next piece come
+// into shared memory (each thread its own elements, so only it waits) while
+// this one's are turned, kept in registers between the maximum and the codes,
+// and written.  CTAs past kv_ctas turn the queries.
 template <typename T, int D, bool INT8>
 __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ AppendArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
   constexpr float Q = INT8 ? 127.f : 448.f;
-  __shared__ float red[8];
+  extern __shared__ __align__(16) uint8_t stage_raw[];  // [2][kPasses][2][threads][4]
+  __shared__ float red[2][8];
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS, rpp = blockDim.x / GS;
   const LaneMap m = lane_map<D>(a.nr, l);
 
@@ -105,123 +131,170 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ Appen
     float cs[4], sn[4], gq[8];
     lane_angles(a.nr, m, l, live ? a.start[b] + t : 0, cs, sn);
     lane_gain(a.nr.q_gain, m, gq);
-    for (int i = 0; i < a.chunk; ++i) {
-      const int h = h0 + i;
-      const bool on = live && m.used && h < a.Hq;
-      float x[8] = {};
-      if (on) {
-        load4(a.q.at(b, t, h) + m.e0, x);
-        load4(a.q.at(b, t, h) + m.e1, x + 4);
-      }
-      norm_rotate<D>(a.nr, m, gq, x, cs, sn);
-      if (on) {
-        store4(a.qo.at(b, t, h) + m.e0, x);
-        store4(a.qo.at(b, t, h) + m.e1, x + 4);
-      }
-    }
-    return;
-  }
-
-  int it = blockIdx.x;
-  const int h = it % a.c.heads;
-  it /= a.c.heads;
-  const int side = it & 1;
-  it >>= 1;
-  const int j = it % a.jmax, b = it / a.jmax;
-  const int start = a.start[b];
-  const int n = a.n_new ? a.n_new[b] : a.T_;
-  if (start < 0 || n < 0 || n > a.T_ || (int64_t)start + n > (int64_t)a.c.max_blocks * a.c.bt) {
-    if (threadIdx.x == 0) atomicOr(a.c.status, kStatusCache);
-    return;
-  }
-  const int bj = start / a.c.bt + j;
-  const int lo = j ? 0 : start - bj * a.c.bt;
-  const int64_t left = (int64_t)start + n - (int64_t)bj * a.c.bt;
-  const int hi = left < a.c.bt ? (int)left : a.c.bt;
-  if (n == 0 || hi <= lo) return;
-  const int blk = a.c.table[(int64_t)b * a.c.max_blocks + bj];
-  if (blk < 0 || blk >= a.c.n_blocks) {
-    if (threadIdx.x == 0) atomicOr(a.c.status, kStatusCache);
-    return;
-  }
-  const int64_t bh = (int64_t)blk * a.c.heads + h;
-  float* scale = (side ? a.c.vs : a.c.ks) + bh;
-  uint8_t* codes = (side ? a.c.vc : a.c.kc) + bh * a.c.bt * D;
-  const Rows<T>& src = side ? a.v : a.k;
-  const bool turn = !side && a.has_nr;
-  float gk[8];
-  lane_gain(turn ? a.nr.k_gain : nullptr, m, gk);
-
-  float x[kPasses][8];
-  float top = 0.f;
-  bool bad = false;
+    const int n = live && m.used ? min(a.chunk, a.Hq - h0) : 0;
+    for (int i0 = 0; i0 < a.chunk; i0 += kBatch) {
+      float x[kBatch][8];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int r = lo + p * rpp + grp;
-    const bool on = m.used && r < hi;
+      for (int i = 0; i < kBatch; ++i) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[p][i] = 0.f;
-    if (on) {
-      const T* s = src.at(b, bj * a.c.bt + r - start, h);
-      load4(s + m.e0, x[p]);
-      load4(s + m.e1, x[p] + 4);
-    }
-  }
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int r = lo + p * rpp + grp;
-    if (lo + p * rpp < hi) {  // uniform over the CTA
-      if (turn) {
-        float cs[4], sn[4];
-        lane_angles(a.nr, m, l, bj * a.c.bt + r, cs, sn);
-        norm_rotate<D>(a.nr, m, gk, x[p], cs, sn);
+        for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
+        if (i0 + i < n) {
+          load4(a.q.at(b, t, h0 + i0 + i) + m.e0, x[i]);
+          load4(a.q.at(b, t, h0 + i0 + i) + m.e1, x[i] + 4);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = fabsf(x[p][i]);
-        if (y <= FLT_MAX) {
-          top = fmaxf(top, m.used && r < hi ? y : 0.f);
-        } else {  // NaN -> 0; an infinity saturates
-          bad |= m.used && r < hi;
-          x[p][i] = isnan(x[p][i]) ? 0.f : copysignf(FLT_MAX, x[p][i]);
+      for (int i = 0; i < kBatch; ++i) {
+        norm_rotate<D>(a.nr, m, gq, x[i], cs, sn);
+        if (i0 + i < n) {
+          store4(a.qo.at(b, t, h0 + i0 + i) + m.e0, x[i]);
+          store4(a.qo.at(b, t, h0 + i0 + i) + m.e1, x[i] + 4);
         }
       }
     }
+    return;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  if (blockDim.x > 32) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) top = fmaxf(top, red[w]);
-  }
-  const float s0 = lo ? *scale : 0.f;
-  float s1 = fmaxf(s0, __fdiv_rn(top, Q));
-  if (s1 < FLT_MIN) s1 = 0.f;  // 1 / s1 stays finite
-  const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
-  __syncthreads();  // every thread has read the old scale
-  if (threadIdx.x == 0) *scale = s1;
-  if (bad) atomicOr(a.c.status, kStatusNonFinite);
-  if (s1 > s0 && m.used) {
-    for (int r = grp; r < lo; r += rpp) {  // rows held already: the scale has grown
-      uint32_t* w0 = reinterpret_cast<uint32_t*>(codes + r * D + m.e0);
-      uint32_t* w1 = reinterpret_cast<uint32_t*>(codes + r * D + m.e1);
-      float y[8];
-      codes_float4<INT8>(*w0, y);
-      codes_float4<INT8>(*w1, y + 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= s0;
-      *w0 = float4_codes<INT8>(y, inv);
-      *w1 = float4_codes<INT8>(y + 4, inv);
+
+  const int step = blockDim.x * 4;
+  auto piece_of = [&](int it) -> Piece {
+    Piece p;
+    p.h = it % a.c.heads;
+    it /= a.c.heads;
+    p.side = it & 1;
+    it >>= 1;
+    const int j = it % a.jmax;
+    p.b = it / a.jmax;
+    p.start = a.start[p.b];
+    p.lo = p.hi = 0;
+    p.blk = -1;
+    const int n = a.n_new ? a.n_new[p.b] : a.T_;
+    if (p.start < 0 || n < 0 || n > a.T_ || (int64_t)p.start + n > (int64_t)a.c.max_blocks * a.c.bt) {
+      if (threadIdx.x == 0) atomicOr(a.c.status, kStatusCache);
+      return p;
     }
-  }
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int r = lo + p * rpp + grp;
-    if (m.used && r < hi) {
-      *reinterpret_cast<uint32_t*>(codes + r * D + m.e0) = float4_codes<INT8>(x[p], inv);
-      *reinterpret_cast<uint32_t*>(codes + r * D + m.e1) = float4_codes<INT8>(x[p] + 4, inv);
+    p.bj = p.start / a.c.bt + j;
+    const int64_t left = (int64_t)p.start + n - (int64_t)p.bj * a.c.bt;
+    p.lo = j ? 0 : p.start - p.bj * a.c.bt;
+    const int hi = left < a.c.bt ? (int)left : a.c.bt;
+    if (n == 0 || hi <= p.lo) return p;
+    p.blk = a.c.table[(int64_t)p.b * a.c.max_blocks + p.bj];
+    if (p.blk < 0 || p.blk >= a.c.n_blocks) {
+      if (threadIdx.x == 0) atomicOr(a.c.status, kStatusCache);
+      return p;
     }
+    p.hi = hi;
+    return p;
+  };
+  auto fetch = [&](const Piece& p, int buf) {
+    const Rows<T>& src = p.side ? a.v : a.k;
+    T* to = reinterpret_cast<T*>(stage_raw) + buf * kPasses * 2 * step + threadIdx.x * 4;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = p.lo + i * rpp + grp;
+      if (m.used && r < p.hi) {
+        const T* s = src.at(p.b, p.bj * a.c.bt + r - p.start, p.h);
+        copy4_async(to + 2 * i * step, s + m.e0);
+        copy4_async(to + (2 * i + 1) * step, s + m.e1);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  float gk[8];
+  lane_gain(a.has_nr ? a.nr.k_gain : nullptr, m, gk);
+  Piece cur = piece_of(blockIdx.x);
+  fetch(cur, 0);
+  int buf = 0, turn_of = 0;  // `red` alternates over the pieces that use it
+  for (int it = blockIdx.x; it < a.pieces; it += a.kv_ctas, buf ^= 1) {
+    Piece nxt = cur;
+    if (it + a.kv_ctas < a.pieces) {
+      nxt = piece_of(it + a.kv_ctas);
+      fetch(nxt, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    if (cur.hi > cur.lo) {  // uniform over the CTA
+      const int lo = cur.lo, hi = cur.hi;
+      const int64_t bh = (int64_t)cur.blk * a.c.heads + cur.h;
+      float* scale = (cur.side ? a.c.vs : a.c.ks) + bh;
+      uint8_t* codes = (cur.side ? a.c.vc : a.c.kc) + bh * a.c.bt * D;
+      const bool turn = !cur.side && a.has_nr;
+      const float s0 = lo ? *scale : 0.f;
+      const T* from = reinterpret_cast<const T*>(stage_raw) + buf * kPasses * 2 * step + threadIdx.x * 4;
+      float x[kPasses][8];
+      float top = 0.f;
+      bool bad = false;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = lo + p * rpp + grp;
+        const bool on = m.used && r < hi;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[p][i] = 0.f;
+        if (on) {
+          load4(from + 2 * p * step, x[p]);
+          load4(from + (2 * p + 1) * step, x[p] + 4);
+        }
+        if (turn && lo + p * rpp < hi) {  // uniform over the CTA
+          float cs[4], sn[4];
+          lane_angles(a.nr, m, l, cur.bj * a.c.bt + r, cs, sn);
+          norm_rotate<D>(a.nr, m, gk, x[p], cs, sn);
+        }
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[p][i]));
+        bool odd = !(big <= FLT_MAX);  // a NaN alone does not show in a maximum
+#pragma unroll
+        for (int i = 0; i < 8; ++i) odd |= x[p][i] != x[p][i];
+        if (odd && on) {  // NaN -> 0; an infinity saturates
+          bad = true;
+          big = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (fabsf(x[p][i]) <= FLT_MAX) big = fmaxf(big, fabsf(x[p][i]));
+            else x[p][i] = isnan(x[p][i]) ? 0.f : copysignf(FLT_MAX, x[p][i]);
+          }
+        }
+        if (on) top = fmaxf(top, big);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      if (blockDim.x > 32) {
+        if ((threadIdx.x & 31) == 0) red[turn_of][threadIdx.x >> 5] = top;
+        __syncthreads();  // also: every thread has read the old scale
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) top = fmaxf(top, red[turn_of][w]);
+      } else {
+        __syncwarp();
+      }
+      turn_of ^= 1;
+      float s1 = fmaxf(s0, __fdiv_rn(top, Q));
+      if (s1 < FLT_MIN) s1 = 0.f;  // 1 / s1 stays finite
+      const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
+      if (threadIdx.x == 0) *scale = s1;
+      if (bad) atomicOr(a.c.status, kStatusNonFinite);
+      if (s1 > s0 && m.used) {
+        for (int r = grp; r < lo; r += rpp) {  // rows held already: the scale has grown
+          uint32_t* w0 = reinterpret_cast<uint32_t*>(codes + r * D + m.e0);
+          uint32_t* w1 = reinterpret_cast<uint32_t*>(codes + r * D + m.e1);
+          float y[8];
+          codes_float4<INT8>(*w0, y);
+          codes_float4<INT8>(*w1, y + 4);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= s0;
+          *w0 = float4_codes<INT8>(y, inv);
+          *w1 = float4_codes<INT8>(y + 4, inv);
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = lo + p * rpp + grp;
+        if (m.used && r < hi) {
+          *reinterpret_cast<uint32_t*>(codes + r * D + m.e0) = float4_codes<INT8>(x[p], inv);
+          *reinterpret_cast<uint32_t*>(codes + r * D + m.e1) = float4_codes<INT8>(x[p] + 4, inv);
+        }
+      }
+    }
+    cur = nxt;
   }
 }
 
@@ -294,10 +367,19 @@ zg_status nr_args(const zg_norm_rope* nr, int dim, const char* call, NormRopeArg
   o->eps = nr->eps;
   o->q_gain = nr->q_gain;
   o->k_gain = nr->k_gain;
-  for (int i = 0; i < nr->rot_dim / 2; ++i) {
-    const double f = nr->freq ? nr->freq[i] : std::pow(nr->theta, -2.0 * i / nr->rot_dim);
-    if (!(f >= 0.0 && f <= 4.0)) return bad_arg(call, "freq must be in [0, 4]");
-    o->turns[i] = (uint64_t)(f / 6.283185307179586476925 * 18446744073709551616.0);
+  // theta^(-2i/rot_dim) by doubling: seven powers and one product each (seven roundings at most) instead of 64 powers
+  double f[64] = {1.0};
+  const int n = nr->rot_dim / 2;
+  if (nr->freq)
+    for (int i = 0; i < n; ++i) f[i] = nr->freq[i];
+  else
+    for (int w = 1; w < n; w *= 2) {
+      const double r = std::pow(nr->theta, -2.0 * w / nr->rot_dim);
+      for (int i = w; i < std::min(2 * w, n); ++i) f[i] = f[i - w] * r;
+    }
+  for (int i = 0; i < n; ++i) {
+    if (!(f[i] >= 0.0 && f[i] <= 4.0)) return bad_arg(call, "freq must be in [0, 4]");
+    o->turns[i] = (uint64_t)(f[i] / 6.283185307179586476925 * 18446744073709551616.0);
   }
   return ZG_OK;
 }
@@ -439,26 +521,31 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
   int groups = 1;
   while (groups * kPasses < std::min(T, bt)) groups *= 2;
   const int threads = std::max(32, groups * lanes);
-  const int64_t kv = (int64_t)B * jmax * 2 * cache->heads;
+  const int64_t pieces = (int64_t)B * jmax * 2 * cache->heads;
   const int64_t tokens = (int64_t)B * T;
   const int chunk = Hq ? head_chunk(tokens, Hq, lanes) : 1, nchunk = Hq ? (Hq + chunk - 1) / chunk : 0;
   const int64_t qc = (tokens * nchunk * lanes + threads - 1) / threads;
-  if (kv + qc > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^31 CTAs");
+  if (pieces + qc > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^31 CTAs");
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
+  // resident CTAs (128 registers a thread: 512 threads an SM; their buffers inside 200 KB) walk the pieces
+  const size_t smem = 2 * (size_t)kPasses * threads * 8 * (k->dtype == ZG_F32 ? 4 : 2);
+  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>(512 / threads, (200 << 10) / smem));
+  const int64_t kv = std::min<int64_t>(pieces, resident * sm_count());
+  cudaError_t err = cudaSuccess;
   for_type(k->dtype, [&](auto e) {
     using E = typename decltype(e)::type;
     const AppendArgs<E> a = {view(cache, table, max_blocks, status), rows_of<E>(k), rows_of<E>(v), rows_of<E>(q),
-                             rows_of<E>(q_out), start, n_new, B, T, Hq, (int32_t)jmax, (int32_t)kv, chunk, nchunk,
-                             nr != nullptr, na};
+                             rows_of<E>(q_out), start, n_new, B, T, Hq, (int32_t)jmax, (int32_t)pieces, (int32_t)kv,
+                             chunk, nchunk, nr != nullptr, na};
     for_dim(cache->dim, [&](auto dv) {
       constexpr int D = decltype(dv)::value;
-      if (cache->format == ZG_KV_INT8)
-        k_kv_append<E, D, true><<<(unsigned)(kv + qc), threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-      else
-        k_kv_append<E, D, false><<<(unsigned)(kv + qc), threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      auto kern = cache->format == ZG_KV_INT8 ? k_kv_append<E, D, true> : k_kv_append<E, D, false>;
+      if (smem > 48 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (err == cudaSuccess) kern<<<(unsigned)(kv + qc), threads, smem, static_cast<cudaStream_t>(stream)>>>(a);
     });
   });
+  if (err != cudaSuccess) return cuda_fail(err, "cache append launch");
   return after_launch("cache append launch");
 } catch (...) {
   return ZG_ERR_OUT_OF_MEMORY;

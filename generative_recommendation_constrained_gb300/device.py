@@ -2,6 +2,8 @@
 workspace and outputs; the library's kernels do all the work."""
 from __future__ import annotations
 
+import struct
+
 import numpy as np
 import torch
 
@@ -75,6 +77,9 @@ _ROW_TYPES = {torch.float32: Z.ZG_F32, torch.bfloat16: Z.ZG_BF16, torch.float16:
 _CODE_TYPES = {torch.float8_e4m3fn: Z.ZG_KV_E4M3, torch.int8: Z.ZG_KV_INT8}
 
 
+_pack_rows = struct.Struct("Piiqqq").pack      # zg_rows as bytes: a fraction of a ctypes struct's cost
+
+
 def _rows(x: torch.Tensor | None):
     """zg_rows of a [B, T, heads, dim] tensor whose last dimension is contiguous."""
     if x is None:
@@ -85,11 +90,14 @@ def _rows(x: torch.Tensor | None):
     sb, st, sh, se = x.stride()
     if se != 1:
         raise ValueError("the last dimension of the rows must be contiguous")
-    return Z.zg_rows(x.data_ptr(), dt, 0, sb, st, sh)
+    if sb < 0 or st < 0 or sh < 0:
+        raise ValueError("strides of the rows must not be negative")
+    return _pack_rows(x.data_ptr(), dt, 0, sb, st, sh)
 
 
-def _stream(stream):
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream
+def _stream(stream, x: torch.Tensor):
+    """The stream given, or the current one of x's device (its number alone: a Stream object costs 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(x.device.index) if stream is None else stream
 
 
 def _int32(x: torch.Tensor | None, shape, name: str):
@@ -129,7 +137,7 @@ class NormRope:
                 raise ValueError("an output must have its input's shape")
         Z.zg_qk_norm_rope(self.struct, _rows(q), _rows(k), _rows(q_out) if q is not None else None,
                           _rows(k_out) if k is not None else None, positions, B, T,
-                          0 if q is None else q.shape[2], 0 if k is None else k.shape[2], self.dim, _stream(stream))
+                          0 if q is None else q.shape[2], 0 if k is None else k.shape[2], self.dim, _stream(stream, x))
         return q_out, k_out
 
 
@@ -190,7 +198,7 @@ class KVCache:
                 raise ValueError("q_out must have q's shape")
         Z.zg_kv_append(self.struct, norm_rope.struct if norm_rope is not None else None, _rows(k), _rows(v), _rows(q),
                        _rows(q_out) if q is not None else None, 0 if q is None else q.shape[2], table,
-                       table.shape[1], start, n_new, B, T, _stream(stream))
+                       table.shape[1], start, n_new, B, T, _stream(stream, k))
         return q_out
 
     def read(self, table, start, n=None, k_out=None, v_out=None, stream: int | None = None):
@@ -204,7 +212,8 @@ class KVCache:
         _int32(table, (B, table.shape[1]), "table")
         _int32(start, (B,), "start")
         _int32(n, (B,), "n")
-        Z.zg_kv_read(self.struct, table, table.shape[1], start, n, B, T, _rows(k_out), _rows(v_out), _stream(stream))
+        Z.zg_kv_read(self.struct, table, table.shape[1], start, n, B, T, _rows(k_out), _rows(v_out),
+                     _stream(stream, x))
         return k_out, v_out
 
 
@@ -233,5 +242,5 @@ class CacheAttention:
         _int32(n_rows, (self.B,), "n_rows")
         Z.zg_kv_attention(self.cache.struct, table, self.max_blocks, length, n_rows, _rows(q), self._out_rows,
                           self.lse, self.B, self.R, self.Hq, self.scale, self.causal, self.ws, self.ws_bytes,
-                          _stream(stream))
+                          _stream(stream, q))
         return self.out, self.lse

@@ -149,7 +149,7 @@ def test_attention_refusals(zg):
     f(**{**ok, "B": 0})
     f(**{**ok, "R": 0})
     from generative_recommendation_constrained_gb300._lib import lib
-    assert lib.zg_kv_attention_workspace_size(c, 4, 1, 1, 2, None) == 1
+    assert lib.zg_kv_attention_workspace_size(C.byref(c), 4, 1, 1, 2, None) == 1
 
 
 def test_workspace_covers_smaller_calls(zg):
