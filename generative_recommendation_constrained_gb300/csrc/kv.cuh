@@ -129,19 +129,19 @@ struct NormRopeArgs {
   uint64_t turns[64];
 };
 
-// What one lane holds of a head: elements e0..e0+3 and e1..e1+3.  Rotated
-// lanes hold four whole pairs: (e0 + i, e1 + i), or interleaved neighbours.
+// What one lane holds of a head: elements e0..e0+3 and e1..e1+3, four pairs:
+// (e0 + i, e1 + i), or INTER neighbours.  Pairs past rot_dim are not turned.
 struct LaneMap {
   int e0, e1;
   bool used, rotated;
 };
 
-template <int D>
+template <int D, bool INTER>
 __device__ __forceinline__ LaneMap lane_map(const NormRopeArgs& a, int l) {
   LaneMap m;
   m.used = l < HeadLanes<D>::kUsed;
   m.rotated = m.used && 8 * l < a.rot;
-  if (a.inter || !m.rotated) {
+  if (INTER || !m.rotated) {
     m.e0 = 8 * l;
     m.e1 = 8 * l + 4;
   } else {
@@ -149,6 +149,31 @@ __device__ __forceinline__ LaneMap lane_map(const NormRopeArgs& a, int l) {
     m.e1 = 4 * l + a.rot / 2;
   }
   return m;
+}
+
+// Pairs of floats in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // Sine and cosine of turn * 2^-32 of a full turn: the nearest quarter off,
@@ -172,60 +197,94 @@ __device__ __forceinline__ void turn_sincos(int32_t turn, float& sn, float& cs) 
   cs = (quarter + 1) & 2 ? -b : b;
 }
 
-__device__ __forceinline__ void lane_angles(const NormRopeArgs& a, const LaneMap& m, int l, int pos, float* cs,
-                                            float* sn) {
+// The turn of a lane's four pairs at one position, gains included: the pair
+// (u, v) becomes (u uu + v uv, u vu + v vv) times the norm's factor.
+struct Turn {
+  float uu[4], uv[4], vu[4], vv[4];
+};
+
+// Gains of a lane's pairs (nullptr: 1).
+struct LaneGain {
+  float u[4], v[4];
+};
+template <bool INTER>
+__device__ __forceinline__ LaneGain lane_gain(const float* gain, const LaneMap& m) {
+  LaneGain g;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    cs[i] = 1.f;
+    g.u[i] = g.v[i] = 1.f;
+    if (gain && m.used) {
+      g.u[i] = gain[INTER ? m.e0 + 2 * i : m.e0 + i];
+      g.v[i] = gain[INTER ? m.e0 + 2 * i + 1 : m.e1 + i];
+    }
+  }
+  return g;
+}
+
+__device__ __forceinline__ void lane_angles(const NormRopeArgs& a, const LaneMap& m, int l, int pos, float* sn,
+                                            float* cs) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
     sn[i] = 0.f;
+    cs[i] = 1.f;
     if (m.rotated) turn_sincos((int32_t)(((uint64_t)(int64_t)pos * a.turns[4 * l + i]) >> 32), sn[i], cs[i]);
   }
 }
 
+__device__ __forceinline__ Turn turn_of(const float* sn, const float* cs, const LaneGain& g) {
+  Turn t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t.uu[i] = g.u[i] * cs[i];
+    t.uv[i] = -g.v[i] * sn[i];
+    t.vu[i] = g.u[i] * sn[i];
+    t.vv[i] = g.v[i] * cs[i];
+  }
+  return t;
+}
+
 // x[0..3] = elements e0.., x[4..7] = elements e1.. of one head, in place.
 // Every lane of the warp takes part (group sums by shuffles).
-template <int D>
-__device__ __forceinline__ void norm_rotate(const NormRopeArgs& a, const LaneMap& m, const float* gain, float* x,
-                                            const float* cs, const float* sn) {
+template <int D, bool INTER>
+__device__ __forceinline__ void norm_rotate(const NormRopeArgs& a, const Turn& t, float* x) {
+  float inv = 1.f;
   if (a.norm) {
-    float ss = 0.f;
+    uint64_t s2 = mul2(pair(x[0], x[1]), pair(x[0], x[1]));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int i = 2; i < 8; i += 2) s2 = fma2(pair(x[i], x[i + 1]), pair(x[i], x[i + 1]), s2);
+    float ss, s1;
+    unpair(s2, ss, s1);
+    ss += s1;
 #pragma unroll
     for (int o = HeadLanes<D>::kGroup / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    const float inv = rsqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * gain[i];
+    inv = rsqrtf(ss * (1.f / D) + a.eps);
   }
-  if (m.rotated) {
-    if (a.inter) {
+  if constexpr (INTER) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = x[2 * i], v = x[2 * i + 1];
-        x[2 * i] = u * cs[i] - v * sn[i];
-        x[2 * i + 1] = u * sn[i] + v * cs[i];
-      }
-    } else {
+    for (int i = 0; i < 4; ++i) {
+      const float u = x[2 * i], v = x[2 * i + 1];
+      x[2 * i] = (u * t.uu[i] + v * t.uv[i]) * inv;
+      x[2 * i + 1] = (u * t.vu[i] + v * t.vv[i]) * inv;
+    }
+  } else {
+    const uint64_t i2 = pair(inv, inv);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = x[i], v = x[4 + i];
-        x[i] = u * cs[i] - v * sn[i];
-        x[4 + i] = u * sn[i] + v * cs[i];
-      }
+    for (int i = 0; i < 4; i += 2) {
+      const uint64_t u = pair(x[i], x[i + 1]), v = pair(x[4 + i], x[5 + i]);
+      const uint64_t y = fma2(u, pair(t.uu[i], t.uu[i + 1]), mul2(v, pair(t.uv[i], t.uv[i + 1])));
+      const uint64_t z = fma2(u, pair(t.vu[i], t.vu[i + 1]), mul2(v, pair(t.vv[i], t.vv[i + 1])));
+      unpair(mul2(y, i2), x[i], x[i + 1]);
+      unpair(mul2(z, i2), x[4 + i], x[5 + i]);
     }
   }
 }
 
-__device__ __forceinline__ void lane_gain(const float* gain, const LaneMap& m, float* g) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) g[i] = 1.f;
-  if (gain && m.used) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      g[i] = gain[m.e0 + i];
-      g[4 + i] = gain[m.e1 + i];
-    }
-  }
+// Four elements from global to shared memory, asynchronously.
+template <typename T>
+__device__ __forceinline__ void copy4_async(T* to, const T* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+               "n"(4 * sizeof(T))
+               : "memory");
 }
 
 // Run-time head size and type as template arguments: f(Dim<D>{}), f(Elem<T>{}).

@@ -36,63 +36,107 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 constexpr int kFewThreads = 128;
 
-// What one lane holds of 16 keys and values: of keys g and g + 8 (lane = 4 g +
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
+}
+
+// What one lane takes of 16 keys and values: of keys g and g + 8 (lane = 4 g +
 // c) the dims of `dim_of`, of values 2c, 2c + 1, 2c + 8, 2c + 9 the dims g * D/8
 // and on.  The order of the dims inside a product is free, so that a lane
-// reads neighbouring bytes and a warp whole rows.
+// reads neighbouring bytes and a warp whole rows.  It waits in shared memory,
+// each lane's own words apart: planes of N bytes a thread, thread after thread.
 template <int D>
 struct Tile16 {
-  static constexpr int KW = D / 16, VW = D / 32;  // words of a key, of a value
-  uint32_t k[2][KW], v[4][VW];
-  float ks, vs;
+  static constexpr int KW = D / 16, VW = D / 32;           // words of a key, of a value
+  static constexpr int KB = 4 * KW, VB = 4 * VW;           // bytes
+  static constexpr int kKey16 = KB / 16, kKey8 = KB % 16 / 8;  // pieces of 16 and 8 bytes a key
+  static constexpr int kVal = D == 96 ? 4 : VB;            // bytes of a piece of a value
+  static constexpr int kBytes = 2 * KB + 4 * VB + 8;       // a lane, with the two scales
   static __device__ __forceinline__ int dim_of(int w, int c) {
     return w < D / 64 * 4 ? w / 4 * 64 + 16 * c + 4 * (w % 4) : D / 64 * 64 + 8 * c + 4 * (w - D / 64 * 4);
   }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < KW; ++i) k[0][i] = k[1][i] = 0;
-#pragma unroll
-    for (int i = 0; i < VW; ++i) v[0][i] = v[1][i] = v[2][i] = v[3][i] = 0;
-    ks = vs = 0.f;
-  }
-  __device__ __forceinline__ void load(const uint8_t* kp, const uint8_t* vp, int g, int c) {
+  // `at`: the slot; `tid` of `threads`
+  static __device__ __forceinline__ void fetch(uint32_t at, int tid, const uint8_t* kp, const uint8_t* vp,
+                                               const float* ks, const float* vs, int g, int c) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const uint8_t* p = kp + (n * 8 + g) * D;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) *reinterpret_cast<uint4*>(&k[n][4 * i]) = ldg16(p + 64 * i + 16 * c);
-      if constexpr (D % 64 != 0) *reinterpret_cast<uint2*>(&k[n][D / 64 * 4]) = ldg8(p + D / 64 * 64 + 8 * c);
+      for (int i = 0; i < kKey16; ++i, at += 16 * kThreadsOf) copy_async<16>(at + 16 * tid, p + 64 * i + 16 * c);
+      if constexpr (kKey8 != 0) {
+        copy_async<8>(at + 8 * tid, p + D / 64 * 64 + 8 * c);
+        at += 8 * kThreadsOf;
+      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint8_t* p = vp + (2 * c + (j & 1) + (j >> 1) * 8) * D + g * (D / 8);
-      if constexpr (D == 128) {
-        *reinterpret_cast<uint4*>(v[j]) = ldg16(p);
-      } else if constexpr (D == 64) {
-        *reinterpret_cast<uint2*>(v[j]) = ldg8(p);
-      } else {
 #pragma unroll
-        for (int u = 0; u < VW; ++u) v[j][u] = ldg4(p + 4 * u);
+      for (int i = 0; i < VB / kVal; ++i, at += kVal * kThreadsOf) copy_async<kVal>(at + kVal * tid, p + i * kVal);
+    }
+    copy_async<4>(at + 4 * tid, ks);
+    copy_async<4>(at + 4 * kThreadsOf + 4 * tid, vs);
+  }
+  static constexpr int kThreadsOf = 128;
+  uint32_t k[2][KW], v[4][VW];
+  float ks, vs;
+  __device__ __forceinline__ void read(const uint8_t* at, int tid) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int i = 0; i < kKey16; ++i, at += 16 * kThreadsOf)
+        *reinterpret_cast<uint4*>(&k[n][4 * i]) = *reinterpret_cast<const uint4*>(at + 16 * tid);
+      if constexpr (kKey8 != 0) {
+        *reinterpret_cast<uint2*>(&k[n][4 * kKey16]) = *reinterpret_cast<const uint2*>(at + 8 * tid);
+        at += 8 * kThreadsOf;
       }
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < VB / kVal; ++i, at += kVal * kThreadsOf) {
+        if constexpr (kVal == 16) *reinterpret_cast<uint4*>(v[j]) = *reinterpret_cast<const uint4*>(at + 16 * tid);
+        else if constexpr (kVal == 8) *reinterpret_cast<uint2*>(v[j]) = *reinterpret_cast<const uint2*>(at + 8 * tid);
+        else v[j][i] = *reinterpret_cast<const uint32_t*>(at + 4 * tid);
+      }
+    ks = *reinterpret_cast<const float*>(at + 4 * tid);
+    vs = *reinterpret_cast<const float*>(at + 4 * kThreadsOf + 4 * tid);
   }
-  // each code is read once: past L1
-  static __device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
-    uint4 x;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
-    return x;
-  }
-  static __device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
-    uint2 x;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
-    return x;
-  }
-  static __device__ __forceinline__ uint32_t ldg4(const uint8_t* p) {
-    uint32_t x;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(x) : "l"(p));
-    return x;
+  // nothing there: a block outside the cache
+  static __device__ __forceinline__ void clear(uint8_t* at, int tid) {
+    // words of a lane are spread over planes of 16, 8 or 4 bytes: clear by the smallest
+    uint32_t w = 0;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int i = 0; i < kKey16; ++i, at += 16 * kThreadsOf) *reinterpret_cast<uint4*>(at + 16 * tid) = make_uint4(w, w, w, w);
+      if constexpr (kKey8 != 0) {
+        *reinterpret_cast<uint2*>(at + 8 * tid) = make_uint2(w, w);
+        at += 8 * kThreadsOf;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < VB / kVal; ++i, at += kVal * kThreadsOf)
+#pragma unroll
+        for (int x = 0; x < kVal / 4; ++x) *reinterpret_cast<uint32_t*>(at + kVal * tid + 4 * x) = w;
+    *reinterpret_cast<uint32_t*>(at + 4 * tid) = w;
+    *reinterpret_cast<uint32_t*>(at + 4 * kThreadsOf + 4 * tid) = w;
   }
 };
+
+// Dynamic shared memory of k_attn_few: the ring of tiles, then (in its place)
+// the warps' sums.
+constexpr int kFewAhead = 3;  // tiles a warp has in its ring
+template <int D, int NT>
+constexpr int few_smem() {
+  const int ring = kFewAhead * Tile16<D>::kBytes * kFewThreads, sums = 4 * 8 * NT * (D + 2) * 4;
+  return ring > sums ? ring : sums;
+}
 
 // Keys go to the CTAs of k_attn_few by the unit of 64 (a tile a warp), all
 // items (request, key head, 8 NT rows) in a row and the same share for each
@@ -116,17 +160,19 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, i
 }
 
 // Few query rows: a row is (token, query head of the group).  Each warp walks
-// its own 16-key tiles straight from global memory into matrix fragments, the
-// next tile's loads in flight under this one's products.  Keys and dims are the
+// its own 16-key tiles, brought by asynchronous copies in the order of the
+// matrix fragments, two tiles ahead (in registers, one ahead, 12 warps an SM had
+// 4.2 TB/s of loads in flight).  Keys and dims are the
 // long side of the products (S^T = K Q^T, O^T = V^T P^T), so that eight rows
 // fill an instruction that sixteen keys or dims by eight rows make.
 template <typename T, int D, bool INT8, int NT>
-__global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant__ AttnArgs a, const Rows<T> q,
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_attn_few(const __grid_constant__ AttnArgs a, const Rows<T> q,
                                                           const Rows<T> out) {
   using Tl = Tile16<D>;
   constexpr int KW = Tl::KW, VW = Tl::VW, NR = 8 * NT;
   __shared__ float sm_m[4][NR], sm_l[4][NR];
-  __shared__ float sm_o[4][NR][D + 2];
+  extern __shared__ __align__(16) uint8_t ring[];  // [kFewAhead] tiles; then float [4][NR][D + 2]
+  auto sm_o = reinterpret_cast<float (*)[NR][D + 2]>(ring);
   __shared__ int sm_sum[4], sm_b, sm_first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int M = a.R * a.G;
@@ -197,16 +243,23 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
       if (lane == 0) atomicOr(a.status, kStatusCache);
       return -1;
     };
-    auto fetch = [&](Tl& x, int t, int blk) {
-      if (blk < 0) return x.zero();
-      const int64_t bh = (int64_t)blk * a.heads + h, at = (bh * a.bt + t * 16 % a.bt) * D;
-      x.load(a.kc + at, a.vc + at, g, c);
-      x.ks = a.ks[bh];
-      x.vs = a.vs[bh];
+    // tile t into its slot; one group a call
+    auto fetch = [&](int t, int slot_of, int blk) {
+      if (t < t1) {
+        uint8_t* at = ring + slot_of * (Tl::kBytes * kFewThreads);
+        if (blk < 0) {
+          Tl::clear(at, threadIdx.x);
+        } else {
+          const int64_t bh = (int64_t)blk * a.heads + h, from = (bh * a.bt + t * 16 % a.bt) * D;
+          Tl::fetch(smem_addr(at), threadIdx.x, a.kc + from, a.vc + from, a.ks + bh, a.vs + bh, g, c);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    Tl cur, nxt;
-    int blk = block_of(t0), blk1 = block_of(t0 + 4);
-    fetch(cur, t0, blk);
+    const int blk0 = block_of(t0), blk1 = block_of(t0 + 4);
+    int blk2 = block_of(t0 + 8);
+    fetch(t0, 0, blk0);
+    fetch(t0 + 4, 1, blk1);
 
     // the rows: lane (g, c) the dims of its words of row g; then the sight and the scale of rows 2c, 2c + 1
     uint32_t qb[NT][KW][2];
@@ -255,9 +308,14 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
         for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
     }
 
+    int ahead = 2;  // the slot of t + 8
     for (int t = t0; t < t1; t += 4) {
-      const int blk2 = block_of(t + 8);
-      if (t + 4 < t1) fetch(nxt, t + 4, blk1);
+      const int blk3 = block_of(t + 12);
+      fetch(t + 8, ahead, blk2);
+      ahead = ahead == kFewAhead - 1 ? 0 : ahead + 1;  // the slot of t + 12, which is the slot of t
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      Tl cur;
+      cur.read(ring + ahead * (Tl::kBytes * kFewThreads), threadIdx.x);
       const int key0 = t * 16;
       float z[NT][4];
 #pragma unroll
@@ -332,10 +390,11 @@ __global__ void __launch_bounds__(kFewThreads) k_attn_few(const __grid_constant_
           for (int n = 0; n < NT; ++n) mma_16816(o[n][2 * u + v], va, pb[n][0], pb[n][1]);
         }
       }
-      cur = nxt;
-      blk1 = blk2;
+      blk2 = blk3;
     }
 
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the sums take the ring's place
     // join the warps: accumulator tile j, element (e, row g or g + 8) is row 2c + e, dim g * D/8 + 2 j (+ 1)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -496,7 +555,7 @@ AttnPlan attn_plan(const zg_kv_cache* c, int max_blocks, int B, int R, int Hq) {
     p.splits = (int)((keys + p.chunk - 1) / p.chunk);
     p.slots = p.splits > 1 ? p.items * p.splits : 0;
   } else {
-    const int resident = p.tile == 16 && c->dim == 128 ? 2 : c->dim > 64 ? 3 : 4;
+    const int resident = p.tile == 16 ? 2 : 4;
     p.ctas = (int)std::min<int64_t>((int64_t)sm_count() * resident, p.items * ((keys + 63) / 64));
     p.slots = p.ctas > 1 && keys > 64 ? 2 * (int64_t)p.ctas : 0;
   }
@@ -583,13 +642,17 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   a.causal = causal != 0;
   a.scale = scale * 1.4426950408889634f;
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
+  cudaError_t err = cudaSuccess;
   auto launch = [&](auto ev, auto dv, auto iv) {
     using E = typename decltype(ev)::type;
     constexpr int D = decltype(dv)::value;
     if (!p.tc) {
       const unsigned ctas = (unsigned)p.ctas;
-      if (p.tile == 8) k_attn_few<E, D, decltype(iv)::value, 1><<<ctas, kFewThreads, 0, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
-      else k_attn_few<E, D, decltype(iv)::value, 2><<<ctas, kFewThreads, 0, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
+      auto kern = p.tile == 8 ? k_attn_few<E, D, decltype(iv)::value, 1> : k_attn_few<E, D, decltype(iv)::value, 2>;
+      const int smem = p.tile == 8 ? few_smem<D, 1>() : few_smem<D, 2>();
+      if (smem > 48 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (err != cudaSuccess) return;
+      kern<<<ctas, kFewThreads, smem, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
     }
     if (p.slots) {
       // may start while the parts are still made; it waits for them before it reads
@@ -617,8 +680,8 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
     if (q->dtype == ZG_BF16) typed(Elem<__nv_bfloat16>{});
     else typed(Elem<__half>{});
   });
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? ZG_OK : cuda_fail(e, "cache attention launch");
+  if (err == cudaSuccess) err = cudaGetLastError();
+  return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache attention launch");
 } catch (...) {
   return ZG_ERR_OUT_OF_MEMORY;
 }

@@ -28,48 +28,74 @@ struct RotateArgs {
   NormRopeArgs nr;
 };
 
-constexpr int kBatch = 4;  // heads whose loads a lane group has in flight
+constexpr int kAhead = 4;  // heads that a lane group has in flight
+
+// `n` heads of one token through a lane group, kAhead of them in flight in
+// shared memory (each thread waits for its own elements alone; `ring`: this
+// thread's first four, `step` elements to the next).  Every lane of the warp
+// takes part `most` times.
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ void turn_heads(const NormRopeArgs& a, const LaneMap& m, const Turn& t, const T* from,
+                                           int64_t from_step, T* to, int64_t to_step, int n, int most, T* ring,
+                                           int step) {
+  from += m.e0;
+  to += m.e0;
+  const int d = m.e1 - m.e0;
+  auto fetch = [&](int i) {
+    if (i < n) {
+      T* s = ring + (i % kAhead) * 2 * step;
+      copy4_async(s, from + i * from_step);
+      copy4_async(s + step, from + i * from_step + d);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) fetch(i);
+  for (int i = 0; i < most; ++i) {
+    fetch(i + kAhead - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    float x[8] = {};
+    if (i < n) {
+      const T* s = ring + (i % kAhead) * 2 * step;
+      load4(s, x);
+      load4(s + step, x + 4);
+    }
+    norm_rotate<D, INTER>(a, t, x);
+    if (i < n) {
+      store4(to + i * to_step, x);
+      store4(to + i * to_step + d, x + 4);
+    }
+  }
+}
 
 // One group of lanes a (token, chunk of heads): the angles are computed once
 // for the chunk.  Heads 0..Hq-1 are the queries, Hq..Hq+Hk-1 the keys.
-template <typename T, int D>
+template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(256) k_norm_rope(const __grid_constant__ RotateArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
+  __shared__ __align__(16) T ring[kAhead * 2 * 256 * 4];
   const int l = threadIdx.x % GS;
   const int64_t g = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS;
   const int64_t token = g / a.nchunk;
   const bool live = token < (int64_t)a.B * a.T_;
   const int b = live ? (int)(token / a.T_) : 0, t = live ? (int)(token % a.T_) : 0;
-  const int h0 = (int)(g % a.nchunk) * a.chunk;
-  const LaneMap m = lane_map<D>(a.nr, l);
-  float cs[4], sn[4], gq[8], gk[8];
-  lane_angles(a.nr, m, l, live && a.nr.rot ? a.pos[token] : 0, cs, sn);
-  lane_gain(a.nr.q_gain, m, gq);
-  lane_gain(a.nr.k_gain, m, gk);
-  const int n = live && m.used ? min(a.chunk, a.Hq + a.Hk - h0) : 0;
-  for (int i0 = 0; i0 < a.chunk; i0 += kBatch) {
-    float x[kBatch][8];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = h0 + i0 + i;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
-      if (i0 + i < n) {
-        const T* p = h < a.Hq ? a.q.at(b, t, h) : a.k.at(b, t, h - a.Hq);
-        load4(p + m.e0, x[i]);
-        load4(p + m.e1, x[i] + 4);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = h0 + i0 + i;
-      norm_rotate<D>(a.nr, m, h < a.Hq ? gq : gk, x[i], cs, sn);
-      if (i0 + i < n) {
-        T* p = h < a.Hq ? a.qo.at(b, t, h) : a.ko.at(b, t, h - a.Hq);
-        store4(p + m.e0, x[i]);
-        store4(p + m.e1, x[i] + 4);
-      }
-    }
+  const int h0 = (int)(g % a.nchunk) * a.chunk, h1 = min(h0 + a.chunk, a.Hq + a.Hk);
+  const LaneMap m = lane_map<D, INTER>(a.nr, l);
+  const bool on = live && m.used;
+  float sn[4], cs[4];
+  lane_angles(a.nr, m, l, live && a.nr.rot ? a.pos[token] : 0, sn, cs);
+  T* mine = ring + threadIdx.x * 4;
+  // a warp's lane groups may hold different chunks: each side as often as the largest needs
+  if (a.Hq) {
+    const Turn tq = turn_of(sn, cs, lane_gain<INTER>(a.nr.q_gain, m));
+    turn_heads<T, D, INTER>(a.nr, m, tq, a.q.at(b, t, h0), a.q.sh, a.qo.at(b, t, h0), a.qo.sh,
+                            on ? min(h1, a.Hq) - h0 : 0, min(a.chunk, a.Hq), mine, 256 * 4);
+  }
+  if (a.Hk) {
+    const Turn tk = turn_of(sn, cs, lane_gain<INTER>(a.nr.k_gain, m));
+    const int k0 = max(h0, a.Hq);
+    turn_heads<T, D, INTER>(a.nr, m, tk, a.k.at(b, t, k0 - a.Hq), a.k.sh, a.ko.at(b, t, k0 - a.Hq), a.ko.sh,
+                            on ? h1 - k0 : 0, min(a.chunk, a.Hk), mine, 256 * 4);
   }
 }
 
@@ -96,14 +122,6 @@ struct AppendArgs {
 
 constexpr int kPasses = 8;  // rows a lane group keeps in registers
 
-// Four elements from global to shared memory, asynchronously.
-template <typename T>
-__device__ __forceinline__ void copy4_async(T* to, const T* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
-               "n"(4 * sizeof(T))
-               : "memory");
-}
-
 // What a CTA writes at a time: one side and head of one block.
 struct Piece {
   int b, h, side, bj, blk, lo, hi, start;  // rows lo..hi-1 of the block; hi <= lo: none
@@ -113,14 +131,14 @@ struct Piece {
 // into shared memory (each thread its own elements, so only it waits) while
 // this one's are turned, kept in registers between the maximum and the codes,
 // and written.  CTAs past kv_ctas turn the queries.
-template <typename T, int D, bool INT8>
+template <typename T, int D, bool INT8, bool INTER>
 __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ AppendArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
   constexpr float Q = INT8 ? 127.f : 448.f;
   extern __shared__ __align__(16) uint8_t stage_raw[];  // [2][kPasses][2][threads][4]
   __shared__ float red[2][8];
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS, rpp = blockDim.x / GS;
-  const LaneMap m = lane_map<D>(a.nr, l);
+  const LaneMap m = lane_map<D, INTER>(a.nr, l);
 
   if (blockIdx.x >= a.kv_ctas) {
     const int64_t g = (int64_t)(blockIdx.x - a.kv_ctas) * rpp + grp;
@@ -128,30 +146,12 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ Appen
     const bool live = token < (int64_t)a.B * a.T_;
     const int b = live ? (int)(token / a.T_) : 0, t = live ? (int)(token % a.T_) : 0;
     const int h0 = (int)(g % a.nchunk) * a.chunk;
-    float cs[4], sn[4], gq[8];
-    lane_angles(a.nr, m, l, live ? a.start[b] + t : 0, cs, sn);
-    lane_gain(a.nr.q_gain, m, gq);
-    const int n = live && m.used ? min(a.chunk, a.Hq - h0) : 0;
-    for (int i0 = 0; i0 < a.chunk; i0 += kBatch) {
-      float x[kBatch][8];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
-        if (i0 + i < n) {
-          load4(a.q.at(b, t, h0 + i0 + i) + m.e0, x[i]);
-          load4(a.q.at(b, t, h0 + i0 + i) + m.e1, x[i] + 4);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        norm_rotate<D>(a.nr, m, gq, x[i], cs, sn);
-        if (i0 + i < n) {
-          store4(a.qo.at(b, t, h0 + i0 + i) + m.e0, x[i]);
-          store4(a.qo.at(b, t, h0 + i0 + i) + m.e1, x[i] + 4);
-        }
-      }
-    }
+    float sn[4], cs[4];
+    lane_angles(a.nr, m, l, live ? a.start[b] + t : 0, sn, cs);
+    const Turn tq = turn_of(sn, cs, lane_gain<INTER>(a.nr.q_gain, m));
+    turn_heads<T, D, INTER>(a.nr, m, tq, a.q.at(b, t, h0), a.q.sh, a.qo.at(b, t, h0), a.qo.sh,
+                            live && m.used ? min(a.chunk, a.Hq - h0) : 0, a.chunk,
+                            reinterpret_cast<T*>(stage_raw) + threadIdx.x * 4, blockDim.x * 4);
     return;
   }
 
@@ -200,11 +200,10 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ Appen
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
-  float gk[8];
-  lane_gain(a.has_nr ? a.nr.k_gain : nullptr, m, gk);
+  const LaneGain gk = lane_gain<INTER>(a.has_nr ? a.nr.k_gain : nullptr, m);
   Piece cur = piece_of(blockIdx.x);
   fetch(cur, 0);
-  int buf = 0, turn_of = 0;  // `red` alternates over the pieces that use it
+  int buf = 0, red_of = 0;  // `red` alternates over the pieces that use it
   for (int it = blockIdx.x; it < a.pieces; it += a.kv_ctas, buf ^= 1) {
     Piece nxt = cur;
     if (it + a.kv_ctas < a.pieces) {
@@ -236,23 +235,26 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ Appen
           load4(from + (2 * p + 1) * step, x[p] + 4);
         }
         if (turn && lo + p * rpp < hi) {  // uniform over the CTA
-          float cs[4], sn[4];
-          lane_angles(a.nr, m, l, cur.bj * a.c.bt + r, cs, sn);
-          norm_rotate<D>(a.nr, m, gk, x[p], cs, sn);
+          float sn[4], cs[4];
+          lane_angles(a.nr, m, l, cur.bj * a.c.bt + r, sn, cs);
+          norm_rotate<D, INTER>(a.nr, turn_of(sn, cs, gk), x[p]);
         }
-        float big = 0.f;
+        float big = 0.f, all = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[p][i]));
-        bool odd = !(big <= FLT_MAX);  // a NaN alone does not show in a maximum
-#pragma unroll
-        for (int i = 0; i < 8; ++i) odd |= x[p][i] != x[p][i];
-        if (odd && on) {  // NaN -> 0; an infinity saturates
-          bad = true;
+        for (int i = 0; i < 8; ++i) {
+          big = fmaxf(big, fabsf(x[p][i]));
+          all += x[p][i];
+        }
+        if (!(fabsf(all) <= FLT_MAX) && on) {  // a NaN or an infinity (or a sum past the range)
           big = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if (fabsf(x[p][i]) <= FLT_MAX) big = fmaxf(big, fabsf(x[p][i]));
-            else x[p][i] = isnan(x[p][i]) ? 0.f : copysignf(FLT_MAX, x[p][i]);
+            if (fabsf(x[p][i]) <= FLT_MAX) {
+              big = fmaxf(big, fabsf(x[p][i]));
+            } else {  // NaN -> 0; an infinity saturates
+              bad = true;
+              x[p][i] = isnan(x[p][i]) ? 0.f : copysignf(FLT_MAX, x[p][i]);
+            }
           }
         }
         if (on) top = fmaxf(top, big);
@@ -260,13 +262,13 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ Appen
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
       if (blockDim.x > 32) {
-        if ((threadIdx.x & 31) == 0) red[turn_of][threadIdx.x >> 5] = top;
+        if ((threadIdx.x & 31) == 0) red[red_of][threadIdx.x >> 5] = top;
         __syncthreads();  // also: every thread has read the old scale
-        for (int w = 0; w < (int)blockDim.x / 32; ++w) top = fmaxf(top, red[turn_of][w]);
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) top = fmaxf(top, red[red_of][w]);
       } else {
         __syncwarp();
       }
-      turn_of ^= 1;
+      red_of ^= 1;
       float s1 = fmaxf(s0, __fdiv_rn(top, Q));
       if (s1 < FLT_MIN) s1 = 0.f;  // 1 / s1 stays finite
       const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
@@ -487,7 +489,8 @@ zg_status zg_qk_norm_rope(const zg_norm_rope* nr, const zg_rows* q, const zg_row
     const RotateArgs<E> a = {rows_of<E>(q), rows_of<E>(k), rows_of<E>(q_out), rows_of<E>(k_out), positions,
                              B, T, Hq, Hk, chunk, nchunk, na};
     for_dim(dim, [&](auto dv) {
-      k_norm_rope<E, decltype(dv)::value><<<(unsigned)ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      auto kern = na.inter ? k_norm_rope<E, decltype(dv)::value, true> : k_norm_rope<E, decltype(dv)::value, false>;
+      kern<<<(unsigned)ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
     });
   });
   return after_launch("norm and rotation launch");
@@ -540,7 +543,9 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
                              chunk, nchunk, nr != nullptr, na};
     for_dim(cache->dim, [&](auto dv) {
       constexpr int D = decltype(dv)::value;
-      auto kern = cache->format == ZG_KV_INT8 ? k_kv_append<E, D, true> : k_kv_append<E, D, false>;
+      auto kern = cache->format == ZG_KV_INT8
+                      ? (na.inter ? k_kv_append<E, D, true, true> : k_kv_append<E, D, true, false>)
+                      : (na.inter ? k_kv_append<E, D, false, true> : k_kv_append<E, D, false, false>);
       if (smem > 48 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (err == cudaSuccess) kern<<<(unsigned)(kv + qc), threads, smem, static_cast<cudaStream_t>(stream)>>>(a);
     });
