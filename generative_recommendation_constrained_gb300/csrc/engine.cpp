@@ -638,14 +638,17 @@ cudaError_t current_context_id(unsigned long long* id) {
       get_id = reinterpret_cast<GetId>(p);
   });
   if (!get_current || !get_id) return cudaErrorNotSupported;
-  // make the runtime's primary context of the current device current on this
-  // thread (cudaSetDevice initialises it; nothing is allocated)
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaSetDevice(dev);
-  if (e != cudaSuccess) return e;
   void* ctx = nullptr;
-  if (get_current(&ctx) != 0 || !ctx) return cudaErrorDeviceUninitialized;
+  if (get_current(&ctx) != 0 || !ctx) {
+    // make the runtime's primary context of the current device current on this
+    // thread (cudaSetDevice initialises it; nothing is allocated).  Only where
+    // there is none: the call takes longer than a launch
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return e;
+    if (get_current(&ctx) != 0 || !ctx) return cudaErrorDeviceUninitialized;
+  }
   if (get_id(ctx, id) != 0) return cudaErrorDeviceUninitialized;
   return cudaSuccess;
 }

@@ -81,9 +81,10 @@ struct Tile16 {
     copy_async<4>(at + 4 * kThreadsOf + 4 * tid, vs);
   }
   static constexpr int kThreadsOf = 128;
-  uint32_t k[2][KW], v[4][VW];
-  float ks, vs;
-  __device__ __forceinline__ void read(const uint8_t* at, int tid) {
+  static constexpr int kValuesAt = 2 * KB * kThreadsOf, kScalesAt = (2 * KB + 4 * VB) * kThreadsOf;
+  static __device__ __forceinline__ void read_keys(const uint8_t* at, int tid, uint32_t (&k)[2][KW], float& ks, float& vs) {
+    ks = *reinterpret_cast<const float*>(at + kScalesAt + 4 * tid);
+    vs = *reinterpret_cast<const float*>(at + kScalesAt + 4 * kThreadsOf + 4 * tid);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
 #pragma unroll
@@ -94,6 +95,9 @@ struct Tile16 {
         at += 8 * kThreadsOf;
       }
     }
+  }
+  static __device__ __forceinline__ void read_values(const uint8_t* at, int tid, uint32_t (&v)[4][VW]) {
+    at += kValuesAt;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -102,8 +106,6 @@ struct Tile16 {
         else if constexpr (kVal == 8) *reinterpret_cast<uint2*>(v[j]) = *reinterpret_cast<const uint2*>(at + 8 * tid);
         else v[j][i] = *reinterpret_cast<const uint32_t*>(at + 4 * tid);
       }
-    ks = *reinterpret_cast<const float*>(at + 4 * tid);
-    vs = *reinterpret_cast<const float*>(at + 4 * kThreadsOf + 4 * tid);
   }
   // nothing there: a block outside the cache
   static __device__ __forceinline__ void clear(uint8_t* at, int tid) {
@@ -131,19 +133,19 @@ struct Tile16 {
 
 // Dynamic shared memory of k_attn_few: the ring of tiles, then (in its place)
 // the warps' sums.
-constexpr int kFewAhead = 3;  // tiles a warp has in its ring
+constexpr int kFewTiles = 4;  // tiles a warp has in its ring: two steps
 template <int D, int NT>
 constexpr int few_smem() {
-  const int ring = kFewAhead * Tile16<D>::kBytes * kFewThreads, sums = 4 * 8 * NT * (D + 2) * 4;
+  const int ring = kFewTiles * Tile16<D>::kBytes * kFewThreads, sums = 4 * 8 * NT * (D + 2) * 4;
   return ring > sums ? ring : sums;
 }
 
-// Keys go to the CTAs of k_attn_few by the unit of 64 (a tile a warp), all
+// Keys go to the CTAs of k_attn_few by the unit of 128 (a step a warp), all
 // items (request, key head, 8 NT rows) in a row and the same share for each
 // CTA, however the histories' lengths differ: an item may lie in several CTAs
 // (the join adds their parts up), and a CTA may hold the end of one item,
 // whole ones and the beginning of another.
-constexpr int kUnit = 64;
+constexpr int kUnit = 128;
 __device__ __forceinline__ int item_keys(const AttnArgs& a, const Seen& s, int m, int nr) {
   // later rows see no less: the item sees what its last row does, or its request's last
   const int last = min(min(m * nr + nr, a.R * a.G) - 1, s.rows * a.G - 1);
@@ -160,106 +162,119 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, i
 }
 
 // Few query rows: a row is (token, query head of the group).  Each warp walks
-// its own 16-key tiles, brought by asynchronous copies in the order of the
-// matrix fragments, two tiles ahead (in registers, one ahead, 12 warps an SM had
-// 4.2 TB/s of loads in flight).  Keys and dims are the
+// its own keys, two tiles of 16 a step (a tile a step left the warps waiting
+// for their own shuffles and products), brought by asynchronous copies in the
+// order of the matrix fragments one step ahead.  Keys and dims are the
 // long side of the products (S^T = K Q^T, O^T = V^T P^T), so that eight rows
 // fill an instruction that sixteen keys or dims by eight rows make.
 template <typename T, int D, bool INT8, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_attn_few(const __grid_constant__ AttnArgs a, const Rows<T> q,
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const __grid_constant__ AttnArgs a, const Rows<T> q,
                                                           const Rows<T> out) {
   using Tl = Tile16<D>;
   constexpr int KW = Tl::KW, VW = Tl::VW, NR = 8 * NT;
   __shared__ float sm_m[4][NR], sm_l[4][NR];
-  extern __shared__ __align__(16) uint8_t ring[];  // [kFewAhead] tiles; then float [4][NR][D + 2]
+  extern __shared__ __align__(16) uint8_t ring[];  // [kFewTiles] tiles; then float [4][NR][D + 2]
   auto sm_o = reinterpret_cast<float (*)[NR][D + 2]>(ring);
   __shared__ int sm_sum[4], sm_b, sm_first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int M = a.R * a.G;
 
-  // every request's units, their sum, and the request in which this CTA's share begins
-  int total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    const int begin = pass ? (int)((int64_t)blockIdx.x * ((total + gridDim.x - 1) / gridDim.x)) : 0;
-    int before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kFewThreads) {
-      const int b = b0 + threadIdx.x;
-      int n = 0;
-      if (b < a.B) n = request_units(a, seen_of(a, b, pass == 0 && blockIdx.x == 0), NR);
-      int x = n;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be put in place; it waits
+
+  // every request's units, their sum, and the request in which this CTA's share begins (a thread a request; over
+  // again for the second only where there are more requests than threads)
+  int total = 0, n = 0, before = 0;  // of the thread's request
+  auto scan = [&](int b0, bool report) -> int {
+    const int b = b0 + threadIdx.x;
+    n = b < a.B ? request_units(a, seen_of(a, b, report), NR) : 0;
+    int x = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) sm_sum[warp] = x;
-      __syncthreads();
-      int all = 0;
-      for (int w = 0; w < 4; ++w) {
-        if (w < warp) x += sm_sum[w];
-        all += sm_sum[w];
-      }
-      const int first = before + x - n;
-      if (pass) {
-        if (b < a.B && first <= begin && begin < first + n) {
-          sm_b = b;
-          sm_first = first;
-        }
-        if (blockIdx.x == 0 && b < a.B && a.prefix) {
-          a.prefix[b] = first;
-          if (b == a.B - 1) a.prefix[a.B] = first + n;
-        }
-      }
-      before += all;
-      __syncthreads();
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
     }
-    total = before;
+    if (lane == 31) sm_sum[warp] = x;
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < 4; ++w) {
+      if (w < warp) x += sm_sum[w];
+      all += sm_sum[w];
+    }
+    before = x - n;
+    return all;
+  };
+  for (int b0 = 0; b0 < a.B; b0 += kFewThreads) {
+    if (b0) __syncthreads();
+    total += scan(b0, blockIdx.x == 0);
   }
   const int share = (total + gridDim.x - 1) / gridDim.x;
   int u = blockIdx.x * share;
   const int u_end = min(total, u + share);
   if (u >= u_end) return;
+  int sum = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kFewThreads) {
+    int all = total;
+    if (a.B > kFewThreads) {
+      __syncthreads();
+      all = scan(b0, false);
+    }
+    if (sum + before <= u && u < sum + before + n) {
+      sm_b = b0 + threadIdx.x;
+      sm_first = sum + before;
+    }
+    sum += all;
+  }
+  __syncthreads();
   int b = sm_b, first = sm_first;  // `first`: units before request b, then before the item
   Seen s = seen_of(a, b, false);
-  // the item: (head, rows), units one row of items after the other
-  int h = 0, m = 0, units = item_units(a, s, 0, NR);
+  // the item: (head, rows)
+  const int per_head = request_units(a, s, NR) / a.heads;
+  int h = (u - first) / per_head, m = 0, units = item_units(a, s, 0, NR);
+  first += h * per_head;
   while (first + units <= u) {
     first += units;
-    if (++m == a.mt) m = 0, ++h;
-    units = item_units(a, s, m, NR);
+    units = item_units(a, s, ++m, NR);
   }
 
   while (u < u_end) {
     const int vmax = item_keys(a, s, m, NR);
     const int v_end = min(u_end, first + units);  // units [u, v_end) of this item are ours
-    const int t0 = (u - first) * (kUnit / 16) + warp, t1 = min((vmax + 15) / 16, (v_end - first) * (kUnit / 16));
+    // steps of 32 keys, in turn to the warps
+    const int t0 = (u - first) * (kUnit / 32) + warp, t1 = min((vmax + 31) / 32, (v_end - first) * (kUnit / 32));
     const bool whole = u == first && v_end == first + units;
     const int slot = 2 * blockIdx.x + (u > (int)blockIdx.x * share ? 1 : 0);
+    if (a.info && u == first && threadIdx.x == 0)  // for the join: the item's first slot, and in how many CTAs it lies
+      a.info[((int64_t)b * a.heads + h) * a.mt + m] = make_int2(slot, (first + units - 1) / share - blockIdx.x + 1);
 
-    auto block_of = [&](int t) -> int {
-      if (t >= t1) return -1;
-      const int blk = a.table[(int64_t)b * a.max_blocks + t * 16 / a.bt];
+    auto block_of = [&](int t, int half) -> int {
+      const int key = t * 32 + half * 16;
+      if (t >= t1 || key >= vmax) return -1;
+      const int blk = a.table[(int64_t)b * a.max_blocks + (key >> a.bt_log2)];
       if (blk >= 0 && blk < a.n_blocks) return blk;
       if (lane == 0) atomicOr(a.status, kStatusCache);
       return -1;
     };
-    // tile t into its slot; one group a call
-    auto fetch = [&](int t, int slot_of, int blk) {
+    // the two tiles of step t into their slot; one group a call
+    auto fetch = [&](int t, int slot_of, int b0, int b1) {
       if (t < t1) {
-        uint8_t* at = ring + slot_of * (Tl::kBytes * kFewThreads);
-        if (blk < 0) {
-          Tl::clear(at, threadIdx.x);
-        } else {
-          const int64_t bh = (int64_t)blk * a.heads + h, from = (bh * a.bt + t * 16 % a.bt) * D;
-          Tl::fetch(smem_addr(at), threadIdx.x, a.kc + from, a.vc + from, a.ks + bh, a.vs + bh, g, c);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int blk = half ? b1 : b0;
+          uint8_t* at = ring + (2 * slot_of + half) * (Tl::kBytes * kFewThreads);
+          if (blk < 0) {
+            Tl::clear(at, threadIdx.x);
+          } else {
+            const int64_t bh = (int64_t)blk * a.heads + h, from = (bh * a.bt + ((t * 32 + half * 16) & (a.bt - 1))) * D;
+            Tl::fetch(smem_addr(at), threadIdx.x, a.kc + from, a.vc + from, a.ks + bh, a.vs + bh, g, c);
+          }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const int blk0 = block_of(t0), blk1 = block_of(t0 + 4);
-    int blk2 = block_of(t0 + 8);
-    fetch(t0, 0, blk0);
-    fetch(t0 + 4, 1, blk1);
+    int b0 = block_of(t0, 0), b1 = block_of(t0, 1);
+    const int b0n = block_of(t0 + 4, 0), b1n = block_of(t0 + 4, 1);
+    fetch(t0, 0, b0, b1);
+    b0 = b0n, b1 = b1n;
 
     // the rows: lane (g, c) the dims of its words of row g; then the sight and the scale of rows 2c, 2c + 1
     uint32_t qb[NT][KW][2];
@@ -308,45 +323,64 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_attn_few(const
         for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
     }
 
-    int ahead = 2;  // the slot of t + 8
-    for (int t = t0; t < t1; t += 4) {
-      const int blk3 = block_of(t + 12);
-      fetch(t + 8, ahead, blk2);
-      ahead = ahead == kFewAhead - 1 ? 0 : ahead + 1;  // the slot of t + 12, which is the slot of t
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-      Tl cur;
-      cur.read(ring + ahead * (Tl::kBytes * kFewThreads), threadIdx.x);
-      const int key0 = t * 16;
-      float z[NT][4];
+    int slot_of = 0;
+    for (int t = t0; t < t1; t += 4, slot_of ^= 1) {
+      const int b0n = block_of(t + 8, 0), b1n = block_of(t + 8, 1);
+      fetch(t + 4, slot_of ^ 1, b0, b1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      const uint8_t* tiles = ring + 2 * slot_of * (Tl::kBytes * kFewThreads);
+      const int key0 = t * 32;
+      float z[2][NT][4], lv[2], iv[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t k[2][KW];
+        float ks, vs;
+        Tl::read_keys(tiles + half * (Tl::kBytes * kFewThreads), threadIdx.x, k, ks, vs);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[half][n][j] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t ka[4];
+          codes_half4<INT8>(k[0][w], ka[0], ka[2]);
+          codes_half4<INT8>(k[1][w], ka[1], ka[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_16816(z[half][n], ka, qb[n][w][0], qb[n][w][1]);
+        }
+        lv[half] = scale_log2(vs);
+        iv[half] = exp2_fast(-lv[half]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f = fz[n][e] * ks;
+            z[half][n][e] = fmaf(z[half][n][e], f, lv[half]);
+            z[half][n][2 + e] = fmaf(z[half][n][2 + e], f, lv[half]);
+          }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) z[n][k] = 0.f;
+        for (int e = 0; e < 2; ++e)
+          if (key0 + 32 > vis[n][e]) {  // keys that the row does not see
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        uint32_t ka[4];
-        codes_half4<INT8>(cur.k[0][w], ka[0], ka[2]);
-        codes_half4<INT8>(cur.k[1][w], ka[1], ka[3]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma_16816(z[n], ka, qb[n][w][0], qb[n][w][1]);
-      }
-      const float ks = cur.ks, lv = scale_log2(cur.vs), iv = exp2_fast(-lv);
-      uint32_t pb[NT][2];
+            for (int j = 0; j < 4; ++j)
+              if (key0 + 16 * (j >> 1) + 8 * (j & 1) + g >= vis[n][e]) z[j >> 1][n][2 * (j & 1) + e] = -INFINITY;
+          }
+      uint32_t pb[2][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        // whether any score passes the reference: each lane asks for its own, the largest is found only then
         float tm[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float f = fz[n][e] * ks;
-          z[n][e] = key0 + g < vis[n][e] ? fmaf(z[n][e], f, lv) : -INFINITY;
-          z[n][2 + e] = key0 + g + 8 < vis[n][e] ? fmaf(z[n][2 + e], f, lv) : -INFINITY;
-          tm[e] = fmaxf(z[n][e], z[n][2 + e]);
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xFFFFFFFFu, tm[e], x));
-        }
+        for (int e = 0; e < 2; ++e)
+          tm[e] = fmaxf(fmaxf(z[0][n][e], z[0][n][2 + e]), fmaxf(z[1][n][e], z[1][n][2 + e]));
         if (__any_sync(0xFFFFFFFFu, tm[0] > mx[n][0] + 8.f || tm[1] > mx[n][1] + 8.f)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xFFFFFFFFu, tm[e], x));
             const float nm = fmaxf(mx[n][e], tm[e]);
             const float f = mx[n][e] == -INFINITY ? 0.f : exp2_fast(mx[n][e] - nm);
             mx[n][e] = nm;
@@ -358,39 +392,47 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_attn_few(const
             }
           }
         }
-        float p[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mu = mx[n][e] == -INFINITY ? 0.f : mx[n][e];
-          p[e] = exp2_fast(z[n][e] - mu);
-          p[2 + e] = exp2_fast(z[n][2 + e] - mu);
-          l[n][e] = fmaf(p[e] + p[2 + e], iv, l[n][e]);
-        }
-        pb[n][0] = transpose8(pack_half2(p[0], p[1]));  // (key, rows) -> (row, keys)
-        pb[n][1] = transpose8(pack_half2(p[2], p[3]));
-      }
-      if (key0 + 16 > s.len) {  // behind the history: not defined, may be NaN
+        for (int half = 0; half < 2; ++half) {
+          float p[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (key0 + 2 * c + (j & 1) + (j >> 1) * 8 >= s.len)
-#pragma unroll
-            for (int u = 0; u < VW; ++u) cur.v[j][u] = 0;
-      }
-#pragma unroll
-      for (int u = 0; u < VW; ++u) {
-        uint32_t x[4], y[4];  // of four dims: keys 2c, 2c + 1, and 8 on
-        codes_half4<INT8>(__byte_perm(cur.v[0][u], cur.v[1][u], 0x5140), x[0], x[1]);
-        codes_half4<INT8>(__byte_perm(cur.v[0][u], cur.v[1][u], 0x7362), x[2], x[3]);
-        codes_half4<INT8>(__byte_perm(cur.v[2][u], cur.v[3][u], 0x5140), y[0], y[1]);
-        codes_half4<INT8>(__byte_perm(cur.v[2][u], cur.v[3][u], 0x7362), y[2], y[3]);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t va[4] = {x[2 * v], x[2 * v + 1], y[2 * v], y[2 * v + 1]};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_16816(o[n][2 * u + v], va, pb[n][0], pb[n][1]);
+          for (int e = 0; e < 2; ++e) {
+            const float mu = mx[n][e] == -INFINITY ? 0.f : mx[n][e];
+            p[e] = exp2_fast(z[half][n][e] - mu);
+            p[2 + e] = exp2_fast(z[half][n][2 + e] - mu);
+            l[n][e] = fmaf(p[e] + p[2 + e], iv[half], l[n][e]);
+          }
+          pb[half][n][0] = transpose8(pack_half2(p[0], p[1]));  // (key, rows) -> (row, keys)
+          pb[half][n][1] = transpose8(pack_half2(p[2], p[3]));
         }
       }
-      blk2 = blk3;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t vw[4][VW];
+        Tl::read_values(tiles + half * (Tl::kBytes * kFewThreads), threadIdx.x, vw);
+        if (key0 + 16 * half + 16 > s.len) {  // behind the history: not defined, may be NaN
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (key0 + 16 * half + 2 * c + (j & 1) + (j >> 1) * 8 >= s.len)
+#pragma unroll
+              for (int w = 0; w < VW; ++w) vw[j][w] = 0;
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          uint32_t x[4], y[4];  // of four dims: keys 2c, 2c + 1, and 8 on
+          codes_half4<INT8>(__byte_perm(vw[0][w], vw[1][w], 0x5140), x[0], x[1]);
+          codes_half4<INT8>(__byte_perm(vw[0][w], vw[1][w], 0x7362), x[2], x[3]);
+          codes_half4<INT8>(__byte_perm(vw[2][w], vw[3][w], 0x5140), y[0], y[1]);
+          codes_half4<INT8>(__byte_perm(vw[2][w], vw[3][w], 0x7362), y[2], y[3]);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint32_t va[4] = {x[2 * v], x[2 * v + 1], y[2 * v], y[2 * v + 1]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_16816(o[n][2 * w + v], va, pb[half][n][0], pb[half][n][1]);
+          }
+        }
+      }
+      b0 = b0n, b1 = b1n;
     }
 
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -474,37 +516,31 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
   const int64_t br = w / a.Hq;
   const int r = (int)(br % a.R), b = (int)(br / a.R);
   const int i = r * a.G + qh % a.G, m = i / a.tile;
-  const Seen s = seen_of(a, b, false);
-  int parts, cta = 0, later = 0;  // few rows: the first CTA that has some of the item, and whether it has other items first
-  int64_t slot0 = 0, step = 1;
-  if (a.prefix) {
+  const int64_t item = ((int64_t)b * a.heads + qh / a.G) * a.mt + m;
+  int parts;
+  int64_t slot0, later, step;  // slots of the parts: slot0, then later + step, later + 2 step, ...
+  if (a.info) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int h = qh / a.G, share = (a.prefix[a.B] + a.ctas - 1) / a.ctas;
-    int i0 = a.prefix[b] + request_units(a, s, a.tile) / a.heads * h, units = 0;
-    for (int j = 0; j <= m; ++j) {
-      i0 += units;
-      units = item_units(a, s, j, a.tile);
-    }
-    cta = i0 / share;
-    later = i0 > cta * share;
-    parts = (i0 + units - 1) / share - cta + 1;
-    slot0 = 2 * cta, step = 2;
+    const int2 e = a.info[item];
+    parts = e.y;
+    slot0 = e.x, later = e.x & ~1, step = 2;
   } else {
+    const Seen s = seen_of(a, b, false);
     const int last = min(min((m + 1) * a.tile, a.R * a.G) - 1, s.rows * a.G - 1);
     parts = parts_of(a, last < m * a.tile ? 0 : visible(a, s, last / a.G));
-    slot0 = (((int64_t)b * a.heads + qh / a.G) * a.mt + m) * a.splits;
+    slot0 = later = item * a.splits, step = 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
   if (parts <= 1) return;
   const float* ml = a.part + a.slots * a.tile * D;
-  auto row_of = [&](int sp) -> int64_t { return (slot0 + sp * step + (sp == 0 ? later : 0)) * a.tile + i % a.tile; };
+  auto row_of = [&](int sp) -> int64_t { return (sp ? later + sp * step : slot0) * a.tile + i % a.tile; };
   float top = -INFINITY;
   for (int sp = lane; sp < parts; sp += 32) top = fmaxf(top, ml[row_of(sp) * 2]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   float sum = 0.f, x[4] = {};
   if (top != -INFINITY && lane < kLanes) {
-#pragma unroll 4
+#pragma unroll 8
     for (int sp = 0; sp < parts; ++sp) {
       const int64_t pi = row_of(sp);
       const float2 e = *reinterpret_cast<const float2*>(ml + pi * 2);
@@ -555,11 +591,11 @@ AttnPlan attn_plan(const zg_kv_cache* c, int max_blocks, int B, int R, int Hq) {
     p.splits = (int)((keys + p.chunk - 1) / p.chunk);
     p.slots = p.splits > 1 ? p.items * p.splits : 0;
   } else {
-    const int resident = p.tile == 16 ? 2 : 4;
-    p.ctas = (int)std::min<int64_t>((int64_t)sm_count() * resident, p.items * ((keys + 63) / 64));
-    p.slots = p.ctas > 1 && keys > 64 ? 2 * (int64_t)p.ctas : 0;
+    const int resident = p.tile == 16 ? 2 : 3;
+    p.ctas = (int)std::min<int64_t>((int64_t)sm_count() * resident, p.items * ((keys + 127) / 128));
+    p.slots = p.ctas > 1 && keys > 128 ? 2 * (int64_t)p.ctas : 0;
   }
-  p.bytes = p.slots ? ((size_t)p.slots * p.tile * (c->dim + 2) + B + 1) * 4 : 0;
+  p.bytes = p.slots ? ((size_t)p.slots * p.tile * (c->dim + 2) + (p.tc ? 0 : 2 * p.items)) * 4 : 0;
   return p;
 }
 
@@ -609,8 +645,8 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   const AttnPlan p = attn_plan(cache, max_blocks, B, R, Hq);
   if (p.bytes && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < p.bytes))
     return bad_arg(call, "workspace must hold zg_kv_attention_workspace_size bytes, 256-byte aligned");
-  if (p.items * std::max<int64_t>(p.tc ? p.splits : ((int64_t)max_blocks * cache->block_tokens + 63) / 64, 1) > 0x7FFFFFFF)
-    return fail(ZG_ERR_UNSUPPORTED, "zg_kv_attention: more than 2^31 units of work (B * Hq * keys of a table / 64)");
+  if (p.items * std::max<int64_t>(p.tc ? p.splits : ((int64_t)max_blocks * cache->block_tokens + 127) / 128, 1) > 0x7FFFFFFF)
+    return fail(ZG_ERR_UNSUPPORTED, "zg_kv_attention: more than 2^31 units of work (B * heads * keys of a table / 128)");
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
   AttnArgs a = {};
@@ -627,6 +663,7 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   a.n_blocks = cache->n_blocks;
   a.heads = cache->heads;
   a.bt = cache->block_tokens;
+  while ((1 << a.bt_log2) < a.bt) ++a.bt_log2;
   a.max_blocks = max_blocks;
   a.B = B;
   a.R = R;
@@ -637,7 +674,8 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   a.splits = p.splits;
   a.ctas = p.ctas;
   a.slots = p.slots;
-  if (!p.tc && p.slots) a.prefix = static_cast<int32_t*>(workspace) + (size_t)p.slots * p.tile * (cache->dim + 2);
+  if (!p.tc && p.slots)  // an even count of floats: 8-byte aligned
+    a.info = reinterpret_cast<int2*>(a.part + (size_t)p.slots * p.tile * (cache->dim + 2));
   a.chunk = p.chunk;
   a.causal = causal != 0;
   a.scale = scale * 1.4426950408889634f;

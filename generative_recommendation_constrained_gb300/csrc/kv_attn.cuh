@@ -13,8 +13,8 @@ struct AttnArgs {
   float* lse;
   float* part;      // [slot][tile][D] outputs, then [slot][tile][2] (max, sum)
   int64_t slots;    // many rows: item * splits + part; few rows: two a CTA
-  int32_t* prefix;  // few rows: [B + 1] units before each request
-  int32_t n_blocks, heads, bt, max_blocks;
+  int2* info;       // few rows: each item's first slot and number of parts
+  int32_t n_blocks, heads, bt, bt_log2, max_blocks;
   int32_t B, R, Hq, G, splits, ctas, causal;
   int32_t tile, mt;  // query rows an item (power of two), such items a (request, key head)
   int32_t chunk;     // keys of a part, a multiple of 64

@@ -44,9 +44,10 @@ __device__ __forceinline__ void turn_heads(const NormRopeArgs& a, const LaneMap&
   auto fetch = [&](int i) {
     if (i < n) {
       T* s = ring + (i % kAhead) * 2 * step;
-      copy4_async(s, from + i * from_step);
-      copy4_async(s + step, from + i * from_step + d);
+      copy4_async(s, from);
+      copy4_async(s + step, from + d);
     }
+    from += from_step;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
@@ -62,9 +63,10 @@ __device__ __forceinline__ void turn_heads(const NormRopeArgs& a, const LaneMap&
     }
     norm_rotate<D, INTER>(a, t, x);
     if (i < n) {
-      store4(to + i * to_step, x);
-      store4(to + i * to_step + d, x + 4);
+      store4(to, x);
+      store4(to + d, x + 4);
     }
+    to += to_step;
   }
 }
 
@@ -188,19 +190,21 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ Appen
   auto fetch = [&](const Piece& p, int buf) {
     const Rows<T>& src = p.side ? a.v : a.k;
     T* to = reinterpret_cast<T*>(stage_raw) + buf * kPasses * 2 * step + threadIdx.x * 4;
+    const T* s = src.at(p.b, p.bj * a.c.bt + p.lo + grp - p.start, p.h) + m.e0;
+    const int64_t down = rpp * src.st;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int r = p.lo + i * rpp + grp;
-      if (m.used && r < p.hi) {
-        const T* s = src.at(p.b, p.bj * a.c.bt + r - p.start, p.h);
-        copy4_async(to + 2 * i * step, s + m.e0);
-        copy4_async(to + (2 * i + 1) * step, s + m.e1);
+    for (int i = 0; i < kPasses; ++i, s += down) {
+      if (m.used && p.lo + i * rpp + grp < p.hi) {
+        copy4_async(to + 2 * i * step, s);
+        copy4_async(to + (2 * i + 1) * step, s + (m.e1 - m.e0));
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   const LaneGain gk = lane_gain<INTER>(a.has_nr ? a.nr.k_gain : nullptr, m);
+  float ds[4], dc[4];
+  lane_angles(a.nr, m, l, rpp, ds, dc);
   Piece cur = piece_of(blockIdx.x);
   fetch(cur, 0);
   int buf = 0, red_of = 0;  // `red` alternates over the pieces that use it
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ Appen
       const bool turn = !cur.side && a.has_nr;
       const float s0 = lo ? *scale : 0.f;
       const T* from = reinterpret_cast<const T*>(stage_raw) + buf * kPasses * 2 * step + threadIdx.x * 4;
-      float x[kPasses][8];
+      float x[kPasses][8], sn[4], cs[4];
       float top = 0.f;
       bool bad = false;
 #pragma unroll
@@ -235,8 +239,17 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ Appen
           load4(from + (2 * p + 1) * step, x[p] + 4);
         }
         if (turn && lo + p * rpp < hi) {  // uniform over the CTA
-          float sn[4], cs[4];
-          lane_angles(a.nr, m, l, cur.bj * a.c.bt + r, sn, cs);
+          // rows rpp apart: the next angle by one complex product (at most 7 of them, each within 2^-23)
+          if (p == 0) {
+            lane_angles(a.nr, m, l, cur.bj * a.c.bt + r, sn, cs);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float s = sn[i] * dc[i] + cs[i] * ds[i];
+              cs[i] = cs[i] * dc[i] - sn[i] * ds[i];
+              sn[i] = s;
+            }
+          }
           norm_rotate<D, INTER>(a.nr, turn_of(sn, cs, gk), x[p]);
         }
         float big = 0.f, all = 0.f;
