@@ -37,106 +37,54 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 constexpr int kFewThreads = 128;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
-  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
-}
 
-// What one lane takes of 16 keys and values: of keys g and g + 8 (lane = 4 g +
-// c) the dims of `dim_of`, of values 2c, 2c + 1, 2c + 8, 2c + 9 the dims g * D/8
-// and on.  The order of the dims inside a product is free, so that a lane
-// reads neighbouring bytes and a warp whole rows.  It waits in shared memory,
-// each lane's own words apart: planes of N bytes a thread, thread after thread.
+// What one lane takes of 16 keys and values (rows of D codes in shared
+// memory): of keys g and g + 8 (lane = 4 g + c) the dims of `dim_of`, of values
+// 2c, 2c + 1, 2c + 8, 2c + 9 the dims g * D/8 and on.  The order of the dims
+// inside a product is free, so that a lane reads neighbouring bytes.
 template <int D>
 struct Tile16 {
-  static constexpr int KW = D / 16, VW = D / 32;           // words of a key, of a value
-  static constexpr int KB = 4 * KW, VB = 4 * VW;           // bytes
-  static constexpr int kKey16 = KB / 16, kKey8 = KB % 16 / 8;  // pieces of 16 and 8 bytes a key
-  static constexpr int kVal = D == 96 ? 4 : VB;            // bytes of a piece of a value
-  static constexpr int kBytes = 2 * KB + 4 * VB + 8;       // a lane, with the two scales
+  static constexpr int KW = D / 16, VW = D / 32;  // words of a key, of a value
+  static constexpr int kBytes = 16 * D;           // of the keys, of the values
   static __device__ __forceinline__ int dim_of(int w, int c) {
     return w < D / 64 * 4 ? w / 4 * 64 + 16 * c + 4 * (w % 4) : D / 64 * 64 + 8 * c + 4 * (w - D / 64 * 4);
   }
-  // `at`: the slot; `tid` of `threads`
-  static __device__ __forceinline__ void fetch(uint32_t at, int tid, const uint8_t* kp, const uint8_t* vp,
-                                               const float* ks, const float* vs, int g, int c) {
+  static __device__ __forceinline__ void keys(const uint8_t* at, int g, int c, uint32_t (&k)[2][KW]) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const uint8_t* p = kp + (n * 8 + g) * D;
-#pragma unroll
-      for (int i = 0; i < kKey16; ++i, at += 16 * kThreadsOf) copy_async<16>(at + 16 * tid, p + 64 * i + 16 * c);
-      if constexpr (kKey8 != 0) {
-        copy_async<8>(at + 8 * tid, p + D / 64 * 64 + 8 * c);
-        at += 8 * kThreadsOf;
+      const uint8_t* p = at + (n * 8 + g) * D;
+      if constexpr (D == 128) {
+        // rows of 128 bytes: odd rows read their halves the other way round, so that eight lanes meet all banks
+        const int o = (g & 1) * 64;
+        const uint4 x = *reinterpret_cast<const uint4*>(p + o + 16 * c);
+        const uint4 y = *reinterpret_cast<const uint4*>(p + (64 - o) + 16 * c);
+        *reinterpret_cast<uint4*>(&k[n][0]) = o ? y : x;
+        *reinterpret_cast<uint4*>(&k[n][4]) = o ? x : y;
+      } else {
+        if constexpr (D >= 64) *reinterpret_cast<uint4*>(&k[n][0]) = *reinterpret_cast<const uint4*>(p + 16 * c);
+        if constexpr (D % 64 != 0)
+          *reinterpret_cast<uint2*>(&k[n][D / 64 * 4]) = *reinterpret_cast<const uint2*>(p + D / 64 * 64 + 8 * c);
       }
     }
+  }
+  static __device__ __forceinline__ void values(const uint8_t* at, int g, int c, uint32_t (&v)[4][VW]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint8_t* p = vp + (2 * c + (j & 1) + (j >> 1) * 8) * D + g * (D / 8);
+      const uint8_t* p = at + (2 * c + (j & 1) + (j >> 1) * 8) * D + g * (D / 8);
+      if constexpr (D == 128) *reinterpret_cast<uint4*>(v[j]) = *reinterpret_cast<const uint4*>(p);
+      else if constexpr (D == 64) *reinterpret_cast<uint2*>(v[j]) = *reinterpret_cast<const uint2*>(p);
+      else
 #pragma unroll
-      for (int i = 0; i < VB / kVal; ++i, at += kVal * kThreadsOf) copy_async<kVal>(at + kVal * tid, p + i * kVal);
+        for (int w = 0; w < VW; ++w) v[j][w] = *reinterpret_cast<const uint32_t*>(p + 4 * w);
     }
-    copy_async<4>(at + 4 * tid, ks);
-    copy_async<4>(at + 4 * kThreadsOf + 4 * tid, vs);
-  }
-  static constexpr int kThreadsOf = 128;
-  static constexpr int kValuesAt = 2 * KB * kThreadsOf, kScalesAt = (2 * KB + 4 * VB) * kThreadsOf;
-  static __device__ __forceinline__ void read_keys(const uint8_t* at, int tid, uint32_t (&k)[2][KW], float& ks, float& vs) {
-    ks = *reinterpret_cast<const float*>(at + kScalesAt + 4 * tid);
-    vs = *reinterpret_cast<const float*>(at + kScalesAt + 4 * kThreadsOf + 4 * tid);
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-#pragma unroll
-      for (int i = 0; i < kKey16; ++i, at += 16 * kThreadsOf)
-        *reinterpret_cast<uint4*>(&k[n][4 * i]) = *reinterpret_cast<const uint4*>(at + 16 * tid);
-      if constexpr (kKey8 != 0) {
-        *reinterpret_cast<uint2*>(&k[n][4 * kKey16]) = *reinterpret_cast<const uint2*>(at + 8 * tid);
-        at += 8 * kThreadsOf;
-      }
-    }
-  }
-  static __device__ __forceinline__ void read_values(const uint8_t* at, int tid, uint32_t (&v)[4][VW]) {
-    at += kValuesAt;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < VB / kVal; ++i, at += kVal * kThreadsOf) {
-        if constexpr (kVal == 16) *reinterpret_cast<uint4*>(v[j]) = *reinterpret_cast<const uint4*>(at + 16 * tid);
-        else if constexpr (kVal == 8) *reinterpret_cast<uint2*>(v[j]) = *reinterpret_cast<const uint2*>(at + 8 * tid);
-        else v[j][i] = *reinterpret_cast<const uint32_t*>(at + 4 * tid);
-      }
-  }
-  // nothing there: a block outside the cache
-  static __device__ __forceinline__ void clear(uint8_t* at, int tid) {
-    // words of a lane are spread over planes of 16, 8 or 4 bytes: clear by the smallest
-    uint32_t w = 0;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-#pragma unroll
-      for (int i = 0; i < kKey16; ++i, at += 16 * kThreadsOf) *reinterpret_cast<uint4*>(at + 16 * tid) = make_uint4(w, w, w, w);
-      if constexpr (kKey8 != 0) {
-        *reinterpret_cast<uint2*>(at + 8 * tid) = make_uint2(w, w);
-        at += 8 * kThreadsOf;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < VB / kVal; ++i, at += kVal * kThreadsOf)
-#pragma unroll
-        for (int x = 0; x < kVal / 4; ++x) *reinterpret_cast<uint32_t*>(at + kVal * tid + 4 * x) = w;
-    *reinterpret_cast<uint32_t*>(at + 4 * tid) = w;
-    *reinterpret_cast<uint32_t*>(at + 4 * kThreadsOf + 4 * tid) = w;
   }
 };
 
-// Dynamic shared memory of k_attn_few: the ring of tiles, then (in its place)
-// the warps' sums.
-constexpr int kFewTiles = 4;  // tiles a warp has in its ring: two steps
+// Dynamic shared memory of k_attn_few: each warp's ring of two steps (two
+// tiles of keys, two of values each), then (in its place) the warps' sums.
 template <int D, int NT>
 constexpr int few_smem() {
-  const int ring = kFewTiles * Tile16<D>::kBytes * kFewThreads, sums = 4 * 8 * NT * (D + 2) * 4;
+  const int ring = 4 * 2 * 4 * Tile16<D>::kBytes, sums = 4 * 8 * NT * (D + 2) * 4;
   return ring > sums ? ring : sums;
 }
 
@@ -163,22 +111,45 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, i
 
 // Few query rows: a row is (token, query head of the group).  Each warp walks
 // its own keys, two tiles of 16 a step (a tile a step left the warps waiting
-// for their own shuffles and products), brought by asynchronous copies in the
-// order of the matrix fragments one step ahead.  Keys and dims are the
+// for their own shuffles and products), brought by bulk copies one step ahead
+// (16-byte copies a lane, in the order of the fragments, stopped at 4.9 TB/s
+// without any work behind them).  Keys and dims are the
 // long side of the products (S^T = K Q^T, O^T = V^T P^T), so that eight rows
 // fill an instruction that sixteen keys or dims by eight rows make.
+constexpr uint32_t kFewSpin = 1u << 20;  // polls of a wait at most
+__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, uint32_t limit) {
+  const uint32_t at = smem_addr(bar);
+  bool done = false;
+  for (uint32_t it = 0; it < limit && !done; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    done = ok;
+  }
+  return __all_sync(0xFFFFFFFFu, done);
+}
+
 template <typename T, int D, bool INT8, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const __grid_constant__ AttnArgs a, const Rows<T> q,
-                                                          const Rows<T> out) {
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const __grid_constant__ AttnArgs a,
+                                                                                const Rows<T> q, const Rows<T> out,
+                                                                                uint32_t spin) {
   using Tl = Tile16<D>;
   constexpr int KW = Tl::KW, VW = Tl::VW, NR = 8 * NT;
   __shared__ float sm_m[4][NR], sm_l[4][NR];
-  extern __shared__ __align__(16) uint8_t ring[];  // [kFewTiles] tiles; then float [4][NR][D + 2]
+  extern __shared__ __align__(128) uint8_t ring[];  // [warp][step][side][tile]; then float [4][NR][D + 2]
+  __shared__ uint64_t full[4][2];  // [warp][step]: its copies have landed
   auto sm_o = reinterpret_cast<float (*)[NR][D + 2]>(ring);
   __shared__ int sm_sum[4], sm_b, sm_first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int M = a.R * a.G;
 
+  if (threadIdx.x < 8) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[0][0] + threadIdx.x)));
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  uint32_t issued = 0, taken = 0;  // steps of this warp, over all its items
+  bool good = true;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be put in place; it waits
 
   // every request's units, their sum, and the request in which this CTA's share begins (a thread a request; over
@@ -254,27 +225,37 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       if (lane == 0) atomicOr(a.status, kStatusCache);
       return -1;
     };
-    // the two tiles of step t into their slot; one group a call
-    auto fetch = [&](int t, int slot_of, int b0, int b1) {
-      if (t < t1) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int blk = half ? b1 : b0;
-          uint8_t* at = ring + (2 * slot_of + half) * (Tl::kBytes * kFewThreads);
-          if (blk < 0) {
-            Tl::clear(at, threadIdx.x);
-          } else {
-            const int64_t bh = (int64_t)blk * a.heads + h, from = (bh * a.bt + ((t * 32 + half * 16) & (a.bt - 1))) * D;
-            Tl::fetch(smem_addr(at), threadIdx.x, a.kc + from, a.vc + from, a.ks + bh, a.vs + bh, g, c);
-          }
-        }
+    // the tiles of step t into the warp's next slot: lanes 0-3 a copy each, (half, side)
+    uint8_t* mine = ring + warp * (2 * 4 * Tl::kBytes);
+    auto fetch = [&](int t, int b0, int b1) {
+      if (t >= t1) return;
+      const uint32_t bar = smem_addr(&full[warp][issued & 1]);
+      const int blk = lane & 1 ? b1 : b0, key = t * 32 + (lane & 1) * 16;
+      const uint32_t bytes = ((b0 >= 0) + (b1 >= 0)) * 2 * Tl::kBytes;
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+      __syncwarp();
+      if (lane < 4 && blk >= 0) {
+        const int64_t from = (((int64_t)blk * a.heads + h) * a.bt + (key & (a.bt - 1))) * D;
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                smem_addr(mine + ((issued & 1) * 4 + lane) * Tl::kBytes)),
+            "l"((lane & 2 ? a.vc : a.kc) + from), "r"(Tl::kBytes), "r"(bar)
+            : "memory");
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++issued;
+    };
+    auto scales = [&](int blk, float& ks, float& vs) {
+      ks = blk < 0 ? 0.f : a.ks[(int64_t)blk * a.heads + h];
+      vs = blk < 0 ? 0.f : a.vs[(int64_t)blk * a.heads + h];
     };
     int b0 = block_of(t0, 0), b1 = block_of(t0, 1);
-    const int b0n = block_of(t0 + 4, 0), b1n = block_of(t0 + 4, 1);
-    fetch(t0, 0, b0, b1);
-    b0 = b0n, b1 = b1n;
+    fetch(t0, b0, b1);
+    float ks[2], vs[2];
+    scales(b0, ks[0], vs[0]);
+    scales(b1, ks[1], vs[1]);
+    bool ok0 = b0 >= 0, ok1 = b1 >= 0;
+    b0 = block_of(t0 + 4, 0), b1 = block_of(t0 + 4, 1);
 
     // the rows: lane (g, c) the dims of its words of row g; then the sight and the scale of rows 2c, 2c + 1
     uint32_t qb[NT][KW][2];
@@ -312,6 +293,15 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       }
     }
 
+    int vmin = 0x7FFFFFFF;  // of the rows there are: keys before it need no mask
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (m * NR + n * 8 + 2 * c + e < M) vmin = min(vmin, vis[n][e]);
+    vmin = min(vmin, __shfl_xor_sync(0xFFFFFFFFu, vmin, 1));
+    vmin = min(vmin, __shfl_xor_sync(0xFFFFFFFFu, vmin, 2));
+
     float o[NT][D / 16][4], mx[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -323,19 +313,22 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
         for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
     }
 
-    int slot_of = 0;
-    for (int t = t0; t < t1; t += 4, slot_of ^= 1) {
+    for (int t = t0; t < t1; t += 4) {
       const int b0n = block_of(t + 8, 0), b1n = block_of(t + 8, 1);
-      fetch(t + 4, slot_of ^ 1, b0, b1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      const uint8_t* tiles = ring + 2 * slot_of * (Tl::kBytes * kFewThreads);
+      fetch(t + 4, b0, b1);
+      float ksn[2], vsn[2];
+      scales(b0, ksn[0], vsn[0]);
+      scales(b1, ksn[1], vsn[1]);
+      const uint8_t* tiles = mine + (taken & 1) * 4 * Tl::kBytes;
+      good = wait_full(&full[warp][taken & 1], (taken >> 1) & 1, spin);
+      if (!good) break;
+      ++taken;
       const int key0 = t * 32;
       float z[2][NT][4], lv[2], iv[2];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t k[2][KW];
-        float ks, vs;
-        Tl::read_keys(tiles + half * (Tl::kBytes * kFewThreads), threadIdx.x, k, ks, vs);
+        Tl::keys(tiles + half * Tl::kBytes, g, c, k);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -348,26 +341,28 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma_16816(z[half][n], ka, qb[n][w][0], qb[n][w][1]);
         }
-        lv[half] = scale_log2(vs);
+        lv[half] = scale_log2(vs[half]);
         iv[half] = exp2_fast(-lv[half]);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float f = fz[n][e] * ks;
+            const float f = fz[n][e] * ks[half];
             z[half][n][e] = fmaf(z[half][n][e], f, lv[half]);
             z[half][n][2 + e] = fmaf(z[half][n][2 + e], f, lv[half]);
           }
       }
+      // keys that a row does not see, and tiles that are not there
+      if (!ok0 || !ok1 || key0 + 32 > vmin) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (key0 + 32 > vis[n][e]) {  // keys that the row does not see
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (key0 + 16 * (j >> 1) + 8 * (j & 1) + g >= vis[n][e]) z[j >> 1][n][2 * (j & 1) + e] = -INFINITY;
-          }
+              if (key0 + 16 * (j >> 1) + 8 * (j & 1) + g >= vis[n][e] || !(j >> 1 ? ok1 : ok0))
+                z[j >> 1][n][2 * (j & 1) + e] = -INFINITY;
+      }
       uint32_t pb[2][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -409,11 +404,11 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t vw[4][VW];
-        Tl::read_values(tiles + half * (Tl::kBytes * kFewThreads), threadIdx.x, vw);
-        if (key0 + 16 * half + 16 > s.len) {  // behind the history: not defined, may be NaN
+        Tl::values(tiles + (2 + half) * Tl::kBytes, g, c, vw);
+        if (key0 + 16 * half + 16 > vmax || !(half ? ok1 : ok0)) {  // behind what is seen: not defined, may be NaN
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (key0 + 16 * half + 2 * c + (j & 1) + (j >> 1) * 8 >= s.len)
+            if (key0 + 16 * half + 2 * c + (j & 1) + (j >> 1) * 8 >= vmax || !(half ? ok1 : ok0))
 #pragma unroll
               for (int w = 0; w < VW; ++w) vw[j][w] = 0;
         }
@@ -432,10 +427,16 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
           }
         }
       }
+      __syncwarp();  // every lane has read the slot: the next fetch may fill it
+      ok0 = b0 >= 0, ok1 = b1 >= 0;
       b0 = b0n, b1 = b1n;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) ks[half] = ksn[half], vs[half] = vsn[half];
     }
-
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!good) {  // a copy has not come: recorded; what is still on its way lands before the CTA ends
+      if (lane == 0) atomicOr(a.status, kStatusTimeout);
+      for (; taken < issued; ++taken) wait_full(&full[warp][taken & 1], (taken >> 1) & 1, kFewSpin);
+    }
     __syncthreads();  // the sums take the ring's place
     // join the warps: accumulator tile j, element (e, row g or g + 8) is row 2c + e, dim g * D/8 + 2 j (+ 1)
 #pragma unroll
@@ -490,7 +491,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
               top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
       }
     }
-    __syncthreads();  // the joined warps' buffers are free again
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (__syncthreads_or(!good)) return;  // the joined warps' buffers are free again
     u = v_end;
     if (u < u_end) {
       first += units;
@@ -688,9 +690,9 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
       const unsigned ctas = (unsigned)p.ctas;
       auto kern = p.tile == 8 ? k_attn_few<E, D, decltype(iv)::value, 1> : k_attn_few<E, D, decltype(iv)::value, 2>;
       const int smem = p.tile == 8 ? few_smem<D, 1>() : few_smem<D, 2>();
-      if (smem > 48 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (err != cudaSuccess) return;
-      kern<<<ctas, kFewThreads, smem, sm>>>(a, rows_of<E>(q), rows_of<E>(out));
+      kern<<<ctas, kFewThreads, smem, sm>>>(a, rows_of<E>(q), rows_of<E>(out), std::min(wait_limit(), kFewSpin));
     }
     if (p.slots) {
       // may start while the parts are still made; it waits for them before it reads

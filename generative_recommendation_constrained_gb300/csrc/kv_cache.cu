@@ -559,7 +559,7 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
       auto kern = cache->format == ZG_KV_INT8
                       ? (na.inter ? k_kv_append<E, D, true, true> : k_kv_append<E, D, true, false>)
                       : (na.inter ? k_kv_append<E, D, false, true> : k_kv_append<E, D, false, false>);
-      if (smem > 48 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (err == cudaSuccess) kern<<<(unsigned)(kv + qc), threads, smem, static_cast<cudaStream_t>(stream)>>>(a);
     });
   });
