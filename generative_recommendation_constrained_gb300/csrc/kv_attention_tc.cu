@@ -18,6 +18,8 @@
 // beyond, P lies over S and they wait for the product that reads it.  While
 // one tile's softmax runs the tensor cores work for the other.  P is handed
 // over in halves of 64 keys, so that its product starts during the softmax.
+// An item of one query tile takes both places: each has the same queries and
+// every other step, and their sums are joined at the end.
 //
 // A key block's scale multiplies its scores, a value block's scale enters the
 // exponent (kv_attention.cu has the formula), so neither costs anything an
@@ -54,7 +56,7 @@ struct TcShape {
   static_assert(kSmem <= 225 * 1024, "with the barriers inside 227 KiB");
   // Ring entries in the order of their use.  Apart: keys 0, keys 1, values 0, keys 2, values 1, ..., one entry for
   // the keys behind the last step empty.  Else: keys 0, values 0, keys 1, ...
-  static __device__ __forceinline__ int entries(int steps) { return kApart ? 2 * steps + 1 : 2 * steps; }
+  static __device__ __forceinline__ int entries(int steps) { return kApart && steps ? 2 * steps + 1 : 2 * steps; }
   static __device__ __forceinline__ int keys(int t) { return kApart ? (t ? 2 * t - 1 : 0) : 2 * t; }
   static __device__ __forceinline__ int values(int t) { return kApart ? 2 * t + 2 : 2 * t + 1; }
   static __device__ __forceinline__ int side(int n) { return kApart ? (n > 0 && !(n & 1)) : n & 1; }
@@ -228,9 +230,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // it: scores of t + 1 come after every warp has taken those of t, probabilities of t + 1 after the product of t.
   __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw], wide_full[kWide], wide_empty[kWide];
   __shared__ uint64_t q_full, s_full[2], s_free[2], p_full[2][2], o_done[2], drained;  // [tile], p_full [tile][half]
-  // of 16 keys each, a ring of eight steps (the codes of step t + 7 come only after the softmax of step t): key
-  // scale, log2 of the value scale, and 2^-that
-  __shared__ float s_ks[8][kGroups], s_lv[8][kGroups], s_iv[8][kGroups];
+  // of 16 keys each, a ring of 16 steps (the codes of step t + 10 come only after the softmax of step t): key scale,
+  // log2 of the value scale, and 2^-that
+  __shared__ float s_ks[16][kGroups], s_lv[16][kGroups], s_iv[16][kGroups];
   __shared__ uint32_t tmem_base;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -260,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Seen s = seen_of(a, b, threadIdx.x == 0);
   const int M = a.R * a.G;
   const int mine = min(M - m * a.tile, a.tile);  // query rows of this item
-  const int tiles = (mine + 127) / 128;          // query tiles in use
+  const int tiles = (mine + 127) / 128;          // query tiles
+  const bool twice = tiles == 1;                 // one tile: both places have it, and every other step
   // later rows see no less: the item sees what its last row does, or its request's last
   const int last = min((m * a.tile + mine - 1) / a.G, s.rows - 1);
   const int vmax = last < m * a.tile / a.G ? 0 : visible(a, s, last);
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&p_full[i][1], 4);
       bar_init(&o_done[i], 1);
     }
-    bar_init(&q_full, 4 * tiles);
+    bar_init(&q_full, 8);
     bar_init(&drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -368,11 +371,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_s = (1u << 4) | ((uint32_t)(kNK >> 3) << 17) | ((128u >> 4) << 24);
       const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
       const uint64_t q0 = desc_k(smem_u32(sq)), k0 = desc_k(smem_u32(wide)), v0 = desc_mn(smem_u32(wide), kNK * 128);
-      auto scores = [&](int t, int i) -> bool {
+      // scores, products of step t in place i; `k`: how many that place has had before
+      auto scores = [&](int t, int i, int k) -> bool {
         const int n = Sh::keys(t), ws = n % kWide;
-        if (i == 0 && !warp_wait(&wide_full[ws], (n / kWide) & 1, spin)) return false;
+        if ((twice || i == 0) && !warp_wait(&wide_full[ws], (n / kWide) & 1, spin)) return false;
         // apart: every warp has the last scores in registers; else the product that reads P in their place is over
-        if (t > 0 && !warp_wait(Sh::kApart ? &s_free[i] : &o_done[i], (t - 1) & 1, spin)) return false;
+        if (k > 0 && !warp_wait(Sh::kApart ? &s_free[i] : &o_done[i], (k - 1) & 1, spin)) return false;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint64_t kd = k0 + ws * (Sh::kTile >> 4), qd = q0 + i * (Sh::kTile >> 4);
         if (elect_one()) {
@@ -382,27 +386,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ss(tmem + Sh::kS + (uint32_t)(i * kNK), qd + off, kd + off, id_s, k > 0);
           }
           commit(&s_full[i]);
-          if (i == tiles - 1) commit(&wide_empty[ws]);
+          if (twice || i == 1) commit(&wide_empty[ws]);
         }
         __syncwarp();
         return true;
       };
-      auto values = [&](int t, int i) -> bool {
+      auto values = [&](int t, int i, int k) -> bool {
         const int n = Sh::values(t), ws = n % kWide;
-        if (i == 0 && !warp_wait(&wide_full[ws], (n / kWide) & 1, spin)) return false;
+        if ((twice || i == 0) && !warp_wait(&wide_full[ws], (n / kWide) & 1, spin)) return false;
         const uint64_t vd = v0 + ws * (Sh::kTile >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!warp_wait(&p_full[i][half], t & 1, spin)) return false;
+          if (!warp_wait(&p_full[i][half], k & 1, spin)) return false;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
 #pragma unroll
-            for (int k = half * 4; k < half * 4 + 4; ++k)
-              mma_ts(tmem + Sh::kO + (uint32_t)(i * D), tmem + Sh::kP + i * Sh::kPStep + (uint32_t)(k * 8),
-                     vd + k * (2048 >> 4), id_o, (t > 0 || k > 0) ? 1u : 0u);
+            for (int j = half * 4; j < half * 4 + 4; ++j)
+              mma_ts(tmem + Sh::kO + (uint32_t)(i * D), tmem + Sh::kP + i * Sh::kPStep + (uint32_t)(j * 8),
+                     vd + j * (2048 >> 4), id_o, (k > 0 || j > 0) ? 1u : 0u);
             if (half) {
               commit(&o_done[i]);
-              if (i == tiles - 1) commit(&wide_empty[ws]);
+              if (twice || i == 1) commit(&wide_empty[ws]);
             }
           }
           __syncwarp();
@@ -410,12 +414,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool good = warp_wait(&q_full, 0, spin);
-      for (int i = 0; i < tiles && good; ++i) good = scores(0, i);
-      for (int t = 0; t < steps && good; ++t) {
-        if constexpr (Sh::kApart)
-          for (int i = 0; i < tiles && good && t + 1 < steps; ++i) good = scores(t + 1, i);
-        for (int i = 0; i < tiles && good; ++i)
-          good = values(t, i) && (Sh::kApart || t + 1 == steps || scores(t + 1, i));
+      if (twice) {
+        for (int t = 0; t < 2 && t < steps && good; ++t) good = scores(t, t, 0);
+        for (int t = 0; t < steps && good; ++t) {
+          const int i = t & 1, k = t >> 1;
+          const bool more = t + 2 < steps;
+          if constexpr (Sh::kApart) good = (!more || scores(t + 2, i, k + 1)) && values(t, i, k);
+          else good = values(t, i, k) && (!more || scores(t + 2, i, k + 1));
+        }
+      } else {
+        for (int i = 0; i < 2 && good; ++i) good = scores(0, i, 0);
+        for (int t = 0; t < steps && good; ++t) {
+          if constexpr (Sh::kApart)
+            for (int i = 0; i < 2 && good && t + 1 < steps; ++i) good = scores(t + 1, i, t + 1);
+          for (int i = 0; i < 2 && good; ++i)
+            good = values(t, i, t) && (Sh::kApart || t + 1 == steps || scores(t + 1, i, t + 1));
+        }
       }
       if (!good && lane == 0) give_up();
       if (elect_one()) commit(&drained);
@@ -450,9 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = (((int64_t)blk * a.heads + h) * a.bt + ((t0 + t) * kNK + 16 * g) % a.bt) * D;
         if (!side) {
           if (lane < kGroups && t < steps) {
-            s_ks[t & 7][g] = ks;
-            s_lv[t & 7][g] = scale_log2(vs);
-            s_iv[t & 7][g] = exp2_fast(-scale_log2(vs));
+            s_ks[t & 15][g] = ks;
+            s_lv[t & 15][g] = scale_log2(vs);
+            s_iv[t & 15][g] = exp2_fast(-scale_log2(vs));
           }
           const int nb = t == tv ? b1 : b2;
           ks = nb < 0 ? 0.f : a.ks[(int64_t)nb * a.heads + h];
@@ -479,13 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int i = warp >> 2;
-    if (i < tiles) {
+    const int i = warp >> 2;  // the place
+    {
       // ------------------------------------------------------------ softmax
-      const int r = threadIdx.x & 127, ri = m * a.tile + threadIdx.x;
-      const bool live = (int)threadIdx.x < mine;
+      const int r = threadIdx.x & 127, ir = twice ? r : threadIdx.x, ri = m * a.tile + ir;  // row of the tile, item, call
+      const bool live = ir < mine;
       const int row = ri / a.G, qh = h * a.G + ri % a.G;
       const int vis = live ? visible(a, s, row) : 0;
+      const int first = twice ? i : 0, stride = twice ? 2 : 1;  // steps of this place
+      const int turns = first < steps ? (steps - first + stride - 1) / stride : 0;
       // lanes of a row when a warp moves its 32 rows: four elements each, kAt rows at a time
       constexpr int kLanes = D / 4, kSlot = D == 96 ? 32 : kLanes, kAt = 32 / kSlot;
       const int l4 = lane % kSlot, e = 4 * l4;
@@ -531,8 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t o_at = tmem + Sh::kO + (uint32_t)(i * D) + lanes;
       float mx = -INFINITY, l = 0.f;
       bool good = true;
-      for (int t = 0; t < steps; ++t) {
-        if (!warp_wait(&s_full[i], t & 1, spin)) {
+      for (int k = 0; k < turns; ++k) {
+        const int t = first + k * stride;
+        if (!warp_wait(&s_full[i], k & 1, spin)) {
           good = false;
           break;
         }
@@ -558,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 3; j + 1 < 16; j += 2) gm = max3(gm, z[16 * g + j], z[16 * g + j + 1]);
           gm = fmaxf(gm, z[16 * g + 15]);
           // a key scale of 0 must not meet an infinite score
-          tm = fmaxf(tm, fmaf(gm, fmaxf(fz * s_ks[t & 7][g], 1e-37f), s_lv[t & 7][g]));
+          tm = fmaxf(tm, fmaf(gm, fmaxf(fz * s_ks[t & 15][g], 1e-37f), s_lv[t & 15][g]));
         }
         float al = 1.f;
         const bool move = __any_sync(0xFFFFFFFFu, tm > mx + 8.f);
@@ -571,14 +588,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mu = mx == -INFINITY ? 0.f : mx;
         // the product of the last step has read its probabilities, and is in the sums (with P over S the scores have
         // waited for it)
-        if (Sh::kApart && t > 0) {
-          if (!warp_wait(&o_done[i], (t - 1) & 1, spin)) {
+        if (Sh::kApart && k > 0) {
+          if (!warp_wait(&o_done[i], (k - 1) & 1, spin)) {
             good = false;
             break;
           }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         }
-        if (move && t > 0) {
+        if (move && k > 0) {
 #pragma unroll
           for (int d = 0; d < D; d += 16) {  // few at a time: the scores stay in registers
             uint32_t o[16];
@@ -593,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t pr[16];
 #pragma unroll
           for (int g = g2; g < g2 + 2; ++g) {
-            const float f = fmaxf(fz * s_ks[t & 7][g], 1e-37f), c = s_lv[t & 7][g] - mu;
+            const float f = fmaxf(fz * s_ks[t & 15][g], 1e-37f), c = s_lv[t & 15][g] - mu;
             const uint64_t f2 = pair(f, f), c2 = pair(c, c);
             uint64_t sum = 0;  // 0.f, 0.f
 #pragma unroll
@@ -606,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float a0, a1;
             unpair(sum, a0, a1);
-            l = fmaf(a0 + a1, s_iv[t & 7][g], l);
+            l = fmaf(a0 + a1, s_iv[t & 15][g], l);
           }
           tmem_store16(p_at + 8 * g2, pr);
           if (g2 % (kGroups / 2) == kGroups / 2 - 2) {
@@ -617,21 +634,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (good && steps > 0) good = warp_wait(&o_done[i], (steps - 1) & 1, spin);
+      if (good && turns > 0) good = warp_wait(&o_done[i], (turns - 1) & 1, spin);
       if (!good && lane == 0) give_up();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      float own = 1.f, other = 0.f;  // what the two places' sums count for
+      float* sum1 = reinterpret_cast<float*>(wide);  // [D + 2][128]: place 1's sums, reference and row sum
+      if (twice) {
+        if (i == 1) {
+          // every product is complete in both places before the ring is written over
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+          for (int d = 0; d < D; d += 16) {
+            uint32_t o[16];
+            if (turns > 0) tmem_load16(o_at + d, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum1[(d + j) * 128 + r] = turns > 0 ? __uint_as_float(o[j]) : 0.f;
+          }
+          sum1[D * 128 + r] = mx;
+          sum1[(D + 1) * 128 + r] = l;
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+        } else {
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          const float m1 = sum1[D * 128 + r], l1 = sum1[(D + 1) * 128 + r], top = fmaxf(mx, m1);
+          own = mx == -INFINITY ? 0.f : exp2_fast(mx - top);
+          other = m1 == -INFINITY ? 0.f : exp2_fast(m1 - top);
+          mx = top;
+          l = l * own + l1 * other;
+        }
+      }
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int64_t pi = ((int64_t)item * a.splits + split) * a.tile + threadIdx.x;
-      if (good) {
+      const int64_t pi = ((int64_t)item * a.splits + split) * a.tile + ir;
+      if (good && !(twice && i == 1)) {
         uint8_t* tile = sq + i * Sh::kTile;  // every product that reads the queries is complete
 #pragma unroll
         for (int d = 0; d < D; d += 32) {
           uint32_t o[32];
-          if (steps > 0) {
+          if (turns > 0) {
             tmem_load(o_at + d, o);
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0;
+          }
+          if (twice) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              o[j] = __float_as_uint(__uint_as_float(o[j]) * own + sum1[(d + j) * 128 + r] * other);
           }
           const float* x = reinterpret_cast<const float*>(o);
           if (parts > 1) {

@@ -320,45 +320,66 @@ struct ReadArgs {
   CacheView c;
   Rows<T> ko, vo;
   const int32_t *start, *n;
-  int32_t B, T_, sides, side0;
+  int32_t B, T_, sides, side0, chunk, nchunk;  // heads a group walks; such chunks a (token, side)
 };
 
-// One group of lanes a (token, side, head), eight codes a lane.
+// One group of lanes a (token, side, chunk of heads), eight codes a lane and
+// head, four heads in flight.
 template <typename T, int D, bool INT8>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ ReadArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
   const int l = threadIdx.x % GS;
-  int64_t g = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS;
-  const int h = (int)(g % a.c.heads);
-  g /= a.c.heads;
-  const int side = a.side0 + (int)(g % a.sides);
-  g /= a.sides;
-  if (g >= (int64_t)a.B * a.T_ || l >= HeadLanes<D>::kUsed) return;
-  const int t = (int)(g % a.T_), b = (int)(g / a.T_);
-  const int n = a.n ? a.n[b] : a.T_;
-  const int start = a.start[b];
-  float x[8] = {};
+  const int64_t g = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS;
+  if (g >= (int64_t)a.B * a.T_ * a.sides * a.nchunk || l >= HeadLanes<D>::kUsed) return;
+  uint32_t x = (uint32_t)g;  // below 2^31 / GS CTAs of 256 / GS groups
+  const int h0 = (int)(x % a.nchunk) * a.chunk, h1 = min(h0 + a.chunk, a.c.heads);
+  x /= a.nchunk;
+  const int side = a.side0 + (int)(x % a.sides);
+  x /= a.sides;
+  const int t = (int)(x % a.T_), b = (int)(x / a.T_);
+  const int n = a.n ? a.n[b] : a.T_, start = a.start[b];
+  int blk = -1, row = 0;
   if (t < n) {
     const int64_t p = (int64_t)start + t;
-    int blk = -1;
-    if (start >= 0 && p < (int64_t)a.c.max_blocks * a.c.bt)
-      blk = a.c.table[(int64_t)b * a.c.max_blocks + p / a.c.bt];
+    if (start >= 0 && p < (int64_t)a.c.max_blocks * a.c.bt) {
+      blk = a.c.table[(int64_t)b * a.c.max_blocks + (uint32_t)p / a.c.bt];
+      row = (uint32_t)p % a.c.bt;
+    }
     if (blk < 0 || blk >= a.c.n_blocks) {
       if (l == 0) atomicOr(a.c.status, kStatusCache);
-    } else {
-      const int64_t bh = (int64_t)blk * a.c.heads + h;
-      const float s = (side ? a.c.vs : a.c.ks)[bh];
-      const uint8_t* codes = (side ? a.c.vc : a.c.kc) + (bh * a.c.bt + p % a.c.bt) * D + 8 * l;
-      const uint2 w = *reinterpret_cast<const uint2*>(codes);
-      codes_float4<INT8>(w.x, x);
-      codes_float4<INT8>(w.y, x + 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= s;
+      blk = -1;
     }
   }
-  T* o = (side ? a.vo : a.ko).at(b, t, h) + 8 * l;
-  store4(o, x);
-  store4(o + 4, x + 4);
+  const Rows<T>& out = side ? a.vo : a.ko;
+  T* o = out.at(b, t, h0) + 8 * l;
+  const int64_t bh = (int64_t)max(blk, 0) * a.c.heads + h0;
+  const float* scale = (side ? a.c.vs : a.c.ks) + bh;
+  const uint8_t* codes = (side ? a.c.vc : a.c.kc) + (bh * a.c.bt + row) * D + 8 * l;
+  for (int h = h0; h < h1; h += 4, scale += 4, codes += 4 * a.c.bt * D) {
+    uint2 w[4];
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = make_uint2(0, 0);
+      s[i] = 0.f;
+      if (blk >= 0 && h + i < h1) {
+        w[i] = *reinterpret_cast<const uint2*>(codes + i * a.c.bt * D);
+        s[i] = scale[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (h + i >= h1) break;
+      float y[8];
+      codes_float4<INT8>(w[i].x, y);
+      codes_float4<INT8>(w[i].y, y + 4);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] *= s[i];
+      store4(o, y);
+      store4(o + 4, y + 4);
+      o += out.sh;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -583,14 +604,16 @@ zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int32_t max
   if (!start) return bad_arg(call, "start is NULL");
   if (B == 0 || T == 0) return ZG_OK;
   const int sides = (k_out ? 1 : 0) + (v_out ? 1 : 0);
-  const int64_t ctas = ((int64_t)B * T * sides * cache->heads * group_lanes(cache->dim) + 255) / 256;
-  if (ctas > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_read: more than 2^31 CTAs");
+  const int lanes = group_lanes(cache->dim);
+  const int chunk = head_chunk((int64_t)B * T * sides, cache->heads, lanes), nchunk = (cache->heads + chunk - 1) / chunk;
+  const int64_t groups = (int64_t)B * T * sides * nchunk, ctas = (groups * lanes + 255) / 256;
+  if (groups > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_read: more than 2^31 (token, side, head chunk)s");
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
   for_type(dt, [&](auto e) {
     using E = typename decltype(e)::type;
     const ReadArgs<E> a = {view(cache, table, max_blocks, status), rows_of<E>(k_out), rows_of<E>(v_out), start, n,
-                           B, T, sides, k_out ? 0 : 1};
+                           B, T, sides, k_out ? 0 : 1, chunk, nchunk};
     for_dim(cache->dim, [&](auto dv) {
       constexpr int D = decltype(dv)::value;
       if (cache->format == ZG_KV_INT8)
