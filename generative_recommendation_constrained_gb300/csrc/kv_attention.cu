@@ -573,7 +573,13 @@ struct AttnPlan {
   size_t bytes;
 };
 
-constexpr int kFewRows = 32;  // query rows a key head up to which k_attn_few is the faster
+// Query rows a key head up to which k_attn_few is taken.  Measured (us, few
+// against many rows; 4 heads, e4m3), at 16, 24, 32 and 48 rows:
+//   32 requests of  2,000 tokens, 64 dims: 20.8/33.1  27.8/33.0  30.9/33.1  43.3/33.0
+//                                128 dims: 26.8/37.7  36.9/37.1  40.4/37.1  59.7/37.2
+//    4 requests of 30,000 tokens, 64 dims: 31.0/55.7  45.3/55.6  47.4/55.6  53.4/55.9
+//                                128 dims: 41.1/59.7  61.1/59.8  63.7/59.7  70.8/60.2
+inline int few_rows(int dim) { return dim <= 64 ? 32 : 24; }
 
 // Few rows: as many CTAs as are resident, or one for each unit that the
 // histories may have.  Many rows: one CTA an item, its keys in parts only where
@@ -582,7 +588,7 @@ constexpr int kFewRows = 32;  // query rows a key head up to which k_attn_few is
 AttnPlan attn_plan(const zg_kv_cache* c, int max_blocks, int B, int R, int Hq) {
   AttnPlan p = {};
   const int64_t M = (int64_t)R * (Hq / c->heads);
-  p.tc = M > kFewRows;
+  p.tc = M > few_rows(c->dim);
   p.tile = p.tc ? attn_tc_tile(M) : M > 8 ? 16 : 8;
   p.mt = (int)((M + p.tile - 1) / p.tile);
   p.items = (int64_t)B * c->heads * p.mt;

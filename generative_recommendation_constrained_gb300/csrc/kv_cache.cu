@@ -134,7 +134,7 @@ struct Piece {
 // this one's are turned, kept in registers between the maximum and the codes,
 // and written.  CTAs past kv_ctas turn the queries.
 template <typename T, int D, bool INT8, bool INTER>
-__global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ AppendArgs<T> a) {
+__global__ void __launch_bounds__(256, 2) k_kv_append(const __grid_constant__ AppendArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
   constexpr float Q = INT8 ? 127.f : 448.f;
   extern __shared__ __align__(16) uint8_t stage_raw[];  // [2][kPasses][2][threads][4]
@@ -228,49 +228,66 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ Appen
       float x[kPasses][8], sn[4], cs[4];
       float top = 0.f;
       bool bad = false;
+      // four passes at a time without a branch between them, so that their chains of shuffles and roots overlap
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const int r = lo + p * rpp + grp;
-        const bool on = m.used && r < hi;
+      for (int p0 = 0; p0 < kPasses; p0 += 4) {
+        const bool some = lo + p0 * rpp < hi;  // uniform over the CTA
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[p][i] = 0.f;
-        if (on) {
-          load4(from + 2 * p * step, x[p]);
-          load4(from + (2 * p + 1) * step, x[p] + 4);
-        }
-        if (turn && lo + p * rpp < hi) {  // uniform over the CTA
-          // rows rpp apart: the next angle by one complex product (at most 7 of them, each within 2^-23)
-          if (p == 0) {
-            lane_angles(a.nr, m, l, cur.bj * a.c.bt + r, sn, cs);
-          } else {
+        for (int p = p0; p < p0 + 4; ++p) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float s = sn[i] * dc[i] + cs[i] * ds[i];
-              cs[i] = cs[i] * dc[i] - sn[i] * ds[i];
-              sn[i] = s;
-            }
+          for (int i = 0; i < 8; ++i) x[p][i] = 0.f;
+          if (m.used && lo + p * rpp + grp < hi) {
+            load4(from + 2 * p * step, x[p]);
+            load4(from + (2 * p + 1) * step, x[p] + 4);
           }
-          norm_rotate<D, INTER>(a.nr, turn_of(sn, cs, gk), x[p]);
         }
-        float big = 0.f, all = 0.f;
+        if (!some) continue;
+        if (turn) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          big = fmaxf(big, fabsf(x[p][i]));
-          all += x[p][i];
+          for (int p = p0; p < p0 + 4; ++p) {
+            // rows rpp apart: the next angle by one complex product (at most 7 of them, each within 2^-23)
+            if (p == 0) {
+              lane_angles(a.nr, m, l, cur.bj * a.c.bt + lo + grp, sn, cs);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float s = sn[i] * dc[i] + cs[i] * ds[i];
+                cs[i] = cs[i] * dc[i] - sn[i] * ds[i];
+                sn[i] = s;
+              }
+            }
+            norm_rotate<D, INTER>(a.nr, turn_of(sn, cs, gk), x[p]);
+          }
         }
-        if (!(fabsf(all) <= FLT_MAX) && on) {  // a NaN or an infinity (or a sum past the range)
+        float big = 0.f;
+        uint64_t all2 = 0;  // 0.f, 0.f
+#pragma unroll
+        for (int p = p0; p < p0 + 4; ++p) {  // rows that are not there are zero
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            big = fmaxf(big, fmaxf(fabsf(x[p][i]), fabsf(x[p][i + 1])));
+            all2 = add2(all2, pair(x[p][i], x[p][i + 1]));
+          }
+        }
+        float all, all1;
+        unpair(all2, all, all1);
+        if (!(fabsf(all + all1) <= FLT_MAX)) {  // a NaN or an infinity (or a sum past the range)
           big = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (fabsf(x[p][i]) <= FLT_MAX) {
-              big = fmaxf(big, fabsf(x[p][i]));
-            } else {  // NaN -> 0; an infinity saturates
-              bad = true;
-              x[p][i] = isnan(x[p][i]) ? 0.f : copysignf(FLT_MAX, x[p][i]);
+          for (int p = p0; p < p0 + 4; ++p)
+            if (m.used && lo + p * rpp + grp < hi) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (fabsf(x[p][i]) <= FLT_MAX) {
+                  big = fmaxf(big, fabsf(x[p][i]));
+                } else {  // NaN -> 0; an infinity saturates
+                  bad = true;
+                  x[p][i] = isnan(x[p][i]) ? 0.f : copysignf(FLT_MAX, x[p][i]);
+                }
+              }
             }
-          }
         }
-        if (on) top = fmaxf(top, big);
+        top = fmaxf(top, big);
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));

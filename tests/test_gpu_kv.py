@@ -613,3 +613,25 @@ def test_expired_wait_is_reported(zg, dev):
     finally:
         zg.zg_debug_set_wait_limit(0)
     check_attention(zg, dev, c, q, table, length, None, False)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_example_history_decode(zg, fmt):
+    """The example's path end to end: the request vectors against attention in 64 bits over what the cache holds, and
+    items of the catalogue only."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "history_decode.py")
+    spec = importlib.util.spec_from_file_location("history_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    r = m.main(["--users", "9", "--events", "70", "--fmt", fmt])
+    items = {tuple(s) for s in r["items"].tolist()}
+    assert all(tuple(s) in items for s in r["sids"].reshape(-1, r["sids"].shape[-1]).tolist())
+    assert torch.isfinite(r["rescored"]).all() and torch.isfinite(r["lse"]).all()
+    # the new event's query again, attending in 64 bits
+    q, _, _ = r["layer"].project(r["x"])
+    q, _ = r["layer"].turn(q, None, (r["length"] - 1)[:, None].contiguous())
+    want, _, tol, _ = want_attention(r["cache"], q, r["table"], r["length"], None, False, m.DIM ** -0.5)
+    err = (r["a1"].double().cpu() - want).abs()
+    assert (err <= tol + 2.0 ** -8 * 1.001 * (want.abs() + tol)).all()
