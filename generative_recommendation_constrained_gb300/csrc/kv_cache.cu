@@ -418,8 +418,10 @@ zg_status nr_args(const zg_norm_rope* nr, int dim, const char* call, NormRopeArg
   o->rot = nr->rot_dim;
   o->inter = nr->interleaved != 0;
   o->eps = nr->eps;
-  o->q_gain = nr->q_gain;
-  o->k_gain = nr->k_gain;
+  if (o->norm) {  // the gains belong to the norm
+    o->q_gain = nr->q_gain;
+    o->k_gain = nr->k_gain;
+  }
   // theta^(-2i/rot_dim) by doubling: seven powers and one product each (seven roundings at most) instead of 64 powers
   double f[64] = {1.0};
   const int n = nr->rot_dim / 2;

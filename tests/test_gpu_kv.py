@@ -108,6 +108,10 @@ def test_norm_rope_forms(zg, dev):
     none, ko = dev.NormRope(64, rot_dim=0)(None, k, pos)
     ok(zg)
     near_turned(ko, *turned(k, None, pos, 0, 0, False, True))
+    g = randn((64,), torch.float32, 5)                   # the gains belong to the norm: without it they do nothing
+    ko = dev.NormRope(64, g, g, norm=False)(None, k, pos)[1]
+    ok(zg)
+    near_turned(ko, *turned(k, g, pos, 64, 10000.0, False, False), far=2 ** 31)
     z = torch.zeros((1, 1, 2, 96), device="cuda")
     assert not dev.NormRope(96)(z, z, ints([[4]]))[0].any()
     ok(zg)
@@ -271,6 +275,12 @@ def test_append_turns_keys_and_queries(zg, dev, fmt):
     alone, _ = nr(q, None, pos)
     ok(zg)
     assert torch.equal(q_out, alone)
+    plain = c.append(k, v, table, start, q=q, norm_rope=dev.NormRope(D, g, g, norm=False, rot_dim=96, interleaved=True))
+    ok(zg)
+    near_turned(plain, *turned(q, g, pos, 96, 10000.0, True, False), far=100)
+    c.append(k[:, :19].contiguous(), v[:, :19].contiguous(), table, ints([0, 0]), ints([19, 0]))
+    c.append(k, v, table, start, q=q, norm_rope=nr)
+    ok(zg)
     want, size = turned(k, g, pos, 48, 10000.0, False, True)
     blk, row = place(table, start, bt, T)
     code, s = c.k_codes.float().double().cpu().numpy(), c.k_scale.double().cpu().numpy()
