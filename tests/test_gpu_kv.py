@@ -553,6 +553,29 @@ def test_attention_in_a_graph(zg, dev):
     check_attention(zg, dev, c, q, table, ints([3, 3]), None, True)
 
 
+@pytest.mark.parametrize("R", [1, 10, 160])
+def test_split_attention_in_a_graph(zg, dev, R):
+    """A history in many parts, captured: replays follow the lengths that the device holds then."""
+    c, table, length = build(dev, "int8", 2, 1, 64, 64, [5000, 3000], 80, 5)
+    q = randn((2, R, 2, 64), torch.bfloat16, 5)
+    attn = dev.CacheAttention(c, 2, R, 2, 80, lse=True)
+    assert attn.ws_bytes > 0
+    attn(q, table, length)
+    ok(zg)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        attn(q, table, length)
+    for lengths in ([100, 2999], [4999, 0], [5000, 3000]):
+        length.copy_(ints(lengths))
+        g.replay()
+        ok(zg)
+        got, lse = attn.out.clone(), attn.lse.clone()
+        attn(q, table, length)
+        ok(zg)
+        assert torch.equal(got, attn.out) and torch.equal(lse, attn.lse)
+    check_attention(zg, dev, c, q, table, length, None, False)
+
+
 def test_attention_repeats(zg, dev):
     """The same call gives the same bits."""
     c, table, length = build(dev, "e4m3", 5, 2, 128, 64, [5000, 0, 1, 4097, 300], 90, 12)
