@@ -20,6 +20,11 @@
 // over in halves of 64 keys, so that its product starts during the softmax.
 // An item of one query tile takes both places: each has the same queries and
 // every other step, and their sums are joined at the end.
+// Measured: causal chunks of 2,048 rows over up to 16,384 tokens (2 requests, 16
+// heads over 4 of 128) 399 us, 1.02 PFLOP/s or 54 % of the measured bf16 rate;
+// 256 rows each for 64 requests over up to 2,048 tokens 59 us.  Bound by the
+// chain softmax -> product -> scores of a tile, some 3,300 cycles a step of
+// which the tensor cores work 2,200 for the two.
 //
 // A key block's scale multiplies its scores, a value block's scale enters the
 // exponent (kv_attention.cu has the formula), so neither costs anything an
