@@ -21,10 +21,12 @@
 // An item of one query tile takes both places: each has the same queries and
 // every other step, and their sums are joined at the end.
 // Measured: causal chunks of 2,048 rows over up to 16,384 tokens (2 requests, 16
-// heads over 4 of 128) 399 us, 1.02 PFLOP/s or 54 % of the measured bf16 rate;
+// heads over 4 of 128) 393 us, 1.03 PFLOP/s or 55 % of the measured bf16 rate;
 // 256 rows each for 64 requests over up to 2,048 tokens 59 us.  Bound by the
-// chain softmax -> product -> scores of a tile, some 3,300 cycles a step of
-// which the tensor cores work 2,200 for the two.
+// waits in the chain softmax -> product -> scores of a tile, some 3,300 cycles a
+// step of which the tensor cores work 2,200 for the two: with the widening, the
+// exponentials and the maxima all left out a chunk takes 379 us, with seven
+// eighths of the products 380, with all of them 349.
 //
 // A key block's scale multiplies its scores, a value block's scale enters the
 // exponent (kv_attention.cu has the formula), so neither costs anything an
@@ -99,6 +101,20 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_
     if (done) return true;
   }
   return false;
+}
+// The same for the warp that issues the products, without suspending: it is on
+// the critical path of every step (causal chunks 393 us against 399; the other
+// warps' waits are better suspended, 403 and 424 with theirs spinning too).
+__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
+  const uint32_t a = smem_u32(bar);
+  uint32_t done = 0;
+  for (uint32_t it = 0; it < 32 * limit && !done; ++it)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(a), "r"(parity)
+        : "memory");
+  return __all_sync(0xFFFFFFFFu, done);
 }
 // The same for a whole warp: one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
@@ -379,9 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // scores, products of step t in place i; `k`: how many that place has had before
       auto scores = [&](int t, int i, int k) -> bool {
         const int n = Sh::keys(t), ws = n % kWide;
-        if ((twice || i == 0) && !warp_wait(&wide_full[ws], (n / kWide) & 1, spin)) return false;
+        if ((twice || i == 0) && !spin_wait(&wide_full[ws], (n / kWide) & 1, spin)) return false;
         // apart: every warp has the last scores in registers; else the product that reads P in their place is over
-        if (k > 0 && !warp_wait(Sh::kApart ? &s_free[i] : &o_done[i], (k - 1) & 1, spin)) return false;
+        if (k > 0 && !spin_wait(Sh::kApart ? &s_free[i] : &o_done[i], (k - 1) & 1, spin)) return false;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint64_t kd = k0 + ws * (Sh::kTile >> 4), qd = q0 + i * (Sh::kTile >> 4);
         if (elect_one()) {
@@ -398,11 +414,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto values = [&](int t, int i, int k) -> bool {
         const int n = Sh::values(t), ws = n % kWide;
-        if ((twice || i == 0) && !warp_wait(&wide_full[ws], (n / kWide) & 1, spin)) return false;
+        if ((twice || i == 0) && !spin_wait(&wide_full[ws], (n / kWide) & 1, spin)) return false;
         const uint64_t vd = v0 + ws * (Sh::kTile >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!warp_wait(&p_full[i][half], k & 1, spin)) return false;
+          if (!spin_wait(&p_full[i][half], k & 1, spin)) return false;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
 #pragma unroll
@@ -418,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       };
-      bool good = warp_wait(&q_full, 0, spin);
+      bool good = spin_wait(&q_full, 0, spin);
       if (twice) {
         for (int t = 0; t < 2 && t < steps && good; ++t) good = scores(t, t, 0);
         for (int t = 0; t < steps && good; ++t) {
@@ -439,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!good && lane == 0) give_up();
       if (elect_one()) commit(&drained);
       __syncwarp();
-      if (!warp_wait(&drained, 0, kSpin) && lane == 0) give_up();
+      if (!spin_wait(&drained, 0, kSpin) && lane == 0) give_up();
     } else if (warp == 13) {
       // -------------------------------------------------------------- codes
       // Lane g brings keys 16 g .. 16 g + 15 of a step.  Block numbers and scales are read a step or more ahead of

@@ -136,7 +136,7 @@ struct Piece {
 // this one's are turned, kept in registers between the maximum and the codes,
 // and written.  CTAs past kv_ctas turn the queries.  Bound by issue and the
 // chains of its shuffles: 32 x 2,048 tokens, 16 + 4 heads of 128, bf16 to e4m3
-// with norm and rotation take 160 us (738 MB, 4.6 TB/s); a piece a CTA, loaded
+// with norm and rotation take 156 us (738 MB, 4.7 TB/s); a piece a CTA, loaded
 // into registers, took 387.
 template <typename T, int D, bool INT8, bool INTER>
 __global__ void __launch_bounds__(256, 2) k_kv_append(const __grid_constant__ AppendArgs<T> a) {
@@ -590,9 +590,10 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
   if (pieces + qc > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^31 CTAs");
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
-  // resident CTAs (128 registers a thread: 512 threads an SM; their buffers inside 200 KB) walk the pieces
+  // resident CTAs (128 registers a thread: 512 threads an SM; their buffers inside 200 KB) walk the pieces; where there
+  // are queries too, half of each SM is theirs from the start (32 x 2,048 tokens: 156 us against 160)
   const size_t smem = 2 * (size_t)kPasses * threads * 8 * (k->dtype == ZG_F32 ? 4 : 2);
-  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>(512 / threads, (200 << 10) / smem));
+  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>((Hq ? 256 : 512) / threads, (200 << 10) / smem));
   const int64_t kv = std::min<int64_t>(pieces, resident * sm_count());
   cudaError_t err = cudaSuccess;
   for_type(k->dtype, [&](auto e) {
