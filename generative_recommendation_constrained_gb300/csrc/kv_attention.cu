@@ -116,9 +116,9 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, i
 // without any work behind them).  Keys and dims are the long side of the
 // products (S^T = K Q^T, O^T = V^T P^T), so that eight rows fill an instruction
 // that sixteen keys or dims by eight rows make.  Bound by memory: 8 requests of
-// up to 131,072 tokens (4 heads of 128, int8, 645 MB) take 114 us, 104 of them
+// up to 131,072 tokens (4 heads of 128, int8, 645 MB) take 108 us, 104 of them
 // here (6.2 TB/s) and the rest the join; 64 requests of up to 4,096 tokens (85
-// MB) 29 us, some 6 of them the chain from the lengths to the first codes.
+// MB) 27 us, some 6 of them the chain from the lengths to the first codes.
 constexpr uint32_t kFewSpin = 1u << 20;  // polls of a wait at most
 __device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, uint32_t limit) {
   const uint32_t at = smem_addr(bar);
@@ -509,16 +509,19 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
   }
 }
 
-// Joins the parts of the keys: one warp a (request, row, query head).  Items
-// of one part have their outputs already.
-template <typename T, int D>
+// Joins the parts of the keys, WARPS warps a (request, row, query head), each
+// every WARPS-th part, eight of them in flight.  Items of one part have their
+// outputs already.  Bound by latency: the item's parts, then the sums.
+template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnArgs a, const Rows<T> out) {
   constexpr int kLanes = D / 4;  // lanes that hold four dims
-  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w >= (int64_t)a.B * a.R * a.Hq) return;
-  const int qh = (int)(w % a.Hq);
-  const int64_t br = w / a.Hq;
+  __shared__ float sm_m[8], sm_l[8], sm_x[8][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % WARPS;
+  const int64_t total = (int64_t)a.B * a.R * a.Hq;
+  const int64_t id = (int64_t)blockIdx.x * (8 / WARPS) + warp / WARPS;
+  const int64_t rid = min(id, total - 1);
+  const int qh = (int)(rid % a.Hq);
+  const int64_t br = rid / a.Hq;
   const int r = (int)(br % a.R), b = (int)(br / a.R);
   const int i = r * a.G + qh % a.G, m = i / a.tile;
   const int64_t item = ((int64_t)b * a.heads + qh / a.G) * a.mt + m;
@@ -531,32 +534,67 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
     slot0 = e.x, later = e.x & ~1, step = 2;
   } else {
     const Seen s = seen_of(a, b, false);
-    const int last = min(min((m + 1) * a.tile, a.R * a.G) - 1, s.rows * a.G - 1);
-    parts = parts_of(a, last < m * a.tile ? 0 : visible(a, s, last / a.G));
+    parts = parts_of(a, item_keys(a, s, m, a.tile));
     slot0 = later = item * a.splits, step = 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
-  if (parts <= 1) return;
   const float* ml = a.part + a.slots * a.tile * D;
-  auto row_of = [&](int sp) -> int64_t { return (sp ? later + sp * step : slot0) * a.tile + i % a.tile; };
-  float top = -INFINITY;
-  for (int sp = lane; sp < parts; sp += 32) top = fmaxf(top, ml[row_of(sp) * 2]);
+  float top = -INFINITY, sum = 0.f, x[4] = {};
+  if (parts > 1) {
+    for (int s0 = w; s0 < parts; s0 += 8 * WARPS) {
+      float2 e[8];
+      float y[8][4];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  float sum = 0.f, x[4] = {};
-  if (top != -INFINITY && lane < kLanes) {
-#pragma unroll 8
-    for (int sp = 0; sp < parts; ++sp) {
-      const int64_t pi = row_of(sp);
-      const float2 e = *reinterpret_cast<const float2*>(ml + pi * 2);
-      float y[4];
-      load4(a.part + pi * D + 4 * lane, y);
-      const float f = exp2_fast(e.x - top);
-      sum = fmaf(f, e.y, sum);
+      for (int j = 0; j < 8; ++j) {
+        const int sp = s0 + WARPS * j;
+        e[j] = make_float2(-INFINITY, 0.f);
+        y[j][0] = y[j][1] = y[j][2] = y[j][3] = 0.f;
+        if (sp < parts) {
+          const int64_t at = (sp ? later + sp * step : slot0) * a.tile + i % a.tile;
+          e[j] = *reinterpret_cast<const float2*>(ml + at * 2);
+          if (lane < kLanes) load4(a.part + at * D + 4 * lane, y[j]);
+        }
+      }
+      float nt = top;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = fmaf(f, y[k], x[k]);
+      for (int j = 0; j < 8; ++j) nt = fmaxf(nt, e[j].x);
+      if (nt == -INFINITY) continue;
+      const float f0 = exp2_fast(top - nt);
+      top = nt;
+      sum *= f0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] *= f0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = exp2_fast(e[j].x - nt);
+        sum = fmaf(f, e[j].y, sum);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = fmaf(f, y[j][k], x[k]);
+      }
     }
   }
+  if constexpr (WARPS > 1) {
+    if (lane == 0) sm_m[warp] = top, sm_l[warp] = sum;
+    if (lane < kLanes) store4(&sm_x[warp][4 * lane], x);
+    __syncthreads();
+    if (w) return;
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) top = fmaxf(top, sm_m[warp + k]);
+    const float f0 = top == -INFINITY ? 0.f : exp2_fast(sm_m[warp] - top);
+    sum *= f0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) x[d] *= f0;
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) {
+      const float f = top == -INFINITY ? 0.f : exp2_fast(sm_m[warp + k] - top);
+      sum = fmaf(f, sm_l[warp + k], sum);
+      float y[4] = {};
+      if (lane < kLanes) load4(&sm_x[warp + k][4 * lane], y);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) x[d] = fmaf(f, y[d], x[d]);
+    }
+  }
+  if (id >= total || parts <= 1) return;
   if (lane < kLanes) {
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
@@ -564,10 +602,15 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
     store4(out.at(b, r, qh) + 4 * lane, x);
   }
   if (a.lse && lane == 0)
-    a.lse[w] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+    a.lse[rid] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
 }
 
 // ---------------------------------------------------------------- host side
+
+// Rows up to which the join has four warps a row, not one (128 rows of some 14 parts
+// 108.3 us a call against 111.7, 512 rows of some 4 27.1 against 27.8; eight
+// warps 108.1 and 28.9).
+constexpr int64_t kJoinRows = 4096;
 
 struct AttnPlan {
   bool tc;
@@ -706,7 +749,10 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
     if (p.slots) {
       // may start while the parts are still made; it waits for them before it reads
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)(((int64_t)B * R * Hq + 7) / 8));
+      // several warps a row where the rows alone would leave SMs idle
+      const int64_t rows = (int64_t)B * R * Hq;
+      const int warps = rows <= kJoinRows ? 4 : 1;
+      cfg.gridDim = dim3((unsigned)((rows * warps + 7) / 8));
       cfg.blockDim = dim3(256);
       cfg.stream = sm;
       cudaLaunchAttribute attr = {};
@@ -714,7 +760,7 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
       attr.val.programmaticStreamSerializationAllowed = 1;
       cfg.attrs = &attr;
       cfg.numAttrs = 1;
-      cudaLaunchKernelEx(&cfg, k_attn_join<E, D>, a, rows_of<E>(out));
+      cudaLaunchKernelEx(&cfg, warps == 4 ? k_attn_join<E, D, 4> : k_attn_join<E, D, 1>, a, rows_of<E>(out));
     }
   };
   if (p.tc) {
