@@ -287,6 +287,29 @@ __device__ __forceinline__ void copy4_async(T* to, const T* from) {
                : "memory");
 }
 
+// Kernels of the history cache are launched so that they may start while their
+// predecessor in the stream ends (some 2 us a call: 64 beams 20.7 -> 18.8, 64
+// single tokens 27.1 -> 25.2): each waits here, before it touches memory, until
+// everything before it is complete, and lets its successor be put in place.
+__device__ __forceinline__ void after_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kern)(P...), int64_t ctas, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Run-time head size and type as template arguments: f(Dim<D>{}), f(Elem<T>{}).
 template <int D>
 using Dim = std::integral_constant<int, D>;

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   uint32_t issued = 0, taken = 0;  // steps of this warp, over all its items
   bool good = true;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be put in place; it waits
+  after_predecessor();
 
   // every request's units, their sum, and the request in which this CTA's share begins (a thread a request; over
   // again for the second only where there are more requests than threads)
@@ -516,6 +516,7 @@ template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnArgs a, const Rows<T> out) {
   constexpr int kLanes = D / 4;  // lanes that hold four dims
   __shared__ float sm_m[8], sm_l[8], sm_x[8][D];
+  after_predecessor();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % WARPS;
   const int64_t total = (int64_t)a.B * a.R * a.Hq;
   const int64_t id = (int64_t)blockIdx.x * (8 / WARPS) + warp / WARPS;
@@ -528,7 +529,6 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
   int parts;
   int64_t slot0, later, step;  // slots of the parts: slot0, then later + step, later + 2 step, ...
   if (a.info) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int2 e = a.info[item];
     parts = e.y;
     slot0 = e.x, later = e.x & ~1, step = 2;
@@ -536,7 +536,6 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
     const Seen s = seen_of(a, b, false);
     parts = parts_of(a, item_keys(a, s, m, a.tile));
     slot0 = later = item * a.splits, step = 1;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
   }
   const float* ml = a.part + a.slots * a.tile * D;
   float top = -INFINITY, sum = 0.f, x[4] = {};
@@ -739,28 +738,20 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
     using E = typename decltype(ev)::type;
     constexpr int D = decltype(dv)::value;
     if (!p.tc) {
-      const unsigned ctas = (unsigned)p.ctas;
       auto kern = p.tile == 8 ? k_attn_few<E, D, decltype(iv)::value, 1> : k_attn_few<E, D, decltype(iv)::value, 2>;
       const int smem = p.tile == 8 ? few_smem<D, 1>() : few_smem<D, 2>();
       if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (err != cudaSuccess) return;
-      kern<<<ctas, kFewThreads, smem, sm>>>(a, rows_of<E>(q), rows_of<E>(out), std::min(wait_limit(), kFewSpin));
+      err = launch_early(kern, p.ctas, kFewThreads, smem, sm, a, rows_of<E>(q), rows_of<E>(out),
+                         std::min(wait_limit(), kFewSpin));
+      if (err != cudaSuccess) return;
     }
     if (p.slots) {
-      // may start while the parts are still made; it waits for them before it reads
-      cudaLaunchConfig_t cfg = {};
       // several warps a row where the rows alone would leave SMs idle
       const int64_t rows = (int64_t)B * R * Hq;
       const int warps = rows <= kJoinRows ? 4 : 1;
-      cfg.gridDim = dim3((unsigned)((rows * warps + 7) / 8));
-      cfg.blockDim = dim3(256);
-      cfg.stream = sm;
-      cudaLaunchAttribute attr = {};
-      attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr.val.programmaticStreamSerializationAllowed = 1;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      cudaLaunchKernelEx(&cfg, warps == 4 ? k_attn_join<E, D, 4> : k_attn_join<E, D, 1>, a, rows_of<E>(out));
+      err = launch_early(warps == 4 ? k_attn_join<E, D, 4> : k_attn_join<E, D, 1>, (rows * warps + 7) / 8, 256, 0, sm, a,
+                         rows_of<E>(out));
     }
   };
   if (p.tc) {
@@ -775,7 +766,6 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
     if (q->dtype == ZG_BF16) typed(Elem<__nv_bfloat16>{});
     else typed(Elem<__half>{});
   });
-  if (err == cudaSuccess) err = cudaGetLastError();
   return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache attention launch");
 } catch (...) {
   return ZG_ERR_OUT_OF_MEMORY;

@@ -257,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+  after_predecessor();
+
   // CTAs start in the order of their numbers: the requests with most to read first, the last rows of each first
   int it = blockIdx.x;
   const int split = it % a.splits;
@@ -761,8 +763,8 @@ cudaError_t launch_attn_tc(const AttnArgs& a, const zg_rows* q, const zg_rows* o
     auto kern = k_attn_tc<E, D, decltype(iv)::value>;
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TcShape<D>::kSmem);
     if (err != cudaSuccess) return;
-    kern<<<(unsigned)items, kThreads, TcShape<D>::kSmem, st>>>(a, rows_of<E>(q), rows_of<E>(out), std::min(wait_limit(), kSpin));
-    err = cudaGetLastError();
+    err = launch_early(kern, items, kThreads, TcShape<D>::kSmem, st, a, rows_of<E>(q), rows_of<E>(out),
+                       std::min(wait_limit(), kSpin));
   };
   for_dim(dim, [&](auto dv) {
     auto typed = [&](auto ev) {

@@ -78,6 +78,7 @@ template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(256) k_norm_rope(const __grid_constant__ RotateArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
   __shared__ __align__(16) T ring[kAhead * 2 * 256 * 4];
+  after_predecessor();
   const int l = threadIdx.x % GS;
   const int64_t g = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS;
   const int64_t token = g / a.nchunk;
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(256, 2) k_kv_append(const __grid_constant__ Ap
   __shared__ float red[2][8];
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS, rpp = blockDim.x / GS;
   const LaneMap m = lane_map<D, INTER>(a.nr, l);
+  after_predecessor();
 
   if (blockIdx.x >= a.kv_ctas) {
     const int64_t g = (int64_t)(blockIdx.x - a.kv_ctas) * rpp + grp;
@@ -351,6 +353,7 @@ struct ReadArgs {
 template <typename T, int D, bool INT8>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ ReadArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
+  after_predecessor();
   const int l = threadIdx.x % GS;
   const int64_t g = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS;
   if (g >= (int64_t)a.B * a.T_ * a.sides * a.nchunk || l >= HeadLanes<D>::kUsed) return;
@@ -467,11 +470,6 @@ int head_chunk(int64_t tokens, int heads, int lanes) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(heads, all / room));
 }
 
-zg_status after_launch(const char* what) {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? ZG_OK : cuda_fail(e, what);
-}
-
 }  // namespace
 
 zg_status bad_arg(const char* call, const std::string& what) {
@@ -543,16 +541,17 @@ zg_status zg_qk_norm_rope(const zg_norm_rope* nr, const zg_rows* q, const zg_row
   const int chunk = head_chunk(tokens, heads, lanes), nchunk = (heads + chunk - 1) / chunk;
   const int64_t ctas = (tokens * nchunk * lanes + 255) / 256;
   if (ctas > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_qk_norm_rope: more than 2^31 CTAs");
+  cudaError_t err = cudaSuccess;
   for_type(dt, [&](auto e) {
     using E = typename decltype(e)::type;
     const RotateArgs<E> a = {rows_of<E>(q), rows_of<E>(k), rows_of<E>(q_out), rows_of<E>(k_out), positions,
                              B, T, Hq, Hk, chunk, nchunk, na};
     for_dim(dim, [&](auto dv) {
       auto kern = na.inter ? k_norm_rope<E, decltype(dv)::value, true> : k_norm_rope<E, decltype(dv)::value, false>;
-      kern<<<(unsigned)ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      err = launch_early(kern, ctas, 256, 0, static_cast<cudaStream_t>(stream), a);
     });
   });
-  return after_launch("norm and rotation launch");
+  return err == cudaSuccess ? ZG_OK : cuda_fail(err, "norm and rotation launch");
 } catch (...) {
   return ZG_ERR_OUT_OF_MEMORY;
 }
@@ -607,11 +606,10 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
                       ? (na.inter ? k_kv_append<E, D, true, true> : k_kv_append<E, D, true, false>)
                       : (na.inter ? k_kv_append<E, D, false, true> : k_kv_append<E, D, false, false>);
       if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (err == cudaSuccess) kern<<<(unsigned)(kv + qc), threads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+      if (err == cudaSuccess) err = launch_early(kern, kv + qc, threads, smem, static_cast<cudaStream_t>(stream), a);
     });
   });
-  if (err != cudaSuccess) return cuda_fail(err, "cache append launch");
-  return after_launch("cache append launch");
+  return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache append launch");
 } catch (...) {
   return ZG_ERR_OUT_OF_MEMORY;
 }
@@ -636,19 +634,18 @@ zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int32_t max
   if (groups > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_read: more than 2^31 (token, side, head chunk)s");
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
+  cudaError_t err = cudaSuccess;
   for_type(dt, [&](auto e) {
     using E = typename decltype(e)::type;
     const ReadArgs<E> a = {view(cache, table, max_blocks, status), rows_of<E>(k_out), rows_of<E>(v_out), start, n,
                            B, T, sides, k_out ? 0 : 1, chunk, nchunk};
     for_dim(cache->dim, [&](auto dv) {
       constexpr int D = decltype(dv)::value;
-      if (cache->format == ZG_KV_INT8)
-        k_kv_read<E, D, true><<<(unsigned)ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-      else
-        k_kv_read<E, D, false><<<(unsigned)ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      auto kern = cache->format == ZG_KV_INT8 ? k_kv_read<E, D, true> : k_kv_read<E, D, false>;
+      err = launch_early(kern, ctas, 256, 0, static_cast<cudaStream_t>(stream), a);
     });
   });
-  return after_launch("cache read launch");
+  return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache read launch");
 } catch (...) {
   return ZG_ERR_OUT_OF_MEMORY;
 }
