@@ -21,7 +21,7 @@
 // An item of one query tile takes both places: each has the same queries and
 // every other step, and their sums are joined at the end.
 // Measured: causal chunks of 2,048 rows over up to 16,384 tokens (2 requests, 16
-// heads over 4 of 128) 393 us, 1.03 PFLOP/s or 55 % of the measured bf16 rate;
+// heads over 4 of 128) 391 us, 1.04 PFLOP/s or 55 % of the measured bf16 rate;
 // 256 rows each for 64 requests over up to 2,048 tokens 59 us.  Bound by the
 // waits in the chain softmax -> product -> scores of a tile, some 3,300 cycles a
 // step of which the tensor cores work 2,200 for the two: with the widening, the

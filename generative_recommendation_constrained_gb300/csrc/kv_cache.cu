@@ -72,7 +72,7 @@ __device__ __forceinline__ void turn_heads(const NormRopeArgs& a, const LaneMap&
 
 // One group of lanes a (token, chunk of heads): the angles are computed once
 // for the chunk.  Bound by memory: 32 x 4,096 tokens of 20 heads of 128 (bf16,
-// 1.34 GB in and out) take 205 us, 6.56 TB/s of 6.75 copied; with a head at a
+// 1.34 GB in and out) take 202 us, 6.63 TB/s of 6.75 copied; with a head at a
 // time in registers 338 us, with four 571 (94 registers).  Heads 0..Hq-1 are the queries, Hq..Hq+Hk-1 the keys.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(256) k_norm_rope(const __grid_constant__ RotateArgs<T> a) {
@@ -137,7 +137,7 @@ struct Piece {
 // this one's are turned, kept in registers between the maximum and the codes,
 // and written.  CTAs past kv_ctas turn the queries.  Bound by issue and the
 // chains of its shuffles: 32 x 2,048 tokens, 16 + 4 heads of 128, bf16 to e4m3
-// with norm and rotation take 156 us (738 MB, 4.7 TB/s); a piece a CTA, loaded
+// with norm and rotation take 154 us (738 MB, 4.8 TB/s); a piece a CTA, loaded
 // into registers, took 387.
 template <typename T, int D, bool INT8, bool INTER>
 __global__ void __launch_bounds__(256, 2) k_kv_append(const __grid_constant__ AppendArgs<T> a) {
@@ -349,7 +349,7 @@ struct ReadArgs {
 
 // One group of lanes a (token, side, chunk of heads), eight codes a lane and
 // head, four heads in flight.  16 x 1,000 tokens of 4 heads of 64 written and
-// read back: 18.4 us (22.6 with a group a head and its divisions).
+// read back: 15.4 us (a group a head, with its divisions, 4 us more).
 template <typename T, int D, bool INT8>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ ReadArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
