@@ -688,13 +688,13 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   zg_status st;
   if ((st = check_cache(cache, table, max_blocks, call)) != ZG_OK) return st;
   if ((st = check_attn(cache, max_blocks, B, R, Hq, call)) != ZG_OK) return st;
+  if (B == 0 || R == 0) return ZG_OK;
   if ((st = check_rows(q, "q", -1, call)) != ZG_OK) return st;
   if (q->dtype == ZG_F32) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_attention: q must be ZG_BF16 or ZG_F16");
   if ((st = check_rows(out, "out", q->dtype, call)) != ZG_OK) return st;
   if (!length) return bad_arg(call, "length is NULL");
   if (!(scale > 0.f && std::isfinite(scale))) return bad_arg(call, "scale must be finite and > 0");
   if (lse && reinterpret_cast<uintptr_t>(lse) % 4) return bad_arg(call, "lse must be 4-byte aligned");
-  if (B == 0 || R == 0) return ZG_OK;
   const AttnPlan p = attn_plan(cache, max_blocks, B, R, Hq);
   if (p.bytes && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < p.bytes))
     return bad_arg(call, "workspace must hold zg_kv_attention_workspace_size bytes, 256-byte aligned");

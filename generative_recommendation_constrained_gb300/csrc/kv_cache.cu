@@ -72,7 +72,7 @@ __device__ __forceinline__ void turn_heads(const NormRopeArgs& a, const LaneMap&
 
 // One group of lanes a (token, chunk of heads): the angles are computed once
 // for the chunk.  Bound by memory: 32 x 4,096 tokens of 20 heads of 128 (bf16,
-// 1.34 GB in and out) take 202 us, 6.63 TB/s of 6.75 copied; with a head at a
+// 1.34 GB in and out) take 203 us, 6.6 TB/s of 6.75 copied; with a head at a
 // time in registers 338 us, with four 571 (94 registers).  Heads 0..Hq-1 are the queries, Hq..Hq+Hk-1 the keys.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(256) k_norm_rope(const __grid_constant__ RotateArgs<T> a) {
@@ -137,7 +137,7 @@ struct Piece {
 // this one's are turned, kept in registers between the maximum and the codes,
 // and written.  CTAs past kv_ctas turn the queries.  Bound by issue and the
 // chains of its shuffles: 32 x 2,048 tokens, 16 + 4 heads of 128, bf16 to e4m3
-// with norm and rotation take 154 us (738 MB, 4.8 TB/s); a piece a CTA, loaded
+// with norm and rotation take 155 us (738 MB, 4.8 TB/s); a piece a CTA, loaded
 // into registers, took 387.
 template <typename T, int D, bool INT8, bool INTER>
 __global__ void __launch_bounds__(256, 2) k_kv_append(const __grid_constant__ AppendArgs<T> a) {
@@ -349,7 +349,8 @@ struct ReadArgs {
 
 // One group of lanes a (token, side, chunk of heads), eight codes a lane and
 // head, four heads in flight.  16 x 1,000 tokens of 4 heads of 64 written and
-// read back: 15.4 us (a group a head, with its divisions, 4 us more).
+// read back: 17.5 us (a group a head, with its
+// divisions, 4 us more).
 template <typename T, int D, bool INT8>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ ReadArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
@@ -523,6 +524,7 @@ zg_status zg_qk_norm_rope(const zg_norm_rope* nr, const zg_rows* q, const zg_row
   if (!nr) return bad_arg(call, "norm_rope is NULL");
   if (!dim_ok(dim)) return fail(ZG_ERR_UNSUPPORTED, "zg_qk_norm_rope: dim must be 32, 64, 96 or 128");
   if (B < 0 || T < 0) return bad_arg(call, "B and T must be >= 0");
+  if (B == 0 || T == 0) return ZG_OK;
   if (Hq < 0 || Hk < 0 || Hq > 1024 || Hk > 1024) return bad_arg(call, "Hq and Hk must be in [0, 1024]");
   if ((!q) != (Hq == 0) || (!k) != (Hk == 0))
     return bad_arg(call, "q and k are NULL exactly when their head count is 0");
@@ -536,7 +538,6 @@ zg_status zg_qk_norm_rope(const zg_norm_rope* nr, const zg_rows* q, const zg_row
   if ((st = nr_args(nr, dim, call, &na)) != ZG_OK) return st;
   if (na.rot && !positions) return bad_arg(call, "positions is NULL");
   const int64_t tokens = (int64_t)B * T;
-  if (tokens == 0) return ZG_OK;
   const int lanes = group_lanes(dim), heads = Hq + Hk;
   const int chunk = head_chunk(tokens, heads, lanes), nchunk = (heads + chunk - 1) / chunk;
   const int64_t ctas = (tokens * nchunk * lanes + 255) / 256;
@@ -563,6 +564,7 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
   zg_status st;
   if ((st = check_cache(cache, table, max_blocks, call)) != ZG_OK) return st;
   if (B < 0 || T < 0) return bad_arg(call, "B and T must be >= 0");
+  if (B == 0 || T == 0) return ZG_OK;
   if ((st = check_rows(k, "k", -1, call)) != ZG_OK || (st = check_rows(v, "v", k->dtype, call)) != ZG_OK) return st;
   if (Hq < 0 || Hq > 1024 || (!q) != (Hq == 0))
     return bad_arg(call, "Hq must be in [0, 1024], and 0 exactly when q is NULL");
@@ -575,7 +577,6 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
   if (!start) return bad_arg(call, "start is NULL");
   NormRopeArgs na;
   if ((st = nr_args(nr, cache->dim, call, &na)) != ZG_OK) return st;
-  if (B == 0 || T == 0) return ZG_OK;
   const int bt = cache->block_tokens, lanes = group_lanes(cache->dim);
   const int64_t jmax = ((int64_t)T + bt - 2) / bt + 1;
   // eight rows a lane group at most: groups for min(T, bt) rows, whole warps
@@ -621,12 +622,12 @@ zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int32_t max
   zg_status st;
   if ((st = check_cache(cache, table, max_blocks, call)) != ZG_OK) return st;
   if (B < 0 || T < 0) return bad_arg(call, "B and T must be >= 0");
+  if (B == 0 || T == 0) return ZG_OK;
   if (!k_out && !v_out) return bad_arg(call, "neither k_out nor v_out given");
   const int dt = k_out ? k_out->dtype : v_out->dtype;
   if (k_out && (st = check_rows(k_out, "k_out", dt, call)) != ZG_OK) return st;
   if (v_out && (st = check_rows(v_out, "v_out", dt, call)) != ZG_OK) return st;
   if (!start) return bad_arg(call, "start is NULL");
-  if (B == 0 || T == 0) return ZG_OK;
   const int sides = (k_out ? 1 : 0) + (v_out ? 1 : 0);
   const int lanes = group_lanes(cache->dim);
   const int chunk = head_chunk((int64_t)B * T * sides, cache->heads, lanes), nchunk = (cache->heads + chunk - 1) / chunk;

@@ -90,6 +90,8 @@ def _rows(x: torch.Tensor | None):
     sb, st, sh, se = x.stride()
     if se != 1:
         raise ValueError("the last dimension of the rows must be contiguous")
+    if not x.is_cuda:
+        raise ValueError("the rows must be on the GPU")
     if sb < 0 or st < 0 or sh < 0:
         raise ValueError("strides of the rows must not be negative")
     return _pack_rows(x.data_ptr(), dt, 0, sb, st, sh)
@@ -101,8 +103,8 @@ def _stream(stream, x: torch.Tensor):
 
 
 def _int32(x: torch.Tensor | None, shape, name: str):
-    if x is not None and (x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+    if x is not None and (x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous() or not x.is_cuda):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on the GPU")
 
 
 class NormRope:
@@ -113,8 +115,9 @@ class NormRope:
     def __init__(self, dim: int, q_gain=None, k_gain=None, eps: float = 1e-6, rot_dim: int | None = None,
                  theta: float = 10000.0, interleaved: bool = False, norm: bool = True, freq=None):
         for g in (q_gain, k_gain):
-            if g is not None and (g.dtype != torch.float32 or tuple(g.shape) != (dim,) or not g.is_contiguous()):
-                raise ValueError("gains must be contiguous float32 tensors of shape [dim]")
+            if g is not None and (g.dtype != torch.float32 or tuple(g.shape) != (dim,) or not g.is_contiguous() or
+                                  not g.is_cuda):
+                raise ValueError("gains must be contiguous float32 tensors of shape [dim] on the GPU")
         self.dim, self.q_gain, self.k_gain = dim, q_gain, k_gain
         self.struct = Z.make_norm_rope(norm, eps, q_gain, k_gain, dim if rot_dim is None else rot_dim, interleaved,
                                        theta, freq)
@@ -167,8 +170,8 @@ class KVCache:
                 raise ValueError("k_codes and v_codes must be alike")
             if like is None and (x.dtype != torch.float32 or x.shape != k_codes.shape[:2]):
                 raise ValueError("scales must be float32 [n_blocks, heads]")
-        if not all(x.is_contiguous() for x in (k_codes, v_codes, k_scale, v_scale)):
-            raise ValueError("codes and scales must be contiguous")
+        if not all(x.is_contiguous() and x.is_cuda for x in (k_codes, v_codes, k_scale, v_scale)):
+            raise ValueError("codes and scales must be contiguous and on the GPU")
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.n_blocks, self.heads, self.block_tokens, self.dim = k_codes.shape
         self.struct = Z.make_kv_cache(_CODE_TYPES[k_codes.dtype], self.n_blocks, self.heads, self.block_tokens,

@@ -620,6 +620,19 @@ def test_cache_past_32_bits(zg, dev):
     check_attention(zg, dev, c, randn((2, 20, 8, dim), torch.bfloat16, 5), table, ints([300, 257]), None, False)
 
 
+def test_empty_tensors(zg, dev):
+    """Calls of no tokens or no requests: nothing runs, nothing changes."""
+    c = new_cache(dev, "int8", 4, 16, 2, 64)
+    x = torch.empty((1, 0, 2, 64), device="cuda", dtype=torch.bfloat16)
+    t = ints([[0, 1]])
+    c.append(x, x, t, ints([0]), q=x, norm_rope=dev.NormRope(64))
+    c.read(t, ints([0]), None, x, x)
+    assert dev.NormRope(64)(x, x, torch.empty((1, 0), dtype=torch.int32, device="cuda"))[0].shape == x.shape
+    assert dev.CacheAttention(c, 1, 0, 2, 2)(x, t, ints([5]))[0].numel() == 0
+    ok(zg)
+    assert (c.k_codes.view(torch.uint8) == 0x7F).all()
+
+
 def test_wrappers_refuse_shapes(dev):
     c = dev.KVCache(4, 16, 2, 64)
     x = torch.zeros((1, 2, 2, 64), device="cuda", dtype=torch.bfloat16)
@@ -627,7 +640,10 @@ def test_wrappers_refuse_shapes(dev):
     for f in (lambda: c.append(x, x[:, :1], t, s), lambda: c.append(x, x, t.long(), s), lambda: c.append(x, x, t, ints([0, 0])),
               lambda: c.append(x.double(), x, t, s), lambda: c.read(t, s, None, x[:, :, :1]),
               lambda: dev.CacheAttention(c, 1, 1, 2, 2)(x, t, s), lambda: dev.CacheAttention(c, 1, 2, 2, 3)(x, t, s),
-              lambda: dev.KVCache.over(c.k_codes, c.v_codes, c.k_scale, c.v_scale[:2])):
+              lambda: dev.KVCache.over(c.k_codes, c.v_codes, c.k_scale, c.v_scale[:2]),
+              lambda: dev.KVCache.over(c.k_codes.cpu(), c.v_codes.cpu(), c.k_scale.cpu(), c.v_scale.cpu()),
+              lambda: c.append(x.cpu(), x, t, s), lambda: c.append(x, x, t.cpu(), s), lambda: c.append(x, x, t, s.cpu()),
+              lambda: dev.NormRope(64, torch.ones(64))):
         with pytest.raises(ValueError):
             f()
 

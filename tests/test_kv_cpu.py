@@ -152,6 +152,17 @@ def test_attention_refusals(zg):
     assert lib.zg_kv_attention_workspace_size(C.byref(c), 4, 1, 1, 2, None) == 1
 
 
+def test_empty_calls_need_no_rows(zg):
+    """Sizes of 0 do nothing, and an empty tensor has no address."""
+    c, n, e, r = cache(zg), nrope(zg), rows(zg, data=None), rows(zg)
+    for B, T in ((0, 3), (3, 0)):
+        zg.zg_qk_norm_rope(n, e, e, e, e, None, B, T, 2, 2, 64)
+        zg.zg_kv_append(c, n, e, e, None, None, 0, P, 4, None, None, B, T)
+        zg.zg_kv_read(c, P, 4, None, None, B, T, e, e)
+        zg.zg_kv_attention(c, P, 4, None, None, e, e, None, B, T, 2, 1.0, False, None, 0)
+    refused(zg, 1, "B and T", zg.zg_kv_read, c, P, 4, P, None, -1, 0, r, r)
+
+
 def test_workspace_covers_smaller_calls(zg):
     """A workspace sized for a batch serves no less than the same batch needs: equal sizes, equal answers."""
     c = cache(zg)
