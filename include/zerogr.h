@@ -514,7 +514,9 @@ ZG_API zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int3
  * scaled by a power of two first; both relative 2^-11), codes exactly; sums,
  * maxima and outputs are 32-bit.  Cached e4m3 codes within length must not
  * be NaN; nothing behind it is used.  Hq a multiple of heads, at most 1024;
- * B * R * Hq below 2^31. */
+ * B * R * Hq below 2^31, and the tables' tokens / 128 * B * heads (times the
+ * row tiles of an item) too, else ZG_ERR_UNSUPPORTED.  Kernels may start while
+ * their predecessor in the stream ends; they wait before they touch memory. */
 ZG_API zg_status zg_kv_attention_workspace_size(const zg_kv_cache* cache, int32_t max_blocks, int32_t B,
                                                 int32_t R, int32_t Hq, size_t* bytes);
 ZG_API zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,
