@@ -4,7 +4,11 @@
 //
 //   norm     y = x / sqrt(mean(x^2) + eps) * gain over a head
 //   rotation (a, b) -> (a cos - b sin, a sin + b cos) by position * frequency
-//   code     rne(y / scale), scale = max |y| of a (block, head) / Q
+//   code     rne(y * inv), scale = max |y| of a (block, head) / Q, and inv the
+//            reciprocal of max |y| * (1 / Q), which differs from the scale's
+//            in its last bits at most: a tensor divided by a number is a
+//            product with the number's reciprocal in torch, and the codes
+//            equal those of elementary float32 operations bit for bit
 //
 // A lane holds eight elements of a head as two vectors of four that make four
 // whole rotation pairs, so the rotation needs no exchange between lanes and
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(256, 2) k_kv_append(const __grid_constant__ Ap
       red_of ^= 1;
       float s1 = fmaxf(s0, __fdiv_rn(top, Q));
       if (s1 < FLT_MIN) s1 = 0.f;  // 1 / s1 stays finite
-      const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
+      const float inv = s1 > 0.f ? __frcp_rn(fmaxf(s0, top * (1.f / Q))) : 0.f;
       if (threadIdx.x == 0) *scale = s1;
       if (bad) atomicOr(a.c.status, kStatusNonFinite);
       if (s1 > s0 && m.used) {

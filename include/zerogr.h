@@ -481,6 +481,10 @@ ZG_API zg_status zg_qk_norm_rope(const zg_norm_rope* nr, const zg_rows* q, const
  *     (int8); below 2^-126 it is held as 0;
  *   code = x * (1 / scale), rounded to nearest even, within +-Q; the rows
  *     that the block already holds are coded again if the scale has grown.
+ *     The reciprocal is that of max(its scale, largest |x| * (1 / Q)), each
+ *     step rounded to 32 bits, so that codes equal bit for bit those of the
+ *     same steps in elementary float32 operations; the stored scale, the
+ *     quotient rounded once, differs from it in its last bits at most.
  * A NaN is stored as 0 and an infinity as +-Q of the block's finite values;
  * either is recorded for zg_check_device_status, so no NaN enters a cache.
  * nr (may be NULL) is applied to the keys on the way, at positions start[b]

@@ -230,6 +230,51 @@ def test_append_recodes_held_rows(zg, dev):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("dim, heads, bt", [(96, 4, 16), (64, 4, 32), (128, 2, 128), (32, 1, 64)])
+def test_append_codes_of_elementary_operations(zg, dev, fmt, dtype, dim, heads, bt):
+    """Codes are bit for bit those of the same steps in torch's float32, where a division by a number is a product
+    with its reciprocal; the stored scale is the quotient rounded once, at most two units in the last place off."""
+    Q, B, T, more = QMAX[fmt], 3, 1001, 2 * bt + 5
+    nb = -(-(T + more) // bt)
+
+    def coded(y):
+        y = y.clamp(-Q, Q)
+        return (y.round().to(torch.int8) if fmt == "int8" else y.to(torch.float8_e4m3fn)).view(torch.uint8)
+
+    def blocks(x, first):        # [B, T, heads, dim] from row `first` of a block on -> [B, blocks, bt, heads, dim], zeros around
+        n = -(-(first + x.shape[1]) // bt)
+        y = torch.zeros((B, n * bt, heads, dim), device="cuda")
+        y[:, first:first + x.shape[1]] = x.float()
+        return y.view(B, n, bt, heads, dim)
+
+    c = new_cache(dev, fmt, B * nb, bt, heads, dim)
+    table = torch.randperm(B * nb, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda().view(B, nb).contiguous()
+    for start, x in ((0, randn((B, T, 2 * heads, dim), dtype, 3)), (T, randn((B, more, 2 * heads, dim), dtype, 4, scale=3.0))):
+        n, j, first = x.shape[1], start // bt, start % bt
+        at = table[:, j:-(-(start + n) // bt)].long()
+        sides = ((x[:, :, :heads], c.k_codes, c.k_scale), (x[:, :, heads:], c.v_codes, c.v_scale))
+        before = [(codes.view(torch.uint8)[at[:, 0]].clone(), scales[at[:, 0]].clone()) for _, codes, scales in sides]
+        c.append(x[:, :, :heads], x[:, :, heads:], table, ints([start] * B))
+        ok(zg)
+        for (src, codes, scales), (old, s0) in zip(sides, before):
+            f = blocks(src, first)
+            s = f.abs().amax((2, 4)) / Q
+            if first:
+                s[:, 0] = torch.maximum(s[:, 0], s0)
+            inverse = 1.0 / s
+            want = coded(f * inverse[:, :, None, :, None]).permute(0, 1, 3, 2, 4)
+            got = codes.view(torch.uint8)[at]
+            row = torch.arange(at.shape[1] * bt, device="cuda").view(1, -1, 1, bt, 1)
+            assert not ((got != want) & (row >= first) & (row < first + n)).any()
+            if first:                # rows held before: coded again where the scale has grown
+                held = old.view(codes.dtype).float() * s0[:, :, None, None]
+                again = torch.where((s[:, 0] > s0)[:, :, None, None], coded(held * inverse[:, 0, :, None, None]), old)
+                assert torch.equal(got[:, 0, :, :first], again[:, :, :first])
+            assert ((scales[at].double() - s.double()).abs() <= s.double() * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_append_special_values(zg, dev, fmt):
     c = new_cache(dev, fmt, 2, 16, 1, 64)
     x = torch.zeros((1, 2, 1, 64), device="cuda")
