@@ -36,8 +36,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 constexpr int kFewThreads = 128;
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 // What one lane takes of 16 keys and values (rows of D codes in shared
 // memory): of keys g and g + 8 (lane = 4 g + c) the dims of `dim_of`, of values
 // 2c, 2c + 1, 2c + 8, 2c + 9 the dims g * D/8 and on.  The order of the dims
@@ -120,20 +118,6 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, i
 // here (6.3 TB/s) and the rest the join; 64 requests of up to 4,096 tokens (85
 // MB) 25 us, some 6 of them the chain from the lengths to the first codes.
 constexpr uint32_t kFewSpin = 1u << 20;  // polls of a wait at most
-__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, uint32_t limit) {
-  const uint32_t at = smem_addr(bar);
-  bool done = false;
-  for (uint32_t it = 0; it < limit && !done; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(at), "r"(parity)
-        : "memory");
-    done = ok;
-  }
-  return __all_sync(0xFFFFFFFFu, done);
-}
 
 template <typename T, int D, bool INT8, int NT>
 __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const __grid_constant__ AttnArgs a,
@@ -149,7 +133,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int M = a.R * a.G;
 
-  if (threadIdx.x < 8) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[0][0] + threadIdx.x)));
+  if (threadIdx.x < 8) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&full[0][0] + threadIdx.x)));
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   uint32_t issued = 0, taken = 0;  // steps of this warp, over all its items
   bool good = true;
@@ -210,6 +194,16 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
     units = item_units(a, s, ++m, NR);
   }
 
+  auto next_item = [&]() {
+    first += units;
+    if (++m == a.mt) m = 0, ++h;
+    if (h == a.heads) {
+      h = 0;
+      s = seen_of(a, ++b, false);
+    }
+    units = item_units(a, s, m, NR);
+  };
+
   while (u < u_end) {
     const int vmax = item_keys(a, s, m, NR);
     const int v_end = min(u_end, first + units);  // units [u, v_end) of this item are ours
@@ -232,7 +226,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
     uint8_t* mine = ring + warp * (2 * 4 * Tl::kBytes);
     auto fetch = [&](int t, int b0, int b1) {
       if (t >= t1) return;
-      const uint32_t bar = smem_addr(&full[warp][issued & 1]);
+      const uint32_t bar = smem_u32(&full[warp][issued & 1]);
       const int blk = lane & 1 ? b1 : b0, key = t * 32 + (lane & 1) * 16;
       const uint32_t bytes = ((b0 >= 0) + (b1 >= 0)) * 2 * Tl::kBytes;
       if (lane == 0)
@@ -242,7 +236,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
         const int64_t from = (((int64_t)blk * a.heads + h) * a.bt + (key & (a.bt - 1))) * D;
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                smem_addr(mine + ((issued & 1) * 4 + lane) * Tl::kBytes)),
+                smem_u32(mine + ((issued & 1) * 4 + lane) * Tl::kBytes)),
             "l"((lane & 2 ? a.vc : a.kc) + from), "r"(Tl::kBytes), "r"(bar)
             : "memory");
       }
@@ -323,7 +317,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       scales(b0, ksn[0], vsn[0]);
       scales(b1, ksn[1], vsn[1]);
       const uint8_t* tiles = mine + (taken & 1) * 4 * Tl::kBytes;
-      good = wait_full(&full[warp][taken & 1], (taken >> 1) & 1, spin);
+      good = warp_wait(&full[warp][taken & 1], (taken >> 1) & 1, spin);
       if (!good) break;
       ++taken;
       const int key0 = t * 32;
@@ -438,7 +432,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
     }
     if (!good) {  // a copy has not come: recorded; what is still on its way lands before the CTA ends
       if (lane == 0) atomicOr(a.status, kStatusTimeout);
-      for (; taken < issued; ++taken) wait_full(&full[warp][taken & 1], (taken >> 1) & 1, kFewSpin);
+      for (; taken < issued; ++taken) warp_wait(&full[warp][taken & 1], (taken >> 1) & 1, kFewSpin);
     }
     __syncthreads();  // the sums take the ring's place
     // join the warps: accumulator tile j, element (e, row g or g + 8) is row 2c + e, dim g * D/8 + 2 j (+ 1)
@@ -495,16 +489,18 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (__syncthreads_or(!good)) return;  // the joined warps' buffers are free again
+    const bool gone = __syncthreads_or(!good);  // the joined warps' buffers are free again
     u = v_end;
-    if (u < u_end) {
-      first += units;
-      if (++m == a.mt) m = 0, ++h;
-      if (h == a.heads) {
-        h = 0;
-        s = seen_of(a, ++b, false);
+    if (u < u_end) next_item();
+    if (gone) {
+      // the items that begin in the rest of the share are left out: one part, which the join passes by (their outputs are
+      // not defined), since it would follow whatever the workspace holds there
+      while (u < u_end) {
+        if (a.info && threadIdx.x == 0) a.info[((int64_t)b * a.heads + h) * a.mt + m] = make_int2(0, 1);
+        u = first + units;
+        if (u < u_end) next_item();
       }
-      units = item_units(a, s, m, NR);
+      return;
     }
   }
 }
@@ -532,6 +528,10 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
     const int2 e = a.info[item];
     parts = e.y;
     slot0 = e.x, later = e.x & ~1, step = 2;
+    if (e.x < 0 || parts < 1 || (e.x >> 1) + (int64_t)parts > a.slots / 2) {  // another call has written the workspace
+      if (lane == 0) atomicOr(a.status, kStatusCache);
+      parts = 1;
+    }
   } else {
     const Seen s = seen_of(a, b, false);
     parts = parts_of(a, item_keys(a, s, m, a.tile));

@@ -70,39 +70,13 @@ struct TcShape {
   static __device__ __forceinline__ int step(int n) { return kApart ? (n & 1 ? (n + 1) / 2 : n ? n / 2 - 1 : 0) : n / 2; }
 };
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(n));
 }
 __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Bounded wait for the phase of the given parity; false on expiry.  A poll
-// suspends the thread for up to a microsecond or so; under a limit of a few
-// polls (the debug hook's) it does not, so that the wait does run out.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
-  const uint32_t a = smem_u32(bar);
-  for (uint32_t it = 0; it < limit; ++it) {
-    uint32_t done;
-    if (limit > 64)
-      asm volatile(
-          "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-          : "=r"(done)
-          : "r"(a), "r"(parity)
-          : "memory");
-    else
-      asm volatile(
-          "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-          : "=r"(done)
-          : "r"(a), "r"(parity)
-          : "memory");
-    if (done) return true;
-  }
-  return false;
-}
-// The same for the warp that issues the products, without suspending: it is on
+// bar_wait for the warp that issues the products, without suspending: it is on
 // the critical path of every step (causal chunks 393 us against 399; the other
 // warps' waits are better suspended, 403 and 424 with theirs spinning too).
 __device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
@@ -115,10 +89,6 @@ __device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, uint32
         : "r"(a), "r"(parity)
         : "memory");
   return __all_sync(0xFFFFFFFFu, done);
-}
-// The same for a whole warp: one answer for all its lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
-  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, limit));
 }
 
 // One lane of the (converged) warp.

@@ -73,6 +73,36 @@ __device__ __forceinline__ int row_exponent(float top) {
   return max(e, -120);
 }
 
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// Bounded wait for the phase of the given parity; false on expiry.  A poll
+// suspends the thread for up to a microsecond or so; under a limit of a few
+// polls (the debug hook's) it does not, so that the wait does run out.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
+  const uint32_t a = smem_u32(bar);
+  for (uint32_t it = 0; it < limit; ++it) {
+    uint32_t done;
+    if (limit > 64)
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+          : "=r"(done)
+          : "r"(a), "r"(parity)
+          : "memory");
+    else
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+          : "=r"(done)
+          : "r"(a), "r"(parity)
+          : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+// The same for a whole warp: one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, limit));
+}
 
 // Many query rows: the products on the tensor cores' tcgen05 path
 // (kv_attention_tc.cu).  Query rows of an item, and its launch.

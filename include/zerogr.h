@@ -552,8 +552,9 @@ ZG_API void zg_debug_inject_build_failure(int32_t point, int32_t after);
  * kernels set instead of trapping (bit 0: row out of range, bit 1: token out
  * of range, bit 2: a bounded wait in a tensor-core kernel expired, bit 3:
  * tensor-memory allocation failed, bit 4: a select found fewer candidates
- * than its own cut guarantees, bit 5: a history cache's block number or length
- * out of range, bit 6: a NaN or an infinity written to a history cache).
+ * than its own cut guarantees, bit 5: a history cache's block number or length,
+ * or a workspace entry of its attention, out of range, bit 6: a NaN or an
+ * infinity written to a history cache).
  * Non-zero -> ZG_ERR_DEVICE_STATUS. */
 ZG_API zg_status zg_check_device_status(void* stream);
 

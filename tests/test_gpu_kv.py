@@ -709,6 +709,34 @@ def test_expired_wait_is_reported(zg, dev):
     check_attention(zg, dev, c, q, table, length, None, False)
 
 
+@pytest.mark.parametrize("R, G", [(1, 2), (9, 1)])
+def test_expired_wait_of_few_rows_is_reported(zg, dev, R, G):
+    """The same for few rows, where a CTA's share holds several items and items lie in several CTAs: the items that a
+    CTA leaves out are passed by, whatever the workspace held before."""
+    lengths = [1 + 31 * b % 200 for b in range(120)] + [20000, 0, 3000, 9000]
+    c, table, length = build(dev, "int8", len(lengths), 2, 64, 64, lengths, 313, 3)
+    q = randn((len(lengths), R, 2 * G, 64), torch.bfloat16, 3)
+    attn = dev.CacheAttention(c, len(lengths), R, 2 * G, 313)
+    assert attn.ws_bytes > 0
+    attn.ws.fill_(0x41)
+    zg.zg_debug_set_wait_limit(1)
+    try:
+        attn(q, table, length)
+        torch.cuda.synchronize()
+        with pytest.raises(zg.ZgError, match="wait expired"):
+            zg.zg_check_device_status(0)
+    finally:
+        zg.zg_debug_set_wait_limit(0)
+    want = torch.full_like(attn.out, math.nan)
+    want.copy_(attn(q, table, length)[0])
+    ok(zg)
+    some = [3, 117, 120, 121, 122]
+    check_attention(zg, dev, c, q[some].contiguous(), table[some].contiguous(), length[some].contiguous(), None, False)
+    attn.ws.fill_(0x41)
+    assert torch.equal(attn(q, table, length)[0], want)
+    ok(zg)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_example_history_decode(zg, fmt):
     """The example's path end to end: the request vectors against attention in 64 bits over what the cache holds, and
