@@ -102,6 +102,16 @@ def _stream(stream, x: torch.Tensor):
     return torch._C._cuda_getCurrentRawStream(x.device.index) if stream is None else stream
 
 
+def _out_like(x: torch.Tensor, stream):
+    """A new output like x for work on `stream`.  It comes from that stream's memory: a block that the current stream
+    has given back may still be read by work queued there."""
+    if stream is None or stream == torch._C._cuda_getCurrentRawStream(x.device.index):
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    on = torch.cuda.ExternalStream(stream, device=x.device) if stream else torch.cuda.default_stream(x.device)
+    with torch.cuda.stream(on):
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _int32(x: torch.Tensor | None, shape, name: str):
     if x is not None and (x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous() or not x.is_cuda):
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on the GPU")
@@ -124,7 +134,8 @@ class NormRope:
 
     def __call__(self, q, k, positions, q_out=None, k_out=None, stream: int | None = None):
         """Rows q [B, T, Hq, dim] and k [B, T, Hk, dim] (either may be None) at int32 positions [B, T]; outputs
-        default to new tensors and may be the inputs themselves."""
+        default to new tensors and may be the inputs themselves.  New tensors belong to `stream` (the raw handle; the
+        current stream when None) as if made while it was current."""
         x = q if q is not None else k
         B, T = x.shape[:2]
         _int32(positions, (B, T), "positions")
@@ -132,9 +143,9 @@ class NormRope:
             if i is not None and (i.shape[:2] != x.shape[:2] or i.shape[3] != self.dim):
                 raise ValueError("q and k must be [B, T, heads, dim]")
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _out_like(q, stream)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            k_out = _out_like(k, stream)
         for i, o in ((q, q_out), (k, k_out)):
             if i is not None and o.shape != i.shape:
                 raise ValueError("an output must have its input's shape")
@@ -181,7 +192,7 @@ class KVCache:
                stream: int | None = None):
         """Writes k, v [B, T, heads, dim] behind the start[b] tokens that each request holds (n_new[b] of the T
         rows, all when None); norm_rope turns the keys on the way, and q [B, T, Hq, dim] into q_out, which is
-        returned."""
+        returned (a new tensor when None; it belongs to `stream`, as in NormRope)."""
         B, T = k.shape[:2]
         if k.shape != v.shape or k.shape[2] != self.heads or k.shape[3] != self.dim:
             raise ValueError("k and v must be [B, T, heads, dim] of the cache")
@@ -196,7 +207,7 @@ class KVCache:
             if q.shape[:2] != k.shape[:2] or q.shape[3] != self.dim:
                 raise ValueError("q must be [B, T, Hq, dim]")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                q_out = _out_like(q, stream)
             elif q_out.shape != q.shape:
                 raise ValueError("q_out must have q's shape")
         Z.zg_kv_append(self.struct, norm_rope.struct if norm_rope is not None else None, _rows(k), _rows(v), _rows(q),

@@ -567,6 +567,32 @@ def test_attention_strides_and_streams(zg, dev):
         assert torch.equal(o[..., :64], want) and not wide[:, :, :5].any() and not wide[..., 64:].any()
 
 
+def test_new_outputs_on_another_stream(zg, dev):
+    """Outputs made by a call on a stream that is not the current one are none of the current stream's memory: blocks
+    given back there may still be read by queued work."""
+    q = randn((4, 300, 4, 64), torch.bfloat16, 1)
+    pos = torch.arange(300, dtype=torch.int32, device="cuda").repeat(4, 1).contiguous()
+    nr = dev.NormRope(64)
+    c = new_cache(dev, "int8", 80, 16, 4, 64)
+    table = torch.arange(80, dtype=torch.int32, device="cuda").view(4, 20).contiguous()
+    start = ints([0] * 4)
+    want = nr(q, None, pos)[0].clone()
+    ok(zg)
+    free = [torch.empty_like(q) for _ in range(4)]
+    mine = {x.data_ptr() for x in free}
+    del free                                     # four blocks of the outputs' size in the current stream's memory
+    for handle in (torch.cuda.Stream().cuda_stream, 0):
+        with torch.cuda.stream(torch.cuda.Stream()) if handle == 0 else torch.cuda.stream(None):
+            here = [torch.empty_like(q) for _ in range(4)]
+            taken = mine | {x.data_ptr() for x in here}
+            del here
+            outs = [*nr(q, q, pos, stream=handle), c.append(q, q, table, start, q=q, norm_rope=nr, stream=handle)]
+        ok(zg)
+        assert all(torch.equal(o, want) for o in outs)
+        if handle:
+            assert not taken & {o.data_ptr() for o in outs}
+
+
 def test_attention_in_a_graph(zg, dev):
     """Write, then attend, captured once and replayed on new data."""
     c = new_cache(dev, "e4m3", 8, 16, 2, 64)

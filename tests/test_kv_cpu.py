@@ -1,6 +1,7 @@
 """Refusals and sizes of the history-cache calls, without a GPU: every argument
 check comes before any CUDA call, so the pointers here are never followed."""
 import ctypes as C
+import math
 
 import pytest
 
@@ -175,3 +176,73 @@ def test_binding_structs_match_the_header(zg):
     """Sizes of the argument structs as the C compiler lays them out."""
     from generative_recommendation_constrained_gb300 import _lib
     assert C.sizeof(_lib.zg_rows) == 40 and C.sizeof(_lib.zg_kv_cache) == 56 and C.sizeof(_lib.zg_norm_rope) == 48
+
+
+class Rows:
+    """A stand-in for a tensor on the GPU: what the wrappers ask of one."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype=None, index=0):
+        import torch
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype or torch.bfloat16, torch.device("cuda", index)
+
+    def stride(self):
+        return tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
+
+    def dim(self):
+        return len(self.shape)
+
+    def data_ptr(self):
+        return P
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.device.index
+
+
+@pytest.fixture
+def fake_cuda(zg, monkeypatch):
+    """The wrappers with a current device and stream (handle 7) of no GPU; calls into the library are recorded."""
+    import contextlib
+
+    import torch
+    from generative_recommendation_constrained_gb300 import device
+    seen = {"stream": 7, "made": [], "calls": [], "device": 0}
+
+    @contextlib.contextmanager
+    def current(s):
+        before, seen["stream"] = seen["stream"], s
+        yield
+        seen["stream"] = before
+
+    def empty(shape, dtype=None, device=None):
+        seen["made"].append(seen["stream"])
+        return Rows(shape, dtype, torch.device(device).index or 0)
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.cuda, "stream", current)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: seen["device"])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: seen["stream"], raising=False)
+    for name in ("zg_qk_norm_rope", "zg_kv_append", "zg_kv_read", "zg_kv_attention"):
+        monkeypatch.setattr(device.Z, name, lambda *a, name=name: seen["calls"].append((name, a[-1])))
+    monkeypatch.setattr(device.Z, "zg_kv_attention_workspace_size", lambda *a: 256)
+    return device, seen
+
+
+@pytest.mark.parametrize("stream, of", [(None, 7), (7, 7), (42, 42), (0, 0)])
+def test_outputs_belong_to_the_stream_that_writes_them(fake_cuda, stream, of):
+    """A new output comes from the memory of the stream that the kernel runs on, not from the current one's."""
+    import torch
+    dev, seen = fake_cuda
+    x, pos = Rows((2, 3, 4, 64)), Rows((2, 3), torch.int32)
+    nr = dev.NormRope(64)
+    nr(x, x, pos, stream=stream)
+    assert seen["made"] == [of, of] and seen["calls"] == [("zg_qk_norm_rope", of)]
+    codes, scales = Rows((8, 4, 16, 64), torch.int8), Rows((8, 4), torch.float32)
+    dev.KVCache.over(codes, codes, scales, scales).append(x, x, Rows((2, 5), torch.int32), Rows((2,), torch.int32), q=x,
+                                                          norm_rope=nr, stream=stream)
+    assert seen["made"] == [of] * 3 and seen["calls"][1:] == [("zg_kv_append", of)]
