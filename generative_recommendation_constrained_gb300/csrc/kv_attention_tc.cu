@@ -433,13 +433,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Lane g brings keys 16 g .. 16 g + 15 of a step.  Block numbers and scales are read a step or more ahead of
       // their use.
       const int g = lane % kGroups;
-      auto block_of = [&](int t) -> int {  // -1: behind the history, or outside the cache (recorded)
+      auto block_of = [&](int t) -> int {  // -1: behind the history; -2: outside the cache (recorded)
         const int key = (t0 + t) * kNK + 16 * g;
         if (t >= steps || key >= s.len) return -1;
         const int blk = a.table[(int64_t)b * a.max_blocks + key / a.bt];
         if (blk >= 0 && blk < a.n_blocks) return blk;
         if (lane < kGroups) atomicOr(a.status, kStatusCache);
-        return -1;
+        return -2;
       };
       // blocks of the step whose values come next and of the three behind it; scales of the step whose keys come next
       int tv = 0, b0 = block_of(0), b1 = block_of(1), b2 = block_of(2), b3 = block_of(3);
@@ -458,12 +458,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!side) {
           if (lane < kGroups && t < steps) {
             s_ks[t & 15][g] = ks;
-            s_lv[t & 15][g] = scale_log2(vs);
-            s_iv[t & 15][g] = exp2_fast(-scale_log2(vs));
+            // a block outside the cache: its scores become -inf, its keys count in no sum
+            s_lv[t & 15][g] = blk == -2 ? -INFINITY : scale_log2(vs);
+            s_iv[t & 15][g] = blk == -2 ? 0.f : exp2_fast(-scale_log2(vs));
           }
           const int nb = t == tv ? b1 : b2;
           ks = nb < 0 ? 0.f : a.ks[(int64_t)nb * a.heads + h];
           vs = nb < 0 ? 0.f : a.vs[(int64_t)nb * a.heads + h];
+        }
+        if (lane < kGroups && blk == -2) {  // and its codes are zero, not what the entry held before
+          uint4* to = reinterpret_cast<uint4*>(raw + rs * Sh::kCodes + 16 * g * D);
+          for (int i = 0; i < D; ++i) to[i] = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later copy into the entry
         }
         __syncwarp();
         if (lane == 0)

@@ -385,6 +385,37 @@ def test_bad_tables_are_reported(zg, dev):
     check_attention(zg, dev, c, q, good, ints([20]), None, False)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("R, bt, width", [(1, 64, 5), (7, 16, 40), (64, 64, 5), (64, 16, 300), (300, 32, 21)])
+def test_keys_of_bad_blocks_are_left_out(zg, dev, fmt, dim, R, bt, width):
+    """Blocks outside the cache, first, in the middle, at a history's end: recorded, and the rest of the history is
+    attended to as if their keys were not there, for few rows and many; a history of such blocks alone gives nothing."""
+    n = [width * bt, (width - 1) * bt - 3, 2 * bt]
+    c, table, length = build(dev, fmt, 3, 2, dim, bt, n, width, 7)
+    q = randn((3, R, 4, dim), torch.bfloat16, 2)
+    bad = [[0, width // 2], [width - 2], [0, 1]]
+    broken = table.clone()
+    kept, left = torch.full_like(table, -5), []
+    for b, out in enumerate(bad):
+        for i in out:
+            broken[b, i] = c.n_blocks + 7 * i if i % 2 else -1 - i
+        stay = [i for i in range(-(-n[b] // bt)) if i not in out]
+        kept[b, :len(stay)] = table[b, stay]
+        left.append(n[b] - sum(min(bt, n[b] - i * bt) for i in out))
+    a = dev.CacheAttention(c, 3, R, 4, width, lse=True)
+    got, lse = (t.clone() for t in a(q, broken, length))
+    torch.cuda.synchronize()
+    with pytest.raises(zg.ZgError, match="out of range"):
+        zg.zg_check_device_status(0)
+    want, wlse, tol, ltol = want_attention(c, q, kept, ints(left), None, False, a.scale)
+    err = (got.double().cpu() - want).abs()
+    assert (err <= tol + U[q.dtype] * 1.001 * (want.abs() + tol)).all()
+    assert torch.equal(lse.cpu() == -math.inf, wlse == -math.inf) and not got[2].any()
+    seen = wlse > -math.inf
+    assert ((lse.double().cpu() - wlse).abs()[seen] <= ltol[seen]).all()
+
+
 # -------------------------------------------------------------------- attention
 
 def fill(c, seed):
