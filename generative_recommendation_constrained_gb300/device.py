@@ -77,11 +77,13 @@ _ROW_TYPES = {torch.float32: Z.ZG_F32, torch.bfloat16: Z.ZG_BF16, torch.float16:
 _CODE_TYPES = {torch.float8_e4m3fn: Z.ZG_KV_E4M3, torch.int8: Z.ZG_KV_INT8}
 
 
+# The library launches on the current device; the classes below refuse tensors of another one.
+
 _pack_rows = struct.Struct("Piiqqq").pack      # zg_rows as bytes: a fraction of a ctypes struct's cost
 
 
-def _rows(x: torch.Tensor | None):
-    """zg_rows of a [B, T, heads, dim] tensor whose last dimension is contiguous."""
+def _rows(x: torch.Tensor | None, gpu: int):
+    """zg_rows of a [B, T, heads, dim] tensor on device `gpu` whose last dimension is contiguous."""
     if x is None:
         return None
     dt = _ROW_TYPES.get(x.dtype)
@@ -90,31 +92,42 @@ def _rows(x: torch.Tensor | None):
     sb, st, sh, se = x.stride()
     if se != 1:
         raise ValueError("the last dimension of the rows must be contiguous")
-    if not x.is_cuda:
-        raise ValueError("the rows must be on the GPU")
+    if x.get_device() != gpu:
+        raise ValueError(f"the rows must be on the GPU, on the current device (cuda:{gpu})")
     if sb < 0 or st < 0 or sh < 0:
         raise ValueError("strides of the rows must not be negative")
     return _pack_rows(x.data_ptr(), dt, 0, sb, st, sh)
 
 
-def _stream(stream, x: torch.Tensor):
-    """The stream given, or the current one of x's device (its number alone: a Stream object costs 3 us)."""
-    return torch._C._cuda_getCurrentRawStream(x.device.index) if stream is None else stream
+def _stream(stream, gpu: int):
+    """The stream given, or the current one of device `gpu` (its number alone: a Stream object costs 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream
 
 
-def _out_like(x: torch.Tensor, stream):
+def _out_like(x: torch.Tensor, stream, gpu: int):
     """A new output like x for work on `stream`.  It comes from that stream's memory: a block that the current stream
     has given back may still be read by work queued there."""
-    if stream is None or stream == torch._C._cuda_getCurrentRawStream(x.device.index):
+    if stream is None or stream == torch._C._cuda_getCurrentRawStream(gpu):
         return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    on = torch.cuda.ExternalStream(stream, device=x.device) if stream else torch.cuda.default_stream(x.device)
+    on = torch.cuda.ExternalStream(stream, device=gpu) if stream else torch.cuda.default_stream(gpu)
     with torch.cuda.stream(on):
         return torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
-def _int32(x: torch.Tensor | None, shape, name: str):
-    if x is not None and (x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous() or not x.is_cuda):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on the GPU")
+def _int32(x: torch.Tensor | None, shape, name: str, gpu: int):
+    if x is not None and (x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous() or
+                          x.get_device() != gpu):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on the GPU, on the current device "
+                         f"(cuda:{gpu})")
+
+
+def _current(held: int, what: str) -> int:
+    """The current device, on which the library launches: what a call is given, and what it `held` before (-1: nothing),
+    has to be there."""
+    gpu = torch.cuda.current_device()
+    if held != gpu and held >= 0:
+        raise ValueError(f"{what} on cuda:{held}, but the current device is cuda:{gpu}")
+    return gpu
 
 
 class NormRope:
@@ -128,6 +141,9 @@ class NormRope:
             if g is not None and (g.dtype != torch.float32 or tuple(g.shape) != (dim,) or not g.is_contiguous() or
                                   not g.is_cuda):
                 raise ValueError("gains must be contiguous float32 tensors of shape [dim] on the GPU")
+        self.gpu = max([g.get_device() for g in (q_gain, k_gain) if g is not None], default=-1)
+        if any(g is not None and g.get_device() != self.gpu for g in (q_gain, k_gain)):
+            raise ValueError("gains must be on one device")
         self.dim, self.q_gain, self.k_gain = dim, q_gain, k_gain
         self.struct = Z.make_norm_rope(norm, eps, q_gain, k_gain, dim if rot_dim is None else rot_dim, interleaved,
                                        theta, freq)
@@ -137,21 +153,23 @@ class NormRope:
         default to new tensors and may be the inputs themselves.  New tensors belong to `stream` (the raw handle; the
         current stream when None) as if made while it was current."""
         x = q if q is not None else k
+        gpu = _current(self.gpu, "the gains are")
         B, T = x.shape[:2]
-        _int32(positions, (B, T), "positions")
+        _int32(positions, (B, T), "positions", gpu)
         for i in (q, k):
             if i is not None and (i.shape[:2] != x.shape[:2] or i.shape[3] != self.dim):
                 raise ValueError("q and k must be [B, T, heads, dim]")
         if q is not None and q_out is None:
-            q_out = _out_like(q, stream)
+            q_out = _out_like(q, stream, gpu)
         if k is not None and k_out is None:
-            k_out = _out_like(k, stream)
+            k_out = _out_like(k, stream, gpu)
         for i, o in ((q, q_out), (k, k_out)):
             if i is not None and o.shape != i.shape:
                 raise ValueError("an output must have its input's shape")
-        Z.zg_qk_norm_rope(self.struct, _rows(q), _rows(k), _rows(q_out) if q is not None else None,
-                          _rows(k_out) if k is not None else None, positions, B, T,
-                          0 if q is None else q.shape[2], 0 if k is None else k.shape[2], self.dim, _stream(stream, x))
+        Z.zg_qk_norm_rope(self.struct, _rows(q, gpu), _rows(k, gpu), _rows(q_out, gpu) if q is not None else None,
+                          _rows(k_out, gpu) if k is not None else None, positions, B, T,
+                          0 if q is None else q.shape[2], 0 if k is None else k.shape[2], self.dim,
+                          _stream(stream, gpu))
         return q_out, k_out
 
 
@@ -183,6 +201,9 @@ class KVCache:
                 raise ValueError("scales must be float32 [n_blocks, heads]")
         if not all(x.is_contiguous() and x.is_cuda for x in (k_codes, v_codes, k_scale, v_scale)):
             raise ValueError("codes and scales must be contiguous and on the GPU")
+        self.gpu = k_codes.get_device()
+        if any(x.get_device() != self.gpu for x in (v_codes, k_scale, v_scale)):
+            raise ValueError("codes and scales must be on one device")
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.n_blocks, self.heads, self.block_tokens, self.dim = k_codes.shape
         self.struct = Z.make_kv_cache(_CODE_TYPES[k_codes.dtype], self.n_blocks, self.heads, self.block_tokens,
@@ -193,6 +214,7 @@ class KVCache:
         """Writes k, v [B, T, heads, dim] behind the start[b] tokens that each request holds (n_new[b] of the T
         rows, all when None); norm_rope turns the keys on the way, and q [B, T, Hq, dim] into q_out, which is
         returned (a new tensor when None; it belongs to `stream`, as in NormRope)."""
+        gpu = _current(self.gpu, "the cache is")
         B, T = k.shape[:2]
         if k.shape != v.shape or k.shape[2] != self.heads or k.shape[3] != self.dim:
             raise ValueError("k and v must be [B, T, heads, dim] of the cache")
@@ -200,34 +222,37 @@ class KVCache:
             raise ValueError("table must be [B, max_blocks]")
         if norm_rope is not None and norm_rope.dim != self.dim:
             raise ValueError("norm_rope and the cache differ in dim")
-        _int32(table, (B, table.shape[1]), "table")
-        _int32(start, (B,), "start")
-        _int32(n_new, (B,), "n_new")
+        if norm_rope is not None:
+            _current(norm_rope.gpu, "the gains are")
+        _int32(table, (B, table.shape[1]), "table", gpu)
+        _int32(start, (B,), "start", gpu)
+        _int32(n_new, (B,), "n_new", gpu)
         if q is not None:
             if q.shape[:2] != k.shape[:2] or q.shape[3] != self.dim:
                 raise ValueError("q must be [B, T, Hq, dim]")
             if q_out is None:
-                q_out = _out_like(q, stream)
+                q_out = _out_like(q, stream, gpu)
             elif q_out.shape != q.shape:
                 raise ValueError("q_out must have q's shape")
-        Z.zg_kv_append(self.struct, norm_rope.struct if norm_rope is not None else None, _rows(k), _rows(v), _rows(q),
-                       _rows(q_out) if q is not None else None, 0 if q is None else q.shape[2], table,
-                       table.shape[1], start, n_new, B, T, _stream(stream, k))
+        Z.zg_kv_append(self.struct, norm_rope.struct if norm_rope is not None else None, _rows(k, gpu), _rows(v, gpu),
+                       _rows(q, gpu), _rows(q_out, gpu) if q is not None else None, 0 if q is None else q.shape[2], table,
+                       table.shape[1], start, n_new, B, T, _stream(stream, gpu))
         return q_out
 
     def read(self, table, start, n=None, k_out=None, v_out=None, stream: int | None = None):
         """Tokens start[b] .. start[b] + n[b] - 1 back into k_out, v_out [B, T, heads, dim] (either may be None);
         rows from n[b] on become zero."""
         x = k_out if k_out is not None else v_out
+        gpu = _current(self.gpu, "the cache is")
         B, T = x.shape[:2]
         for o in (k_out, v_out):
             if o is not None and tuple(o.shape) != (B, T, self.heads, self.dim):
                 raise ValueError("outputs must be [B, T, heads, dim] of the cache")
-        _int32(table, (B, table.shape[1]), "table")
-        _int32(start, (B,), "start")
-        _int32(n, (B,), "n")
-        Z.zg_kv_read(self.struct, table, table.shape[1], start, n, B, T, _rows(k_out), _rows(v_out),
-                     _stream(stream, x))
+        _int32(table, (B, table.shape[1]), "table", gpu)
+        _int32(start, (B,), "start", gpu)
+        _int32(n, (B,), "n", gpu)
+        Z.zg_kv_read(self.struct, table, table.shape[1], start, n, B, T, _rows(k_out, gpu), _rows(v_out, gpu),
+                     _stream(stream, gpu))
         return k_out, v_out
 
 
@@ -237,24 +262,25 @@ class CacheAttention:
 
     def __init__(self, cache: KVCache, B: int, R: int, Hq: int, max_blocks: int, causal: bool = False,
                  scale: float | None = None, dtype=torch.bfloat16, lse: bool = False):
-        device = cache.k_codes.device
+        device, gpu = cache.k_codes.device, _current(cache.gpu, "the cache is")   # the workspace's size is the device's
         self.cache, self.B, self.R, self.Hq, self.max_blocks = cache, B, R, Hq, max_blocks
         self.causal, self.scale = causal, cache.dim ** -0.5 if scale is None else scale
         self.ws_bytes = Z.zg_kv_attention_workspace_size(cache.struct, max_blocks, B, R, Hq)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.out = torch.empty((B, R, Hq, cache.dim), dtype=dtype, device=device)
         self.lse = torch.empty((B, R, Hq), dtype=torch.float32, device=device) if lse else None
-        self._out_rows = _rows(self.out)
+        self._out_rows = _rows(self.out, gpu)
 
     def __call__(self, q, table, length, n_rows=None, stream: int | None = None):
         """q [B, R, Hq, dim] over the first length[b] tokens of each request; returns (out, lse or None), this
         object's own buffers."""
         if tuple(q.shape) != tuple(self.out.shape):
             raise ValueError("q must be [B, R, Hq, dim]")
-        _int32(table, (self.B, self.max_blocks), "table")
-        _int32(length, (self.B,), "length")
-        _int32(n_rows, (self.B,), "n_rows")
-        Z.zg_kv_attention(self.cache.struct, table, self.max_blocks, length, n_rows, _rows(q), self._out_rows,
+        gpu = _current(self.cache.gpu, "the cache is")
+        _int32(table, (self.B, self.max_blocks), "table", gpu)
+        _int32(length, (self.B,), "length", gpu)
+        _int32(n_rows, (self.B,), "n_rows", gpu)
+        Z.zg_kv_attention(self.cache.struct, table, self.max_blocks, length, n_rows, _rows(q, gpu), self._out_rows,
                           self.lse, self.B, self.R, self.Hq, self.scale, self.causal, self.ws, self.ws_bytes,
-                          _stream(stream, q))
+                          _stream(stream, gpu))
         return self.out, self.lse

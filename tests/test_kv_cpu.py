@@ -184,7 +184,8 @@ class Rows:
 
     def __init__(self, shape, dtype=None, index=0):
         import torch
-        self.shape, self.dtype, self.device = torch.Size(shape), dtype or torch.bfloat16, torch.device("cuda", index)
+        self.shape = torch.Size(shape if isinstance(shape, tuple) else (shape,))
+        self.dtype, self.device = dtype or torch.bfloat16, torch.device("cuda", index)
 
     def stride(self):
         return tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
@@ -246,3 +247,44 @@ def test_outputs_belong_to_the_stream_that_writes_them(fake_cuda, stream, of):
     dev.KVCache.over(codes, codes, scales, scales).append(x, x, Rows((2, 5), torch.int32), Rows((2,), torch.int32), q=x,
                                                           norm_rope=nr, stream=stream)
     assert seen["made"] == [of] * 3 and seen["calls"][1:] == [("zg_kv_append", of)]
+
+
+def test_tensors_of_another_device_are_refused(fake_cuda):
+    """The library launches on the current device, so every tensor of a call has to be there; nothing is called
+    otherwise."""
+    import torch
+    dev, seen = fake_cuda
+    i32, f32, i8 = torch.int32, torch.float32, torch.int8
+
+    def cache(index, odd=None):
+        return dev.KVCache.over(*(Rows(s, t, odd if j == 3 and odd is not None else index)
+                                  for j, (s, t) in enumerate((((8, 4, 16, 64), i8), ((8, 4, 16, 64), i8), ((8, 4), f32), ((8, 4), f32)))))
+
+    x, y = Rows((2, 3, 4, 64)), Rows((2, 3, 4, 64), index=1)
+    table, start = Rows((2, 5), i32), Rows((2,), i32)
+    pos, gain = Rows((2, 3), i32), Rows((64,), f32, 1)
+    c, nr = cache(0), dev.NormRope(64)
+    attn = dev.CacheAttention(c, 2, 3, 4, 5)
+    for f in (lambda: nr(y, None, pos), lambda: nr(x, y, pos), lambda: nr(x, None, Rows((2, 3), i32, 1)), lambda: nr(x, None, pos, y),
+              lambda: dev.NormRope(64, gain)(x, None, pos), lambda: dev.NormRope(64, gain, Rows((64,), f32)),
+              lambda: c.append(y, y, table, start), lambda: c.append(x, y, table, start),
+              lambda: c.append(x, x, Rows((2, 5), i32, 1), start), lambda: c.append(x, x, table, Rows((2,), i32, 1)),
+              lambda: c.append(x, x, table, start, Rows((2,), i32, 1)), lambda: c.append(x, x, table, start, q=y, norm_rope=nr),
+              lambda: c.append(x, x, table, start, q=x, norm_rope=dev.NormRope(64, gain)), lambda: cache(1).append(x, x, table, start),
+              lambda: cache(0, 1), lambda: c.read(table, start, None, y), lambda: c.read(Rows((2, 5), i32, 1), start, None, x),
+              lambda: cache(1).read(table, start, None, x), lambda: attn(y, table, start), lambda: attn(x, Rows((2, 5), i32, 1), start),
+              lambda: attn(x, table, start, Rows((2,), i32, 1)), lambda: dev.CacheAttention(cache(1), 2, 3, 4, 5)):
+        with pytest.raises(ValueError, match="device"):
+            f()
+    seen["device"] = 1
+    for f in (lambda: c.append(x, x, table, start), lambda: c.read(table, start, None, x), lambda: attn(x, table, start),
+              lambda: nr(x, None, pos)):
+        with pytest.raises(ValueError, match="device"):
+            f()
+    assert seen["calls"] == []
+    seen["device"] = 0
+    nr(x, x, pos)
+    c.append(x, x, table, start)
+    c.read(table, start, None, x)
+    attn(x, table, start)
+    assert [name for name, _ in seen["calls"]] == ["zg_qk_norm_rope", "zg_kv_append", "zg_kv_read", "zg_kv_attention"]
