@@ -153,6 +153,8 @@ class NormRope:
         default to new tensors and may be the inputs themselves.  New tensors belong to `stream` (the raw handle; the
         current stream when None) as if made while it was current."""
         x = q if q is not None else k
+        if x is None:
+            raise ValueError("neither q nor k given")
         gpu = _current(self.gpu, "the gains are")
         B, T = x.shape[:2]
         _int32(positions, (B, T), "positions", gpu)
@@ -243,6 +245,10 @@ class KVCache:
         """Tokens start[b] .. start[b] + n[b] - 1 back into k_out, v_out [B, T, heads, dim] (either may be None);
         rows from n[b] on become zero."""
         x = k_out if k_out is not None else v_out
+        if x is None:
+            raise ValueError("neither k_out nor v_out given")
+        if table.dim() != 2:
+            raise ValueError("table must be [B, max_blocks]")
         gpu = _current(self.gpu, "the cache is")
         B, T = x.shape[:2]
         for o in (k_out, v_out):

@@ -288,3 +288,17 @@ def test_tensors_of_another_device_are_refused(fake_cuda):
     c.read(table, start, None, x)
     attn(x, table, start)
     assert [name for name, _ in seen["calls"]] == ["zg_qk_norm_rope", "zg_kv_append", "zg_kv_read", "zg_kv_attention"]
+
+
+def test_wrappers_want_something_to_do(fake_cuda):
+    import torch
+    dev, seen = fake_cuda
+    codes, scales = Rows((8, 4, 16, 64), torch.int8), Rows((8, 4), torch.float32)
+    c = dev.KVCache.over(codes, codes, scales, scales)
+    start = Rows((2,), torch.int32)
+    for f, words in ((lambda: dev.NormRope(64)(None, None, None), "neither"),
+                     (lambda: c.read(Rows((2, 5), torch.int32), start), "neither"),
+                     (lambda: c.read(Rows((10,), torch.int32), start, None, Rows((2, 3, 4, 64))), "max_blocks")):
+        with pytest.raises(ValueError, match=words):
+            f()
+    assert seen["calls"] == []
