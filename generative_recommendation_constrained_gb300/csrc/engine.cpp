@@ -20,6 +20,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "context_id.h"
 #include "zg_internal.h"
 
 namespace zg {
@@ -638,19 +639,15 @@ cudaError_t current_context_id(unsigned long long* id) {
       get_id = reinterpret_cast<GetId>(p);
   });
   if (!get_current || !get_id) return cudaErrorNotSupported;
-  void* ctx = nullptr;
-  if (get_current(&ctx) != 0 || !ctx) {
-    // make the runtime's primary context of the current device current on this
-    // thread (cudaSetDevice initialises it; nothing is allocated).  Only where
-    // there is none: the call takes longer than a launch
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaSetDevice(dev);
-    if (e != cudaSuccess) return e;
-    if (get_current(&ctx) != 0 || !ctx) return cudaErrorDeviceUninitialized;
-  }
-  if (get_id(ctx, id) != 0) return cudaErrorDeviceUninitialized;
-  return cudaSuccess;
+  const int e = live_context_id(
+      get_current, get_id,
+      [] {  // cudaSetDevice initialises the primary context; nothing is allocated
+        int dev = 0;
+        const cudaError_t err = cudaGetDevice(&dev);
+        return (int)(err == cudaSuccess ? cudaSetDevice(dev) : err);
+      },
+      id);
+  return e < 0 ? cudaErrorDeviceUninitialized : (cudaError_t)e;
 }
 
 zg_status fail(zg_status code, const std::string& msg) {

@@ -41,3 +41,17 @@ def test_plain_c_program(lib, tmp_path):
     assert stats == {"unique": "5", "rows3": "4", "nnz3": "5", "maxfan3": "2", "bytes3": stats["bytes3"]}
     assert int(stats["bytes3"]) >= 16 + 4 * 5 + 2 * 5
     assert lines["bad"] == "token status 1 message set"
+
+
+def test_context_id_after_a_reset(tmp_path):
+    """The look-up of the current context's id recovers where the thread's handle is of a context that a reset has
+    ended (stand-ins of the driver's calls)."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        pytest.skip("no C++ compiler")
+    exe = str(tmp_path / "context_id")
+    r = subprocess.run([cxx, "-std=c++17", "-Wall", "-Wextra", "-Werror", os.path.join(ROOT, "tests", "c", "context_id.cpp"),
+                        "-I", os.path.join(PKG, "csrc"), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert out.returncode == 0 and out.stdout.count("ok ") == 6, out.stdout
