@@ -252,6 +252,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
     scales(b0, ks[0], vs[0]);
     scales(b1, ks[1], vs[1]);
     bool ok0 = b0 >= 0, ok1 = b1 >= 0;
+    const bool small = small_scale(vs[0]);
+    float last_lv = kNoScale;
     b0 = block_of(t0 + 4, 0), b1 = block_of(t0 + 4, 1);
 
     // the rows: lane (g, c) the dims of its words of row g; then the sight and the scale of rows 2c, 2c + 1
@@ -322,6 +324,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       ++taken;
       const int key0 = t * 32;
       float z[2][NT][4], lv[2], iv[2];
+      if (last_lv == kNoScale) last_lv = scale_log2(vs[0], scale_log2(vs[1], kNoScale));
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t k[2][KW];
@@ -338,8 +341,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma_16816(z[half][n], ka, qb[n][w][0], qb[n][w][1]);
         }
-        lv[half] = scale_log2(vs[half]);
-        iv[half] = exp2_fast(-lv[half]);
+        last_lv = lv[half] = scale_log2(vs[half], last_lv);
+        iv[half] = sum_weight(lv[half], small);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -375,8 +378,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
             for (int x = 4; x < 32; x <<= 1) tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xFFFFFFFFu, tm[e], x));
             const float nm = fmaxf(mx[n][e], tm[e]);
             const float f = mx[n][e] == -INFINITY ? 0.f : exp2_fast(mx[n][e] - nm);
+            l[n][e] = moved_sum(l[n][e], mx[n][e], nm);
             mx[n][e] = nm;
-            l[n][e] *= f;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
               o[n][j][e] *= f;
@@ -402,10 +405,11 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       for (int half = 0; half < 2; ++half) {
         uint32_t vw[4][VW];
         Tl::values(tiles + (2 + half) * Tl::kBytes, g, c, vw);
-        if (key0 + 16 * half + 16 > vmax || !(half ? ok1 : ok0)) {  // behind what is seen: not defined, may be NaN
+        const bool some = (half ? ok1 : ok0) && has_scale(vs[half]);
+        if (key0 + 16 * half + 16 > vmax || !some) {  // behind what is seen: not defined, may be NaN
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (key0 + 16 * half + 2 * c + (j & 1) + (j >> 1) * 8 >= vmax || !(half ? ok1 : ok0))
+            if (key0 + 16 * half + 2 * c + (j & 1) + (j >> 1) * 8 >= vmax || !some)
 #pragma unroll
               for (int w = 0; w < VW; ++w) vw[j][w] = 0;
         }
@@ -443,13 +447,14 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], x);
         const int r = n * 8 + 2 * c + e;
+        const PartEnd end = part_end(mx[n][e], l[n][e], small);
         if (g == 0) {
-          sm_m[warp][r] = mx[n][e];
-          sm_l[warp][r] = l[n][e];
+          sm_m[warp][r] = end.m;
+          sm_l[warp][r] = end.l;
         }
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
-          *reinterpret_cast<float2*>(&sm_o[warp][r][g * (D / 8) + 2 * j]) = make_float2(o[n][j][e], o[n][j][2 + e]);
+          *reinterpret_cast<float2*>(&sm_o[warp][r][g * (D / 8) + 2 * j]) = make_float2(o[n][j][e] * end.down, o[n][j][2 + e] * end.down);
       }
     __syncthreads();
     for (int i = threadIdx.x; i < NR * (D / 4); i += kFewThreads) {

@@ -207,6 +207,9 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The codes of a block outside the cache, and the values of one without a scale.
+__device__ __align__(16) uint8_t g_no_codes[16 * 128];
+
 template <typename T, int D, bool INT8>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tc(const __grid_constant__ AttnArgs a, const Rows<T> q, const Rows<T> out, uint32_t spin) {
@@ -222,9 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw], wide_full[kWide], wide_empty[kWide];
   __shared__ uint64_t q_full, s_full[2], s_free[2], p_full[2][2], o_done[2], drained;  // [tile], p_full [tile][half]
   // of 16 keys each, a ring of 16 steps (the codes of step t + 10 come only after the softmax of step t): key scale,
-  // log2 of the value scale, and 2^-that
+  // log2 of the value scale, and what a weight counts for in the row's sum
   __shared__ float s_ks[16][kGroups], s_lv[16][kGroups], s_iv[16][kGroups];
   __shared__ uint32_t tmem_base;
+  __shared__ bool s_small;  // of this part's sums (kv_attn.cuh)
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   after_predecessor();
@@ -444,6 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // blocks of the step whose values come next and of the three behind it; scales of the step whose keys come next
       int tv = 0, b0 = block_of(0), b1 = block_of(1), b2 = block_of(2), b3 = block_of(3);
       float ks = b0 < 0 ? 0.f : a.ks[(int64_t)b0 * a.heads + h], vs = b0 < 0 ? 0.f : a.vs[(int64_t)b0 * a.heads + h];
+      const bool small = __shfl_sync(0xFFFFFFFFu, small_scale(vs), 0);
+      if (lane == 0) s_small = small;  // seen by all who see the first codes
+      float last_lv = kNoScale;      // of this lane's group, in the step before
+      bool none0 = false, none1 = false;  // its values have no scale: in the step whose values come next, and behind it
       int issued = 0;
       bool good = true;
       for (int n = 0; n < Sh::entries(steps); ++n) {
@@ -453,23 +461,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           good = false;
           break;
         }
-        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, lane < kGroups && blk >= 0)) * (16u * (uint32_t)D);
-        const int64_t at = (((int64_t)blk * a.heads + h) * a.bt + ((t0 + t) * kNK + 16 * g) % a.bt) * D;
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, lane < kGroups && blk != -1)) * (16u * (uint32_t)D);
         if (!side) {
+          float lv = log2_fast(vs), iv = sum_weight(lv, small);
+          const uint32_t some = __ballot_sync(0xFFFFFFFFu, has_scale(vs)) & ((1u << kGroups) - 1);
+          if (some != (1u << kGroups) - 1) {  // rare, and at the end: where a scale of 0 stands (kv_attn.cuh)
+            const uint32_t upto = some & ((2u << g) - 1);
+            const float before = __shfl_sync(0xFFFFFFFFu, last_lv, kGroups - 1);
+            const float first = __shfl_sync(0xFFFFFFFFu, lv, some ? __ffs(some) - 1 : 0);
+            const float near = __shfl_sync(0xFFFFFFFFu, lv, upto ? 31 - __clz(upto) : 0);
+            last_lv = lv = upto ? near : some && before == kNoScale ? first : before;
+            iv = sum_weight(lv, small);
+            if (blk == -2) lv = -INFINITY, iv = 0.f;  // outside the cache: no score, no part in a sum
+          } else {
+            last_lv = lv;
+          }
           if (lane < kGroups && t < steps) {
             s_ks[t & 15][g] = ks;
-            // a block outside the cache: its scores become -inf, its keys count in no sum
-            s_lv[t & 15][g] = blk == -2 ? -INFINITY : scale_log2(vs);
-            s_iv[t & 15][g] = blk == -2 ? 0.f : exp2_fast(-scale_log2(vs));
+            s_lv[t & 15][g] = lv;
+            s_iv[t & 15][g] = iv;
           }
+          (t == tv ? none0 : none1) = !has_scale(vs);
           const int nb = t == tv ? b1 : b2;
           ks = nb < 0 ? 0.f : a.ks[(int64_t)nb * a.heads + h];
           vs = nb < 0 ? 0.f : a.vs[(int64_t)nb * a.heads + h];
-        }
-        if (lane < kGroups && blk == -2) {  // and its codes are zero, not what the entry held before
-          uint4* to = reinterpret_cast<uint4*>(raw + rs * Sh::kCodes + 16 * g * D);
-          for (int i = 0; i < D; ++i) to[i] = make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later copy into the entry
         }
         __syncwarp();
         if (lane == 0)
@@ -477,11 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                        "r"(bytes)
                        : "memory");
         __syncwarp();
-        if (lane < kGroups && blk >= 0)
-          bulk_load(raw + rs * Sh::kCodes + 16 * g * D, (side ? a.vc : a.kc) + at, 16 * D, &raw_full[rs]);
+        const int64_t at = (((int64_t)blk * a.heads + h) * a.bt + ((t0 + t) * kNK + 16 * g) % a.bt) * D;
+        if (lane < kGroups && blk != -1)
+          bulk_load(raw + rs * Sh::kCodes + 16 * g * D, blk < 0 || (side && none0) ? g_no_codes : (side ? a.vc : a.kc) + at,
+                    16 * D, &raw_full[rs]);
         issued = n + 1;
         if (side) {
           ++tv;
+          none0 = none1;
           b0 = b1, b1 = b2, b2 = b3, b3 = block_of(tv + 3);
         }
       }
@@ -580,9 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool move = __any_sync(0xFFFFFFFFu, tm > mx + 8.f);
         if (move) {
           const float nm = fmaxf(mx, tm);
-          if (nm != mx) al = exp2_fast(mx - nm);
+          if (nm != mx) {
+            al = exp2_fast(mx - nm);
+            l = moved_sum(l, mx, nm);
+          }
           mx = nm;
-          l *= al;
         }
         const float mu = mx == -INFINITY ? 0.f : mx;
         // the product of the last step has read its probabilities, and is in the sums (with P over S the scores have
@@ -636,7 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (good && turns > 0) good = warp_wait(&o_done[i], (turns - 1) & 1, spin);
       if (!good && lane == 0) give_up();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      float own = 1.f, other = 0.f;  // what the two places' sums count for
+      const PartEnd end = part_end(mx, l, turns > 0 && good && s_small);
+      mx = end.m;
+      l = end.l;
+      float own = end.down, other = 0.f;  // factors of the two places' sums
       float* sum1 = reinterpret_cast<float*>(wide);  // [D + 2][128]: place 1's sums, reference and row sum
       if (twice) {
         if (i == 1) {
@@ -647,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t o[16];
             if (turns > 0) tmem_load16(o_at + d, o);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum1[(d + j) * 128 + r] = turns > 0 ? __uint_as_float(o[j]) : 0.f;
+            for (int j = 0; j < 16; ++j) sum1[(d + j) * 128 + r] = turns > 0 ? __uint_as_float(o[j]) * own : 0.f;
           }
           sum1[D * 128 + r] = mx;
           sum1[(D + 1) * 128 + r] = l;
@@ -656,13 +679,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("bar.sync 1, 256;" ::: "memory");
           asm volatile("bar.sync 1, 256;" ::: "memory");
           const float m1 = sum1[D * 128 + r], l1 = sum1[(D + 1) * 128 + r], top = fmaxf(mx, m1);
-          own = mx == -INFINITY ? 0.f : exp2_fast(mx - top);
+          const float f = mx == -INFINITY ? 0.f : exp2_fast(mx - top);
+          own *= f;
           other = m1 == -INFINITY ? 0.f : exp2_fast(m1 - top);
           mx = top;
-          l = l * own + l1 * other;
+          l = l * f + l1 * other;
         }
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (parts == 1) {  // no join: outputs
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        own *= inv;
+        other *= inv;
+      }
       const int64_t pi = ((int64_t)item * a.splits + split) * a.tile + ir;
       if (good && !(twice && i == 1)) {
         uint8_t* tile = sq + i * Sh::kTile;  // every product that reads the queries is complete
@@ -675,10 +703,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0;
           }
-          if (twice) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              o[j] = __float_as_uint(__uint_as_float(o[j]) * own + sum1[(d + j) * 128 + r] * other);
+          for (int j = 0; j < 32; ++j) {
+            float y = __uint_as_float(o[j]) * own;
+            if (twice) y += sum1[(d + j) * 128 + r] * other;
+            o[j] = __float_as_uint(y);
           }
           const float* x = reinterpret_cast<const float*>(o);
           if (parts > 1) {
@@ -691,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; j += 8)
               *reinterpret_cast<uint4*>(tile + ((d + j) / 64) * (128 * 128) + r * 128 +
                                         (((((d + j) % 64) / 8) ^ (r & 7)) << 4)) =
-                  make_uint4(pack2<T>(x[j] * inv, x[j + 1] * inv), pack2<T>(x[j + 2] * inv, x[j + 3] * inv),
-                             pack2<T>(x[j + 4] * inv, x[j + 5] * inv), pack2<T>(x[j + 6] * inv, x[j + 7] * inv));
+                  make_uint4(pack2<T>(x[j], x[j + 1]), pack2<T>(x[j + 2], x[j + 3]), pack2<T>(x[j + 4], x[j + 5]),
+                             pack2<T>(x[j + 6], x[j + 7]));
           }
         }
         if (parts == 1) {  // whole rows out, as the queries came in
@@ -710,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (live && parts > 1) {
           float* ml = a.part + a.slots * a.tile * D + pi * 2;
-          ml[0] = l > 0.f ? mx : -INFINITY;
+          ml[0] = mx;
           ml[1] = l;
         } else if (live && a.lse) {
           a.lse[((int64_t)b * a.R + row) * a.Hq + qh] = l > 0.f ? (mx + log2f(l)) * 0.693147180559945f : -INFINITY;

@@ -59,9 +59,42 @@ __device__ __forceinline__ float log2_fast(float x) {
   return y;
 }
 
-// log2 of a value block's scale; a scale of 0 (all its codes are 0) stands at
-// the floor, so that its keys still count in the row's sum.
-__device__ __forceinline__ float scale_log2(float vs) { return vs > 0x1p-100f ? log2_fast(vs) : -100.f; }
+// log2 of a value block's scale.  With a scale of 0 (so count those below
+// 2^-126) the values are 0 and their codes are left out, but the keys count in
+// the row's sum: the scale stands where the last one before it does, or else
+// the first of the same step, or else at kNoScale, so that its weights neither
+// vanish beside the others' nor make theirs vanish.
+constexpr float kNoScale = -100.f;
+__device__ __forceinline__ bool has_scale(float vs) { return vs >= 0x1p-126f; }
+__device__ __forceinline__ float scale_log2(float vs, float last) { return has_scale(vs) ? log2_fast(vs) : last; }
+
+// What a key's weight counts for in the row's sum is 1 / scale.  Scales range
+// from 2^-126 to 2^121, more than a sum of many such terms has room for in 32
+// bits: where a part's keys begin with a scale this small, its sums are kept
+// times 2^-40.
+__device__ __forceinline__ bool small_scale(float vs) { return has_scale(vs) && vs < 0x1p-64f; }
+__device__ __forceinline__ float sum_weight(float lv, bool small) { return exp2_fast(-lv) * (small ? 0x1p-40f : 1.f); }
+
+// A row's sum when its reference moves from m to n: by halves, since a sum over
+// small scales outlives a factor below 2^-126.
+__device__ __forceinline__ float moved_sum(float l, float m, float n) {
+  const float h = m == -INFINITY ? 0.f : exp2_fast(0.5f * (m - n));
+  return l * h * h;
+}
+
+// A row at its part's end in the terms in which parts are joined: the sum
+// brought near 1, the reference moved by as much, so that it is that of the
+// scores alone and the scales of different parts do not meet; `down` is the
+// factor of the row's output.
+struct PartEnd {
+  float m, l, down;
+};
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ PartEnd part_end(float m, float l, bool small) {
+  if (!(l > 0.f)) return {-INFINITY, l, 1.f};
+  const int kept = small ? 40 : 0, e = min((int)(__float_as_uint(l) >> 23) - 127 + kept, 126);  // a subnormal sum: -127
+  return {m + (float)e, l * power_of_2(kept - e), power_of_2(-e)};
+}
 
 // Parts that the keys of an item are in.
 __device__ __forceinline__ int parts_of(const AttnArgs& a, int keys) { return max(1, (keys + a.chunk - 1) / a.chunk); }

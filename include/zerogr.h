@@ -517,8 +517,9 @@ ZG_API zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int3
  * Query and probability enter the products as half values (a query row
  * scaled by a power of two first; both relative 2^-11), codes exactly; sums,
  * maxima and outputs are 32-bit.  Cached e4m3 codes within length must not
- * be NaN; nothing behind it is used, and keys of a block outside the cache
- * count as not there.  Hq a multiple of heads, at most 1024;
+ * be NaN; value scales below 2^-126 count as 0;
+ * nothing behind it is used, and keys of a block outside the cache count as
+ * not there.  Hq a multiple of heads, at most 1024;
  * B * R * Hq below 2^31, and the tables' tokens / 128 * B * heads (times the
  * row tiles of an item) too, else ZG_ERR_UNSUPPORTED.  Kernels may start while
  * their predecessor in the stream ends; they wait before they touch memory. */

@@ -578,6 +578,40 @@ def test_attention_scale_of_unseen_blocks(zg, dev, fmt):
         check_attention(zg, dev, c, q, table, length, None, False)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("factor", [2.0 ** -96, 2.0 ** -105, 2.0 ** -112, 2.0 ** 60, 2.0 ** 115])
+@pytest.mark.parametrize("R, n", [(1, 320), (12, 5000), (64, 700), (150, 3000)])
+def test_attention_value_scales_of_any_size(zg, dev, fmt, factor, R, n):
+    """Value scales from the smallest that a write holds (2^-126) up to where values leave 32 bits."""
+    c, table, length = build(dev, fmt, 2, 1, 64, 64, [n, 77], -(-n // 64), 3)
+    c.v_scale.copy_((c.v_scale * factor).clamp(2.0 ** -126, 2.0 ** 118))
+    c.v_scale[table[1, 0].long()] = 0                # a block of nothing first
+    c.v_codes.view(torch.uint8)[table[1, 0].long()] = 0
+    check_attention(zg, dev, c, randn((2, R, 2, 64), torch.bfloat16, 2), table, length, None, False)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("bt", [16, 64])
+@pytest.mark.parametrize("R, n", [(1, 700), (10, 4000), (64, 700), (150, 3000)])
+def test_attention_blocks_of_nothing(zg, dev, fmt, bt, R, n):
+    """Blocks whose values are all zero (scale 0) weigh in the softmax, whatever the scales around them: at the
+    beginning, between and at the end, beside scales of 2^40 and of 2^-40, and alone."""
+    c, table, length = build(dev, fmt, 4, 1, 64, bt, [n, n - 1, n // 2, 100], -(-n // bt), 3)
+    g = torch.Generator().manual_seed(5)
+    for b, factor in ((0, 2.0 ** 40), (1, 2.0 ** -40), (2, None), (3, 0)):
+        blk = table[b][table[b] >= 0].long()
+        f = torch.full((len(blk), 1), 1.0 if factor is None else factor, device="cuda")
+        if factor is None:
+            f = torch.exp2(torch.randint(-50, 50, (len(blk), 1), generator=g).float()).cuda()
+        none = (torch.rand(len(blk), generator=g) < 0.5).cuda()
+        none[0] = True
+        f[none] = 0
+        c.v_scale[blk] *= f
+        c.v_codes.view(torch.uint8)[blk[none]] = 0
+    check_attention(zg, dev, c, randn((4, R, 2, 64), torch.bfloat16, 2), table, length, None, False)
+    check_attention(zg, dev, c, randn((4, R, 2, 64), torch.bfloat16, 4), table, length, None, True)
+
+
 def test_attention_strides_and_streams(zg, dev):
     """q inside a packed buffer, outputs into a wider one, on a stream that is not the current one."""
     c, table, length = build(dev, "int8", 2, 2, 64, 32, [100, 77], 5, 2)
