@@ -605,6 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx = nm;
         }
         const float mu = mx == -INFINITY ? 0.f : mx;
+        // A score enters the exponent unrounded and mu rounded, so that a row's weights are off by a common factor, up to
+        // 2^(ulp(mu)); from 2^26 on that could leave a half's range, and scores are taken times a power of two that
+        // keeps it within 2^4.  There scores that differ by their last bit lie 8 apart or more.
+        const int far = (int)((__float_as_uint(mu) >> 23) & 0xFF) - (127 + 25);
+        const float down = power_of_2(-max(far, 0)), fd = fz * down, md = mu * down;
         // the product of the last step has read its probabilities, and is in the sums (with P over S the scores have
         // waited for it)
         if (Sh::kApart && k > 0) {
@@ -629,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t pr[16];
 #pragma unroll
           for (int g = g2; g < g2 + 2; ++g) {
-            const float f = fmaxf(fz * s_ks[t & 15][g], 1e-37f), c = s_lv[t & 15][g] - mu;
+            const float f = fmaxf(fd * s_ks[t & 15][g], 1e-37f), c = fmaf(s_lv[t & 15][g], down, -md);
             const uint64_t f2 = pair(f, f), c2 = pair(c, c);
             uint64_t sum = 0;  // 0.f, 0.f
 #pragma unroll

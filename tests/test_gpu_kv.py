@@ -612,6 +612,19 @@ def test_attention_blocks_of_nothing(zg, dev, fmt, bt, R, n):
     check_attention(zg, dev, c, randn((4, R, 2, 64), torch.bfloat16, 4), table, length, None, True)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("scale", [1e2, 1e6, 1e8, 1e12, 1e30])
+@pytest.mark.parametrize("R, n", [(1, 320), (64, 320), (200, 2000)])
+def test_attention_scores_of_any_size(zg, dev, dim, R, n, scale):
+    """Scores far past the size at which 32 bits hold single units: finite, one value or a mean of values as near as
+    the scores' own rounding leaves them."""
+    c, table, length = build(dev, "int8", 1, 1, dim, 64, [n], -(-n // 64), 3)
+    check_attention(zg, dev, c, randn((1, R, 2, dim), torch.bfloat16, 3), table, length, None, False, scale=scale)
+    same = c.k_codes[table[0, 0].long(), :, :1].clone()              # all keys of the second block alike
+    c.k_codes[table[0, 1].long()] = same
+    check_attention(zg, dev, c, randn((1, R, 2, dim), torch.float16, 4), table, length, None, True, scale=scale)
+
+
 def test_attention_strides_and_streams(zg, dev):
     """q inside a packed buffer, outputs into a wider one, on a stream that is not the current one."""
     c, table, length = build(dev, "int8", 2, 2, 64, 32, [100, 77], 5, 2)
