@@ -99,11 +99,12 @@ __device__ __forceinline__ PartEnd part_end(float m, float l, bool small) {
 // Parts that the keys of an item are in.
 __device__ __forceinline__ int parts_of(const AttnArgs& a, int keys) { return max(1, (keys + a.chunk - 1) / a.chunk); }
 
-// The power of two that brings a row's largest |q| to [1, 2), as an exponent.
+// The power of two that brings a row's largest |q| to [1, 2), as an exponent;
+// from 2^127 on to [2, 4), since its reciprocal has to be a normal number.
 __device__ __forceinline__ int row_exponent(float top) {
-  if (!(top > 0.f) || !(top <= 3.0e38f)) return 0;
+  if (!(top > 0.f) || !(top < INFINITY)) return 0;
   const int e = (int)((__float_as_uint(top) >> 23) & 0xFF) - 127;
-  return max(e, -120);
+  return min(max(e, -120), 126);
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -625,6 +625,19 @@ def test_attention_scores_of_any_size(zg, dev, dim, R, n, scale):
     check_attention(zg, dev, c, randn((1, R, 2, dim), torch.float16, 4), table, length, None, True, scale=scale)
 
 
+@pytest.mark.parametrize("top", [1e-38, 1e-30, 1.6e38, 2e38, 3.2e38])
+@pytest.mark.parametrize("R", [1, 10, 64, 200])
+def test_attention_queries_of_any_size(zg, dev, R, top):
+    """Query rows up to the largest bf16 and down to the smallest normal ones, beside one of ordinary size."""
+    c, table, length = build(dev, "int8", 1, 1, 64, 64, [320], 5, 3)
+    q = randn((1, R, 2, 64), torch.float32, 2)
+    q = q / q.abs().amax(-1, keepdim=True) * top
+    q[0, R // 2, 1] = randn((64,), torch.float32, 3)
+    q = q.to(torch.bfloat16)
+    assert torch.isfinite(q).all()
+    check_attention(zg, dev, c, q, table, length, None, False, scale=min(2.0 / top, 1e30))
+
+
 def test_attention_strides_and_streams(zg, dev):
     """q inside a packed buffer, outputs into a wider one, on a stream that is not the current one."""
     c, table, length = build(dev, "int8", 2, 2, 64, 32, [100, 77], 5, 2)
