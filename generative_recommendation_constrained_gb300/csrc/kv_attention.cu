@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
           ml[1] = sum;
         }
       } else {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int tr = ri / a.G, th = h * a.G + ri % a.G;
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] *= inv;
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
   }
   if (id >= total || parts <= 1) return;
   if (lane < kLanes) {
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] *= inv;
     store4(out.at(b, r, qh) + 4 * lane, x);

@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (parts == 1) {  // no join: outputs
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         own *= inv;
         other *= inv;
       }
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ml[0] = mx;
           ml[1] = l;
         } else if (live && a.lse) {
-          a.lse[((int64_t)b * a.R + row) * a.Hq + qh] = l > 0.f ? (mx + log2f(l)) * 0.693147180559945f : -INFINITY;
+          a.lse[((int64_t)b * a.R + row) * a.Hq + qh] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.693147180559945f;
         }
       }
     }

@@ -85,13 +85,15 @@ __device__ __forceinline__ float moved_sum(float l, float m, float n) {
 // A row at its part's end in the terms in which parts are joined: the sum
 // brought near 1, the reference moved by as much, so that it is that of the
 // scores alone and the scales of different parts do not meet; `down` is the
-// factor of the row's output.
+// factor of the row's output.  A NaN among the row's scores leaves its sum NaN;
+// an infinite reference carries that through every join.
 struct PartEnd {
   float m, l, down;
 };
 __device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 __device__ __forceinline__ PartEnd part_end(float m, float l, bool small) {
-  if (!(l > 0.f)) return {-INFINITY, l, 1.f};
+  if (isnan(l)) return {INFINITY, l, 1.f};
+  if (!(l > 0.f)) return {-INFINITY, 0.f, 1.f};
   const int kept = small ? 40 : 0, e = min((int)(__float_as_uint(l) >> 23) - 127 + kept, 126);  // a subnormal sum: -127
   return {m + (float)e, l * power_of_2(kept - e), power_of_2(-e)};
 }

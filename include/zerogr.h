@@ -513,7 +513,8 @@ ZG_API zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int3
  *     rows are the history's last tokens), otherwise all length[b].
  *   out: q's type (ZG_BF16 or ZG_F16); lse (may be NULL): device float32
  *     [B][R][Hq], log sum exp(scale * q k).  A row that sees nothing gives
- *     zeros and -inf.  Outputs over parts of a history merge by their lse.
+ *     zeros and -inf, one whose query holds a NaN gives NaN.  Outputs over
+ *     parts of a history merge by their lse.
  * Query and probability enter the products as half values (a query row
  * scaled by a power of two first; both relative 2^-11), codes exactly; sums,
  * maxima and outputs are 32-bit.  Cached e4m3 codes within length must not

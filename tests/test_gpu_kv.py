@@ -638,6 +638,36 @@ def test_attention_queries_of_any_size(zg, dev, R, top):
     check_attention(zg, dev, c, q, table, length, None, False, scale=min(2.0 / top, 1e30))
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("R, n", [(1, 320), (1, 5000), (3, 320), (11, 9000), (64, 320), (64, 20000), (120, 90), (300, 5000)])
+def test_attention_of_a_nan(zg, dev, R, n, causal, value):
+    """A query row with a NaN (or an infinity: codes of both signs and none) has NaN for its output and its
+    log-sum-exp, in one part and in many; the rows beside it are none the wiser, and a row that sees nothing stays
+    empty whatever its query holds."""
+    c, table, length = build(dev, "int8", 2, 1, 64, 64, [n, 70], -(-n // 64), 3)
+    c.k_codes[table[:, 0].long(), :, :, 5] = torch.tensor([0, 1, -1, 2], dtype=torch.int8, device="cuda").repeat(16)
+    q = randn((2, R, 2, 64), torch.bfloat16, 2)
+    bad = R // 2
+    want = q.clone()
+    q[:, bad, 1, 5] = value
+    rows = ints([R, max(1, R - 2)])
+    q[1, R - 1, :, 7] = value              # a row behind the last but for R of 1
+    a = dev.CacheAttention(c, 2, R, 2, table.shape[1], causal=causal, lse=True)
+    o1, l1 = (t.clone() for t in a(want, table, length, rows))
+    o2, l2 = a(q, table, length, rows)
+    ok(zg)
+    sees = torch.tensor([[(m - (nr - 1 - r) if causal else m) if r < nr else 0 for r in range(R)]
+                         for m, nr in zip((n, 70), rows.tolist())], device="cuda") > 0
+    hit = torch.zeros((2, R, 2), dtype=torch.bool, device="cuda")
+    hit[:, bad, 1] = True
+    hit[1, R - 1] = True
+    hit &= sees[..., None]
+    assert hit.any() and torch.isnan(o2[hit]).all() and torch.isnan(l2[hit]).all()
+    assert torch.equal(o2[~hit], o1[~hit]) and torch.equal(l2[~hit], l1[~hit])
+    assert not o2[~sees].any() and (l2[~sees] == -math.inf).all()
+
+
 def test_attention_strides_and_streams(zg, dev):
     """q inside a packed buffer, outputs into a wider one, on a stream that is not the current one."""
     c, table, length = build(dev, "int8", 2, 2, 64, 32, [100, 77], 5, 2)
