@@ -661,6 +661,8 @@ zg_status check_attn(const zg_kv_cache* c, int32_t max_blocks, int32_t B, int32_
   if (B < 0 || R < 0) return bad_arg(call, "B and R must be >= 0");
   if (Hq < 1 || Hq > 1024 || Hq % c->heads) return bad_arg(call, "Hq must be a multiple of cache.heads, at most 1024");
   if ((int64_t)B * R >= 0x80000000LL / Hq) return bad_arg(call, "B * R * Hq must be below 2^31");
+  if ((int64_t)max_blocks * c->block_tokens > kMostTokens)
+    return fail(ZG_ERR_UNSUPPORTED, std::string(call) + ": more than 2^31 - 2^20 tokens in a table");
   return ZG_OK;
 }
 
@@ -703,8 +705,8 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   const AttnPlan p = attn_plan(cache, max_blocks, B, R, Hq);
   if (p.bytes && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < p.bytes))
     return bad_arg(call, "workspace must hold zg_kv_attention_workspace_size bytes, 256-byte aligned");
-  if (p.items * std::max<int64_t>(p.tc ? p.splits : ((int64_t)max_blocks * cache->block_tokens + 127) / 128, 1) > 0x7FFFFFFF)
-    return fail(ZG_ERR_UNSUPPORTED, "zg_kv_attention: more than 2^31 units of work (B * heads * keys of a table / 128)");
+  if (p.items * std::max<int64_t>(p.tc ? p.splits : ((int64_t)max_blocks * cache->block_tokens + 127) / 128, 1) > kMostUnits)
+    return fail(ZG_ERR_UNSUPPORTED, "zg_kv_attention: more than 2^31 - 2^20 units of work (B * heads * keys of a table / 128)");
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
   AttnArgs a = {};

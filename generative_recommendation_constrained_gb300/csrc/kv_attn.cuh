@@ -17,7 +17,7 @@ struct AttnArgs {
   int32_t n_blocks, heads, bt, bt_log2, max_blocks;
   int32_t B, R, Hq, G, splits, ctas, causal;
   int32_t tile, mt;  // query rows an item (power of two), such items a (request, key head)
-  int32_t chunk;     // keys of a part, a multiple of 64
+  int32_t chunk;     // keys of a part, a multiple of 512, up to 2^30
   float scale;  // scale * log2(e)
 };
 
@@ -98,8 +98,12 @@ __device__ __forceinline__ PartEnd part_end(float m, float l, bool small) {
   return {m + (float)e, l * power_of_2(kept - e), power_of_2(-e)};
 }
 
+// Tokens of a table at most, and units of work of a call: room below 2^31 for
+// the steps that kernels look ahead and for a share more than there are.
+constexpr int64_t kMostTokens = 0x7FF00000, kMostUnits = 0x7FF00000;
+
 // Parts that the keys of an item are in.
-__device__ __forceinline__ int parts_of(const AttnArgs& a, int keys) { return max(1, (keys + a.chunk - 1) / a.chunk); }
+__device__ __forceinline__ int parts_of(const AttnArgs& a, int keys) { return 1 + max(keys - 1, 0) / a.chunk; }
 
 // The power of two that brings a row's largest |q| to [1, 2), as an exponent;
 // from 2^127 on to [2, 4), since its reciprocal has to be a normal number.

@@ -793,6 +793,26 @@ def test_parts_merge_by_lse(zg, dev):
     assert (merged - whole.out.float()).abs().max() <= 3 * 2.0 ** -10 * float((o1.abs().max() + o2.abs().max()))
 
 
+def test_attention_of_tables_near_2_31_tokens(zg, dev):
+    """A length of 2^31 - 2^20 beside a short one: a table of one block again and again, so that outputs are the block's own and the
+    log-sum-exp grows by the logarithm of its count."""
+    B, blocks, bt, D = 2, 2 ** 24 - 2 ** 13, 128, 32
+    c = dev.KVCache(2, bt, 1, D, "int8")
+    fill(c, 1)
+    table = torch.zeros((B, blocks), dtype=torch.int32, device="cuda")
+    lengths = [blocks * bt] + [bt] * (B - 1)
+    q = randn((B, 64, 1, D), torch.bfloat16, 2)
+    o, lse = dev.CacheAttention(c, B, 64, 1, blocks, lse=True)(q, table, ints(lengths))
+    o1, l1 = dev.CacheAttention(c, B, 64, 1, 1, lse=True)(q, table[:, :1].contiguous(), ints([bt] * B))
+    ok(zg)
+    gain = torch.tensor([math.log(n / bt) for n in lengths], device="cuda")[:, None, None]
+    # each part's sums are of 2^25 / 16 terms in 32 bits, each rounded to 2^-24: a drift of 1 / 8 at most
+    assert ((lse - l1 - gain).abs() < 0.25).all(), float((lse - l1 - gain).abs().max())
+    assert torch.equal(o[1:], o1[1:])
+    # weights and their sum drift apart by as much at most
+    assert ((o - o1).abs().float() < 0.25 * float(o1.abs().max())).all()
+
+
 def test_cache_past_32_bits(zg, dev):
     """A pool whose codes pass 4 GiB a side: blocks at its end."""
     heads, bt, dim, n = 8, 128, 128, 33000

@@ -153,6 +153,19 @@ def test_attention_refusals(zg):
     assert lib.zg_kv_attention_workspace_size(C.byref(c), 4, 1, 1, 2, None) == 1
 
 
+def test_attention_leaves_room_below_2_31(zg):
+    """Tables and units of work so near 2^31 that a look ahead would pass it are refused."""
+    c, r = cache(zg), rows(zg)
+    most = (2 ** 31 - 2 ** 20) // 16
+    a = dict(n_rows=None, q=r, out=r, lse=None, R=1, Hq=2, scale=1.0, causal=False, workspace=P, ws_bytes=1 << 60)
+    refused(zg, 4, "tokens in a table", zg.zg_kv_attention, c, P, most + 1, P, B=1, **a)
+    refused(zg, 4, "tokens in a table", zg.zg_kv_attention_workspace_size, c, most + 1, 1, 1, 2)
+    assert zg.zg_kv_attention_workspace_size(c, most, 1, 1, 2) > 0
+    # 2 heads, tables of 2^20 - 1 units of 128 tokens: 1,024 requests make 2^31 - 2^11, 1,025 more than 2^31
+    for B in (1024, 1025):
+        refused(zg, 4, "units of work", zg.zg_kv_attention, c, P, (2 ** 20 - 1) * 8, P, B=B, **a)
+
+
 def test_empty_calls_need_no_rows(zg):
     """Sizes of 0 do nothing, and an empty tensor has no address."""
     c, n, e, r = cache(zg), nrope(zg), rows(zg, data=None), rows(zg)
