@@ -415,6 +415,13 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ ReadArg
 
 // ---------------------------------------------------------------- host side
 
+// Tokens (rows) of a call at most, so that products with heads and lanes (2^11 and 2^4
+// at most) stay inside 64 bits.
+constexpr int64_t kMostRows = (int64_t)1 << 40;
+// Pieces of a write and CTAs at most: a CTA that steps past the last piece
+// stays below 2^31.
+constexpr int64_t kMostPieces = 0x7FF00000;
+
 bool dim_ok(int d) { return d == 32 || d == 64 || d == 96 || d == 128; }
 
 // zg_norm_rope (NULL: neither norm nor rotation) as a kernel argument.
@@ -542,6 +549,7 @@ zg_status zg_qk_norm_rope(const zg_norm_rope* nr, const zg_rows* q, const zg_row
   if ((st = nr_args(nr, dim, call, &na)) != ZG_OK) return st;
   if (na.rot && !positions) return bad_arg(call, "positions is NULL");
   const int64_t tokens = (int64_t)B * T;
+  if (tokens > kMostRows) return fail(ZG_ERR_UNSUPPORTED, "zg_qk_norm_rope: more than 2^40 tokens");
   const int lanes = group_lanes(dim), heads = Hq + Hk;
   const int chunk = head_chunk(tokens, heads, lanes), nchunk = (heads + chunk - 1) / chunk;
   const int64_t ctas = (tokens * nchunk * lanes + 255) / 256;
@@ -582,16 +590,16 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
   NormRopeArgs na;
   if ((st = nr_args(nr, cache->dim, call, &na)) != ZG_OK) return st;
   const int bt = cache->block_tokens, lanes = group_lanes(cache->dim);
-  const int64_t jmax = ((int64_t)T + bt - 2) / bt + 1;
+  const int64_t tokens = (int64_t)B * T, jmax = ((int64_t)T + bt - 2) / bt + 1;
+  if (tokens > kMostRows) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^40 tokens");
   // eight rows a lane group at most: groups for min(T, bt) rows, whole warps
   int groups = 1;
   while (groups * kPasses < std::min(T, bt)) groups *= 2;
   const int threads = std::max(32, groups * lanes);
   const int64_t pieces = (int64_t)B * jmax * 2 * cache->heads;
-  const int64_t tokens = (int64_t)B * T;
   const int chunk = Hq ? head_chunk(tokens, Hq, lanes) : 1, nchunk = Hq ? (Hq + chunk - 1) / chunk : 0;
   const int64_t qc = (tokens * nchunk * lanes + threads - 1) / threads;
-  if (pieces + qc > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^31 CTAs");
+  if (pieces + qc > kMostPieces) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^31 - 2^20 pieces and CTAs");
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
   // resident CTAs (128 registers a thread: 512 threads an SM; their buffers inside 200 KB) walk the pieces; where there
@@ -632,6 +640,7 @@ zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int32_t max
   if (k_out && (st = check_rows(k_out, "k_out", dt, call)) != ZG_OK) return st;
   if (v_out && (st = check_rows(v_out, "v_out", dt, call)) != ZG_OK) return st;
   if (!start) return bad_arg(call, "start is NULL");
+  if ((int64_t)B * T > kMostRows) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_read: more than 2^40 tokens");
   const int sides = (k_out ? 1 : 0) + (v_out ? 1 : 0);
   const int lanes = group_lanes(cache->dim);
   const int chunk = head_chunk((int64_t)B * T * sides, cache->heads, lanes), nchunk = (cache->heads + chunk - 1) / chunk;

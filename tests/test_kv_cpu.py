@@ -166,6 +166,19 @@ def test_attention_leaves_room_below_2_31(zg):
         refused(zg, 4, "units of work", zg.zg_kv_attention, c, P, (2 ** 20 - 1) * 8, P, B=B, **a)
 
 
+def test_sizes_past_64_bits_are_refused(zg):
+    """B and T whose products with heads and lanes leave 64 bits, and writes of so many pieces that a step past the
+    last leaves 32: refused before any launch."""
+    c, n, r, far = cache(zg, heads=1024, dim=128), nrope(zg, rot_dim=128), rows(zg), 2 ** 31 - 1
+    for B, T in ((far, far), (2 ** 30, 2 ** 11), (2 ** 21, 2 ** 20)):
+        refused(zg, 4, "tokens", zg.zg_qk_norm_rope, n, r, r, r, r, P, B, T, 1024, 1024, 128)
+        refused(zg, 4, "tokens", zg.zg_kv_append, c, n, r, r, r, r, 1024, P, 4, P, None, B, T)
+        refused(zg, 4, "tokens", zg.zg_kv_read, c, P, 4, P, None, B, T, r, r)
+    one = cache(zg, heads=1)
+    for B in (2 ** 30 - 1, 2 ** 30 - 2 ** 18, 2 ** 30 + 1):        # two pieces each
+        refused(zg, 4, "pieces", zg.zg_kv_append, one, None, r, r, None, None, 0, P, 4, P, None, B, 1)
+
+
 def test_empty_calls_need_no_rows(zg):
     """Sizes of 0 do nothing, and an empty tensor has no address."""
     c, n, e, r = cache(zg), nrope(zg), rows(zg, data=None), rows(zg)
