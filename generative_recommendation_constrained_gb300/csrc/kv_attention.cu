@@ -681,7 +681,10 @@ zg_status zg_kv_attention_workspace_size(const zg_kv_cache* cache, int32_t max_b
   if (!bytes) return bad_arg(call, "bytes is NULL");
   if ((st = check_cache(cache, &no_table, max_blocks, call)) != ZG_OK) return st;
   if ((st = check_attn(cache, max_blocks, B, R, Hq, call)) != ZG_OK) return st;
+  // what this batch and every smaller one needs: of many rows a small batch is split into parts where a large one,
+  // with an item for every SM, is not
   *bytes = attn_plan(cache, max_blocks, B, R, Hq).bytes;
+  for (int b = 1; b < std::min(B, sm_count()); ++b) *bytes = std::max(*bytes, attn_plan(cache, max_blocks, b, R, Hq).bytes);
   return ZG_OK;
 } catch (...) {
   return ZG_ERR_OUT_OF_MEMORY;

@@ -523,7 +523,9 @@ ZG_API zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int3
  * not there.  Hq a multiple of heads, at most 1024;
  * B * R * Hq below 2^31; a table's tokens, and tokens / 128 * B * heads (times
  * the row tiles of an item), at most 2^31 - 2^20, else ZG_ERR_UNSUPPORTED.  Kernels may start while
- * their predecessor in the stream ends; they wait before they touch memory. */
+ * their predecessor in the stream ends; they wait before they touch memory.
+ * The workspace's size serves this B and every smaller one, for the same table
+ * width, R and Hq. */
 ZG_API zg_status zg_kv_attention_workspace_size(const zg_kv_cache* cache, int32_t max_blocks, int32_t B,
                                                 int32_t R, int32_t Hq, size_t* bytes);
 ZG_API zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,

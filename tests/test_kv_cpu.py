@@ -198,6 +198,16 @@ def test_workspace_covers_smaller_calls(zg):
     assert a == zg.zg_kv_attention_workspace_size(c, 4096, 2, 3, 4) and isinstance(a, int)
 
 
+@pytest.mark.parametrize("R", [1, 9, 64, 256, 700])
+@pytest.mark.parametrize("blocks", [3, 500, 65536])
+def test_workspace_serves_every_smaller_batch(zg, R, blocks):
+    """A workspace sized for the largest batch is enough for each smaller one: sizes never fall with the batch."""
+    c = cache(zg, heads=4)
+    sizes = [zg.zg_kv_attention_workspace_size(c, blocks, B, R, 4) for B in range(0, 200)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert zg.zg_kv_attention_workspace_size(c, blocks, 5000, R, 4) >= sizes[-1]
+
+
 def test_binding_structs_match_the_header(zg):
     """Sizes of the argument structs as the C compiler lays them out."""
     from generative_recommendation_constrained_gb300 import _lib
