@@ -181,7 +181,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // 2e-9).  Some 20 instructions against 40 of sincospif, in kernels that come
 // near their issue limit.
 __device__ __forceinline__ void turn_sincos(int32_t turn, float& sn, float& cs) {
-  const int32_t quarter = (turn + 0x20000000) >> 30;
+  const int32_t quarter = (int32_t)((uint32_t)turn + 0x20000000u) >> 30;  // wraps
   const float t = (float)(int32_t)((uint32_t)turn - ((uint32_t)quarter << 30)) * (6.283185307f / 4294967296.f);
   const float u = t * t;
   float s = fmaf(u, 2.7557319e-6f, -1.9841270e-4f), c = fmaf(u, -2.7557319e-7f, 2.4801587e-5f);

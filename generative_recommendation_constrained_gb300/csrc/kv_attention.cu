@@ -735,7 +735,6 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   a.tile = p.tile;
   a.mt = p.mt;
   a.splits = p.splits;
-  a.ctas = p.ctas;
   a.slots = p.slots;
   if (!p.tc && p.slots)  // an even count of floats: 8-byte aligned
     a.info = reinterpret_cast<int2*>(a.part + (size_t)p.slots * p.tile * (cache->dim + 2));

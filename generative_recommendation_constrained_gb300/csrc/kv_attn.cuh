@@ -15,7 +15,7 @@ struct AttnArgs {
   int64_t slots;    // many rows: item * splits + part; few rows: two a CTA
   int2* info;       // few rows: each item's first slot and number of parts
   int32_t n_blocks, heads, bt, bt_log2, max_blocks;
-  int32_t B, R, Hq, G, splits, ctas, causal;
+  int32_t B, R, Hq, G, splits, causal;
   int32_t tile, mt;  // query rows an item (power of two), such items a (request, key head)
   int32_t chunk;     // keys of a part, a multiple of 512, up to 2^30
   float scale;  // scale * log2(e)
