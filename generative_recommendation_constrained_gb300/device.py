@@ -115,8 +115,7 @@ def _out_like(x: torch.Tensor, stream, gpu: int):
 
 
 def _int32(x: torch.Tensor | None, shape, name: str, gpu: int):
-    if x is not None and (x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous() or
-                          x.get_device() != gpu):
+    if x is not None and (x.dtype != torch.int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != gpu):
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on the GPU, on the current device "
                          f"(cuda:{gpu})")
 
@@ -124,7 +123,7 @@ def _int32(x: torch.Tensor | None, shape, name: str, gpu: int):
 def _current(held: int, what: str) -> int:
     """The current device, on which the library launches: what a call is given, and what it `held` before (-1: nothing),
     has to be there."""
-    gpu = torch.cuda.current_device()
+    gpu = torch._C._cuda_getDevice()     # current_device() without its check of the start-up: there are tensors already
     if held != gpu and held >= 0:
         raise ValueError(f"{what} on cuda:{held}, but the current device is cuda:{gpu}")
     return gpu
@@ -224,7 +223,7 @@ class KVCache:
             raise ValueError("table must be [B, max_blocks]")
         if norm_rope is not None and norm_rope.dim != self.dim:
             raise ValueError("norm_rope and the cache differ in dim")
-        if norm_rope is not None:
+        if norm_rope is not None and norm_rope.gpu != gpu and norm_rope.gpu >= 0:
             _current(norm_rope.gpu, "the gains are")
         _int32(table, (B, table.shape[1]), "table", gpu)
         _int32(start, (B,), "start", gpu)

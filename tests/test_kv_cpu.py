@@ -263,6 +263,7 @@ def fake_cuda(zg, monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: seen["device"])
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: seen["device"], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: seen["stream"], raising=False)
     for name in ("zg_qk_norm_rope", "zg_kv_append", "zg_kv_read", "zg_kv_attention"):
         monkeypatch.setattr(device.Z, name, lambda *a, name=name: seen["calls"].append((name, a[-1])))
