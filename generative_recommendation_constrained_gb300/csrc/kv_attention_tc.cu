@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto block_of = [&](int t) -> int {  // -1: behind the history; -2: outside the cache (recorded)
         const int key = (t0 + t) * kNK + 16 * g;
         if (t >= steps || key >= s.len) return -1;
-        const int blk = a.table[(int64_t)b * a.max_blocks + key / a.bt];
+        const int blk = a.table[(int64_t)b * a.max_blocks + (key >> a.bt_log2)];
         if (blk >= 0 && blk < a.n_blocks) return blk;
         if (lane < kGroups) atomicOr(a.status, kStatusCache);
         return -2;
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        "r"(bytes)
                        : "memory");
         __syncwarp();
-        const int64_t at = (((int64_t)blk * a.heads + h) * a.bt + ((t0 + t) * kNK + 16 * g) % a.bt) * D;
+        const int64_t at = (((int64_t)blk * a.heads + h) * a.bt + (((t0 + t) * kNK + 16 * g) & (a.bt - 1))) * D;
         if (lane < kGroups && blk != -1)
           bulk_load(raw + rs * Sh::kCodes + 16 * g * D, blk < 0 || (side && none0) ? g_no_codes : (side ? a.vc : a.kc) + at,
                     16 * D, &raw_full[rs]);
@@ -709,10 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j) o[j] = 0;
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float y = __uint_as_float(o[j]) * own;
-            if (twice) y += sum1[(d + j) * 128 + r] * other;
-            o[j] = __float_as_uint(y);
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * own);
+          if (twice) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              o[j] = __float_as_uint(__uint_as_float(o[j]) + sum1[(d + j) * 128 + r] * other);
           }
           const float* x = reinterpret_cast<const float*>(o);
           if (parts > 1) {
