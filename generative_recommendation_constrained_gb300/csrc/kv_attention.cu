@@ -611,10 +611,12 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
 
 // ---------------------------------------------------------------- host side
 
-// Rows up to which the join has four warps a row, not one (128 rows of some 14 parts
-// 108.3 us a call against 111.7, 512 rows of some 4 27.1 against 27.8; eight
-// warps 108.1 and 28.9).
-constexpr int64_t kJoinRows = 4096;
+// Rows up to which the join has four warps a row, not one.  Measured (us a call of
+// single tokens, four warps against one): 128 rows of some 14 parts 108.3/111.7,
+// 512 of some 4 27.1/27.8; 1,024 rows (32 requests of 4,000 tokens, 32 heads over
+// 4) 35.0/33.7, 4,096 (of 1,000) 41.0/35.6, 16,384 (of 300) 81.2/64.7.  Eight
+// warps take 108.1 and 28.9 for the first two.
+constexpr int64_t kJoinRows = 512;
 
 struct AttnPlan {
   bool tc;
