@@ -114,9 +114,9 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, i
 // without any work behind them).  Keys and dims are the long side of the
 // products (S^T = K Q^T, O^T = V^T P^T), so that eight rows fill an instruction
 // that sixteen keys or dims by eight rows make.  Bound by memory: 8 requests of
-// up to 131,072 tokens (4 heads of 128, int8, 645 MB) take 106 us, 102 of them
-// here (6.3 TB/s) and the rest the join; 64 requests of up to 4,096 tokens (85
-// MB) 25 us, some 6 of them the chain from the lengths to the first codes.
+// up to 131,072 tokens (4 heads of 128, int8, 645 MB) take 107 us, some 103 of
+// them here (6.3 TB/s) and the rest the join; 64 requests of up to 4,096 tokens
+// (85 MB) 26 us, some 6 of them the chain from the lengths to the first codes.
 constexpr uint32_t kFewSpin = 1u << 20;  // polls of a wait at most
 
 template <typename T, int D, bool INT8, int NT>

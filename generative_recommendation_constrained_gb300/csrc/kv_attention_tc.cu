@@ -21,12 +21,16 @@
 // An item of one query tile takes both places: each has the same queries and
 // every other step, and their sums are joined at the end.
 // Measured: causal chunks of 2,048 rows over up to 16,384 tokens (2 requests, 16
-// heads over 4 of 128) 391 us, 1.04 PFLOP/s or 55 % of the measured bf16 rate;
-// 256 rows each for 64 requests over up to 2,048 tokens 59 us.  Bound by the
-// waits in the chain softmax -> product -> scores of a tile, some 3,300 cycles a
-// step of which the tensor cores work 2,200 for the two: with the widening, the
-// exponentials and the maxima all left out a chunk takes 379 us, with seven
-// eighths of the products 380, with all of them 349.
+// heads over 4 of 128) 388 us, 1.04 PFLOP/s or 55 % of the measured bf16 rate;
+// 256 rows each for 64 requests over up to 2,048 tokens 61 us.  By the counters
+// the tensor pipe is active 42 % of the chunk's time and 58 % of the cycles in
+// which an SM has a CTA (28 % pass without one: 256 items on 152 SMs), 25 % and
+// 32 % of the 256 rows'.  Bound by the waits in the chain softmax -> product ->
+// scores of a tile: with the widening, the exponentials and the maxima all left
+// out a chunk took 379 us (of 399 then), with seven eighths of the products 380,
+// with all of them 349.  The loader of the codes is on that chain too: what it
+// does before it asks for a step's codes costs the whole kernel (scales after
+// the copies 431 us, divisions by the block's size 392, shifts 388).
 //
 // A key block's scale multiplies its scores, a value block's scale enters the
 // exponent (kv_attention.cu has the formula), so neither costs anything an
@@ -77,8 +81,9 @@ __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // bar_wait for the warp that issues the products, without suspending: it is on
-// the critical path of every step (causal chunks 393 us against 399; the other
-// warps' waits are better suspended, 403 and 424 with theirs spinning too).
+// the critical path of every step (causal chunks 393 us against 399 when it was
+// made so; the other warps' waits are better suspended, 403 and 424 with theirs
+// spinning too).
 __device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
   const uint32_t a = smem_u32(bar);
   uint32_t done = 0;

@@ -63,7 +63,9 @@ __device__ __forceinline__ float log2_fast(float x) {
 // 2^-126) the values are 0 and their codes are left out, but the keys count in
 // the row's sum: the scale stands where the last one before it does, or else
 // the first of the same step, or else at kNoScale, so that its weights neither
-// vanish beside the others' nor make theirs vanish.
+// vanish beside the others' nor make theirs vanish.  (Where a part begins with
+// blocks of scale 0 and goes on with scales below 2^-114, those values lose
+// bits: half a step is 2^-125 then.)
 constexpr float kNoScale = -100.f;
 __device__ __forceinline__ bool has_scale(float vs) { return vs >= 0x1p-126f; }
 __device__ __forceinline__ float scale_log2(float vs, float last) { return has_scale(vs) ? log2_fast(vs) : last; }

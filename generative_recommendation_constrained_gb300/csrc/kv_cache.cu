@@ -141,7 +141,7 @@ struct Piece {
 // this one's are turned, kept in registers between the maximum and the codes,
 // and written.  CTAs past kv_ctas turn the queries.  Bound by issue and the
 // chains of its shuffles: 32 x 2,048 tokens, 16 + 4 heads of 128, bf16 to e4m3
-// with norm and rotation take 155 us (738 MB, 4.8 TB/s); a piece a CTA, loaded
+// with norm and rotation take 156 us (738 MB, 4.7 TB/s); a piece a CTA, loaded
 // into registers, took 387.
 template <typename T, int D, bool INT8, bool INTER>
 __global__ void __launch_bounds__(256, 2) k_kv_append(const __grid_constant__ AppendArgs<T> a) {
@@ -353,8 +353,7 @@ struct ReadArgs {
 
 // One group of lanes a (token, side, chunk of heads), eight codes a lane and
 // head, four heads in flight.  16 x 1,000 tokens of 4 heads of 64 written and
-// read back: 17.5 us (a group a head, with its
-// divisions, 4 us more).
+// read back: 17.8 us (a group a head, with its divisions, 4 us more).
 template <typename T, int D, bool INT8>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ ReadArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;

@@ -516,14 +516,19 @@ ZG_API zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int3
  *     zeros and -inf, one whose query holds a NaN gives NaN.  Outputs over
  *     parts of a history merge by their lse.
  * Query and probability enter the products as half values (a query row
- * scaled by a power of two first; both relative 2^-11), codes exactly; sums,
- * maxima and outputs are 32-bit.  Cached e4m3 codes within length must not
- * be NaN; value scales below 2^-126 count as 0;
- * nothing behind it is used, and keys of a block outside the cache count as
- * not there.  Hq a multiple of heads, at most 1024;
- * B * R * Hq below 2^31; a table's tokens, and tokens / 128 * B * heads (times
- * the row tiles of an item), at most 2^31 - 2^20, else ZG_ERR_UNSUPPORTED.  Kernels may start while
- * their predecessor in the stream ends; they wait before they touch memory.
+ * scaled by a power of two first), codes exactly; sums, maxima and outputs
+ * are 32-bit.  A half is relative 2^-11 down to 2^-14 of the row's largest
+ * query element, or of the row's reference (a probability near its largest);
+ * below, the error is 2^-25 of it: a key's probability then counts in the
+ * row's sum in full and in its output to 2^-25, so that n keys of such
+ * probabilities cost up to n * 2^-25 of the values' size (2^17 keys: 2^-8).
+ * Cached e4m3 codes within length must not be NaN; value scales below 2^-126
+ * count as 0; nothing behind length is used, and keys of a block outside the
+ * cache count as not there.
+ * Hq a multiple of heads, at most 1024; B * R * Hq below 2^31; a table's
+ * tokens, and tokens / 128 * B * heads (times the row tiles of an item), at
+ * most 2^31 - 2^20, else ZG_ERR_UNSUPPORTED.  Kernels may start while their
+ * predecessor in the stream ends; they wait before they touch memory.
  * The workspace's size serves this B and every smaller one, for the same table
  * width, R and Hq. */
 ZG_API zg_status zg_kv_attention_workspace_size(const zg_kv_cache* cache, int32_t max_blocks, int32_t B,
