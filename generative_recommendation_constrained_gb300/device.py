@@ -157,19 +157,22 @@ class NormRope:
         gpu = _current(self.gpu, "the gains are")
         B, T = x.shape[:2]
         _int32(positions, (B, T), "positions", gpu)
-        for i in (q, k):
-            if i is not None and (i.shape[:2] != x.shape[:2] or i.shape[3] != self.dim):
-                raise ValueError("q and k must be [B, T, heads, dim]")
+        heads = [0, 0]
+        for n, i in enumerate((q, k)):
+            if i is not None:
+                shape = i.shape                          # each look at a tensor's shape costs 0.1 us
+                if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != self.dim:
+                    raise ValueError("q and k must be [B, T, heads, dim]")
+                heads[n] = shape[2]
+                o = (q_out, k_out)[n]
+                if o is not None and o.shape != shape:
+                    raise ValueError("an output must have its input's shape")
         if q is not None and q_out is None:
             q_out = _out_like(q, stream, gpu)
         if k is not None and k_out is None:
             k_out = _out_like(k, stream, gpu)
-        for i, o in ((q, q_out), (k, k_out)):
-            if i is not None and o.shape != i.shape:
-                raise ValueError("an output must have its input's shape")
         Z.zg_qk_norm_rope(self.struct, _rows(q, gpu), _rows(k, gpu), _rows(q_out, gpu) if q is not None else None,
-                          _rows(k_out, gpu) if k is not None else None, positions, B, T,
-                          0 if q is None else q.shape[2], 0 if k is None else k.shape[2], self.dim,
+                          _rows(k_out, gpu) if k is not None else None, positions, B, T, heads[0], heads[1], self.dim,
                           _stream(stream, gpu))
         return q_out, k_out
 
@@ -216,28 +219,32 @@ class KVCache:
         rows, all when None); norm_rope turns the keys on the way, and q [B, T, Hq, dim] into q_out, which is
         returned (a new tensor when None; it belongs to `stream`, as in NormRope)."""
         gpu = _current(self.gpu, "the cache is")
-        B, T = k.shape[:2]
-        if k.shape != v.shape or k.shape[2] != self.heads or k.shape[3] != self.dim:
+        shape = k.shape                                  # each look at a tensor's shape costs 0.1 us
+        if len(shape) != 4 or v.shape != shape or shape[2] != self.heads or shape[3] != self.dim:
             raise ValueError("k and v must be [B, T, heads, dim] of the cache")
+        B, T, _, _ = shape
         if table.dim() != 2:
             raise ValueError("table must be [B, max_blocks]")
+        width, Hq = table.shape[1], 0
         if norm_rope is not None and norm_rope.dim != self.dim:
             raise ValueError("norm_rope and the cache differ in dim")
         if norm_rope is not None and norm_rope.gpu != gpu and norm_rope.gpu >= 0:
             _current(norm_rope.gpu, "the gains are")
-        _int32(table, (B, table.shape[1]), "table", gpu)
+        _int32(table, (B, width), "table", gpu)
         _int32(start, (B,), "start", gpu)
         _int32(n_new, (B,), "n_new", gpu)
         if q is not None:
-            if q.shape[:2] != k.shape[:2] or q.shape[3] != self.dim:
+            q_shape = q.shape
+            if len(q_shape) != 4 or q_shape[0] != B or q_shape[1] != T or q_shape[3] != self.dim:
                 raise ValueError("q must be [B, T, Hq, dim]")
+            Hq = q_shape[2]
             if q_out is None:
                 q_out = _out_like(q, stream, gpu)
-            elif q_out.shape != q.shape:
+            elif q_out.shape != q_shape:
                 raise ValueError("q_out must have q's shape")
         Z.zg_kv_append(self.struct, norm_rope.struct if norm_rope is not None else None, _rows(k, gpu), _rows(v, gpu),
-                       _rows(q, gpu), _rows(q_out, gpu) if q is not None else None, 0 if q is None else q.shape[2], table,
-                       table.shape[1], start, n_new, B, T, _stream(stream, gpu))
+                       _rows(q, gpu), _rows(q_out, gpu) if q is not None else None, Hq, table, width, start, n_new, B, T,
+                       _stream(stream, gpu))
         return q_out
 
     def read(self, table, start, n=None, k_out=None, v_out=None, stream: int | None = None):
@@ -249,14 +256,15 @@ class KVCache:
         if table.dim() != 2:
             raise ValueError("table must be [B, max_blocks]")
         gpu = _current(self.gpu, "the cache is")
-        B, T = x.shape[:2]
-        for o in (k_out, v_out):
-            if o is not None and tuple(o.shape) != (B, T, self.heads, self.dim):
-                raise ValueError("outputs must be [B, T, heads, dim] of the cache")
-        _int32(table, (B, table.shape[1]), "table", gpu)
+        shape, width = x.shape, table.shape[1]
+        if len(shape) != 4 or shape[2] != self.heads or shape[3] != self.dim or (x is k_out and v_out is not None and
+                                                                                 v_out.shape != shape):
+            raise ValueError("outputs must be [B, T, heads, dim] of the cache")
+        B, T, _, _ = shape
+        _int32(table, (B, width), "table", gpu)
         _int32(start, (B,), "start", gpu)
         _int32(n, (B,), "n", gpu)
-        Z.zg_kv_read(self.struct, table, table.shape[1], start, n, B, T, _rows(k_out, gpu), _rows(v_out, gpu),
+        Z.zg_kv_read(self.struct, table, width, start, n, B, T, _rows(k_out, gpu), _rows(v_out, gpu),
                      _stream(stream, gpu))
         return k_out, v_out
 
@@ -274,12 +282,12 @@ class CacheAttention:
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.out = torch.empty((B, R, Hq, cache.dim), dtype=dtype, device=device)
         self.lse = torch.empty((B, R, Hq), dtype=torch.float32, device=device) if lse else None
-        self._out_rows = _rows(self.out, gpu)
+        self._shape, self._out_rows = self.out.shape, _rows(self.out, gpu)
 
     def __call__(self, q, table, length, n_rows=None, stream: int | None = None):
         """q [B, R, Hq, dim] over the first length[b] tokens of each request; returns (out, lse or None), this
         object's own buffers."""
-        if tuple(q.shape) != tuple(self.out.shape):
+        if q.shape != self._shape:
             raise ValueError("q must be [B, R, Hq, dim]")
         gpu = _current(self.cache.gpu, "the cache is")
         _int32(table, (self.B, self.max_blocks), "table", gpu)
