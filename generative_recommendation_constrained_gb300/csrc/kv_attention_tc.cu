@@ -21,7 +21,7 @@
 // An item of one query tile takes both places: each has the same queries and
 // every other step, and their sums are joined at the end.
 // Measured: causal chunks of 2,048 rows over up to 16,384 tokens (2 requests, 16
-// heads over 4 of 128) 388 us, 1.04 PFLOP/s or 55 % of the measured bf16 rate;
+// heads over 4 of 128) 387 us, 1.05 PFLOP/s or 55 % of the measured bf16 rate;
 // 256 rows each for 64 requests over up to 2,048 tokens 61 us.  By the counters
 // the tensor pipe is active 42 % of the chunk's time and 58 % of the cycles in
 // which an SM has a CTA (28 % pass without one: 256 items on 152 SMs), 25 % and
@@ -30,7 +30,7 @@
 // out a chunk took 379 us (of 399 then), with seven eighths of the products 380,
 // with all of them 349.  The loader of the codes is on that chain too: what it
 // does before it asks for a step's codes costs the whole kernel (scales after
-// the copies 431 us, divisions by the block's size 392, shifts 388).
+// the copies 431 us, divisions by the block's size 392, shifts 387).
 //
 // A key block's scale multiplies its scores, a value block's scale enters the
 // exponent (kv_attention.cu has the formula), so neither costs anything an
