@@ -353,7 +353,7 @@ struct ReadArgs {
 
 // One group of lanes a (token, side, chunk of heads), eight codes a lane and
 // head, four heads in flight.  16 x 1,000 tokens of 4 heads of 64 written and
-// read back: 15.8 us (a group a head, with its divisions, 4 us more).
+// read back: 17 us (a group a head, with its divisions, 4 us more).
 template <typename T, int D, bool INT8>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ ReadArgs<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
