@@ -80,8 +80,8 @@ class zg_trace(C.Structure):
                 ("ms_fused", C.c_float), ("ms_total", C.c_float)]
 
 
-ZG_KV_E4M3, ZG_KV_INT8 = 0, 1
-KV_FORMATS = {"e4m3": ZG_KV_E4M3, "int8": ZG_KV_INT8}
+ZG_KV_E4M3, ZG_KV_INT8, ZG_KV_E2M1 = 0, 1, 4
+KV_FORMATS = {"e4m3": ZG_KV_E4M3, "int8": ZG_KV_INT8, "e2m1": ZG_KV_E2M1}
 
 
 class zg_rows(C.Structure):

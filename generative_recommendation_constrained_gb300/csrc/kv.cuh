@@ -111,6 +111,30 @@ __device__ __forceinline__ uint32_t float4_codes(const float* v, float inv) {
   }
 }
 
+// Eight 4-bit codes (e2m1, the first in the lowest bits) as halves times the
+// pair of scales `s`.  A code has two significant bits and a scale four, so the
+// product is a half exactly.
+__device__ __forceinline__ void e2m1_half8(uint32_t w, uint32_t s, uint32_t* h) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+      " cvt.rn.f16x2.e2m1x2 %1, b1;\n cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<__half2*>(&h[i]) =
+        __hmul2(*reinterpret_cast<__half2*>(&h[i]), *reinterpret_cast<const __half2*>(&s));
+}
+// A scale byte u is the half whose bits are u << 7 (five bits of exponent,
+// three of mantissa): twice the same, and those of two bytes.
+__device__ __forceinline__ uint32_t scale_twice(uint32_t u) { return u * 0x00800080u; }
+__device__ __forceinline__ uint32_t scale_pair(uint32_t u, uint32_t v) { return (u << 7) | (v << 23); }
+
+// Codes and scale bytes of a row of D elements in 4 bits.
+template <int D>
+struct Row4 {
+  static constexpr int kCodes = D / 2, kScales = D / 16;
+};
+
 // Lanes of a head's row: eight elements a lane, groups of a power of two
 // (a head of 96 leaves four of its sixteen lanes idle).
 template <int D>
@@ -287,6 +311,56 @@ __device__ __forceinline__ void copy4_async(T* to, const T* from) {
                : "memory");
 }
 
+constexpr int kAhead = 4;  // heads that a lane group has in flight
+
+// `n` heads of one token through a lane group, kAhead of them in flight in
+// shared memory (each thread waits for its own elements alone; `ring`: this
+// thread's first four, `step` elements to the next).  Every lane of the warp
+// takes part `most` times.
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ void turn_heads(const NormRopeArgs& a, const LaneMap& m, const Turn& t, const T* from,
+                                           int64_t from_step, T* to, int64_t to_step, int n, int most, T* ring,
+                                           int step) {
+  from += m.e0;
+  to += m.e0;
+  const int d = m.e1 - m.e0;
+  auto fetch = [&](int i) {
+    if (i < n) {
+      T* s = ring + (i % kAhead) * 2 * step;
+      copy4_async(s, from);
+      copy4_async(s + step, from + d);
+    }
+    from += from_step;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) fetch(i);
+  for (int i = 0; i < most; ++i) {
+    fetch(i + kAhead - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    float x[8] = {};
+    if (i < n) {
+      const T* s = ring + (i % kAhead) * 2 * step;
+      load4(s, x);
+      load4(s + step, x + 4);
+    }
+    norm_rotate<D, INTER>(a, t, x);
+    if (i < n) {
+      store4(to, x);
+      store4(to + d, x + 4);
+    }
+    to += to_step;
+  }
+}
+
+struct CacheView {
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  int32_t n_blocks, heads, bt, max_blocks;
+  const int32_t* table;
+  uint32_t* status;
+};
+
 // Kernels of the history cache are launched so that they may start while their
 // predecessor in the stream ends (some 2 us a call: 64 beams 20.7 -> 18.8, 64
 // single tokens 27.1 -> 25.2): each waits here, before it touches memory, until
@@ -327,6 +401,39 @@ void for_dim(int dim, F&& f) {
     default: f(Dim<128>{}); break;
   }
 }
+
+template <typename F>
+void for_format(int format, F&& f) {
+  switch (format) {
+    case ZG_KV_E4M3: f(std::integral_constant<int, ZG_KV_E4M3>{}); break;
+    case ZG_KV_INT8: f(std::integral_constant<int, ZG_KV_INT8>{}); break;
+    default: f(std::integral_constant<int, ZG_KV_E2M1>{}); break;
+  }
+}
+
+template <typename F>
+void for_type(int dtype, F&& f) {
+  if (dtype == ZG_F32) f(Elem<float>{});
+  else if (dtype == ZG_BF16) f(Elem<__nv_bfloat16>{});
+  else f(Elem<__half>{});
+}
+
+inline int group_lanes(int dim) { return dim == 96 ? 16 : dim / 8; }
+
+// Heads a lane group walks: all of a token's when there are tokens enough for
+// every SM, fewer when there are not.
+inline int head_chunk(int64_t tokens, int heads, int lanes) {
+  const int64_t room = (int64_t)sm_count() * 1024;  // threads that keep the memory busy
+  const int64_t all = tokens * heads * lanes;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(heads, all / room));
+}
+
+// 4-bit codes (kv_cache4.cu); `chunk` heads a lane group, `nchunk` such chunks a token (a token and side)
+cudaError_t launch_append4(const CacheView& c, int dim, const NormRopeArgs* nr, const zg_rows* k, const zg_rows* v,
+                           const zg_rows* q, const zg_rows* q_out, int32_t Hq, const int32_t* start, const int32_t* n_new,
+                           int32_t B, int32_t T, int chunk, int nchunk, cudaStream_t st);
+cudaError_t launch_read4(const CacheView& c, int dim, const zg_rows* k_out, const zg_rows* v_out, const int32_t* start,
+                         const int32_t* n, int32_t B, int32_t T, int chunk, int nchunk, cudaStream_t st);
 
 // host checks shared by the entry points (kv_cache.cu)
 zg_status bad_arg(const char* call, const std::string& what);

@@ -1,10 +1,11 @@
-// Attention over a history cache held in 8 bits.
+// Attention over a history cache held in 8 or 4 bits.
 //
 //   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j)
 //
 // in one pass over the cache.  Codes enter the products exactly as halves.  A
 // key block's scale multiplies its scores; a value block's scale s enters the
-// exponent: with z the score in log2 units,
+// exponent (4-bit codes take their scales, one for 16 elements, as halves on
+// the way; the formula's are 1 then): with z the score in log2 units,
 //
 //   w_j = exp2(z_j + log2 s_j - m),  out = sum_j w_j code_j / sum_j w_j / s_j
 //
@@ -78,11 +79,75 @@ struct Tile16 {
   }
 };
 
+// The same of 4-bit codes: 16 rows of D/2 bytes, then their scale bytes.  A
+// word is eight codes; of keys a lane takes the dims c * D/4 and on (rows side
+// by side: every bank once), of values whole words (and a half one where 64 does not divide D),
+// so that a word never lies in two scales.
+template <int D>
+struct Tile16x4 {
+  static constexpr int KW = D / 32;                           // words of a key
+  static constexpr int FW = D / 64, HW = D % 64 / 32;         // whole words of a value, half ones
+  static constexpr int kCodes = 16 * Row4<D>::kCodes, kBytes = kCodes + 16 * Row4<D>::kScales;
+  // the first of the four dims of product w of the keys
+  static __device__ __forceinline__ int dim_of(int w, int c) { return c * (D / 4) + 4 * w; }
+  // the first of the two dims of product j of the values
+  static __device__ __forceinline__ int value_dim(int j, int g) {
+    return j < 4 * FW ? g * 8 * FW + 2 * j : 64 * FW + 4 * g + 2 * (j - 4 * FW);
+  }
+  static __device__ __forceinline__ void keys(const uint8_t* at, int g, int c, uint32_t (&k)[2][KW],
+                                              uint32_t (&s)[2][KW]) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const uint8_t* p = at + (n * 8 + g) * Row4<D>::kCodes + c * (D / 8);
+      const uint8_t* u = at + kCodes + (n * 8 + g) * Row4<D>::kScales;
+      if constexpr (KW == 4) *reinterpret_cast<uint4*>(k[n]) = *reinterpret_cast<const uint4*>(p);
+      else if constexpr (KW == 2) *reinterpret_cast<uint2*>(k[n]) = *reinterpret_cast<const uint2*>(p);
+      else
+#pragma unroll
+        for (int w = 0; w < KW; ++w) k[n][w] = *reinterpret_cast<const uint32_t*>(p + 4 * w);
+      if constexpr (KW == 4) {
+        const uint32_t two = *reinterpret_cast<const uint16_t*>(u + 2 * c);
+        s[n][0] = s[n][1] = scale_twice(two & 0xFF);
+        s[n][2] = s[n][3] = scale_twice(two >> 8);
+      } else {
+#pragma unroll
+        for (int w = 0; w < KW; ++w) s[n][w] = scale_twice(u[(c * (D / 4) + 8 * w) / 16]);
+      }
+    }
+  }
+  // Words of keys 2c, 2c + 1, 2c + 8, 2c + 9 and their scales; keys from `seen` on (not defined, may be NaN) as zeros.
+  static __device__ __forceinline__ void values(const uint8_t* at, int g, int c, int seen, uint32_t (&v)[4][FW + HW],
+                                                uint32_t (&s)[4][FW + HW]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 2 * c + (j & 1) + (j >> 1) * 8;
+      const uint8_t* p = at + row * Row4<D>::kCodes;
+      const uint8_t* u = at + kCodes + row * Row4<D>::kScales;
+      if constexpr (FW == 2) {
+        *reinterpret_cast<uint2*>(v[j]) = *reinterpret_cast<const uint2*>(p + 8 * g);
+        s[j][0] = s[j][1] = row < seen ? u[g] : 0;
+      } else {
+        if constexpr (FW) {
+          v[j][0] = *reinterpret_cast<const uint32_t*>(p + 4 * g);
+          s[j][0] = row < seen ? u[g / 2] : 0;
+        }
+        if constexpr (HW) {
+          v[j][FW] = *reinterpret_cast<const uint16_t*>(p + 32 * FW + 2 * g);
+          s[j][FW] = row < seen ? u[4 * FW + g / 4] : 0;
+        }
+      }
+    }
+  }
+};
+
+template <int D, int FMT>
+constexpr int kTileBytes = FMT == ZG_KV_E2M1 ? Tile16x4<D>::kBytes : Tile16<D>::kBytes;
+
 // Dynamic shared memory of k_attn_few: each warp's ring of two steps (two
 // tiles of keys, two of values each), then (in its place) the warps' sums.
-template <int D, int NT>
+template <int D, int NT, int FMT>
 constexpr int few_smem() {
-  const int ring = 4 * 2 * 4 * Tile16<D>::kBytes, sums = 4 * 8 * NT * (D + 2) * 4;
+  const int ring = 4 * 2 * 4 * kTileBytes<D, FMT>, sums = 4 * 8 * NT * (D + 2) * 4;
   return ring > sums ? ring : sums;
 }
 
@@ -119,12 +184,14 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, i
 // (85 MB) 26 us, some 6 of them the chain from the lengths to the first codes.
 constexpr uint32_t kFewSpin = 1u << 20;  // polls of a wait at most
 
-template <typename T, int D, bool INT8, int NT>
+template <typename T, int D, int FMT, int NT>
 __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const __grid_constant__ AttnArgs a,
                                                                                 const Rows<T> q, const Rows<T> out,
                                                                                 uint32_t spin) {
   using Tl = Tile16<D>;
-  constexpr int KW = Tl::KW, VW = Tl::VW, NR = 8 * NT;
+  using Tl4 = Tile16x4<D>;
+  constexpr bool k4 = FMT == ZG_KV_E2M1, INT8 = FMT == ZG_KV_INT8;
+  constexpr int KW = Tl::KW, VW = Tl::VW, NR = 8 * NT, kBytes = kTileBytes<D, FMT>;
   __shared__ float sm_m[4][NR], sm_l[4][NR];
   extern __shared__ __align__(128) uint8_t ring[];  // [warp][step][side][tile]; then float [4][NR][D + 2]
   __shared__ uint64_t full[4][2];  // [warp][step]: its copies have landed
@@ -223,28 +290,41 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       return -1;
     };
     // the tiles of step t into the warp's next slot: lanes 0-3 a copy each, (half, side)
-    uint8_t* mine = ring + warp * (2 * 4 * Tl::kBytes);
+    uint8_t* mine = ring + warp * (2 * 4 * kBytes);
     auto fetch = [&](int t, int b0, int b1) {
       if (t >= t1) return;
       const uint32_t bar = smem_u32(&full[warp][issued & 1]);
       const int blk = lane & 1 ? b1 : b0, key = t * 32 + (lane & 1) * 16;
-      const uint32_t bytes = ((b0 >= 0) + (b1 >= 0)) * 2 * Tl::kBytes;
+      const uint32_t bytes = ((b0 >= 0) + (b1 >= 0)) * 2 * kBytes;
       if (lane == 0)
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
       __syncwarp();
-      if (lane < 4 && blk >= 0) {
-        const int64_t from = (((int64_t)blk * a.heads + h) * a.bt + (key & (a.bt - 1))) * D;
+      if (lane < (k4 ? 8 : 4) && blk >= 0) {
+        const int64_t row = ((int64_t)blk * a.heads + h) * a.bt + (key & (a.bt - 1));
+        uint8_t* to = mine + ((issued & 1) * 4 + (lane & 3)) * kBytes;
+        const uint8_t* from = lane & 2 ? a.vc : a.kc;
+        int64_t at = row * D;
+        uint32_t n = Tl::kBytes;
+        if constexpr (k4) {  // lanes 4-7: the scale bytes
+          const bool s = lane >= 4;
+          at = row * (s ? Row4<D>::kScales : Row4<D>::kCodes);
+          n = 16 * (s ? Row4<D>::kScales : Row4<D>::kCodes);
+          if (s) from = lane & 2 ? a.vg : a.kg, to += Tl4::kCodes;
+        }
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                smem_u32(mine + ((issued & 1) * 4 + lane) * Tl::kBytes)),
-            "l"((lane & 2 ? a.vc : a.kc) + from), "r"(Tl::kBytes), "r"(bar)
+                smem_u32(to)),
+            "l"(from + at), "r"(n), "r"(bar)
             : "memory");
       }
       ++issued;
     };
     auto scales = [&](int blk, float& ks, float& vs) {
-      ks = blk < 0 ? 0.f : a.ks[(int64_t)blk * a.heads + h];
-      vs = blk < 0 ? 0.f : a.vs[(int64_t)blk * a.heads + h];
+      ks = vs = 1.f;  // of 4-bit codes, whose scales are in the halves already
+      if constexpr (!k4) {
+        ks = blk < 0 ? 0.f : a.ks[(int64_t)blk * a.heads + h];
+        vs = blk < 0 ? 0.f : a.vs[(int64_t)blk * a.heads + h];
+      }
     };
     int b0 = block_of(t0, 0), b1 = block_of(t0, 1);
     fetch(t0, b0, b1);
@@ -270,7 +350,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       for (int w = 0; w < KW; ++w) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[w][k] = 0.f;
-        if (sees > 0) load4(q.at(b, row, h * a.G + i % a.G) + Tl::dim_of(w, c), x[w]);
+        if (sees > 0) load4(q.at(b, row, h * a.G + i % a.G) + (k4 ? Tl4::dim_of(w, c) : Tl::dim_of(w, c)), x[w]);
       }
 #pragma unroll
       for (int w = 0; w < KW; ++w)
@@ -318,7 +398,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       float ksn[2], vsn[2];
       scales(b0, ksn[0], vsn[0]);
       scales(b1, ksn[1], vsn[1]);
-      const uint8_t* tiles = mine + (taken & 1) * 4 * Tl::kBytes;
+      const uint8_t* tiles = mine + (taken & 1) * 4 * kBytes;
       good = warp_wait(&full[warp][taken & 1], (taken >> 1) & 1, spin);
       if (!good) break;
       ++taken;
@@ -327,19 +407,36 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       if (last_lv == kNoScale) last_lv = scale_log2(vs[0], scale_log2(vs[1], kNoScale));
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        uint32_t k[2][KW];
-        Tl::keys(tiles + half * Tl::kBytes, g, c, k);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) z[half][n][j] = 0.f;
+        if constexpr (k4) {
+          uint32_t k[2][Tl4::KW], ku[2][Tl4::KW];
+          Tl4::keys(tiles + half * kBytes, g, c, k, ku);
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          uint32_t ka[4];
-          codes_half4<INT8>(k[0][w], ka[0], ka[2]);
-          codes_half4<INT8>(k[1][w], ka[1], ka[3]);
+          for (int w = 0; w < Tl4::KW; ++w) {
+            uint32_t x[4], y[4];  // of eight dims: keys g and g + 8
+            e2m1_half8(k[0][w], ku[0][w], x);
+            e2m1_half8(k[1][w], ku[1][w], y);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_16816(z[half][n], ka, qb[n][w][0], qb[n][w][1]);
+            for (int v = 0; v < 2; ++v) {
+              const uint32_t ka[4] = {x[2 * v], y[2 * v], x[2 * v + 1], y[2 * v + 1]};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_16816(z[half][n], ka, qb[n][2 * w + v][0], qb[n][2 * w + v][1]);
+            }
+          }
+        } else {
+          uint32_t k[2][KW];
+          Tl::keys(tiles + half * kBytes, g, c, k);
+#pragma unroll
+          for (int w = 0; w < KW; ++w) {
+            uint32_t ka[4];
+            codes_half4<INT8>(k[0][w], ka[0], ka[2]);
+            codes_half4<INT8>(k[1][w], ka[1], ka[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_16816(z[half][n], ka, qb[n][w][0], qb[n][w][1]);
+          }
         }
         last_lv = lv[half] = scale_log2(vs[half], last_lv);
         iv[half] = sum_weight(lv[half], small);
@@ -403,8 +500,30 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        if constexpr (k4) {
+          // the codes of two keys side by side in a byte, so that a conversion gives a pair of keys of one dim
+          uint32_t vw[4][Tl4::FW + Tl4::HW], vu[4][Tl4::FW + Tl4::HW];
+          Tl4::values(tiles + (2 + half) * kBytes, g, c, (half ? ok1 : ok0) ? vmax - key0 - 16 * half : 0, vw, vu);
+#pragma unroll
+          for (int w = 0; w < Tl4::FW + Tl4::HW; ++w) {
+            uint32_t x[2][4], y[2][4];  // [keys 2c and on, 8 on]: dims 0, 2, 4, 6 and 1, 3, 5, 7 of the word
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t k0 = vw[2 * i][w], k1 = vw[2 * i + 1][w], s = scale_pair(vu[2 * i][w], vu[2 * i + 1][w]);
+              e2m1_half8((k0 & 0x0F0F0F0Fu) | ((k1 & 0x0F0F0F0Fu) << 4), s, x[i]);
+              e2m1_half8(((k0 >> 4) & 0x0F0F0F0Fu) | (k1 & 0xF0F0F0F0u), s, y[i]);
+            }
+#pragma unroll
+            for (int v = 0; v < (w < Tl4::FW ? 4 : 2); ++v) {
+              const uint32_t va[4] = {x[0][v], y[0][v], x[1][v], y[1][v]};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_16816(o[n][4 * w + v], va, pb[half][n][0], pb[half][n][1]);
+            }
+          }
+          continue;
+        }
         uint32_t vw[4][VW];
-        Tl::values(tiles + (2 + half) * Tl::kBytes, g, c, vw);
+        Tl::values(tiles + (2 + half) * kBytes, g, c, vw);
         const bool some = (half ? ok1 : ok0) && has_scale(vs[half]);
         if (key0 + 16 * half + 16 > vmax || !some) {  // behind what is seen: not defined, may be NaN
 #pragma unroll
@@ -439,7 +558,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       for (; taken < issued; ++taken) warp_wait(&full[warp][taken & 1], (taken >> 1) & 1, kFewSpin);
     }
     __syncthreads();  // the sums take the ring's place
-    // join the warps: accumulator tile j, element (e, row g or g + 8) is row 2c + e, dim g * D/8 + 2 j (+ 1)
+    // join the warps: accumulator tile j, element (e, row g or g + 8) is row 2c + e, dim g * D/8 + 2 j (+ 1) (4 bits: value_dim(j, g))
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -454,7 +573,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
         }
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
-          *reinterpret_cast<float2*>(&sm_o[warp][r][g * (D / 8) + 2 * j]) = make_float2(o[n][j][e] * end.down, o[n][j][2 + e] * end.down);
+          *reinterpret_cast<float2*>(&sm_o[warp][r][k4 ? Tl4::value_dim(j, g) : g * (D / 8) + 2 * j]) = make_float2(o[n][j][e] * end.down, o[n][j][2 + e] * end.down);
       }
     __syncthreads();
     for (int i = threadIdx.x; i < NR * (D / 4); i += kFewThreads) {
@@ -719,6 +838,8 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
   a.vc = static_cast<const uint8_t*>(cache->v_codes);
   a.ks = cache->k_scale;
   a.vs = cache->v_scale;
+  a.kg = reinterpret_cast<const uint8_t*>(cache->k_scale);
+  a.vg = reinterpret_cast<const uint8_t*>(cache->v_scale);
   a.table = table;
   a.length = length;
   a.n_rows = n_rows;
@@ -749,8 +870,9 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
     using E = typename decltype(ev)::type;
     constexpr int D = decltype(dv)::value;
     if (!p.tc) {
-      auto kern = p.tile == 8 ? k_attn_few<E, D, decltype(iv)::value, 1> : k_attn_few<E, D, decltype(iv)::value, 2>;
-      const int smem = p.tile == 8 ? few_smem<D, 1>() : few_smem<D, 2>();
+      constexpr int FMT = decltype(iv)::value;
+      auto kern = p.tile == 8 ? k_attn_few<E, D, FMT, 1> : k_attn_few<E, D, FMT, 2>;
+      const int smem = p.tile == 8 ? few_smem<D, 1, FMT>() : few_smem<D, 2, FMT>();
       if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (err != cudaSuccess) return;
       err = launch_early(kern, p.ctas, kFewThreads, smem, sm, a, rows_of<E>(q), rows_of<E>(out),
@@ -766,14 +888,11 @@ zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table, int32_
     }
   };
   if (p.tc) {
-    const cudaError_t e = launch_attn_tc(a, q, out, cache->dim, cache->format == ZG_KV_INT8, p.items * p.splits, sm);
+    const cudaError_t e = launch_attn_tc(a, q, out, cache->dim, cache->format, p.items * p.splits, sm);
     if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
   }
   for_dim(cache->dim, [&](auto dv) {
-    auto typed = [&](auto ev) {
-      if (cache->format == ZG_KV_INT8) launch(ev, dv, std::true_type{});
-      else launch(ev, dv, std::false_type{});
-    };
+    auto typed = [&](auto ev) { for_format(cache->format, [&](auto fv) { launch(ev, dv, fv); }); };
     if (q->dtype == ZG_BF16) typed(Elem<__nv_bfloat16>{});
     else typed(Elem<__half>{});
   });

@@ -52,14 +52,16 @@ constexpr int kGroups = kNK / 16;   // groups of 16 keys: one block, one scale e
 constexpr int kSoftRegs = 184, kOtherRegs = 72;
 constexpr uint32_t kSpin = 1u << 20;  // polls of a wait at most; of those before exit always
 
-template <int D>
+template <int D, int FMT>
 struct TcShape {
   static constexpr bool kApart = D <= 64;              // P beside S
   static constexpr int kWide = kApart ? 6 : 3;         // ring entries of halves, each the keys or values of a step
   static constexpr int kRaw = kApart ? 6 : 4;          // ring entries of codes
   static constexpr int kSub = (D + 63) / 64;           // 64-dim subtiles (128-byte rows)
   static constexpr int kTile = kSub * 128 * 128;       // bytes of 128 rows of halves: a query tile, a ring entry
-  static constexpr int kCodes = kNK * D;               // bytes of a ring entry of codes
+  static constexpr bool k4 = FMT == ZG_KV_E2M1;        // 4 bits: the scale bytes lie behind a ring entry's codes
+  static constexpr int kRow = k4 ? Row4<D>::kCodes : D;
+  static constexpr int kCodes = kNK * (kRow + (k4 ? Row4<D>::kScales : 0));  // bytes of a ring entry of codes
   static constexpr size_t kSmem = (2 + kWide) * kTile + kRaw * kCodes + 1024;
   // columns of tensor memory; tile i at i * kNK, i * kPStep, i * D of them
   static constexpr uint32_t kS = 0, kP = kApart ? 256 : 0, kPStep = kApart ? 64 : kNK, kO = 512 - 2 * D;
@@ -215,10 +217,10 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
 // The codes of a block outside the cache, and the values of one without a scale.
 __device__ __align__(16) uint8_t g_no_codes[16 * 128];
 
-template <typename T, int D, bool INT8>
+template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tc(const __grid_constant__ AttnArgs a, const Rows<T> q, const Rows<T> out, uint32_t spin) {
-  using Sh = TcShape<D>;
+  using Sh = TcShape<D, FMT>;
   constexpr int kRaw = Sh::kRaw, kWide = Sh::kWide;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp < kSoftWarps + kWidenWarps) {
       // ----------------------------------------------------------- widening
-      constexpr int C16 = D / 16;         // 16-byte pieces of a code row
+      constexpr int C16 = Sh::kRow / 16;  // 16-byte pieces of a code row
       constexpr int N = kNK * C16 / 128;  // pieces a thread: tid, tid + 128, ...
       constexpr int NB = N % 4 ? 2 : 4;   // of them at a time
       const int tid = threadIdx.x - 32 * kSoftWarps;
@@ -336,27 +338,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint8_t* codes = raw + rs * Sh::kCodes + tid * 16;
         uint8_t* to = wide + ws * Sh::kTile;
+        if constexpr (Sh::k4) {
+          // a piece is 32 elements: four stores, of which lanes of the second subtile begin two on (they fall on the
+          // same banks as the first's)
+          const uint8_t* scales = raw + rs * Sh::kCodes + kNK * Sh::kRow;
 #pragma unroll
-        for (int i0 = 0; i0 < N; i0 += NB) {
-          uint4 w[NB];
+          for (int i = 0; i < N; ++i) {
+            const int idx = tid + 128 * i, r = idx / C16, c = idx % C16, j = (c & 1) * 4;
+            const uint4 w = *reinterpret_cast<const uint4*>(codes + 128 * i * 16);
+            uint32_t u = *reinterpret_cast<const uint16_t*>(scales + r * Row4<D>::kScales + 2 * c);
+            if (r >= held) u = 0;  // behind the history: not defined, may be NaN
+            const uint32_t s0 = scale_twice(u & 0xFF), s1 = scale_twice(u >> 8);
+            uint4 h[4];
+            e2m1_half8(w.x, s0, &h[0].x);
+            e2m1_half8(w.y, s0, &h[1].x);
+            e2m1_half8(w.z, s1, &h[2].x);
+            e2m1_half8(w.w, s1, &h[3].x);
+            uint8_t* at = to + (c / 2) * (kNK * 128) + r * 128;
+            const bool swap2 = c >= 2;
 #pragma unroll
-          for (int i = 0; i < NB; ++i) w[i] = *reinterpret_cast<const uint4*>(codes + 128 * (i0 + i) * 16);
-          if (held < kNK) {  // behind the history: not defined, may be NaN
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-              if ((tid + 128 * (i0 + i)) / C16 >= held) w[i] = make_uint4(0, 0, 0, 0);
+            for (int p = 0; p < 4; ++p)
+              *reinterpret_cast<uint4*>(at + (((j + (swap2 ? p ^ 2 : p)) ^ (r & 7)) << 4)) = swap2 ? h[p ^ 2] : h[p];
           }
+        } else {
 #pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            uint32_t a1 = p1 + (i0 + i) * (128 / C16) * 128, a2 = p2 + (i0 + i) * (128 / C16) * 128;
-            if constexpr (D == 96) place(tid + 128 * (i0 + i), a1, a2);
-            uint4 lo, hi;
-            codes_half4<INT8>(w[i].x, lo.x, lo.y);
-            codes_half4<INT8>(w[i].y, lo.z, lo.w);
-            codes_half4<INT8>(w[i].z, hi.x, hi.y);
-            codes_half4<INT8>(w[i].w, hi.z, hi.w);
-            *reinterpret_cast<uint4*>(to + (swap ? a2 : a1)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(to + (swap ? a1 : a2)) = swap ? lo : hi;
+          for (int i0 = 0; i0 < N; i0 += NB) {
+            uint4 w[NB];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) w[i] = *reinterpret_cast<const uint4*>(codes + 128 * (i0 + i) * 16);
+            if (held < kNK) {  // behind the history: not defined, may be NaN
+#pragma unroll
+              for (int i = 0; i < NB; ++i)
+                if ((tid + 128 * (i0 + i)) / C16 >= held) w[i] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              uint32_t a1 = p1 + (i0 + i) * (128 / C16) * 128, a2 = p2 + (i0 + i) * (128 / C16) * 128;
+              if constexpr (D == 96) place(tid + 128 * (i0 + i), a1, a2);
+              uint4 lo, hi;
+              codes_half4<FMT == ZG_KV_INT8>(w[i].x, lo.x, lo.y);
+              codes_half4<FMT == ZG_KV_INT8>(w[i].y, lo.z, lo.w);
+              codes_half4<FMT == ZG_KV_INT8>(w[i].z, hi.x, hi.y);
+              codes_half4<FMT == ZG_KV_INT8>(w[i].w, hi.z, hi.w);
+              *reinterpret_cast<uint4*>(to + (swap ? a2 : a1)) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(to + (swap ? a1 : a2)) = swap ? lo : hi;
+            }
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -452,7 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // blocks of the step whose values come next and of the three behind it; scales of the step whose keys come next
       int tv = 0, b0 = block_of(0), b1 = block_of(1), b2 = block_of(2), b3 = block_of(3);
-      float ks = b0 < 0 ? 0.f : a.ks[(int64_t)b0 * a.heads + h], vs = b0 < 0 ? 0.f : a.vs[(int64_t)b0 * a.heads + h];
+      // of 4-bit codes, whose scales are in the halves already: 1
+      auto scale_of = [&](const float* scales, int blk) -> float {
+        if constexpr (Sh::k4) return 1.f;
+        return blk < 0 ? 0.f : scales[(int64_t)blk * a.heads + h];
+      };
+      float ks = scale_of(a.ks, b0), vs = scale_of(a.vs, b0);
       const bool small = __shfl_sync(0xFFFFFFFFu, small_scale(vs), 0);
       if (lane == 0) s_small = small;  // seen by all who see the first codes
       float last_lv = kNoScale;      // of this lane's group, in the step before
@@ -466,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           good = false;
           break;
         }
-        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, lane < kGroups && blk != -1)) * (16u * (uint32_t)D);
+        const uint32_t bytes =
+            __popc(__ballot_sync(0xFFFFFFFFu, lane < kGroups && blk != -1)) * (uint32_t)(Sh::kCodes / kGroups);
         if (!side) {
           float lv = log2_fast(vs), iv = sum_weight(lv, small);
           const uint32_t some = __ballot_sync(0xFFFFFFFFu, has_scale(vs)) & ((1u << kGroups) - 1);
@@ -481,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             last_lv = lv;
           }
+          if (Sh::k4 && blk == -2) lv = -INFINITY, iv = 0.f;
           if (lane < kGroups && t < steps) {
             s_ks[t & 15][g] = ks;
             s_lv[t & 15][g] = lv;
@@ -488,8 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           (t == tv ? none0 : none1) = !has_scale(vs);
           const int nb = t == tv ? b1 : b2;
-          ks = nb < 0 ? 0.f : a.ks[(int64_t)nb * a.heads + h];
-          vs = nb < 0 ? 0.f : a.vs[(int64_t)nb * a.heads + h];
+          ks = scale_of(a.ks, nb);
+          vs = scale_of(a.vs, nb);
         }
         __syncwarp();
         if (lane == 0)
@@ -497,10 +530,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                        "r"(bytes)
                        : "memory");
         __syncwarp();
-        const int64_t at = (((int64_t)blk * a.heads + h) * a.bt + (((t0 + t) * kNK + 16 * g) & (a.bt - 1))) * D;
-        if (lane < kGroups && blk != -1)
-          bulk_load(raw + rs * Sh::kCodes + 16 * g * D, blk < 0 || (side && none0) ? g_no_codes : (side ? a.vc : a.kc) + at,
-                    16 * D, &raw_full[rs]);
+        const int64_t row = ((int64_t)blk * a.heads + h) * a.bt + (((t0 + t) * kNK + 16 * g) & (a.bt - 1));
+        if (lane < kGroups && blk != -1) {
+          bulk_load(raw + rs * Sh::kCodes + 16 * g * Sh::kRow,
+                    blk < 0 || (side && none0) ? g_no_codes : (side ? a.vc : a.kc) + row * Sh::kRow, 16 * Sh::kRow,
+                    &raw_full[rs]);
+          if constexpr (Sh::k4)
+            bulk_load(raw + rs * Sh::kCodes + kNK * Sh::kRow + 16 * g * Row4<D>::kScales,
+                      blk < 0 ? g_no_codes : (side ? a.vg : a.kg) + row * Row4<D>::kScales, 16 * Row4<D>::kScales,
+                      &raw_full[rs]);
+        }
         issued = n + 1;
         if (side) {
           ++tv;
@@ -770,23 +809,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int attn_tc_tile(int64_t rows) { return rows > 128 ? 256 : 128; }
 
-cudaError_t launch_attn_tc(const AttnArgs& a, const zg_rows* q, const zg_rows* out, int dim, bool int8,
+cudaError_t launch_attn_tc(const AttnArgs& a, const zg_rows* q, const zg_rows* out, int dim, int format,
                            int64_t items, cudaStream_t st) {
   cudaError_t err = cudaSuccess;
   auto go = [&](auto ev, auto dv, auto iv) {
     using E = typename decltype(ev)::type;
     constexpr int D = decltype(dv)::value;
-    auto kern = k_attn_tc<E, D, decltype(iv)::value>;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TcShape<D>::kSmem);
+    constexpr int FMT = decltype(iv)::value;
+    auto kern = k_attn_tc<E, D, FMT>;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TcShape<D, FMT>::kSmem);
     if (err != cudaSuccess) return;
-    err = launch_early(kern, items, kThreads, TcShape<D>::kSmem, st, a, rows_of<E>(q), rows_of<E>(out),
+    err = launch_early(kern, items, kThreads, TcShape<D, FMT>::kSmem, st, a, rows_of<E>(q), rows_of<E>(out),
                        std::min(wait_limit(), kSpin));
   };
   for_dim(dim, [&](auto dv) {
-    auto typed = [&](auto ev) {
-      if (int8) go(ev, dv, std::true_type{});
-      else go(ev, dv, std::false_type{});
-    };
+    auto typed = [&](auto ev) { for_format(format, [&](auto fv) { go(ev, dv, fv); }); };
     if (q->dtype == ZG_BF16) typed(Elem<__nv_bfloat16>{});
     else typed(Elem<__half>{});
   });

@@ -7,7 +7,8 @@ namespace zg {
 
 struct AttnArgs {
   const uint8_t *kc, *vc;
-  const float *ks, *vs;
+  const float *ks, *vs;      // 8 bits: a scale a (block, head)
+  const uint8_t *kg, *vg;    // 4 bits: a scale byte for 16 elements
   const int32_t *table, *length, *n_rows;
   uint32_t* status;
   float* lse;
@@ -149,7 +150,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
 // Many query rows: the products on the tensor cores' tcgen05 path
 // (kv_attention_tc.cu).  Query rows of an item, and its launch.
 int attn_tc_tile(int64_t rows);
-cudaError_t launch_attn_tc(const AttnArgs& a, const zg_rows* q, const zg_rows* out, int dim, bool int8,
+cudaError_t launch_attn_tc(const AttnArgs& a, const zg_rows* q, const zg_rows* out, int dim, int format,
                            int64_t items, cudaStream_t st);
 
 }  // namespace zg

@@ -1,5 +1,5 @@
 // The history cache's writes: per-head norm and rotation, quantised writes,
-// reads.  All are bound by memory; each input element is loaded once and each
+// reads (of 4 bits: kv_cache4.cu).  All are bound by memory; each input element is loaded once and each
 // output written once, with 32-bit arithmetic between.
 //
 //   norm     y = x / sqrt(mean(x^2) + eps) * gain over a head
@@ -31,48 +31,6 @@ struct RotateArgs {
   int32_t B, T_, Hq, Hk, chunk, nchunk;  // heads a group of lanes walks; such chunks a token
   NormRopeArgs nr;
 };
-
-constexpr int kAhead = 4;  // heads that a lane group has in flight
-
-// `n` heads of one token through a lane group, kAhead of them in flight in
-// shared memory (each thread waits for its own elements alone; `ring`: this
-// thread's first four, `step` elements to the next).  Every lane of the warp
-// takes part `most` times.
-template <typename T, int D, bool INTER>
-__device__ __forceinline__ void turn_heads(const NormRopeArgs& a, const LaneMap& m, const Turn& t, const T* from,
-                                           int64_t from_step, T* to, int64_t to_step, int n, int most, T* ring,
-                                           int step) {
-  from += m.e0;
-  to += m.e0;
-  const int d = m.e1 - m.e0;
-  auto fetch = [&](int i) {
-    if (i < n) {
-      T* s = ring + (i % kAhead) * 2 * step;
-      copy4_async(s, from);
-      copy4_async(s + step, from + d);
-    }
-    from += from_step;
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-#pragma unroll
-  for (int i = 0; i < kAhead - 1; ++i) fetch(i);
-  for (int i = 0; i < most; ++i) {
-    fetch(i + kAhead - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-    float x[8] = {};
-    if (i < n) {
-      const T* s = ring + (i % kAhead) * 2 * step;
-      load4(s, x);
-      load4(s + step, x + 4);
-    }
-    norm_rotate<D, INTER>(a, t, x);
-    if (i < n) {
-      store4(to, x);
-      store4(to + d, x + 4);
-    }
-    to += to_step;
-  }
-}
 
 // One group of lanes a (token, chunk of heads): the angles are computed once
 // for the chunk.  Bound by memory: 32 x 4,096 tokens of 20 heads of 128 (bf16,
@@ -109,14 +67,6 @@ __global__ void __launch_bounds__(256) k_norm_rope(const __grid_constant__ Rotat
 }
 
 // ------------------------------------------------------------------- append
-
-struct CacheView {
-  uint8_t *kc, *vc;
-  float *ks, *vs;
-  int32_t n_blocks, heads, bt, max_blocks;
-  const int32_t* table;
-  uint32_t* status;
-};
 
 template <typename T>
 struct AppendArgs {
@@ -464,23 +414,6 @@ CacheView view(const zg_kv_cache* c, const int32_t* table, int32_t max_blocks, u
           c->n_blocks, c->heads, c->block_tokens, max_blocks, table, status};
 }
 
-template <typename F>
-void for_type(int dtype, F&& f) {
-  if (dtype == ZG_F32) f(Elem<float>{});
-  else if (dtype == ZG_BF16) f(Elem<__nv_bfloat16>{});
-  else f(Elem<__half>{});
-}
-
-int group_lanes(int dim) { return dim == 96 ? 16 : dim / 8; }
-
-// Heads a lane group walks: all of a token's when there are tokens enough for
-// every SM, fewer when there are not.
-int head_chunk(int64_t tokens, int heads, int lanes) {
-  const int64_t room = (int64_t)sm_count() * 1024;  // threads that keep the memory busy
-  const int64_t all = tokens * heads * lanes;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(heads, all / room));
-}
-
 }  // namespace
 
 zg_status bad_arg(const char* call, const std::string& what) {
@@ -501,8 +434,8 @@ zg_status check_rows(const zg_rows* r, const char* name, int dtype, const char* 
 
 zg_status check_cache(const zg_kv_cache* c, const int32_t* table, int32_t max_blocks, const char* call) {
   if (!c) return bad_arg(call, "cache is NULL");
-  if (c->format != ZG_KV_E4M3 && c->format != ZG_KV_INT8)
-    return bad_arg(call, "cache.format must be ZG_KV_E4M3 or ZG_KV_INT8");
+  if (c->format != ZG_KV_E4M3 && c->format != ZG_KV_INT8 && c->format != ZG_KV_E2M1)
+    return bad_arg(call, "cache.format must be ZG_KV_E4M3, ZG_KV_INT8 or ZG_KV_E2M1");
   if (c->n_blocks < 1 || c->heads < 1 || c->heads > 1024)
     return bad_arg(call, "cache needs n_blocks >= 1 and heads in [1, 1024]");
   const int t = c->block_tokens;
@@ -512,8 +445,9 @@ zg_status check_cache(const zg_kv_cache* c, const int32_t* table, int32_t max_bl
   if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale) return bad_arg(call, "cache pointer is NULL");
   if ((reinterpret_cast<uintptr_t>(c->k_codes) | reinterpret_cast<uintptr_t>(c->v_codes)) % 16)
     return bad_arg(call, "cache codes must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale)) % 4)
-    return bad_arg(call, "cache scales must be 4-byte aligned");
+  const uintptr_t scales = reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale);
+  if (c->format == ZG_KV_E2M1 && scales % 16) return bad_arg(call, "scale bytes of 4-bit codes must be 16-byte aligned");
+  if (scales % 4) return bad_arg(call, "cache scales must be 4-byte aligned");
   if (!table || reinterpret_cast<uintptr_t>(table) % 4) return bad_arg(call, "table is NULL or not 4-byte aligned");
   if (max_blocks < 1 || (int64_t)max_blocks * c->block_tokens > 0x7FFFFFFF)
     return bad_arg(call, "max_blocks must be >= 1 with max_blocks * block_tokens below 2^31");
@@ -589,6 +523,19 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
   NormRopeArgs na;
   if ((st = nr_args(nr, cache->dim, call, &na)) != ZG_OK) return st;
   const int bt = cache->block_tokens, lanes = group_lanes(cache->dim);
+  if (cache->format == ZG_KV_E2M1) {
+    uint32_t* status = nullptr;
+    const int64_t tokens = (int64_t)B * T;
+    const int heads = Hq + 2 * cache->heads;
+    if (tokens > kMostRows) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^40 tokens");
+    const int chunk = head_chunk(tokens, heads, lanes), nchunk = (heads + chunk - 1) / chunk;
+    const int64_t ctas = (tokens * nchunk * lanes + 255) / 256;
+    if (ctas > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^31 CTAs");
+    if ((st = get_status_ptr(&status)) != ZG_OK) return st;
+    const cudaError_t err = launch_append4(view(cache, table, max_blocks, status), cache->dim, nr ? &na : nullptr, k, v, q,
+                                           q_out, Hq, start, n_new, B, T, chunk, nchunk, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache append launch");
+  }
   const int64_t tokens = (int64_t)B * T, jmax = ((int64_t)T + bt - 2) / bt + 1;
   if (tokens > kMostRows) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^40 tokens");
   // eight rows a lane group at most: groups for min(T, bt) rows, whole warps
@@ -648,6 +595,11 @@ zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int32_t max
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
   cudaError_t err = cudaSuccess;
+  if (cache->format == ZG_KV_E2M1) {
+    err = launch_read4(view(cache, table, max_blocks, status), cache->dim, k_out, v_out, start, n, B, T, chunk, nchunk,
+                       static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache read launch");
+  }
   for_type(dt, [&](auto e) {
     using E = typename decltype(e)::type;
     const ReadArgs<E> a = {view(cache, table, max_blocks, status), rows_of<E>(k_out), rows_of<E>(v_out), start, n,

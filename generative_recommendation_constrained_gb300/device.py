@@ -74,7 +74,7 @@ class Decoder:
 
 
 _ROW_TYPES = {torch.float32: Z.ZG_F32, torch.bfloat16: Z.ZG_BF16, torch.float16: Z.ZG_F16}
-_CODE_TYPES = {torch.float8_e4m3fn: Z.ZG_KV_E4M3, torch.int8: Z.ZG_KV_INT8}
+_CODE_TYPES = {torch.float8_e4m3fn: Z.ZG_KV_E4M3, torch.int8: Z.ZG_KV_INT8, torch.uint8: Z.ZG_KV_E2M1}
 
 
 # The library launches on the current device; the classes below refuse tensors of another one.
@@ -178,14 +178,18 @@ class NormRope:
 
 
 class KVCache:
-    """A cache of keys and values in 8 bits (zg_kv_cache): codes [n_blocks, heads, block_tokens, dim] and a scale a
-    (block, head) and side.  Block tables [B, max_blocks], lengths and counts [B] are int32 device tensors that the
-    caller keeps; entries past a request's tokens are not read."""
+    """A cache of keys and values in 8 or 4 bits (zg_kv_cache).  fmt "e4m3" or "int8": codes [n_blocks, heads,
+    block_tokens, dim] and a float32 scale a (block, head) and side.  "e2m1": uint8 codes [n_blocks, heads,
+    block_tokens, dim / 2], two a byte, and uint8 scales [n_blocks, heads, block_tokens, dim / 16], the upper bits of a
+    half (u << 7).  Block tables [B, max_blocks], lengths and counts [B] are int32 device tensors that the caller keeps;
+    entries past a request's tokens are not read."""
 
     def __init__(self, n_blocks: int, block_tokens: int, heads: int, dim: int, fmt: str = "e4m3", device="cuda"):
-        dt = torch.float8_e4m3fn if Z.KV_FORMATS[fmt] == Z.ZG_KV_E4M3 else torch.int8
-        codes = [torch.empty((n_blocks, heads, block_tokens, dim), dtype=dt, device=device) for _ in range(2)]
-        scales = [torch.empty((n_blocks, heads), dtype=torch.float32, device=device) for _ in range(2)]
+        shape, four = (n_blocks, heads, block_tokens), Z.KV_FORMATS[fmt] == Z.ZG_KV_E2M1
+        dt = {v: k for k, v in _CODE_TYPES.items()}[Z.KV_FORMATS[fmt]]
+        codes = [torch.empty((*shape, dim // 2 if four else dim), dtype=dt, device=device) for _ in range(2)]
+        scales = [torch.empty((*shape, dim // 16), dtype=dt, device=device) if four else
+                  torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
         self._set(*codes, *scales)
 
     @classmethod
@@ -197,11 +201,14 @@ class KVCache:
 
     def _set(self, k_codes, v_codes, k_scale, v_scale):
         if k_codes.dtype not in _CODE_TYPES or k_codes.dim() != 4:
-            raise ValueError("codes must be float8_e4m3fn or int8 [n_blocks, heads, block_tokens, dim]")
+            raise ValueError("codes must be float8_e4m3fn or int8 [n_blocks, heads, block_tokens, dim], or uint8 [.., dim / 2]")
+        four, shape = k_codes.dtype == torch.uint8, tuple(k_codes.shape)
         for x, like in ((v_codes, k_codes), (k_scale, None), (v_scale, None)):
             if like is not None and (x.dtype != like.dtype or x.shape != like.shape):
                 raise ValueError("k_codes and v_codes must be alike")
-            if like is None and (x.dtype != torch.float32 or x.shape != k_codes.shape[:2]):
+            if like is None and four and (x.dtype != torch.uint8 or tuple(x.shape) != (*shape[:3], shape[3] // 8)):
+                raise ValueError("scales of 4-bit codes must be uint8 [n_blocks, heads, block_tokens, dim / 16]")
+            if like is None and not four and (x.dtype != torch.float32 or x.shape != k_codes.shape[:2]):
                 raise ValueError("scales must be float32 [n_blocks, heads]")
         if not all(x.is_contiguous() and x.is_cuda for x in (k_codes, v_codes, k_scale, v_scale)):
             raise ValueError("codes and scales must be contiguous and on the GPU")
@@ -209,7 +216,7 @@ class KVCache:
         if any(x.get_device() != self.gpu for x in (v_codes, k_scale, v_scale)):
             raise ValueError("codes and scales must be on one device")
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
-        self.n_blocks, self.heads, self.block_tokens, self.dim = k_codes.shape
+        self.n_blocks, self.heads, self.block_tokens, self.dim = *shape[:3], shape[3] * (2 if four else 1)
         self.struct = Z.make_kv_cache(_CODE_TYPES[k_codes.dtype], self.n_blocks, self.heads, self.block_tokens,
                                       self.dim, k_codes, v_codes, k_scale, v_scale)
 

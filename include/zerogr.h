@@ -405,7 +405,7 @@ ZG_API size_t zg_static_scratch_bytes(void);
  * The hidden vector of a request (zg_decode's u) comes from a model over the
  * user's history.  These calls are the memory side of that model: queries
  * and keys normalised per head and rotated by position, keys and values held
- * in 8 bits in blocks of tokens, and attention over such a cache for single
+ * in 8 or 4 bits in blocks of tokens, and attention over such a cache for single
  * tokens, for a decode's beams (many query rows, one history) and for causal
  * chunks.  No counterpart in the pages; they serve the model the pages take
  * as given ([Pipeline] stage 1).
@@ -429,19 +429,28 @@ typedef struct {
   int64_t stride_b, stride_t, stride_h;
 } zg_rows;
 
-typedef enum { ZG_KV_E4M3 = 0, ZG_KV_INT8 = 1 } zg_kv_format;
+typedef enum { ZG_KV_E4M3 = 0, ZG_KV_INT8 = 1, ZG_KV_E2M1 = 4 } zg_kv_format;
 
-/* A cache of keys and values in blocks of block_tokens tokens.  Codes are
- * [n_blocks][heads][block_tokens][dim] bytes (e4m3 or two's complement), one
- * float32 scale a (block, head) and side: value = code * scale.  A request's
+/* A cache of keys and values in blocks of block_tokens tokens.  A request's
  * token p is row p % block_tokens of block table[b][p / block_tokens].
- * dim: 32, 64, 96 or 128; block_tokens: 16, 32, 64 or 128; codes 16-byte
- * aligned.  Device memory, caller-owned; needs no initialisation. */
+ * ZG_KV_E4M3, ZG_KV_INT8: codes are [n_blocks][heads][block_tokens][dim] bytes
+ * (e4m3 or two's complement), one float32 scale a (block, head) and side:
+ * value = code * scale.
+ * ZG_KV_E2M1: codes are [n_blocks][heads][block_tokens][dim / 2] bytes of two
+ * 4-bit codes (the earlier element in the low half; bit 3 the sign, bits 0-2
+ * one of 0, 0.5, 1, 1.5, 2, 3, 4, 6), and k_scale, v_scale point (cast) at
+ * [n_blocks][heads][block_tokens][dim / 16] bytes, one for 16 neighbouring
+ * elements: value = code * scale, scale the half whose bits are byte << 7.
+ * Bytes above 226 (10240) do not occur; a token within a length must not hold
+ * them.
+ * dim: 32, 64, 96 or 128; block_tokens: 16, 32, 64 or 128; codes (and the
+ * scales of ZG_KV_E2M1) 16-byte aligned.  Device memory, caller-owned; needs
+ * no initialisation. */
 typedef struct {
   int32_t format, n_blocks, heads, block_tokens, dim, reserved;
   void* k_codes;
   void* v_codes;
-  float* k_scale;
+  float* k_scale; /* ZG_KV_E2M1: bytes */
   float* v_scale;
 } zg_kv_cache;
 
@@ -485,10 +494,15 @@ ZG_API zg_status zg_qk_norm_rope(const zg_norm_rope* nr, const zg_rows* q, const
  *     step rounded to 32 bits, so that codes equal bit for bit those of the
  *     same steps in elementary float32 operations; the stored scale, the
  *     quotient rounded once, differs from it in its last bits at most.
- * A NaN is stored as 0 and an infinity as +-Q of the block's finite values;
- * either is recorded for zg_check_device_status, so no NaN enters a cache.
+ * ZG_KV_E2M1: scale of 16 elements = the nearest to max |x| / 6 of the halves
+ *     that a byte can hold, at most 10240; code = the nearest to x / scale,
+ *     both to nearest even of the exact quotient, the code within +-6; rows
+ *     held already are not touched.  A scale's steps are 2^-17 below 2^-14: 16
+ *     elements none of which passes 6 * 2^-18 are held as 0.
+ * A NaN is stored as 0 and an infinity as +-Q (+-6) of the block's (the 16
+ * elements') finite values; either is recorded for zg_check_device_status, so no NaN enters a cache.
  * nr (may be NULL) is applied to the keys on the way, at positions start[b]
- * + t and before the rounding to 8 bits, and to q (may be NULL) into q_out
+ * + t and before the rounding to codes, and to q (may be NULL) into q_out
  * (all T rows of it).  k, v: [B][T][heads], q: [B][T][Hq], one type.  table:
  * device int32 [B][max_blocks]; start, n_new: device int32 [B].  Blocks
  * written by one call must belong to one request each. */
@@ -522,8 +536,8 @@ ZG_API zg_status zg_kv_read(const zg_kv_cache* cache, const int32_t* table, int3
  * below, the error is 2^-25 of it: a key's probability then counts in the
  * row's sum in full and in its output to 2^-25, so that n keys of such
  * probabilities cost up to n * 2^-25 of the values' size (2^17 keys: 2^-8).
- * Cached e4m3 codes within length must not be NaN; value scales below 2^-126
- * count as 0; nothing behind length is used, and keys of a block outside the
+ * Cached e4m3 codes within length must not be NaN; value scales of 8-bit codes
+ * below 2^-126 count as 0; nothing behind length is used, and keys of a block outside the
  * cache count as not there.
  * Hq a multiple of heads, at most 1024; B * R * Hq below 2^31; a table's
  * tokens, and tokens / 128 * B * heads (times the row tiles of an item), at
