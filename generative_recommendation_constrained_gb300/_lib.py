@@ -136,6 +136,9 @@ def _load():
         "zg_kv_read": [vp, vp, i32, vp, vp, i32, i32, vp, vp, vp],
         "zg_kv_attention_workspace_size": [vp, i32, i32, i32, i32, P(sz)],
         "zg_kv_attention": [vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, C.c_float, i32, vp, sz, vp],
+        "zg_kv_weights": [vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, C.c_float, i32, i32, i32, C.c_float, i32, vp],
+        "zg_kv_evict_workspace_size": [vp, i32, i32, P(sz)],
+        "zg_kv_evict": [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -471,5 +474,28 @@ def zg_kv_attention(cache: zg_kv_cache, table, max_blocks: int, length, n_rows, 
     """q, out: zg_rows or their bytes."""
     st = lib.zg_kv_attention(_ref(cache), _ptr(table), max_blocks, _ptr(length), _ptr(n_rows), _ref(q), _ref(out),
                              _ptr(lse), B, R, Hq, scale, causal, _ptr(workspace), ws_bytes, stream)
+    if st:
+        _check(st)
+
+
+def zg_kv_weights(cache: zg_kv_cache, table, max_blocks: int, length, n_rows, known, q, lse, weights, w_tokens: int,
+                  decay: float, B: int, R: int, Hq: int, scale: float, causal: bool, stream: int = 0):
+    """q: zg_rows or its bytes."""
+    st = lib.zg_kv_weights(_ref(cache), _ptr(table), max_blocks, _ptr(length), _ptr(n_rows), _ptr(known), _ref(q),
+                           _ptr(lse), _ptr(weights), w_tokens, decay, B, R, Hq, scale, causal, stream)
+    if st:
+        _check(st)
+
+
+def zg_kv_evict_workspace_size(cache: zg_kv_cache, B: int, keep: int) -> int:
+    n = C.c_size_t(0)
+    _check(lib.zg_kv_evict_workspace_size(_ref(cache), B, keep, C.byref(n)))
+    return n.value
+
+
+def zg_kv_evict(cache: zg_kv_cache, table, max_blocks: int, length, weights, w_tokens: int, keep: int, recent: int,
+                new_length, kept, B: int, workspace, ws_bytes: int, stream: int = 0):
+    st = lib.zg_kv_evict(_ref(cache), _ptr(table), max_blocks, _ptr(length), _ptr(weights), w_tokens, keep, recent,
+                         _ptr(new_length), _ptr(kept), B, _ptr(workspace), ws_bytes, stream)
     if st:
         _check(st)

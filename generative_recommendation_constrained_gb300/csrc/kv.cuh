@@ -370,9 +370,9 @@ __device__ __forceinline__ void after_predecessor() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 template <typename... P, typename... A>
-inline cudaError_t launch_early(void (*kern)(P...), int64_t ctas, int threads, size_t smem, cudaStream_t st, A... args) {
+inline cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -382,6 +382,11 @@ inline cudaError_t launch_early(void (*kern)(P...), int64_t ctas, int threads, s
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kern)(P...), int64_t ctas, int threads, size_t smem, cudaStream_t st, A... args) {
+  return launch_early(kern, dim3((unsigned)ctas), threads, smem, st, args...);
 }
 
 // Run-time head size and type as template arguments: f(Dim<D>{}), f(Elem<T>{}).

@@ -21,13 +21,6 @@
 namespace zg {
 namespace {
 
-__device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Transposes an 8 x 8 matrix of halves held one row a group of four lanes.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -36,109 +29,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 constexpr int kFewThreads = 128;
-
-// What one lane takes of 16 keys and values (rows of D codes in shared
-// memory): of keys g and g + 8 (lane = 4 g + c) the dims of `dim_of`, of values
-// 2c, 2c + 1, 2c + 8, 2c + 9 the dims g * D/8 and on.  The order of the dims
-// inside a product is free, so that a lane reads neighbouring bytes.
-template <int D>
-struct Tile16 {
-  static constexpr int KW = D / 16, VW = D / 32;  // words of a key, of a value
-  static constexpr int kBytes = 16 * D;           // of the keys, of the values
-  static __device__ __forceinline__ int dim_of(int w, int c) {
-    return w < D / 64 * 4 ? w / 4 * 64 + 16 * c + 4 * (w % 4) : D / 64 * 64 + 8 * c + 4 * (w - D / 64 * 4);
-  }
-  static __device__ __forceinline__ void keys(const uint8_t* at, int g, int c, uint32_t (&k)[2][KW]) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint8_t* p = at + (n * 8 + g) * D;
-      if constexpr (D == 128) {
-        // rows of 128 bytes: odd rows read their halves the other way round, so that eight lanes meet all banks
-        const int o = (g & 1) * 64;
-        const uint4 x = *reinterpret_cast<const uint4*>(p + o + 16 * c);
-        const uint4 y = *reinterpret_cast<const uint4*>(p + (64 - o) + 16 * c);
-        *reinterpret_cast<uint4*>(&k[n][0]) = o ? y : x;
-        *reinterpret_cast<uint4*>(&k[n][4]) = o ? x : y;
-      } else {
-        if constexpr (D >= 64) *reinterpret_cast<uint4*>(&k[n][0]) = *reinterpret_cast<const uint4*>(p + 16 * c);
-        if constexpr (D % 64 != 0)
-          *reinterpret_cast<uint2*>(&k[n][D / 64 * 4]) = *reinterpret_cast<const uint2*>(p + D / 64 * 64 + 8 * c);
-      }
-    }
-  }
-  static __device__ __forceinline__ void values(const uint8_t* at, int g, int c, uint32_t (&v)[4][VW]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint8_t* p = at + (2 * c + (j & 1) + (j >> 1) * 8) * D + g * (D / 8);
-      if constexpr (D == 128) *reinterpret_cast<uint4*>(v[j]) = *reinterpret_cast<const uint4*>(p);
-      else if constexpr (D == 64) *reinterpret_cast<uint2*>(v[j]) = *reinterpret_cast<const uint2*>(p);
-      else
-#pragma unroll
-        for (int w = 0; w < VW; ++w) v[j][w] = *reinterpret_cast<const uint32_t*>(p + 4 * w);
-    }
-  }
-};
-
-// The same of 4-bit codes: 16 rows of D/2 bytes, then their scale bytes.  A
-// word is eight codes; of keys a lane takes the dims c * D/4 and on (rows side
-// by side: every bank once), of values whole words (and a half one where 64 does not divide D),
-// so that a word never lies in two scales.
-template <int D>
-struct Tile16x4 {
-  static constexpr int KW = D / 32;                           // words of a key
-  static constexpr int FW = D / 64, HW = D % 64 / 32;         // whole words of a value, half ones
-  static constexpr int kCodes = 16 * Row4<D>::kCodes, kBytes = kCodes + 16 * Row4<D>::kScales;
-  // the first of the four dims of product w of the keys
-  static __device__ __forceinline__ int dim_of(int w, int c) { return c * (D / 4) + 4 * w; }
-  // the first of the two dims of product j of the values
-  static __device__ __forceinline__ int value_dim(int j, int g) {
-    return j < 4 * FW ? g * 8 * FW + 2 * j : 64 * FW + 4 * g + 2 * (j - 4 * FW);
-  }
-  static __device__ __forceinline__ void keys(const uint8_t* at, int g, int c, uint32_t (&k)[2][KW],
-                                              uint32_t (&s)[2][KW]) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint8_t* p = at + (n * 8 + g) * Row4<D>::kCodes + c * (D / 8);
-      const uint8_t* u = at + kCodes + (n * 8 + g) * Row4<D>::kScales;
-      if constexpr (KW == 4) *reinterpret_cast<uint4*>(k[n]) = *reinterpret_cast<const uint4*>(p);
-      else if constexpr (KW == 2) *reinterpret_cast<uint2*>(k[n]) = *reinterpret_cast<const uint2*>(p);
-      else
-#pragma unroll
-        for (int w = 0; w < KW; ++w) k[n][w] = *reinterpret_cast<const uint32_t*>(p + 4 * w);
-      if constexpr (KW == 4) {
-        const uint32_t two = *reinterpret_cast<const uint16_t*>(u + 2 * c);
-        s[n][0] = s[n][1] = scale_twice(two & 0xFF);
-        s[n][2] = s[n][3] = scale_twice(two >> 8);
-      } else {
-#pragma unroll
-        for (int w = 0; w < KW; ++w) s[n][w] = scale_twice(u[(c * (D / 4) + 8 * w) / 16]);
-      }
-    }
-  }
-  // Words of keys 2c, 2c + 1, 2c + 8, 2c + 9 and their scales; keys from `seen` on (not defined, may be NaN) as zeros.
-  static __device__ __forceinline__ void values(const uint8_t* at, int g, int c, int seen, uint32_t (&v)[4][FW + HW],
-                                                uint32_t (&s)[4][FW + HW]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = 2 * c + (j & 1) + (j >> 1) * 8;
-      const uint8_t* p = at + row * Row4<D>::kCodes;
-      const uint8_t* u = at + kCodes + row * Row4<D>::kScales;
-      if constexpr (FW == 2) {
-        *reinterpret_cast<uint2*>(v[j]) = *reinterpret_cast<const uint2*>(p + 8 * g);
-        s[j][0] = s[j][1] = row < seen ? u[g] : 0;
-      } else {
-        if constexpr (FW) {
-          v[j][0] = *reinterpret_cast<const uint32_t*>(p + 4 * g);
-          s[j][0] = row < seen ? u[g / 2] : 0;
-        }
-        if constexpr (HW) {
-          v[j][FW] = *reinterpret_cast<const uint16_t*>(p + 32 * FW + 2 * g);
-          s[j][FW] = row < seen ? u[4 * FW + g / 4] : 0;
-        }
-      }
-    }
-  }
-};
 
 template <int D, int FMT>
 constexpr int kTileBytes = FMT == ZG_KV_E2M1 ? Tile16x4<D>::kBytes : Tile16<D>::kBytes;
@@ -413,7 +303,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
           for (int j = 0; j < 4; ++j) z[half][n][j] = 0.f;
         if constexpr (k4) {
           uint32_t k[2][Tl4::KW], ku[2][Tl4::KW];
-          Tl4::keys(tiles + half * kBytes, g, c, k, ku);
+          Tl4::keys(tiles + half * kBytes, tiles + half * kBytes + Tl4::kCodes, g, c, k, ku);
 #pragma unroll
           for (int w = 0; w < Tl4::KW; ++w) {
             uint32_t x[4], y[4];  // of eight dims: keys g and g + 8

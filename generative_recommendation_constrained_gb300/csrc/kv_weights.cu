@@ -1,0 +1,301 @@
+// What cached tokens collect of attention:
+//
+//   w_j = decay * w_j + sum over rows and heads of exp(scale * q . k_j - lse)
+//
+// with the rows' log-sum-exps from the attention itself, so one pass over the
+// keys does.  A warp has 32 keys as halves in registers (the long side of the
+// products) and meets all query rows, eight an instruction, which lie in
+// shared memory in the order of the fragments: a key's sum stays in its lanes,
+// nothing is added atomically, and what is not defined behind a history stays
+// with keys that are not written.
+#include <cmath>
+
+#include "kv_attn.cuh"
+
+namespace zg {
+namespace {
+
+constexpr int kWarps = 4, kKeys = 32 * kWarps;  // keys of a CTA's step
+constexpr int kRowsAtOnce = 128;                // query rows in shared memory
+
+struct WeightArgs {
+  const uint8_t* kc;
+  const float* ks;
+  const uint8_t* kg;
+  const int32_t *table, *length, *n_rows, *known;
+  uint32_t* status;
+  const float* lse;
+  float* w;
+  int32_t n_blocks, heads, bt, bt_log2, max_blocks, w_tokens;
+  int32_t B, R, Hq, G, causal, steps;
+  float scale, decay;  // scale * log2(e)
+};
+
+// Codes of a warp's 32 keys as they come from memory.
+template <int D, int FMT>
+struct RawKeys {
+  static constexpr bool k4 = FMT == ZG_KV_E2M1;
+  static constexpr int W = k4 ? Tile16x4<D>::KW : Tile16<D>::KW;
+  uint32_t k[2][2][W];
+  uint32_t s[2][2][k4 ? W : 1];
+  float ks[2];
+};
+
+template <typename T, int D, int FMT>
+__global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constant__ WeightArgs a, const Rows<T> q) {
+  using Raw = RawKeys<D, FMT>;
+  constexpr bool k4 = Raw::k4;
+  constexpr int KS = D / 16;  // products of 16 dims
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint4* frag = reinterpret_cast<uint4*>(smem);  // [row / 8][KS / 2][lane]
+  const int most = min((a.R * a.G + 7) / 8 * 8, kRowsAtOnce);
+  float4* par = reinterpret_cast<float4*>(frag + most / 8 * (KS / 2) * 32);  // [row / 2]: factor, log-sum-exp of both rows
+  int2* sees = reinterpret_cast<int2*>(par + most / 2);                      // [row / 2]: tokens that they see
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  after_predecessor();
+
+  const int h = blockIdx.y, b = blockIdx.z;
+  Seen s = {a.length[b], a.n_rows ? a.n_rows[b] : a.R};
+  const int room = a.max_blocks * a.bt;
+  if (s.len < 0 || s.len > room || s.rows < 0 || s.rows > a.R) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.status, kStatusCache);
+    s.len = min(max(s.len, 0), room);
+    s.rows = min(max(s.rows, 0), a.R);
+  }
+  const int64_t begin = (int64_t)blockIdx.x * a.steps * kKeys;
+  if (begin >= s.len) return;
+  const int key0 = (int)begin;
+  const int steps = min(a.steps, (s.len - key0 + kKeys - 1) / kKeys);
+  const int M = s.rows * a.G;
+  const int known = a.known ? a.known[b] : s.len;
+
+  // the codes of a step's 32 keys of this warp; of blocks outside the cache (recorded) and behind the history: none
+  auto load = [&](int step, Raw& r, int* blk) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int key = key0 + step * kKeys + warp * 32 + n * 16;
+      blk[n] = -1;
+      if (step < steps && key < s.len) {
+        blk[n] = a.table[(int64_t)b * a.max_blocks + (key >> a.bt_log2)];
+        if (blk[n] < 0 || blk[n] >= a.n_blocks) {
+          if (lane == 0) atomicOr(a.status, kStatusCache);
+          blk[n] = -1;
+        }
+      }
+      if (blk[n] < 0) continue;
+      const int64_t bh = (int64_t)blk[n] * a.heads + h, row = bh * a.bt + (key & (a.bt - 1));
+      if constexpr (k4) {
+        Tile16x4<D>::keys(a.kc + row * Row4<D>::kCodes, a.kg + row * Row4<D>::kScales, g, c, r.k[n], r.s[n]);
+      } else {
+        Tile16<D>::keys(a.kc + row * D, g, c, r.k[n]);
+        r.ks[n] = a.ks[bh];
+      }
+    }
+  };
+
+  // rows m0 .. m0 + most - 1 into shared memory: a lane has four dims of a row (a head of 96: 24 lanes), which are
+  // one half of a fragment
+  auto stage = [&](int m0) {
+    constexpr int kLanes = D / 4, kSlot = D == 96 ? 32 : kLanes, kAt = 32 / kSlot;
+    const int l = lane % kSlot, d = 4 * l;
+    int w, cc;  // of the lane's dims: Tile16(x4)::dim_of(w, cc) = d
+    if constexpr (k4) {
+      cc = d / (D / 4), w = d % (D / 4) / 4;
+    } else if (d < D / 64 * 64) {
+      cc = d % 64 / 16, w = d / 64 * 4 + d % 16 / 4;
+    } else {
+      cc = d % 64 % 32 / 8, w = D / 64 * 4 + d % 8 / 4;
+    }
+    for (int r0 = warp * kAt; r0 < most; r0 += kWarps * kAt) {
+      const int r = r0 + lane / kSlot, m = m0 + r;
+      const bool live = m < M;
+      const int row = live ? m / a.G : 0, qh = h * a.G + (live ? m % a.G : 0);
+      float x[4] = {}, ls = -INFINITY;
+      if (live && l < kLanes) load4(q.at(b, row, qh) + d, x);
+      if (live) ls = a.lse[((int64_t)b * a.R + row) * a.Hq + qh];
+      const int vis = !live || ls == -INFINITY ? 0 : a.causal ? max(0, s.len - (s.rows - 1 - row)) : s.len;
+      if (vis == 0) x[0] = x[1] = x[2] = x[3] = 0.f;  // a row that sees nothing, whatever it holds
+      float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+      for (int o = kSlot / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      const int ex = row_exponent(top);
+      const float dn = power_of_2(-ex);
+      if (r < most && l < kLanes)
+        reinterpret_cast<uint2*>(frag)[(((r >> 3) * (KS / 2) + (w >> 1)) * 32 + (r & 7) * 4 + cc) * 2 + (w & 1)] =
+            make_uint2(pack_half2(x[0] * dn, x[1] * dn), pack_half2(x[2] * dn, x[3] * dn));
+      if (r < most && l == 0) {
+        reinterpret_cast<float2*>(par)[r] =
+            make_float2(a.scale * power_of_2(ex), vis == 0 ? INFINITY : ls * 1.4426950408889634f);
+        reinterpret_cast<int*>(sees)[r] = vis;
+      }
+    }
+  };
+
+  Raw raw;
+  int blk[2];
+  load(0, raw, blk);
+  stage(0);
+  __syncthreads();
+  for (int step = 0; step < steps; ++step) {
+    // the keys as fragments
+    uint32_t ka[2][KS][4];
+    float ks[2];
+    bool here[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      here[n] = blk[n] >= 0;
+      ks[n] = k4 ? 1.f : raw.ks[n];
+#pragma unroll
+      for (int w = 0; w < Raw::W; ++w) {
+        if constexpr (k4) {
+          uint32_t x[4], y[4];
+          e2m1_half8(raw.k[n][0][w], raw.s[n][0][w], x);
+          e2m1_half8(raw.k[n][1][w], raw.s[n][1][w], y);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            ka[n][2 * w + v][0] = x[2 * v];
+            ka[n][2 * w + v][1] = y[2 * v];
+            ka[n][2 * w + v][2] = x[2 * v + 1];
+            ka[n][2 * w + v][3] = y[2 * v + 1];
+          }
+        } else {
+          codes_half4<FMT == ZG_KV_INT8>(raw.k[n][0][w], ka[n][w][0], ka[n][w][2]);
+          codes_half4<FMT == ZG_KV_INT8>(raw.k[n][1][w], ka[n][w][1], ka[n][w][3]);
+        }
+      }
+    }
+    load(step + 1, raw, blk);
+    const int first = key0 + step * kKeys + warp * 32;
+    float sum[2][2] = {};  // keys g and g + 8 of both tiles
+    for (int m0 = 0; m0 < M; m0 += most) {
+      if (m0 > 0 || (step > 0 && M > most)) {
+        __syncthreads();
+        stage(m0);
+        __syncthreads();
+      }
+      const int groups = (min(M - m0, most) + 7) / 8;
+      for (int n8 = 0; n8 < groups; ++n8) {
+        float z[2][4] = {};
+#pragma unroll
+        for (int w = 0; w < KS / 2; ++w) {
+          const uint4 f = frag[(n8 * (KS / 2) + w) * 32 + lane];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            mma_16816(z[n], ka[n][2 * w], f.x, f.y);
+            mma_16816(z[n], ka[n][2 * w + 1], f.z, f.w);
+          }
+        }
+        const float4 p = par[n8 * 4 + c];
+        const int2 v = sees[n8 * 4 + c];
+        const bool masked = __any_sync(0xFFFFFFFFu, min(v.x, v.y) < first + 32);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float f0 = p.x * ks[n], f1 = p.z * ks[n];
+          float e[4] = {exp2_fast(fmaf(z[n][0], f0, -p.y)), exp2_fast(fmaf(z[n][1], f1, -p.w)),
+                        exp2_fast(fmaf(z[n][2], f0, -p.y)), exp2_fast(fmaf(z[n][3], f1, -p.w))};
+          if (masked) {
+            const int key = first + 16 * n + g;
+            if (key >= v.x) e[0] = 0.f;
+            if (key >= v.y) e[1] = 0.f;
+            if (key + 8 >= v.x) e[2] = 0.f;
+            if (key + 8 >= v.y) e[3] = 0.f;
+          }
+          sum[n][0] += e[0] + e[1];
+          sum[n][1] += e[2] + e[3];
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sum[n][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][i], 1);
+        sum[n][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][i], 2);
+      }
+    // lane (g, c) writes key g + 8 (c & 1) of tile c / 2
+    const int key = first + 16 * (c >> 1) + 8 * (c & 1) + g;
+    const float mine = c == 0 ? sum[0][0] : c == 1 ? sum[0][1] : c == 2 ? sum[1][0] : sum[1][1];
+    if (key < s.len) {
+      float* w = a.w + ((int64_t)b * a.heads + h) * a.w_tokens + key;
+      const float old = key < known && a.decay != 0.f ? *w * a.decay : 0.f;
+      *w = old + ((c >> 1 ? here[1] : here[0]) ? mine : 0.f);
+    }
+  }
+}
+
+}  // namespace
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,
+                                   const int32_t* length, const int32_t* n_rows, const int32_t* known, const zg_rows* q,
+                                   const float* lse, float* weights, int32_t w_tokens, float decay, int32_t B, int32_t R,
+                                   int32_t Hq, float scale, int32_t causal, void* stream) try {
+  const char* call = "zg_kv_weights";
+  zg_status st;
+  if ((st = check_cache(cache, table, max_blocks, call)) != ZG_OK) return st;
+  if (B < 0 || R < 0) return bad_arg(call, "B and R must be >= 0");
+  if (Hq < 1 || Hq > 1024 || Hq % cache->heads) return bad_arg(call, "Hq must be a multiple of cache.heads, at most 1024");
+  if ((int64_t)B * R >= 0x80000000LL / Hq) return bad_arg(call, "B * R * Hq must be below 2^31");
+  const int64_t tokens = (int64_t)max_blocks * cache->block_tokens;
+  if (tokens > kMostTokens) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_weights: more than 2^31 - 2^20 tokens in a table");
+  if (B > 65535) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_weights: more than 65,535 requests");
+  if (w_tokens < tokens) return bad_arg(call, "w_tokens must be at least max_blocks * block_tokens");
+  if (!(decay >= 0.f && std::isfinite(decay))) return bad_arg(call, "decay must be finite and >= 0");
+  if (!(scale > 0.f && std::isfinite(scale))) return bad_arg(call, "scale must be finite and > 0");
+  if (B == 0 || R == 0) return ZG_OK;
+  if ((st = check_rows(q, "q", -1, call)) != ZG_OK) return st;
+  if (q->dtype == ZG_F32) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_weights: q must be ZG_BF16 or ZG_F16");
+  if (!length) return bad_arg(call, "length is NULL");
+  if (!lse || !weights || (reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(weights)) % 4)
+    return bad_arg(call, "lse and weights must be given, 4-byte aligned");
+  uint32_t* status = nullptr;
+  if ((st = get_status_ptr(&status)) != ZG_OK) return st;
+  WeightArgs a = {};
+  a.kc = static_cast<const uint8_t*>(cache->k_codes);
+  a.ks = cache->k_scale;
+  a.kg = reinterpret_cast<const uint8_t*>(cache->k_scale);
+  a.table = table;
+  a.length = length;
+  a.n_rows = n_rows;
+  a.known = known;
+  a.status = status;
+  a.lse = lse;
+  a.w = weights;
+  a.n_blocks = cache->n_blocks;
+  a.heads = cache->heads;
+  a.bt = cache->block_tokens;
+  while ((1 << a.bt_log2) < a.bt) ++a.bt_log2;
+  a.max_blocks = max_blocks;
+  a.w_tokens = w_tokens;
+  a.B = B;
+  a.R = R;
+  a.Hq = Hq;
+  a.G = Hq / cache->heads;
+  a.causal = causal != 0;
+  a.scale = scale * 1.4426950408889634f;
+  a.decay = decay;
+  const int64_t units = (tokens + kKeys - 1) / kKeys, M = (int64_t)R * a.G;
+  // several steps a CTA, so that its queries are brought in once for them, where steps are many
+  a.steps = (int)std::max<int64_t>(1, std::min<int64_t>(8, units * B * cache->heads / (sm_count() * 32)));
+  const int most = (int)std::min<int64_t>((M + 7) / 8 * 8, kRowsAtOnce);
+  cudaError_t err = cudaSuccess;
+  for_dim(cache->dim, [&](auto dv) {
+    constexpr int D = decltype(dv)::value;
+    const size_t smem = (size_t)most * (2 * D + 8 + 4);
+    auto typed = [&](auto ev) {
+      using E = typename decltype(ev)::type;
+      for_format(cache->format, [&](auto fv) {
+        auto kern = k_kv_weights<E, D, decltype(fv)::value>;
+        err = launch_early(kern, dim3((unsigned)((units + a.steps - 1) / a.steps), cache->heads, B), 32 * kWarps, smem,
+                           static_cast<cudaStream_t>(stream), a, rows_of<E>(q));
+      });
+    };
+    if (q->dtype == ZG_BF16) typed(Elem<__nv_bfloat16>{});
+    else typed(Elem<__half>{});
+  });
+  return err == cudaSuccess ? ZG_OK : cuda_fail(err, "attention weights launch");
+} catch (...) {
+  return ZG_ERR_OUT_OF_MEMORY;
+}

@@ -120,6 +120,20 @@ def _int32(x: torch.Tensor | None, shape, name: str, gpu: int):
                          f"(cuda:{gpu})")
 
 
+def _float32(x: torch.Tensor, shape, name: str, gpu: int):
+    if x.dtype != torch.float32 or x.shape != shape or not x.is_contiguous() or x.get_device() != gpu:
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} on the GPU, on the current "
+                         f"device (cuda:{gpu})")
+
+
+def _weights_of(x: torch.Tensor, B: int, cache, max_blocks: int, gpu: int) -> int:
+    """Tokens of the weights [B, heads, tokens] of a cache's histories."""
+    if x.dim() != 3 or x.shape[2] < max_blocks * cache.block_tokens:
+        raise ValueError("weights must be [B, heads, tokens] with as many tokens as a table holds")
+    _float32(x, (B, cache.heads, x.shape[2]), "weights", gpu)
+    return x.shape[2]
+
+
 def _current(held: int, what: str) -> int:
     """The current device, on which the library launches: what a call is given, and what it `held` before (-1: nothing),
     has to be there."""
@@ -274,6 +288,53 @@ class KVCache:
         Z.zg_kv_read(self.struct, table, width, start, n, B, T, _rows(k_out, gpu), _rows(v_out, gpu),
                      _stream(stream, gpu))
         return k_out, v_out
+
+    def add_weights(self, weights, q, lse, table, length, n_rows=None, known=None, causal: bool = False,
+                    scale: float | None = None, decay: float = 1.0, stream: int | None = None):
+        """Adds what the cached tokens collect of the attention of q [B, R, Hq, dim], with its log-sum-exps lse [B, R,
+        Hq], to weights [B, heads, tokens] (float32, as many tokens as a table holds), times decay before; tokens from
+        known[b] on count as 0 before (None: all are known).  Returns weights."""
+        gpu = _current(self.gpu, "the cache is")
+        shape = q.shape
+        if len(shape) != 4 or shape[3] != self.dim or shape[2] % self.heads:
+            raise ValueError("q must be [B, R, Hq, dim], Hq a multiple of the cache's heads")
+        B, R, Hq, _ = shape
+        if table.dim() != 2:
+            raise ValueError("table must be [B, max_blocks]")
+        width = table.shape[1]
+        _int32(table, (B, width), "table", gpu)
+        for x, name in ((length, "length"), (n_rows, "n_rows"), (known, "known")):
+            _int32(x, (B,), name, gpu)
+        _float32(lse, (B, R, Hq), "lse", gpu)
+        tokens = _weights_of(weights, B, self, width, gpu)
+        Z.zg_kv_weights(self.struct, table, width, length, n_rows, known, _rows(q, gpu), lse, weights, tokens, decay, B, R,
+                        Hq, self.dim ** -0.5 if scale is None else scale, causal, _stream(stream, gpu))
+        return weights
+
+
+class CacheEviction:
+    """Workspace and outputs for repeated zg_kv_evict calls with fixed shapes: B requests over `cache` through tables of
+    max_blocks blocks, each cut to `keep` tokens a head, its last `recent` ones among them."""
+
+    def __init__(self, cache: KVCache, B: int, max_blocks: int, keep: int, recent: int = 0):
+        device = cache.k_codes.device
+        self.cache, self.B, self.max_blocks, self.keep, self.recent = cache, B, max_blocks, keep, recent
+        self.ws_bytes = Z.zg_kv_evict_workspace_size(cache.struct, B, keep)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.length = torch.empty((B,), dtype=torch.int32, device=device)
+        self.kept = torch.empty((B, cache.heads, keep), dtype=torch.int32, device=device)
+
+    def __call__(self, weights, table, length, stream: int | None = None):
+        """Shortens the histories of more than `keep` of the length[b] tokens, in place, and their weights [B, heads,
+        tokens] with them; returns (the new lengths [B], the places that the kept tokens had [B, heads, keep], -1 behind
+        them), this object's own buffers."""
+        gpu = _current(self.cache.gpu, "the cache is")
+        _int32(table, (self.B, self.max_blocks), "table", gpu)
+        _int32(length, (self.B,), "length", gpu)
+        tokens = _weights_of(weights, self.B, self.cache, self.max_blocks, gpu)
+        Z.zg_kv_evict(self.cache.struct, table, self.max_blocks, length, weights, tokens, self.keep, self.recent,
+                      self.length, self.kept, self.B, self.ws, self.ws_bytes, _stream(stream, gpu))
+        return self.length, self.kept
 
 
 class CacheAttention:

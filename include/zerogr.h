@@ -552,6 +552,49 @@ ZG_API zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table,
                                  const zg_rows* out, float* lse, int32_t B, int32_t R, int32_t Hq, float scale,
                                  int32_t causal, void* workspace, size_t ws_bytes, void* stream);
 
+/* What cached tokens collect of attention, for zg_kv_evict:
+ *   weights[b][h][j] = decay * weights[b][h][j] + sum of
+ *                      exp(scale * q . k_j - lse[b][r][i])
+ * over the rows r that see token j and the query heads i of key head h, for j
+ * below length[b]; what lies behind keeps its value.  q, n_rows, causal and
+ * scale as in zg_kv_attention, lse its log-sum-exps (rows of -inf, which saw
+ * nothing, add nothing).
+ *   weights: device float32 [B][heads][w_tokens], w_tokens at least
+ *     max_blocks * block_tokens.
+ *   known: device int32 [B], the tokens whose weights exist already; those of
+ *     the others, and all where decay is 0, count as 0 (NULL: all exist).
+ * Sums are 32-bit, in a fixed order; a term below 2^-126 counts as 0.  Tokens of a block outside the cache
+ * collect nothing (recorded).  B at most 65,535; otherwise the limits of
+ * zg_kv_attention; no workspace. */
+ZG_API zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,
+                               const int32_t* length, const int32_t* n_rows, const int32_t* known,
+                               const zg_rows* q, const float* lse, float* weights, int32_t w_tokens, float decay,
+                               int32_t B, int32_t R, int32_t Hq, float scale, int32_t causal, void* stream);
+
+/* Shortens the histories that hold more than `keep` tokens to `keep`, each key
+ * head for itself: the last `recent` tokens stay, and of the others the keep -
+ * recent of largest weight (equal ones: the earlier; a NaN counts as below
+ * every number).  They move to the places 0 .. keep - 1 in their order, with
+ * their weights, in place; shorter histories stay as they are, and so does
+ * what lies in places from keep on.
+ *   new_length: device int32 [B], min(length, keep) (not length itself).
+ *   kept: device int32 [B][heads][keep], the places that the kept tokens had,
+ *     -1 behind them.
+ * In 8 bits a block's new scale is the largest of its kept rows' old ones,
+ * and rows of a smaller one are coded again as an append does it; in 4 bits
+ * nothing is rounded.  Keys keep the rotation of the position that they were
+ * written at: from then on a token's place is not its position, so later keys
+ * and queries are turned by zg_qk_norm_rope at positions of the caller's, and
+ * appended without a norm_rope.  Blocks of one request must be its own.  Rows
+ * from a block outside the cache become zeros (recorded).
+ * B * heads at most 65,535; keep from 1 to 2^30; recent from 0 to keep.  The
+ * workspace's size serves this B and keep and every smaller ones. */
+ZG_API zg_status zg_kv_evict_workspace_size(const zg_kv_cache* cache, int32_t B, int32_t keep, size_t* bytes);
+ZG_API zg_status zg_kv_evict(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,
+                             const int32_t* length, float* weights, int32_t w_tokens, int32_t keep, int32_t recent,
+                             int32_t* new_length, int32_t* kept, int32_t B, void* workspace, size_t ws_bytes,
+                             void* stream);
+
 /* Test and diagnosis hook, no counterpart in the paper: the number of polls
  * after which a pipeline wait (an mbarrier) of the tensor-core full
  * projection or of the cached attention gives up, records bit 2 in the device

@@ -46,3 +46,61 @@ def test_append_refusals(zg):
     refused(zg, 4, "CTAs", f, c, n, r, r, None, None, 0, P, 4, P, None, 2 ** 20, 2 ** 18)
     f(c, n, r, r, None, None, 0, P, 4, P, None, 0, 1)
     f(c, n, r, r, None, None, 0, P, 4, P, None, 1, 0)
+
+
+def test_weights_refusals(zg):
+    c, r = cache(zg), zg.make_rows(P, zg.ZG_BF16, 256, 128, 64)
+    ok = dict(cache=c, table=P, max_blocks=4, length=P, n_rows=None, known=None, q=r, lse=P, weights=P, w_tokens=64,
+              decay=1.0, B=1, R=1, Hq=2, scale=1.0, causal=False)
+
+    def no(status, words, **kw):
+        refused(zg, status, words, zg.zg_kv_weights, **{**ok, **kw})
+
+    no(1, "Hq", Hq=3)
+    no(1, "B and R", B=-1)
+    no(1, "2^31", B=1 << 15, R=1 << 16)
+    no(4, "65,535", B=65536)
+    no(1, "w_tokens", w_tokens=63)
+    no(1, "decay", decay=-1.0)
+    no(1, "decay", decay=float("nan"))
+    no(1, "scale", scale=float("inf"))
+    no(1, "lse", lse=None)
+    no(1, "lse", weights=P + 2)
+    no(1, "length", length=None)
+    no(4, "ZG_BF16 or ZG_F16", q=zg.make_rows(P, zg.ZG_F32, 256, 128, 64))
+    no(4, "tokens in a table", max_blocks=2 ** 27 - 1, w_tokens=2 ** 31 - 1)
+    zg.zg_kv_weights(**{**ok, "B": 0, "lse": None})
+    zg.zg_kv_weights(**{**ok, "R": 0, "lse": None})
+
+
+def test_evict_refusals(zg):
+    c = cache(zg)
+    ok = dict(cache=c, table=P, max_blocks=4, length=P, weights=P, w_tokens=64, keep=8, recent=2, new_length=2 * P, kept=P, B=1,
+              workspace=P, ws_bytes=1 << 20)
+
+    def no(status, words, **kw):
+        refused(zg, status, words, zg.zg_kv_evict, **{**ok, **kw})
+
+    no(1, "keep", keep=0)
+    no(4, "keep", keep=2 ** 30 + 1)
+    no(1, "recent", recent=9)
+    no(1, "recent", recent=-1)
+    no(1, "B must", B=-1)
+    no(4, "65,535", B=32768)
+    no(1, "w_tokens", w_tokens=63)
+    no(1, "NULL", weights=None)
+    no(1, "NULL", kept=None)
+    no(1, "4-byte", kept=P + 2)
+    no(1, "new_length", new_length=P)
+    no(1, "workspace", workspace=None)
+    no(1, "workspace", workspace=P + 64)
+    no(1, "workspace", ws_bytes=4)
+    no(1, "table", table=None)
+    no(4, "tokens in a table", max_blocks=2 ** 27 - 1, w_tokens=2 ** 31 - 1)
+    zg.zg_kv_evict(**{**ok, "B": 0, "length": None})
+    f = zg.zg_kv_evict_workspace_size
+    refused(zg, 1, "keep", f, c, 1, 0)
+    assert f(c, 3, 100) == 3 * 2 * 4
+    eight = zg.make_kv_cache(zg.ZG_KV_INT8, 8, 2, 16, 64, P, P, P, P)
+    assert all(f(eight, b, k) <= f(eight, b2, k2) for b in (1, 2) for b2 in (b, 30) for k in (1, 50) for k2 in (k, 51))
+    assert f(eight, 3, 100) == (2 * 3 * 2 * 100 + 6) * 4
