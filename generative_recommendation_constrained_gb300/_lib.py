@@ -136,6 +136,7 @@ def _load():
         "zg_kv_read": [vp, vp, i32, vp, vp, i32, i32, vp, vp, vp],
         "zg_kv_attention_workspace_size": [vp, i32, i32, i32, i32, P(sz)],
         "zg_kv_attention": [vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, C.c_float, i32, vp, sz, vp],
+        "zg_prompt_attention": [vp] * 6 + [i32] * 5 + [C.c_float, i32, vp],
         "zg_kv_weights": [vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, C.c_float, i32, i32, i32, C.c_float, i32, vp],
         "zg_kv_evict_workspace_size": [vp, i32, i32, P(sz)],
         "zg_kv_evict": [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp],
@@ -474,6 +475,15 @@ def zg_kv_attention(cache: zg_kv_cache, table, max_blocks: int, length, n_rows, 
     """q, out: zg_rows or their bytes."""
     st = lib.zg_kv_attention(_ref(cache), _ptr(table), max_blocks, _ptr(length), _ptr(n_rows), _ref(q), _ref(out),
                              _ptr(lse), B, R, Hq, scale, causal, _ptr(workspace), ws_bytes, stream)
+    if st:
+        _check(st)
+
+
+def zg_prompt_attention(q, k, v, out, lse, starts, B: int, T: int, Hq: int, Hk: int, dim: int, scale: float,
+                        causal: bool, stream: int = 0):
+    """q, k, v, out: zg_rows or their bytes."""
+    st = lib.zg_prompt_attention(_ref(q), _ref(k), _ref(v), _ref(out), _ptr(lse), _ptr(starts), B, T, Hq, Hk, dim, scale,
+                                 causal, stream)
     if st:
         _check(st)
 

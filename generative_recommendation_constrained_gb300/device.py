@@ -99,19 +99,25 @@ def _rows(x: torch.Tensor | None, gpu: int):
     return _pack_rows(x.data_ptr(), dt, 0, sb, st, sh)
 
 
+def _packed(x: torch.Tensor, gpu: int):
+    """zg_rows of a [T, heads, dim] tensor."""
+    return _rows(x.unsqueeze(0), gpu)
+
+
 def _stream(stream, gpu: int):
     """The stream given, or the current one of device `gpu` (its number alone: a Stream object costs 3 us)."""
     return torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream
 
 
-def _out_like(x: torch.Tensor, stream, gpu: int):
-    """A new output like x for work on `stream`.  It comes from that stream's memory: a block that the current stream
-    has given back may still be read by work queued there."""
+def _out_like(x: torch.Tensor, stream, gpu: int, shape=None, dtype=None):
+    """A new output like x (but for shape and dtype if given) for work on `stream`.  It comes from that stream's memory:
+    a block that the current stream has given back may still be read by work queued there."""
+    shape, dtype = x.shape if shape is None else shape, dtype or x.dtype
     if stream is None or stream == torch._C._cuda_getCurrentRawStream(gpu):
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return torch.empty(shape, dtype=dtype, device=x.device)
     on = torch.cuda.ExternalStream(stream, device=gpu) if stream else torch.cuda.default_stream(gpu)
     with torch.cuda.stream(on):
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return torch.empty(shape, dtype=dtype, device=x.device)
 
 
 def _int32(x: torch.Tensor | None, shape, name: str, gpu: int):
@@ -189,6 +195,40 @@ class NormRope:
                           _rows(k_out, gpu) if k is not None else None, positions, B, T, heads[0], heads[1], self.dim,
                           _stream(stream, gpu))
         return q_out, k_out
+
+
+class PromptAttention:
+    """Attention over whole prompts (zg_prompt_attention): packed sequences, Hq query heads over Hk key heads."""
+
+    def __init__(self, Hq: int, Hk: int, dim: int, causal: bool = True, scale: float | None = None, lse: bool = False):
+        if Hk < 1 or Hq < 1 or Hq % Hk:
+            raise ValueError("Hq must be a multiple of Hk")
+        self.Hq, self.Hk, self.dim, self.causal, self.with_lse = Hq, Hk, dim, causal, lse
+        self.scale = dim ** -0.5 if scale is None else scale
+
+    def __call__(self, q, k, v, starts, out=None, lse=None, stream: int | None = None):
+        """q [T, Hq, dim], k, v [T, Hk, dim]; sequence b is rows starts[b] .. starts[b + 1] - 1 (int32 [B + 1]).  Returns
+        (out, lse or None): out like q (new when None; may be q), lse [T, Hq] float32 if asked for (or given).  New tensors
+        belong to `stream`, as in NormRope."""
+        T = q.shape[0]
+        if tuple(q.shape) != (T, self.Hq, self.dim) or k.shape != v.shape or tuple(k.shape) != (T, self.Hk, self.dim):
+            raise ValueError("q must be [T, Hq, dim], k and v [T, Hk, dim]")
+        gpu = _current(-1, "")
+        if starts.dim() != 1 or starts.shape[0] < 1:
+            raise ValueError("starts must be [B + 1]")
+        _int32(starts, starts.shape, "starts", gpu)
+        if out is None:
+            out = _out_like(q, stream, gpu)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if lse is None and self.with_lse:
+            lse = _out_like(q, stream, gpu, (T, self.Hq), torch.float32)
+        elif lse is not None:
+            _float32(lse, (T, self.Hq), "lse", gpu)
+        Z.zg_prompt_attention(_packed(q, gpu), _packed(k, gpu), _packed(v, gpu), _packed(out, gpu), lse, starts,
+                              starts.shape[0] - 1, T, self.Hq, self.Hk, self.dim, self.scale, self.causal,
+                              _stream(stream, gpu))
+        return out, lse
 
 
 class KVCache:

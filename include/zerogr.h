@@ -552,6 +552,29 @@ ZG_API zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table,
                                  const zg_rows* out, float* lse, int32_t B, int32_t R, int32_t Hq, float scale,
                                  int32_t causal, void* workspace, size_t ws_bytes, void* stream);
 
+/* Attention over whole prompts, before or without a cache: B sequences packed
+ * one behind the other, sequence b the rows starts[b] .. starts[b + 1] - 1 of T;
+ * out = softmax(scale * q k^T) v over its own rows, row i of a sequence over
+ * rows 0 .. i of it when causal, over all of them otherwise.
+ *   q, out: T rows of Hq heads, k, v: T rows of Hk heads, one type, ZG_BF16 or
+ *     ZG_F16 (stride_b is not used); k and v 16-byte aligned with strides of
+ *     multiples of 8 elements, not 0; out may be q itself, and not overlap
+ *     its inputs otherwise.  Query head j reads key head j / (Hq / Hk).
+ *   lse (may be NULL): device float32 [T][Hq], log sum exp(scale * q k).
+ *   starts: device int32 [B + 1], not falling, from 0 to T at most; outputs of
+ *     rows in no sequence are left as they are.  Starts outside that are
+ *     recorded for zg_check_device_status and held inside it.
+ * Products take the rows as they are and probabilities rounded to their type
+ * (relative 2^-9 or 2^-11 of each); scores, sums and maxima are 32-bit.  What a
+ * row does not see never reaches it, whatever it holds (a NaN or an infinity
+ * in rows behind it, or in other sequences); a NaN in its query or in what it
+ * sees gives NaN.
+ * dim 32, 64, 96 or 128; Hq a multiple of Hk, at most 1024; T * Hq below 2^31;
+ * no workspace. */
+ZG_API zg_status zg_prompt_attention(const zg_rows* q, const zg_rows* k, const zg_rows* v, const zg_rows* out,
+                                     float* lse, const int32_t* starts, int32_t B, int32_t T, int32_t Hq,
+                                     int32_t Hk, int32_t dim, float scale, int32_t causal, void* stream);
+
 /* What cached tokens collect of attention, for zg_kv_evict:
  *   weights[b][h][j] = decay * weights[b][h][j] + sum of
  *                      exp(scale * q . k_j - lse[b][r][i])
@@ -597,7 +620,7 @@ ZG_API zg_status zg_kv_evict(const zg_kv_cache* cache, const int32_t* table, int
 
 /* Test and diagnosis hook, no counterpart in the paper: the number of polls
  * after which a pipeline wait (an mbarrier) of the tensor-core full
- * projection or of the cached attention gives up, records bit 2 in the device
+ * projection, of the cached or of the prompt attention gives up, records bit 2 in the device
  * status word and ends the
  * kernel early (its copies and tensor-core operations drained, tensor memory
  * freed).  0 restores the default (2^26 polls, about a second).  Applies to
@@ -620,7 +643,8 @@ ZG_API void zg_debug_inject_build_failure(int32_t point, int32_t after);
  * of range, bit 2: a bounded wait in a tensor-core kernel expired, bit 3:
  * tensor-memory allocation failed, bit 4: a select found fewer candidates
  * than its own cut guarantees, bit 5: a history cache's block number or length,
- * or a workspace entry of its attention, out of range, bit 6: a NaN or an
+ * or a workspace entry of its attention, or a packed sequence's start, out of
+ * range, bit 6: a NaN or an
  * infinity written to a history cache).
  * Non-zero -> ZG_ERR_DEVICE_STATUS. */
 ZG_API zg_status zg_check_device_status(void* stream);
