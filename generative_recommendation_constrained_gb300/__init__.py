@@ -16,7 +16,7 @@ from ._lib import (DTYPES, LIB_PATH, ZG_BF16, ZG_F16, ZG_F32, ZG_FMT_DENSE, ZG_F
                    zg_plan_describe, zg_plan_force, zg_plan_load, zg_plan_save, zg_plan_set_fusion,
                    zg_plan_set_full_projection, zg_plan_set_order, zg_tune, zg_version, KV_FORMATS, ZG_KV_E2M1,
                    ZG_KV_E4M3, ZG_KV_INT8, make_kv_cache, make_norm_rope, make_rows, zg_kv_append, zg_kv_attention,
-                   zg_kv_attention_workspace_size, zg_kv_evict, zg_kv_evict_workspace_size, zg_kv_read, zg_kv_weights,
+                   zg_kv_attention_workspace_size, zg_kv_evict, zg_kv_read, zg_kv_weights,
                    zg_prompt_attention, zg_qk_norm_rope)
 
 __all__ = [
@@ -32,6 +32,6 @@ __all__ = [
     "zg_plan_describe", "zg_plan_force", "zg_plan_load", "zg_plan_save", "zg_plan_set_fusion",
     "zg_plan_set_full_projection", "zg_plan_set_order", "zg_tune", "zg_version",
     "KV_FORMATS", "ZG_KV_E2M1", "ZG_KV_E4M3", "ZG_KV_INT8", "make_kv_cache", "make_norm_rope", "make_rows",
-    "zg_kv_append", "zg_kv_attention", "zg_kv_attention_workspace_size", "zg_kv_evict", "zg_kv_evict_workspace_size", "zg_kv_read",
+    "zg_kv_append", "zg_kv_attention", "zg_kv_attention_workspace_size", "zg_kv_evict", "zg_kv_read",
     "zg_kv_weights", "zg_prompt_attention", "zg_qk_norm_rope",
 ]

@@ -138,8 +138,7 @@ def _load():
         "zg_kv_attention": [vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, C.c_float, i32, vp, sz, vp],
         "zg_prompt_attention": [vp] * 6 + [i32] * 5 + [C.c_float, i32, vp],
         "zg_kv_weights": [vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, C.c_float, i32, i32, i32, C.c_float, i32, vp],
-        "zg_kv_evict_workspace_size": [vp, i32, i32, P(sz)],
-        "zg_kv_evict": [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp],
+        "zg_kv_evict": [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, i32, vp],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -497,15 +496,9 @@ def zg_kv_weights(cache: zg_kv_cache, table, max_blocks: int, length, n_rows, kn
         _check(st)
 
 
-def zg_kv_evict_workspace_size(cache: zg_kv_cache, B: int, keep: int) -> int:
-    n = C.c_size_t(0)
-    _check(lib.zg_kv_evict_workspace_size(_ref(cache), B, keep, C.byref(n)))
-    return n.value
-
-
 def zg_kv_evict(cache: zg_kv_cache, table, max_blocks: int, length, weights, w_tokens: int, keep: int, recent: int,
-                new_length, kept, B: int, workspace, ws_bytes: int, stream: int = 0):
+                new_length, kept, B: int, stream: int = 0):
     st = lib.zg_kv_evict(_ref(cache), _ptr(table), max_blocks, _ptr(length), _ptr(weights), w_tokens, keep, recent,
-                         _ptr(new_length), _ptr(kept), B, _ptr(workspace), ws_bytes, stream)
+                         _ptr(new_length), _ptr(kept), B, stream)
     if st:
         _check(st)

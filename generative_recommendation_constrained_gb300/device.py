@@ -353,14 +353,14 @@ class KVCache:
 
 
 class CacheEviction:
-    """Workspace and outputs for repeated zg_kv_evict calls with fixed shapes: B requests over `cache` through tables of
+    """Outputs for repeated zg_kv_evict calls with fixed shapes: B requests over `cache` through tables of
     max_blocks blocks, each cut to `keep` tokens a head, its last `recent` ones among them."""
 
     def __init__(self, cache: KVCache, B: int, max_blocks: int, keep: int, recent: int = 0):
         device = cache.k_codes.device
         self.cache, self.B, self.max_blocks, self.keep, self.recent = cache, B, max_blocks, keep, recent
-        self.ws_bytes = Z.zg_kv_evict_workspace_size(cache.struct, B, keep)
-        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        if B < 0 or keep < 1 or not 0 <= recent <= keep:
+            raise ValueError("B must be >= 0, keep >= 1 and recent in [0, keep]")
         self.length = torch.empty((B,), dtype=torch.int32, device=device)
         self.kept = torch.empty((B, cache.heads, keep), dtype=torch.int32, device=device)
 
@@ -373,7 +373,7 @@ class CacheEviction:
         _int32(length, (self.B,), "length", gpu)
         tokens = _weights_of(weights, self.B, self.cache, self.max_blocks, gpu)
         Z.zg_kv_evict(self.cache.struct, table, self.max_blocks, length, weights, tokens, self.keep, self.recent,
-                      self.length, self.kept, self.B, self.ws, self.ws_bytes, _stream(stream, gpu))
+                      self.length, self.kept, self.B, _stream(stream, gpu))
         return self.length, self.kept
 
 

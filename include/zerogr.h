@@ -610,13 +610,11 @@ ZG_API zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* table, i
  * and queries are turned by zg_qk_norm_rope at positions of the caller's, and
  * appended without a norm_rope.  Blocks of one request must be its own.  Rows
  * from a block outside the cache become zeros (recorded).
- * B * heads at most 65,535; keep from 1 to 2^30; recent from 0 to keep.  The
- * workspace's size serves this B and keep and every smaller ones. */
-ZG_API zg_status zg_kv_evict_workspace_size(const zg_kv_cache* cache, int32_t B, int32_t keep, size_t* bytes);
+ * B * heads at most 65,535; keep from 1 to 2^30; recent from 0 to keep; no
+ * workspace. */
 ZG_API zg_status zg_kv_evict(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,
                              const int32_t* length, float* weights, int32_t w_tokens, int32_t keep, int32_t recent,
-                             int32_t* new_length, int32_t* kept, int32_t B, void* workspace, size_t ws_bytes,
-                             void* stream);
+                             int32_t* new_length, int32_t* kept, int32_t B, void* stream);
 
 /* Test and diagnosis hook, no counterpart in the paper: the number of polls
  * after which a pipeline wait (an mbarrier) of the tensor-core full

@@ -75,8 +75,7 @@ def test_weights_refusals(zg):
 
 def test_evict_refusals(zg):
     c = cache(zg)
-    ok = dict(cache=c, table=P, max_blocks=4, length=P, weights=P, w_tokens=64, keep=8, recent=2, new_length=2 * P, kept=P, B=1,
-              workspace=P, ws_bytes=1 << 20)
+    ok = dict(cache=c, table=P, max_blocks=4, length=P, weights=P, w_tokens=64, keep=8, recent=2, new_length=2 * P, kept=P, B=1)
 
     def no(status, words, **kw):
         refused(zg, status, words, zg.zg_kv_evict, **{**ok, **kw})
@@ -92,15 +91,6 @@ def test_evict_refusals(zg):
     no(1, "NULL", kept=None)
     no(1, "4-byte", kept=P + 2)
     no(1, "new_length", new_length=P)
-    no(1, "workspace", workspace=None)
-    no(1, "workspace", workspace=P + 64)
-    no(1, "workspace", ws_bytes=4)
     no(1, "table", table=None)
     no(4, "tokens in a table", max_blocks=2 ** 27 - 1, w_tokens=2 ** 31 - 1)
     zg.zg_kv_evict(**{**ok, "B": 0, "length": None})
-    f = zg.zg_kv_evict_workspace_size
-    refused(zg, 1, "keep", f, c, 1, 0)
-    assert f(c, 3, 100) == 3 * 2 * 4
-    eight = zg.make_kv_cache(zg.ZG_KV_INT8, 8, 2, 16, 64, P, P, P, P)
-    assert all(f(eight, b, k) <= f(eight, b2, k2) for b in (1, 2) for b2 in (b, 30) for k in (1, 50) for k2 in (k, 51))
-    assert f(eight, 3, 100) == (2 * 3 * 2 * 100 + 6) * 4
