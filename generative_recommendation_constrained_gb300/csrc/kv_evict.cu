@@ -29,7 +29,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kHeld = 16;        // weights a thread holds; those of longer histories are read again for every pass
+constexpr int kHeld = 32;        // weights a thread holds; those of longer histories are read again for every pass
 constexpr int kMostRanks = 8;    // CTAs of a cluster, at most
 
 struct EvictArgs {
@@ -58,12 +58,17 @@ __device__ __forceinline__ int held(const EvictArgs& a, int b, bool report) {
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs a) {
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
-  __shared__ uint32_t hist[2][kBins];  // one for each half of the warps, then their sum
-  __shared__ uint32_t sums[kSelWarps], found[3];
+  __shared__ __align__(8) uint32_t hist[3][kBins];  // a pass each, so that none is written while another CTA reads it
+  __shared__ uint32_t sums[kSelWarps], found[3][3];
   __shared__ int mine[2];  // of this CTA's tokens: above the last weight, equal to it
   __shared__ int warp_above[kSelWarps], warp_equal[kSelWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.x / ranks, b = bh / a.c.heads, h = bh % a.c.heads;
+  for (int i = tid; i < 3 * kBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+  auto all = [&]() {  // every thread of the cluster
+    if (ranks > 1) cl.sync();
+    else __syncthreads();
+  };
   after_predecessor();
   const int n = held(a, b, tid == 0 && rank == 0 && h == 0);
   int32_t* kept = a.kept + (int64_t)bh * a.keep;
@@ -84,9 +89,11 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
     const int i = lo + 32 * j + lane;
-    u[j] = i < hi ? order_key(w[i]) : 0;
+    u[j] = i < hi ? __float_as_uint(w[i]) : 0;
   }
-  // f(key, whether it is one) for each of the warp's tokens in order, a lane a token, whole warps
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) u[j] = order_key(__uint_as_float(u[j]));
+  // f(key, whether it is one, token) for each of the warp's tokens in order, a lane a token, whole warps
   auto each = [&](auto&& f) {
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
@@ -97,27 +104,32 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     }
   };
   uint32_t key = 0;  // what is known of the last kept weight
-  int above = 0, above_mine = 0, equal_mine = 0;
-  int left = 32;  // bits not known yet
+  int above = 0;     // weights above what is known of it
+  int left = 32;     // bits not known yet
+  __syncthreads();
+#pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int bits = pass < 2 ? 11 : 10, shift = left - bits, bins = 1 << bits;
-    for (int i = tid; i < 2 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
-    __syncthreads();
     each([&](uint32_t x, bool is, int) {
-      if (is && (pass == 0 || x >> left == key >> left)) atomicAdd(&hist[warp & 1][(x >> shift) & (bins - 1)], 1u);
+      if (is && (pass == 0 || x >> left == key >> left)) atomicAdd(&hist[pass][(x >> shift) & (bins - 1)], 1u);
     });
-    __syncthreads();
-    for (int i = tid; i < bins; i += kSelThreads) hist[0][i] += hist[1][i];
-    cl.sync();
+    all();
     // two bins a thread, the largest first; the bin in which the count passes what is wanted
     uint32_t t[2] = {};
     const int bin0 = bins - 1 - 2 * tid;
+    if (bin0 >= 1) {
+      if (ranks == 1) {
+        t[0] = hist[pass][bin0];
+        t[1] = hist[pass][bin0 - 1];
+      } else {
 #pragma unroll
-    for (int r = 0; r < kMostRanks; ++r) {
-      if (r < ranks && bin0 >= 1) {
-        const uint2 x = *reinterpret_cast<const uint2*>(cl.map_shared_rank(&hist[0][bin0 - 1], r));
-        t[0] += x.y;
-        t[1] += x.x;
+        for (int r = 0; r < kMostRanks; ++r) {
+          if (r < ranks) {
+            const uint2 x = *reinterpret_cast<const uint2*>(cl.map_shared_rank(&hist[pass][bin0 - 1], r));
+            t[0] += x.y;
+            t[1] += x.x;
+          }
+        }
       }
     }
     const uint32_t s = t[0] + t[1];
@@ -129,57 +141,49 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     }
     if (lane == 31) sums[warp] = run;
     __syncthreads();
-    uint32_t upto = lane < warp ? sums[lane] : 0;
-    upto = __reduce_add_sync(0xFFFFFFFFu, upto);
-    uint32_t before = run - s + upto + (uint32_t)above;
+    uint32_t before = run - s + (uint32_t)above + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sums[lane] : 0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (before < (uint32_t)want && before + t[j] >= (uint32_t)want) {
-        found[0] = bin0 - j;
-        found[1] = before;
-        found[2] = before + t[j];
+        found[pass][0] = bin0 - j;
+        found[pass][1] = before;
+        found[pass][2] = before + t[j];
       }
       before += t[j];
     }
     __syncthreads();
-    const uint32_t bin = found[0];
-    const bool whole = found[2] == (uint32_t)want;  // all of the bin are kept: no more bits are needed
-    above = (int)found[1];
-    key |= bin << shift;
+    key |= found[pass][0] << shift;
+    above = (int)found[pass][1];
     left = shift;
-    // this CTA's own: those in larger bins are above for good
-    uint32_t over = 0;
-    for (int i = (int)bin + 1 + tid; i < bins; i += kSelThreads) over += hist[0][i];
-    over = __reduce_add_sync(0xFFFFFFFFu, over);
-    if (lane == 0) sums[warp] = over;
-    equal_mine = (int)hist[0][bin];
-    __syncthreads();
-    above_mine += (int)__reduce_add_sync(0xFFFFFFFFu, sums[lane]);
-    cl.sync();  // every CTA has read the histograms
-    if (whole) {  // as if the last weight were the next below the bin, and none equal to it kept
-      key -= 1;
+    if (found[pass][2] == (uint32_t)want) {  // all of the bin are kept: as if the last weight were the next below it,
+      key -= 1;                              // and none equal to it kept
       above = want;
-      above_mine += equal_mine;
-      equal_mine = 0;
       break;
     }
   }
-  // kept before this CTA's tokens: all above the last weight, and of those equal to it the first ones
-  if (tid == 0) mine[0] = above_mine, mine[1] = equal_mine;
+  // kept before this warp's tokens: all above the last weight, and of those equal to it the first ones
   int na = 0, ne = 0;
   each([&](uint32_t x, bool is, int) {
     na += __popc(__ballot_sync(0xFFFFFFFFu, is && x > key));
     ne += __popc(__ballot_sync(0xFFFFFFFFu, is && x == key));
   });
   if (lane == 0) warp_above[warp] = na, warp_equal[warp] = ne;
-  cl.sync();
+  __syncthreads();
   int over = lane < warp ? warp_above[lane] : 0, equal = lane < warp ? warp_equal[lane] : 0;
-  if (lane < rank) {
-    over += *cl.map_shared_rank(&mine[0], lane);
-    equal += *cl.map_shared_rank(&mine[1], lane);
+  if (ranks > 1) {
+    if (warp == 0) {
+      const int all_above = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)warp_above[lane]),
+                all_equal = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)warp_equal[lane]);
+      if (lane == 0) mine[0] = all_above, mine[1] = all_equal;
+    }
+    cl.sync();
+    if (lane < rank) {
+      over += *cl.map_shared_rank(&mine[0], lane);
+      equal += *cl.map_shared_rank(&mine[1], lane);
+    }
   }
-  over = __reduce_add_sync(0xFFFFFFFFu, over);
-  equal = __reduce_add_sync(0xFFFFFFFFu, equal);
+  over = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)over);
+  equal = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)equal);
   const int ties = want - above;  // kept of those equal
   each([&](uint32_t x, bool is, int i) {
     const uint32_t ba = __ballot_sync(0xFFFFFFFFu, is && x > key), be = __ballot_sync(0xFFFFFFFFu, is && x == key),
@@ -189,17 +193,17 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     over += __popc(ba);
     equal += __popc(be);
   });
-  cl.sync();  // nobody leaves while its shared memory is read
+  if (ranks > 1) cl.sync();  // nobody leaves while its shared memory is read
 }
 
-constexpr int kMoveThreads = 256, kRows = 512;  // rows of a CTA's share of a batch: whole blocks
+constexpr int kMoveThreads = 512, kRows = 512;  // rows of a CTA's share of a batch: whole blocks, a thread each
 
 template <int D, int FMT>
 struct MoveShape {
   static constexpr bool k4 = FMT == ZG_KV_E2M1;
   static constexpr int kRow = k4 ? Row4<D>::kCodes : D, kUnits = kRow / 16;
-  static constexpr int kScales = k4 ? Row4<D>::kScales : 4;  // scale bytes of a row; 8 bits: its block's scale
-  static constexpr int kSmem = kRows * (kRow + 8 + kScales + 4);
+  static constexpr int kScales = Row4<D>::kScales;  // scale bytes of a row
+  static constexpr int kSmem = kRows * kRow;
 };
 
 // Four codes of a row coded again by another scale, as the write does it.
@@ -213,19 +217,16 @@ __device__ __forceinline__ uint32_t code_again(uint32_t w, float s0, float inv) 
 }
 
 // One cluster a (request, key head, side); the keys' moves the weights too.
+// Bound by the chain kept place -> block -> row of a batch, of which there is
+// one up to 4,096 kept tokens.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const __grid_constant__ EvictArgs a) {
   using Sh = MoveShape<D, FMT>;
   constexpr bool INT8 = FMT == ZG_KV_INT8;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* rows = smem;                                                // [kRows][kRow]
-  int2* src = reinterpret_cast<int2*>(rows + kRows * Sh::kRow);        // [kRows] block, place (-1: nothing to read)
-  float* weight = reinterpret_cast<float*>(src + kRows);               // [kRows]
-  uint8_t* scale = reinterpret_cast<uint8_t*>(weight + kRows);         // [kRows][kScales]
-  float* scale8 = reinterpret_cast<float*>(scale);
-  __shared__ float new_scale[kRows / 16];
+  extern __shared__ __align__(16) uint8_t rows[];  // [kRows][kRow]
+  __shared__ float row_scale[Sh::k4 ? 1 : kRows], new_scale[Sh::k4 ? 1 : kRows / 16];
   after_predecessor();
   const int bh = blockIdx.z, b = bh / a.c.heads, h = bh % a.c.heads, side = blockIdx.y, tid = threadIdx.x;
   if (held(a, b, false) <= a.keep) return;  // the whole cluster
@@ -236,83 +237,92 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const __grid_consta
   float* scales = side ? a.c.vs : a.c.ks;
   uint8_t* bytes = reinterpret_cast<uint8_t*>(scales);
   float* w = a.w + (int64_t)bh * a.w_tokens;
-  auto block_at = [&](int token) -> int {  // -1 (recorded) outside the cache
-    const int blk = table[token / bt];
-    if (blk >= 0 && blk < a.c.n_blocks) return blk;
-    atomicOr(a.c.status, kStatusCache);
-    return -1;
-  };
-  auto row_of = [&](int blk, int place) -> int64_t { return ((int64_t)blk * a.c.heads + h) * bt + place; };
+  auto good = [&](int blk) { return blk >= 0 && blk < a.c.n_blocks; };
+  auto row_of = [&](int blk, int token) -> int64_t { return ((int64_t)blk * a.c.heads + h) * bt + token % bt; };
 
   for (int64_t first = 0; first < a.keep; first += (int64_t)ranks * kRows) {
     const int64_t r0 = first + (int64_t)rank * kRows;
     const int count = (int)max((int64_t)0, min((int64_t)kRows, a.keep - r0)), base = (int)r0;
-    // where each row comes from, with what is small of it
-    for (int i = tid; i < count; i += kMoveThreads) {
-      const int from = kept[base + i], blk = block_at(from);
-      src[i] = make_int2(blk, from);
-      if (side == 0) weight[i] = w[from];
-      if constexpr (Sh::k4) {
-        const uint16_t* u = reinterpret_cast<const uint16_t*>(bytes + row_of(max(blk, 0), from % bt) * Sh::kScales);
+    // the codes, 16 bytes a copy, four chains at a time
+    for (int x0 = tid; x0 < count * Sh::kUnits; x0 += 4 * kMoveThreads) {
+      int from[4], blk[4];
 #pragma unroll
-        for (int j = 0; j < Sh::kScales / 2; ++j)
-          reinterpret_cast<uint16_t*>(scale + i * Sh::kScales)[j] = blk < 0 ? (uint16_t)0 : u[j];
-      } else {
-        scale8[i] = blk < 0 ? 0.f : scales[(int64_t)blk * a.c.heads + h];
+      for (int k = 0; k < 4; ++k) {
+        const int x = x0 + k * kMoveThreads;
+        from[k] = x < count * Sh::kUnits ? kept[base + x / Sh::kUnits] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) blk[k] = from[k] >= 0 ? table[from[k] / bt] : -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = x0 + k * kMoveThreads;
+        if (x >= count * Sh::kUnits) continue;
+        uint4* to = reinterpret_cast<uint4*>(rows) + x;
+        if (good(blk[k])) {
+          const uint4* p = reinterpret_cast<const uint4*>(codes + row_of(blk[k], from[k]) * Sh::kRow) + x % Sh::kUnits;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(p)
+                       : "memory");
+        } else {
+          *to = make_uint4(0, 0, 0, 0);
+        }
       }
     }
-    __syncthreads();
-    for (int x = tid; x < count * Sh::kUnits; x += kMoveThreads) {
-      const int i = x / Sh::kUnits, col = x % Sh::kUnits;
-      const int2 s = src[i];
-      uint4* to = reinterpret_cast<uint4*>(rows + i * Sh::kRow) + col;
-      if (s.x < 0) {
-        *to = make_uint4(0, 0, 0, 0);
+    // what is small of a row stays with its thread
+    float weight = 0.f;
+    uint16_t u[Sh::k4 ? Sh::kScales / 2 : 1];
+    if (tid < count) {
+      const int from = kept[base + tid], blk = table[from / bt];
+      if (!good(blk)) atomicOr(a.c.status, kStatusCache);
+      if (side == 0) weight = w[from];
+      if constexpr (Sh::k4) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(bytes + row_of(good(blk) ? blk : 0, from) * Sh::kScales);
+#pragma unroll
+        for (int j = 0; j < Sh::kScales / 2; ++j) u[j] = good(blk) ? p[j] : (uint16_t)0;
       } else {
-        const uint4* p = reinterpret_cast<const uint4*>(codes + row_of(s.x, s.y % bt) * Sh::kRow) + col;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(p)
-                     : "memory");
+        row_scale[tid] = good(blk) ? scales[(int64_t)blk * a.c.heads + h] : 0.f;
       }
     }
     if constexpr (!Sh::k4) {  // the new scales of the rows' blocks
+      __syncthreads();
       for (int j = tid >> 5; j * bt < count; j += kMoveThreads / 32) {
         float s = 0.f;
         for (int r = tid & 31; r < bt; r += 32)
-          if (j * bt + r < count) s = fmaxf(s, scale8[j * bt + r]);
+          if (j * bt + r < count) s = fmaxf(s, row_scale[j * bt + r]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
         if ((tid & 31) == 0) new_scale[j] = s;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    cl.sync();  // all of the batch has been read
-    for (int i = tid; i < count; i += kMoveThreads) {
-      const int row = base + i;
-      if (side == 0) w[row] = weight[i];
-      const int blk = block_at(row);
-      if (blk >= 0) {
-        if constexpr (Sh::k4) {
-          uint16_t* u = reinterpret_cast<uint16_t*>(bytes + row_of(blk, row % bt) * Sh::kScales);
+    if (ranks > 1) cl.sync();  // all of the batch has been read
+    else __syncthreads();
+    if (tid < count) {
+      const int row = base + tid, blk = table[row / bt];
+      if (side == 0) w[row] = weight;
+      if (!good(blk)) {
+        atomicOr(a.c.status, kStatusCache);
+      } else if constexpr (Sh::k4) {
+        uint16_t* p = reinterpret_cast<uint16_t*>(bytes + row_of(blk, row) * Sh::kScales);
 #pragma unroll
-          for (int j = 0; j < Sh::kScales / 2; ++j) u[j] = reinterpret_cast<const uint16_t*>(scale + i * Sh::kScales)[j];
-        } else if (row % bt == 0) {
-          scales[(int64_t)blk * a.c.heads + h] = new_scale[i / bt];
-        }
+        for (int j = 0; j < Sh::kScales / 2; ++j) p[j] = u[j];
+      } else if (row % bt == 0) {
+        scales[(int64_t)blk * a.c.heads + h] = new_scale[tid / bt];
       }
     }
+#pragma unroll 4
     for (int x = tid; x < count * Sh::kUnits; x += kMoveThreads) {
-      const int i = x / Sh::kUnits, col = x % Sh::kUnits, row = base + i, blk = table[row / bt];
-      if (blk < 0 || blk >= a.c.n_blocks) continue;  // recorded above
-      uint4 y = reinterpret_cast<const uint4*>(rows + i * Sh::kRow)[col];
+      const int i = x / Sh::kUnits, row = base + i, blk = table[row / bt];
+      if (!good(blk)) continue;  // recorded above
+      uint4 y = reinterpret_cast<const uint4*>(rows)[x];
       if constexpr (!Sh::k4) {
-        const float s0 = scale8[i], s1 = new_scale[i / bt];
+        const float s0 = row_scale[i], s1 = new_scale[i / bt];
         if (s0 != s1) {
           const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
           y = make_uint4(code_again<INT8>(y.x, s0, inv), code_again<INT8>(y.y, s0, inv), code_again<INT8>(y.z, s0, inv),
                          code_again<INT8>(y.w, s0, inv));
         }
       }
-      reinterpret_cast<uint4*>(codes + row_of(blk, row % bt) * Sh::kRow)[col] = y;
+      reinterpret_cast<uint4*>(codes + row_of(blk, row) * Sh::kRow)[x % Sh::kUnits] = y;
     }
     __syncthreads();  // shared memory is free again
   }
@@ -368,9 +378,9 @@ extern "C" zg_status zg_kv_evict(const zg_kv_cache* cache, const int32_t* table,
                         cache->v_scale, cache->n_blocks, cache->heads, cache->block_tokens, max_blocks, table, status},
                        length, weights, new_length, kept, B, w_tokens, keep, recent};
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
-  // as many CTAs a head as hold its weights two a thread, and as leave each SM two
+  // as many CTAs a head as hold its weights four a thread, and as fit the SMs at once
   int ranks = 1;
-  while (ranks < kMostRanks && tokens > (int64_t)ranks * 2 * kSelThreads && bhs * ranks <= sm_count()) ranks *= 2;
+  while (ranks < kMostRanks && tokens > (int64_t)ranks * 4 * kSelThreads && bhs * ranks * 2 <= sm_count()) ranks *= 2;
   cudaError_t err = launch_clusters(k_evict_select, dim3(bhs * ranks), ranks, kSelThreads, 0, sm, a);
   // a batch for all rows where the cluster allows it
   ranks = 1;

@@ -16,7 +16,8 @@ namespace zg {
 namespace {
 
 constexpr int kWarps = 4, kKeys = 32 * kWarps;  // keys of a CTA's step
-constexpr int kRowsAtOnce = 128;                // query rows in shared memory
+constexpr int kStages = 4;                      // steps of a warp in shared memory, one of them in use
+constexpr int kMostSteps = 16;                  // of a CTA
 
 struct WeightArgs {
   const uint8_t* kc;
@@ -27,30 +28,40 @@ struct WeightArgs {
   const float* lse;
   float* w;
   int32_t n_blocks, heads, bt, bt_log2, max_blocks, w_tokens;
-  int32_t B, R, Hq, G, causal, steps;
+  int32_t B, R, Hq, G, causal, steps, rows_at_once;
   float scale, decay;  // scale * log2(e)
 };
 
-// Codes of a warp's 32 keys as they come from memory.
 template <int D, int FMT>
-struct RawKeys {
+struct WeightShape {
   static constexpr bool k4 = FMT == ZG_KV_E2M1;
-  static constexpr int W = k4 ? Tile16x4<D>::KW : Tile16<D>::KW;
-  uint32_t k[2][2][W];
-  uint32_t s[2][2][k4 ? W : 1];
-  float ks[2];
+  static constexpr int kRow = k4 ? Row4<D>::kCodes : D;
+  // a stage: two tiles of 16 keys, then (4 bits) their scale bytes or the two blocks' scales, then the 32 weights
+  static constexpr int kCodes = 32 * kRow, kScales = k4 ? 32 * Row4<D>::kScales : 16, kStage = kCodes + kScales + 128;
+  static constexpr int kRing = kWarps * kStages * kStage;
 };
 
+__device__ __forceinline__ void copy16_async(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4b_async(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+
+// A warp's keys come into its own ring of shared memory three steps ahead, and
+// the weights that they have so far with them; the CTA's block numbers are
+// read before, at once.
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constant__ WeightArgs a, const Rows<T> q) {
-  using Raw = RawKeys<D, FMT>;
-  constexpr bool k4 = Raw::k4;
+  using Sh = WeightShape<D, FMT>;
+  constexpr bool k4 = Sh::k4;
   constexpr int KS = D / 16;  // products of 16 dims
   extern __shared__ __align__(16) uint8_t smem[];
-  uint4* frag = reinterpret_cast<uint4*>(smem);  // [row / 8][KS / 2][lane]
-  const int most = min((a.R * a.G + 7) / 8 * 8, kRowsAtOnce);
+  uint4* frag = reinterpret_cast<uint4*>(smem + Sh::kRing);  // [row / 8][KS / 2][lane]
+  const int most = a.rows_at_once;
   float4* par = reinterpret_cast<float4*>(frag + most / 8 * (KS / 2) * 32);  // [row / 2]: factor, log-sum-exp of both rows
   int2* sees = reinterpret_cast<int2*>(par + most / 2);                      // [row / 2]: tokens that they see
+  __shared__ int s_blk[kMostSteps * kKeys / 16];  // of every 16 keys, -1: not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   after_predecessor();
 
@@ -68,29 +79,46 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
   const int steps = min(a.steps, (s.len - key0 + kKeys - 1) / kKeys);
   const int M = s.rows * a.G;
   const int known = a.known ? a.known[b] : s.len;
-
-  // the codes of a step's 32 keys of this warp; of blocks outside the cache (recorded) and behind the history: none
-  auto load = [&](int step, Raw& r, int* blk) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int key = key0 + step * kKeys + warp * 32 + n * 16;
-      blk[n] = -1;
-      if (step < steps && key < s.len) {
-        blk[n] = a.table[(int64_t)b * a.max_blocks + (key >> a.bt_log2)];
-        if (blk[n] < 0 || blk[n] >= a.n_blocks) {
-          if (lane == 0) atomicOr(a.status, kStatusCache);
-          blk[n] = -1;
-        }
-      }
-      if (blk[n] < 0) continue;
-      const int64_t bh = (int64_t)blk[n] * a.heads + h, row = bh * a.bt + (key & (a.bt - 1));
-      if constexpr (k4) {
-        Tile16x4<D>::keys(a.kc + row * Row4<D>::kCodes, a.kg + row * Row4<D>::kScales, g, c, r.k[n], r.s[n]);
-      } else {
-        Tile16<D>::keys(a.kc + row * D, g, c, r.k[n]);
-        r.ks[n] = a.ks[bh];
+  for (int i = threadIdx.x; i < steps * kKeys / 16; i += 32 * kWarps) {
+    const int key = key0 + 16 * i;
+    int blk = -1;
+    if (key < s.len) {
+      blk = a.table[(int64_t)b * a.max_blocks + (key >> a.bt_log2)];
+      if (blk < 0 || blk >= a.n_blocks) {
+        atomicOr(a.status, kStatusCache);
+        blk = -1;
       }
     }
+    s_blk[i] = blk;
+  }
+
+  float* w = a.w + ((int64_t)b * a.heads + h) * a.w_tokens;
+  uint8_t* ring = smem + warp * (kStages * Sh::kStage);
+  auto fetch = [&](int step) {
+    if (step < steps) {
+      uint8_t* to = ring + step % kStages * Sh::kStage;
+      const int key = key0 + step * kKeys + warp * 32;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int blk = s_blk[step * (kKeys / 16) + warp * 2 + n];
+        if (blk < 0) continue;
+        const int64_t bh = (int64_t)blk * a.heads + h, row = bh * a.bt + ((key + 16 * n) & (a.bt - 1));
+        const uint8_t* from = a.kc + row * Sh::kRow;
+#pragma unroll
+        for (int i = lane; i < Sh::kRow; i += 32) copy16_async(to + (n * Sh::kRow + i) * 16, from + i * 16);
+        if constexpr (k4) {
+          if (lane < Row4<D>::kScales)
+            copy16_async(to + Sh::kCodes + (n * Row4<D>::kScales + lane) * 16,
+                         a.kg + row * Row4<D>::kScales + lane * 16);
+        } else {
+          if (lane == 0) copy4b_async(to + Sh::kCodes + 4 * n, a.ks + bh);
+        }
+      }
+      // of the token that this lane writes (below)
+      const int mine = key + 16 * (c >> 1) + 8 * (c & 1) + g;
+      if (mine < s.len && mine < known) copy4b_async(to + Sh::kCodes + Sh::kScales + 4 * lane, w + mine);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   // rows m0 .. m0 + most - 1 into shared memory: a lane has four dims of a row (a head of 96: 24 lanes), which are
@@ -98,15 +126,17 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
   auto stage = [&](int m0) {
     constexpr int kLanes = D / 4, kSlot = D == 96 ? 32 : kLanes, kAt = 32 / kSlot;
     const int l = lane % kSlot, d = 4 * l;
-    int w, cc;  // of the lane's dims: Tile16(x4)::dim_of(w, cc) = d
+    int dw, cc;  // of the lane's dims: Tile16(x4)::dim_of(dw, cc) = d
     if constexpr (k4) {
-      cc = d / (D / 4), w = d % (D / 4) / 4;
+      cc = d / (D / 4), dw = d % (D / 4) / 4;
     } else if (d < D / 64 * 64) {
-      cc = d % 64 / 16, w = d / 64 * 4 + d % 16 / 4;
+      cc = d % 64 / 16, dw = d / 64 * 4 + d % 16 / 4;
     } else {
-      cc = d % 64 % 32 / 8, w = D / 64 * 4 + d % 8 / 4;
+      cc = d % 64 % 32 / 8, dw = D / 64 * 4 + d % 8 / 4;
     }
-    for (int r0 = warp * kAt; r0 < most; r0 += kWarps * kAt) {
+    const int upto = min(most, (M - m0 + 7) / 8 * 8);
+#pragma unroll 4
+    for (int r0 = warp * kAt; r0 < upto; r0 += kWarps * kAt) {
       const int r = r0 + lane / kSlot, m = m0 + r;
       const bool live = m < M;
       const int row = live ? m / a.G : 0, qh = h * a.G + (live ? m % a.G : 0);
@@ -120,10 +150,10 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
       for (int o = kSlot / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
       const int ex = row_exponent(top);
       const float dn = power_of_2(-ex);
-      if (r < most && l < kLanes)
-        reinterpret_cast<uint2*>(frag)[(((r >> 3) * (KS / 2) + (w >> 1)) * 32 + (r & 7) * 4 + cc) * 2 + (w & 1)] =
+      if (r < upto && l < kLanes)
+        reinterpret_cast<uint2*>(frag)[(((r >> 3) * (KS / 2) + (dw >> 1)) * 32 + (r & 7) * 4 + cc) * 2 + (dw & 1)] =
             make_uint2(pack_half2(x[0] * dn, x[1] * dn), pack_half2(x[2] * dn, x[3] * dn));
-      if (r < most && l == 0) {
+      if (r < upto && l == 0) {
         reinterpret_cast<float2*>(par)[r] =
             make_float2(a.scale * power_of_2(ex), vis == 0 ? INFINITY : ls * 1.4426950408889634f);
         reinterpret_cast<int*>(sees)[r] = vis;
@@ -131,58 +161,69 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
     }
   };
 
-  Raw raw;
-  int blk[2];
-  load(0, raw, blk);
-  stage(0);
-  __syncthreads();
-  for (int step = 0; step < steps; ++step) {
-    // the keys as fragments
-    uint32_t ka[2][KS][4];
-    float ks[2];
-    bool here[2];
+  // all steps for the rows that are in shared memory, then for the next ones
+  for (int m0 = 0; m0 == 0 || m0 < M; m0 += most) {
+    __syncthreads();  // the block numbers are there; the last rows are not read any more
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      here[n] = blk[n] >= 0;
-      ks[n] = k4 ? 1.f : raw.ks[n];
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    stage(m0);
+    __syncthreads();
+    const int groups = (min(M - m0, most) + 7) / 8;
+    for (int step = 0; step < steps; ++step) {
+      fetch(step + kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      const uint8_t* at = ring + step % kStages * Sh::kStage;
+      // the keys as fragments
+      uint32_t ka[2][KS][4];
+      float ks[2];
+      bool here[2];
 #pragma unroll
-      for (int w = 0; w < Raw::W; ++w) {
+      for (int n = 0; n < 2; ++n) {
+        here[n] = s_blk[step * (kKeys / 16) + warp * 2 + n] >= 0;
         if constexpr (k4) {
-          uint32_t x[4], y[4];
-          e2m1_half8(raw.k[n][0][w], raw.s[n][0][w], x);
-          e2m1_half8(raw.k[n][1][w], raw.s[n][1][w], y);
+          constexpr int W = Tile16x4<D>::KW;
+          uint32_t k[2][W], u[2][W];
+          Tile16x4<D>::keys(at + n * 16 * Sh::kRow, at + Sh::kCodes + n * 16 * Row4<D>::kScales, g, c, k, u);
+          ks[n] = 1.f;
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            ka[n][2 * w + v][0] = x[2 * v];
-            ka[n][2 * w + v][1] = y[2 * v];
-            ka[n][2 * w + v][2] = x[2 * v + 1];
-            ka[n][2 * w + v][3] = y[2 * v + 1];
+          for (int i = 0; i < W; ++i) {
+            uint32_t x[4], y[4];
+            e2m1_half8(k[0][i], u[0][i], x);
+            e2m1_half8(k[1][i], u[1][i], y);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              ka[n][2 * i + v][0] = x[2 * v];
+              ka[n][2 * i + v][1] = y[2 * v];
+              ka[n][2 * i + v][2] = x[2 * v + 1];
+              ka[n][2 * i + v][3] = y[2 * v + 1];
+            }
           }
         } else {
-          codes_half4<FMT == ZG_KV_INT8>(raw.k[n][0][w], ka[n][w][0], ka[n][w][2]);
-          codes_half4<FMT == ZG_KV_INT8>(raw.k[n][1][w], ka[n][w][1], ka[n][w][3]);
+          constexpr int W = Tile16<D>::KW;
+          uint32_t k[2][W];
+          Tile16<D>::keys(at + n * 16 * Sh::kRow, g, c, k);
+          ks[n] = reinterpret_cast<const float*>(at + Sh::kCodes)[n];
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            codes_half4<FMT == ZG_KV_INT8>(k[0][i], ka[n][i][0], ka[n][i][2]);
+            codes_half4<FMT == ZG_KV_INT8>(k[1][i], ka[n][i][1], ka[n][i][3]);
+          }
         }
       }
-    }
-    load(step + 1, raw, blk);
-    const int first = key0 + step * kKeys + warp * 32;
-    float sum[2][2] = {};  // keys g and g + 8 of both tiles
-    for (int m0 = 0; m0 < M; m0 += most) {
-      if (m0 > 0 || (step > 0 && M > most)) {
-        __syncthreads();
-        stage(m0);
-        __syncthreads();
-      }
-      const int groups = (min(M - m0, most) + 7) / 8;
+      const float had = reinterpret_cast<const float*>(at + Sh::kCodes + Sh::kScales)[lane];
+      const int first = key0 + step * kKeys + warp * 32;
+      float sum[2][2] = {};  // keys g and g + 8 of both tiles
+#pragma unroll 1
       for (int n8 = 0; n8 < groups; ++n8) {
         float z[2][4] = {};
 #pragma unroll
-        for (int w = 0; w < KS / 2; ++w) {
-          const uint4 f = frag[(n8 * (KS / 2) + w) * 32 + lane];
+        for (int i = 0; i < KS / 2; ++i) {
+          const uint4 f = frag[(n8 * (KS / 2) + i) * 32 + lane];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            mma_16816(z[n], ka[n][2 * w], f.x, f.y);
-            mma_16816(z[n], ka[n][2 * w + 1], f.z, f.w);
+            mma_16816(z[n], ka[n][2 * i], f.x, f.y);
+            mma_16816(z[n], ka[n][2 * i + 1], f.z, f.w);
           }
         }
         const float4 p = par[n8 * 4 + c];
@@ -204,22 +245,23 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
           sum[n][1] += e[2] + e[3];
         }
       }
-    }
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sum[n][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][i], 1);
-        sum[n][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][i], 2);
+        for (int i = 0; i < 2; ++i) {
+          sum[n][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][i], 1);
+          sum[n][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][i], 2);
+        }
+      // lane (g, c) writes key g + 8 (c & 1) of tile c / 2
+      const int key = first + 16 * (c >> 1) + 8 * (c & 1) + g;
+      const float mine = c == 0 ? sum[0][0] : c == 1 ? sum[0][1] : c == 2 ? sum[1][0] : sum[1][1];
+      if (key < s.len) {
+        const float old = m0 > 0 ? w[key] : key < known && a.decay != 0.f ? had * a.decay : 0.f;
+        w[key] = old + ((c >> 1 ? here[1] : here[0]) ? mine : 0.f);
       }
-    // lane (g, c) writes key g + 8 (c & 1) of tile c / 2
-    const int key = first + 16 * (c >> 1) + 8 * (c & 1) + g;
-    const float mine = c == 0 ? sum[0][0] : c == 1 ? sum[0][1] : c == 2 ? sum[1][0] : sum[1][1];
-    if (key < s.len) {
-      float* w = a.w + ((int64_t)b * a.heads + h) * a.w_tokens + key;
-      const float old = key < known && a.decay != 0.f ? *w * a.decay : 0.f;
-      *w = old + ((c >> 1 ? here[1] : here[0]) ? mine : 0.f);
+      __syncwarp();  // the stage is free again
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 }
 
@@ -277,19 +319,24 @@ extern "C" zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* tabl
   a.scale = scale * 1.4426950408889634f;
   a.decay = decay;
   const int64_t units = (tokens + kKeys - 1) / kKeys, M = (int64_t)R * a.G;
-  // several steps a CTA, so that its queries are brought in once for them, where steps are many
-  a.steps = (int)std::max<int64_t>(1, std::min<int64_t>(8, units * B * cache->heads / (sm_count() * 32)));
-  const int most = (int)std::min<int64_t>((M + 7) / 8 * 8, kRowsAtOnce);
+  // several steps a CTA, so that its queries and block numbers are brought in once for them, where steps are many
+  a.steps = (int)std::max<int64_t>(1, std::min<int64_t>(kMostSteps, units * B * cache->heads / (sm_count() * 16)));
   cudaError_t err = cudaSuccess;
   for_dim(cache->dim, [&](auto dv) {
     constexpr int D = decltype(dv)::value;
-    const size_t smem = (size_t)most * (2 * D + 8 + 4);
+    // query rows in shared memory at once: all, or as many as leave an SM two CTAs
+    constexpr int kRowBytes = 2 * D + 12, kRowsAtOnce = 60 * 1024 / kRowBytes / 8 * 8;
+    a.rows_at_once = (int)std::min<int64_t>((M + 7) / 8 * 8, kRowsAtOnce);
     auto typed = [&](auto ev) {
       using E = typename decltype(ev)::type;
       for_format(cache->format, [&](auto fv) {
-        auto kern = k_kv_weights<E, D, decltype(fv)::value>;
-        err = launch_early(kern, dim3((unsigned)((units + a.steps - 1) / a.steps), cache->heads, B), 32 * kWarps, smem,
-                           static_cast<cudaStream_t>(stream), a, rows_of<E>(q));
+        constexpr int FMT = decltype(fv)::value;
+        auto kern = k_kv_weights<E, D, FMT>;
+        const int smem = WeightShape<D, FMT>::kRing + a.rows_at_once * kRowBytes;
+        if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (err == cudaSuccess)
+          err = launch_early(kern, dim3((unsigned)((units + a.steps - 1) / a.steps), cache->heads, B), 32 * kWarps, smem,
+                             static_cast<cudaStream_t>(stream), a, rows_of<E>(q));
       });
     };
     if (q->dtype == ZG_BF16) typed(Elem<__nv_bfloat16>{});
