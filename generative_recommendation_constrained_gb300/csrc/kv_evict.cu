@@ -3,17 +3,16 @@
 // itself, its last `recent` ones and the keep - recent others of largest
 // weight, moved to the front in their order.
 //
-//   k_evict_select  finds them: the weight of the last one kept, 11 + 11 + 10
-//                   bits at a time from histograms of order-preserving integers
-//                   (a cluster of CTAs a head, their histograms added through
-//                   distributed shared memory), then their numbers in order.
-//                   Weights are read once and stay in registers.  Integer
-//                   counts alone: nothing hangs on an order of atomics.
-//   k_evict_move    moves rows in place, a cluster of CTAs a (head, side).
-//                   Row i comes from kept[i] >= i, and kept[] ascends: the
-//                   cluster reads a batch of rows into its shared memory, all
-//                   its CTAs wait for one another, then it is written; what a
-//                   later batch reads lies behind all that is written by then.
+// One cluster of CTAs a (request, key head), in one launch:
+//   select  the weight of the last one kept, 11 + 11 + 10 bits at a time from
+//           histograms of order-preserving integers (the CTAs' histograms added
+//           through distributed shared memory), then the kept numbers in
+//           order.  Weights are read once and stay in shared memory.  Integer
+//           counts alone: nothing hangs on an order of atomics.
+//   move    row i comes from kept[i] >= i, and kept[] ascends: the cluster reads
+//           a batch of rows into its shared memory, all its CTAs wait for one
+//           another, then it is written; what a later batch reads lies behind
+//           all that is written by then.
 //
 // In 8 bits a block's new scale is the largest of its rows' old ones, and rows
 // of a smaller one are coded again.  In 4 bits rows carry their scales along
@@ -27,17 +26,18 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kHeld = 32;        // weights a thread holds; those of longer histories are read again for every pass
-constexpr int kMostRanks = 8;    // CTAs of a cluster, at most
+constexpr int kMostRanks = 8;            // CTAs of a cluster, at most
+constexpr int kMostSmem = 128 * 1024;    // weights of a CTA, then rows of a batch
 
 struct EvictArgs {
   CacheView c;
   const int32_t* length;
   float* w;
   int32_t *new_length, *kept;
-  int32_t B, w_tokens, keep, recent;
+  int32_t w_tokens, keep, recent;
+  int32_t held, rows;  // weights a thread keeps in shared memory; rows of a CTA's share of a batch, whole blocks
 };
 
 // Larger numbers for larger weights; NaN below everything, both zeros the same.
@@ -54,156 +54,13 @@ __device__ __forceinline__ int held(const EvictArgs& a, int b, bool report) {
   return min(max(n, 0), most);
 }
 
-// One cluster a (request, key head).
-__global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs a) {
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
-  __shared__ __align__(8) uint32_t hist[3][kBins];  // a pass each, so that none is written while another CTA reads it
-  __shared__ uint32_t sums[kSelWarps], found[3][3];
-  __shared__ int mine[2];  // of this CTA's tokens: above the last weight, equal to it
-  __shared__ int warp_above[kSelWarps], warp_equal[kSelWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int bh = blockIdx.x / ranks, b = bh / a.c.heads, h = bh % a.c.heads;
-  for (int i = tid; i < 3 * kBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
-  auto all = [&]() {  // every thread of the cluster
-    if (ranks > 1) cl.sync();
-    else __syncthreads();
-  };
-  after_predecessor();
-  const int n = held(a, b, tid == 0 && rank == 0 && h == 0);
-  int32_t* kept = a.kept + (int64_t)bh * a.keep;
-  if (tid == 0 && rank == 0 && h == 0) a.new_length[b] = min(n, a.keep);
-  if (n <= a.keep) {  // stays as it is
-    for (int i = rank * kSelThreads + tid; i < a.keep; i += ranks * kSelThreads) kept[i] = i < n ? i : -1;
-    return;
-  }
-  const int m = n - a.recent, want = a.keep - a.recent;  // `want` of the first m
-  for (int i = rank * kSelThreads + tid; i < a.recent; i += ranks * kSelThreads) kept[want + i] = m + i;
-  if (want == 0) return;
-  const float* w = a.w + (int64_t)bh * a.w_tokens;
-  // this warp's tokens: 32 side by side at a time
-  const int per = ((m + ranks * kSelWarps - 1) / (ranks * kSelWarps) + 31) / 32 * 32;
-  const int64_t from = (int64_t)(rank * kSelWarps + warp) * per;
-  const int lo = (int)min((int64_t)m, from), hi = (int)min((int64_t)m, from + per);
-  uint32_t u[kHeld];
-#pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    const int i = lo + 32 * j + lane;
-    u[j] = i < hi ? __float_as_uint(w[i]) : 0;
-  }
-#pragma unroll
-  for (int j = 0; j < kHeld; ++j) u[j] = order_key(__uint_as_float(u[j]));
-  // f(key, whether it is one, token) for each of the warp's tokens in order, a lane a token, whole warps
-  auto each = [&](auto&& f) {
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-      if (lo + 32 * j < hi) f(u[j], lo + 32 * j + lane < hi, lo + 32 * j + lane);
-    for (int i0 = lo + 32 * kHeld; i0 < hi; i0 += 32) {
-      const int i = i0 + lane;
-      f(i < hi ? order_key(w[i]) : 0, i < hi, i);
-    }
-  };
-  uint32_t key = 0;  // what is known of the last kept weight
-  int above = 0;     // weights above what is known of it
-  int left = 32;     // bits not known yet
-  __syncthreads();
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass < 2 ? 11 : 10, shift = left - bits, bins = 1 << bits;
-    each([&](uint32_t x, bool is, int) {
-      if (is && (pass == 0 || x >> left == key >> left)) atomicAdd(&hist[pass][(x >> shift) & (bins - 1)], 1u);
-    });
-    all();
-    // two bins a thread, the largest first; the bin in which the count passes what is wanted
-    uint32_t t[2] = {};
-    const int bin0 = bins - 1 - 2 * tid;
-    if (bin0 >= 1) {
-      if (ranks == 1) {
-        t[0] = hist[pass][bin0];
-        t[1] = hist[pass][bin0 - 1];
-      } else {
-#pragma unroll
-        for (int r = 0; r < kMostRanks; ++r) {
-          if (r < ranks) {
-            const uint2 x = *reinterpret_cast<const uint2*>(cl.map_shared_rank(&hist[pass][bin0 - 1], r));
-            t[0] += x.y;
-            t[1] += x.x;
-          }
-        }
-      }
-    }
-    const uint32_t s = t[0] + t[1];
-    uint32_t run = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, run, o);
-      if (lane >= o) run += y;
-    }
-    if (lane == 31) sums[warp] = run;
-    __syncthreads();
-    uint32_t before = run - s + (uint32_t)above + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sums[lane] : 0);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (before < (uint32_t)want && before + t[j] >= (uint32_t)want) {
-        found[pass][0] = bin0 - j;
-        found[pass][1] = before;
-        found[pass][2] = before + t[j];
-      }
-      before += t[j];
-    }
-    __syncthreads();
-    key |= found[pass][0] << shift;
-    above = (int)found[pass][1];
-    left = shift;
-    if (found[pass][2] == (uint32_t)want) {  // all of the bin are kept: as if the last weight were the next below it,
-      key -= 1;                              // and none equal to it kept
-      above = want;
-      break;
-    }
-  }
-  // kept before this warp's tokens: all above the last weight, and of those equal to it the first ones
-  int na = 0, ne = 0;
-  each([&](uint32_t x, bool is, int) {
-    na += __popc(__ballot_sync(0xFFFFFFFFu, is && x > key));
-    ne += __popc(__ballot_sync(0xFFFFFFFFu, is && x == key));
-  });
-  if (lane == 0) warp_above[warp] = na, warp_equal[warp] = ne;
-  __syncthreads();
-  int over = lane < warp ? warp_above[lane] : 0, equal = lane < warp ? warp_equal[lane] : 0;
-  if (ranks > 1) {
-    if (warp == 0) {
-      const int all_above = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)warp_above[lane]),
-                all_equal = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)warp_equal[lane]);
-      if (lane == 0) mine[0] = all_above, mine[1] = all_equal;
-    }
-    cl.sync();
-    if (lane < rank) {
-      over += *cl.map_shared_rank(&mine[0], lane);
-      equal += *cl.map_shared_rank(&mine[1], lane);
-    }
-  }
-  over = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)over);
-  equal = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)equal);
-  const int ties = want - above;  // kept of those equal
-  each([&](uint32_t x, bool is, int i) {
-    const uint32_t ba = __ballot_sync(0xFFFFFFFFu, is && x > key), be = __ballot_sync(0xFFFFFFFFu, is && x == key),
-                   below = (1u << lane) - 1;
-    const int my_over = over + __popc(ba & below), my_equal = equal + __popc(be & below);
-    if (is && (x > key || (x == key && my_equal < ties))) kept[my_over + min(my_equal, ties)] = i;
-    over += __popc(ba);
-    equal += __popc(be);
-  });
-  if (ranks > 1) cl.sync();  // nobody leaves while its shared memory is read
-}
-
-constexpr int kMoveThreads = 512, kRows = 512;  // rows of a CTA's share of a batch: whole blocks, a thread each
-
 template <int D, int FMT>
-struct MoveShape {
+struct EvictShape {
   static constexpr bool k4 = FMT == ZG_KV_E2M1;
   static constexpr int kRow = k4 ? Row4<D>::kCodes : D, kUnits = kRow / 16;
-  static constexpr int kScales = Row4<D>::kScales;  // scale bytes of a row
-  static constexpr int kSmem = kRows * kRow;
+  static constexpr int kScales = Row4<D>::kScales;  // scale bytes of a row in 4 bits
+  // rows of keys and of values in shared memory, a thread each for what is small of them
+  static constexpr int kRows = kMostSmem / (2 * kRow) / 128 * 128 < kThreads ? kMostSmem / (2 * kRow) / 128 * 128 : kThreads;
 };
 
 // Four codes of a row coded again by another scale, as the write does it.
@@ -216,113 +73,262 @@ __device__ __forceinline__ uint32_t code_again(uint32_t w, float s0, float inv) 
   return float4_codes<INT8>(y, inv);
 }
 
-// One cluster a (request, key head, side); the keys' moves the weights too.
-// Bound by the chain kept place -> block -> row of a batch, of which there is
-// one up to 4,096 kept tokens.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kMoveThreads) k_evict_move(const __grid_constant__ EvictArgs a) {
-  using Sh = MoveShape<D, FMT>;
+__global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ EvictArgs a) {
+  using Sh = EvictShape<D, FMT>;
   constexpr bool INT8 = FMT == ZG_KV_INT8;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
-  extern __shared__ __align__(16) uint8_t rows[];  // [kRows][kRow]
-  __shared__ float row_scale[Sh::k4 ? 1 : kRows], new_scale[Sh::k4 ? 1 : kRows / 16];
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(8) uint32_t hist[3][kBins];  // a pass each, so that none is written while another CTA reads it
+  __shared__ uint32_t sums[kWarps], found[3][3];
+  __shared__ int mine[2];  // of this CTA's tokens: above the last weight, equal to it
+  __shared__ int warp_above[kWarps], warp_equal[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bh = blockIdx.x / ranks, b = bh / a.c.heads, h = bh % a.c.heads;
+  for (int i = tid; i < 3 * kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+  auto all = [&]() {  // every thread of the cluster
+    if (ranks > 1) cl.sync();
+    else __syncthreads();
+  };
   after_predecessor();
-  const int bh = blockIdx.z, b = bh / a.c.heads, h = bh % a.c.heads, side = blockIdx.y, tid = threadIdx.x;
-  if (held(a, b, false) <= a.keep) return;  // the whole cluster
-  const int bt = a.c.bt;
-  const int32_t* kept = a.kept + (int64_t)bh * a.keep;
-  const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
-  uint8_t* codes = side ? a.c.vc : a.c.kc;
-  float* scales = side ? a.c.vs : a.c.ks;
-  uint8_t* bytes = reinterpret_cast<uint8_t*>(scales);
+  const int n = held(a, b, tid == 0 && rank == 0 && h == 0);
+  int32_t* kept = a.kept + (int64_t)bh * a.keep;
+  if (tid == 0 && rank == 0 && h == 0) a.new_length[b] = min(n, a.keep);
+  if (n <= a.keep) {  // stays as it is
+    for (int i = rank * kThreads + tid; i < a.keep; i += ranks * kThreads) kept[i] = i < n ? i : -1;
+    return;
+  }
   float* w = a.w + (int64_t)bh * a.w_tokens;
+  const int m = n - a.recent, want = a.keep - a.recent;  // `want` of the first m
+  for (int i = rank * kThreads + tid; i < a.recent; i += ranks * kThreads) kept[want + i] = m + i;
+
+  if (want > 0) {
+    // ------------------------------------------------------------- select
+    // this warp's tokens, 32 side by side at a time; a thread's own lie kThreads apart in shared memory
+    uint32_t* mem = reinterpret_cast<uint32_t*>(smem) + tid;
+    const int per = ((m + ranks * kWarps - 1) / (ranks * kWarps) + 31) / 32 * 32;
+    const int64_t from = (int64_t)(rank * kWarps + warp) * per;
+    const int lo = (int)min((int64_t)m, from), hi = (int)min((int64_t)m, from + per);
+#pragma unroll 8
+    for (int j = 0; j < min(a.held, (hi - lo + 31) / 32); ++j) {
+      const int i = lo + 32 * j + lane;
+      mem[j * kThreads] = i < hi ? order_key(w[i]) : 0;
+    }
+    // f(key, whether it is one, token) for each of the warp's tokens in order, a lane a token, whole warps
+    auto each = [&](auto&& f) {
+#pragma unroll 4
+      for (int j = 0; j < (hi - lo + 31) / 32; ++j) {
+        const int i = lo + 32 * j + lane;
+        f(j < a.held ? mem[j * kThreads] : i < hi ? order_key(w[i]) : 0, i < hi, i);
+      }
+    };
+    uint32_t key = 0;  // what is known of the last kept weight
+    int above = 0;     // weights above what is known of it
+    int left = 32;     // bits not known yet
+    __syncthreads();
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass < 2 ? 11 : 10, shift = left - bits, bins = 1 << bits;
+      each([&](uint32_t x, bool is, int) {
+        if (is && (pass == 0 || x >> left == key >> left)) atomicAdd(&hist[pass][(x >> shift) & (bins - 1)], 1u);
+      });
+      all();
+      // two bins a thread, the largest first; the bin in which the count passes what is wanted
+      uint32_t t[2] = {};
+      const int bin0 = bins - 1 - 2 * tid;
+      if (bin0 >= 1) {
+        if (ranks == 1) {
+          t[0] = hist[pass][bin0];
+          t[1] = hist[pass][bin0 - 1];
+        } else {
+#pragma unroll
+          for (int r = 0; r < kMostRanks; ++r) {
+            if (r < ranks) {
+              const uint2 x = *reinterpret_cast<const uint2*>(cl.map_shared_rank(&hist[pass][bin0 - 1], r));
+              t[0] += x.y;
+              t[1] += x.x;
+            }
+          }
+        }
+      }
+      const uint32_t s = t[0] + t[1];
+      uint32_t run = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, run, o);
+        if (lane >= o) run += y;
+      }
+      if (lane == 31) sums[warp] = run;
+      __syncthreads();
+      uint32_t before = run - s + (uint32_t)above + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sums[lane] : 0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (before < (uint32_t)want && before + t[j] >= (uint32_t)want) {
+          found[pass][0] = bin0 - j;
+          found[pass][1] = before;
+          found[pass][2] = before + t[j];
+        }
+        before += t[j];
+      }
+      __syncthreads();
+      key |= found[pass][0] << shift;
+      above = (int)found[pass][1];
+      left = shift;
+      if (found[pass][2] == (uint32_t)want) {  // all of the bin are kept: as if the last weight were the next below it,
+        key -= 1;                              // and none equal to it kept
+        above = want;
+        break;
+      }
+    }
+    // kept before this warp's tokens: all above the last weight, and of those equal to it the first ones
+    int na = 0, ne = 0;
+    each([&](uint32_t x, bool is, int) {
+      na += is && x > key;
+      ne += is && x == key;
+    });
+    na = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)na);
+    ne = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)ne);
+    if (lane == 0) warp_above[warp] = na, warp_equal[warp] = ne;
+    __syncthreads();
+    int over = lane < warp ? warp_above[lane] : 0, equal = lane < warp ? warp_equal[lane] : 0;
+    if (ranks > 1) {
+      if (warp == 0) {
+        const int all_above = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)warp_above[lane]),
+                  all_equal = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)warp_equal[lane]);
+        if (lane == 0) mine[0] = all_above, mine[1] = all_equal;
+      }
+      cl.sync();
+      if (lane < rank) {
+        over += *cl.map_shared_rank(&mine[0], lane);
+        equal += *cl.map_shared_rank(&mine[1], lane);
+      }
+    }
+    over = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)over);
+    equal = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)equal);
+    const int ties = want - above;  // kept of those equal
+    each([&](uint32_t x, bool is, int i) {
+      const uint32_t ba = __ballot_sync(0xFFFFFFFFu, is && x > key), be = __ballot_sync(0xFFFFFFFFu, is && x == key),
+                     below = (1u << lane) - 1;
+      const int my_over = over + __popc(ba & below), my_equal = equal + __popc(be & below);
+      if (is && (x > key || (x == key && my_equal < ties))) kept[my_over + min(my_equal, ties)] = i;
+      over += __popc(ba);
+      equal += __popc(be);
+    });
+  }
+  all();  // the kept numbers are there; nobody reads another's shared memory from here on
+
+  // ----------------------------------------------------------------- move
+  __shared__ float row_scale[2][Sh::k4 ? 1 : Sh::kRows], new_scale[2][Sh::k4 ? 1 : Sh::kRows / 16];
+  const int bt = a.c.bt;
+  const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
   auto good = [&](int blk) { return blk >= 0 && blk < a.c.n_blocks; };
   auto row_of = [&](int blk, int token) -> int64_t { return ((int64_t)blk * a.c.heads + h) * bt + token % bt; };
-
-  for (int64_t first = 0; first < a.keep; first += (int64_t)ranks * kRows) {
-    const int64_t r0 = first + (int64_t)rank * kRows;
-    const int count = (int)max((int64_t)0, min((int64_t)kRows, a.keep - r0)), base = (int)r0;
-    // the codes, 16 bytes a copy, four chains at a time
-    for (int x0 = tid; x0 < count * Sh::kUnits; x0 += 4 * kMoveThreads) {
+  auto codes = [&](int side) { return side ? a.c.vc : a.c.kc; };
+  auto scales = [&](int side) { return side ? a.c.vs : a.c.ks; };
+  auto bytes = [&](int side, int blk, int token) {
+    return reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(scales(side)) + row_of(blk, token) * Sh::kScales);
+  };
+  for (int64_t first = 0; first < a.keep; first += (int64_t)ranks * a.rows) {
+    const int64_t r0 = first + (int64_t)rank * a.rows;
+    const int count = (int)max((int64_t)0, min((int64_t)a.rows, a.keep - r0)), base = (int)r0;
+    const int units = count * Sh::kUnits;  // of 16 bytes, of each side
+    // the codes of both sides, four chains (kept number, block, row) at a time
+    for (int x0 = tid; x0 < units; x0 += 4 * kThreads) {
       int from[4], blk[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int x = x0 + k * kMoveThreads;
-        from[k] = x < count * Sh::kUnits ? kept[base + x / Sh::kUnits] : -1;
+        const int x = x0 + k * kThreads;
+        from[k] = x < units ? __ldcg(kept + base + x / Sh::kUnits) : -1;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) blk[k] = from[k] >= 0 ? table[from[k] / bt] : -1;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int x = x0 + k * kMoveThreads;
-        if (x >= count * Sh::kUnits) continue;
-        uint4* to = reinterpret_cast<uint4*>(rows) + x;
-        if (good(blk[k])) {
-          const uint4* p = reinterpret_cast<const uint4*>(codes + row_of(blk[k], from[k]) * Sh::kRow) + x % Sh::kUnits;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(p)
-                       : "memory");
-        } else {
-          *to = make_uint4(0, 0, 0, 0);
+        const int x = x0 + k * kThreads;
+        if (x >= units) continue;
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          uint4* to = reinterpret_cast<uint4*>(smem) + side * a.rows * Sh::kUnits + x;
+          if (good(blk[k])) {
+            const uint4* p = reinterpret_cast<const uint4*>(codes(side) + row_of(blk[k], from[k]) * Sh::kRow) + x % Sh::kUnits;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(p)
+                         : "memory");
+          } else {
+            *to = make_uint4(0, 0, 0, 0);
+          }
         }
       }
     }
     // what is small of a row stays with its thread
     float weight = 0.f;
-    uint16_t u[Sh::k4 ? Sh::kScales / 2 : 1];
+    uint16_t u[2][Sh::k4 ? Sh::kScales / 2 : 1];
+    int to_blk = -1;
     if (tid < count) {
-      const int from = kept[base + tid], blk = table[from / bt];
-      if (!good(blk)) atomicOr(a.c.status, kStatusCache);
-      if (side == 0) weight = w[from];
-      if constexpr (Sh::k4) {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(bytes + row_of(good(blk) ? blk : 0, from) * Sh::kScales);
+      to_blk = table[(base + tid) / bt];
+      const int from = __ldcg(kept + base + tid), blk = table[from / bt];
+      if (!good(blk) || !good(to_blk)) atomicOr(a.c.status, kStatusCache);
+      weight = __ldcg(w + from);
 #pragma unroll
-        for (int j = 0; j < Sh::kScales / 2; ++j) u[j] = good(blk) ? p[j] : (uint16_t)0;
-      } else {
-        row_scale[tid] = good(blk) ? scales[(int64_t)blk * a.c.heads + h] : 0.f;
+      for (int side = 0; side < 2; ++side) {
+        if constexpr (Sh::k4) {
+          const uint16_t* p = bytes(side, good(blk) ? blk : 0, from);
+#pragma unroll
+          for (int j = 0; j < Sh::kScales / 2; ++j) u[side][j] = good(blk) ? p[j] : (uint16_t)0;
+        } else {
+          row_scale[side][tid] = good(blk) ? scales(side)[(int64_t)blk * a.c.heads + h] : 0.f;
+        }
       }
     }
     if constexpr (!Sh::k4) {  // the new scales of the rows' blocks
       __syncthreads();
-      for (int j = tid >> 5; j * bt < count; j += kMoveThreads / 32) {
-        float s = 0.f;
-        for (int r = tid & 31; r < bt; r += 32)
-          if (j * bt + r < count) s = fmaxf(s, row_scale[j * bt + r]);
+      for (int j = warp; j * bt < count; j += kWarps) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
-        if ((tid & 31) == 0) new_scale[j] = s;
+        for (int side = 0; side < 2; ++side) {
+          float s = 0.f;
+          for (int r = lane; r < bt; r += 32)
+            if (j * bt + r < count) s = fmaxf(s, row_scale[side][j * bt + r]);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
+          if (lane == 0) new_scale[side][j] = s;
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (ranks > 1) cl.sync();  // all of the batch has been read
-    else __syncthreads();
+    all();  // all of the batch has been read
     if (tid < count) {
-      const int row = base + tid, blk = table[row / bt];
-      if (side == 0) w[row] = weight;
-      if (!good(blk)) {
-        atomicOr(a.c.status, kStatusCache);
-      } else if constexpr (Sh::k4) {
-        uint16_t* p = reinterpret_cast<uint16_t*>(bytes + row_of(blk, row) * Sh::kScales);
+      const int row = base + tid;
+      w[row] = weight;
+      if (good(to_blk)) {
 #pragma unroll
-        for (int j = 0; j < Sh::kScales / 2; ++j) p[j] = u[j];
-      } else if (row % bt == 0) {
-        scales[(int64_t)blk * a.c.heads + h] = new_scale[tid / bt];
-      }
-    }
-#pragma unroll 4
-    for (int x = tid; x < count * Sh::kUnits; x += kMoveThreads) {
-      const int i = x / Sh::kUnits, row = base + i, blk = table[row / bt];
-      if (!good(blk)) continue;  // recorded above
-      uint4 y = reinterpret_cast<const uint4*>(rows)[x];
-      if constexpr (!Sh::k4) {
-        const float s0 = row_scale[i], s1 = new_scale[i / bt];
-        if (s0 != s1) {
-          const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
-          y = make_uint4(code_again<INT8>(y.x, s0, inv), code_again<INT8>(y.y, s0, inv), code_again<INT8>(y.z, s0, inv),
-                         code_again<INT8>(y.w, s0, inv));
+        for (int side = 0; side < 2; ++side) {
+          if constexpr (Sh::k4) {
+            uint16_t* p = bytes(side, to_blk, row);
+#pragma unroll
+            for (int j = 0; j < Sh::kScales / 2; ++j) p[j] = u[side][j];
+          } else if (row % bt == 0) {
+            scales(side)[(int64_t)to_blk * a.c.heads + h] = new_scale[side][tid / bt];
+          }
         }
       }
-      reinterpret_cast<uint4*>(codes + row_of(blk, row) * Sh::kRow)[x % Sh::kUnits] = y;
+    }
+#pragma unroll 2
+    for (int x = tid; x < units; x += kThreads) {
+      const int i = x / Sh::kUnits, row = base + i, blk = table[row / bt];
+      if (!good(blk)) continue;  // recorded above
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        uint4 y = reinterpret_cast<const uint4*>(smem)[side * a.rows * Sh::kUnits + x];
+        if constexpr (!Sh::k4) {
+          const float s0 = row_scale[side][i], s1 = new_scale[side][i / bt];
+          if (s0 != s1) {
+            const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
+            y = make_uint4(code_again<INT8>(y.x, s0, inv), code_again<INT8>(y.y, s0, inv), code_again<INT8>(y.z, s0, inv),
+                           code_again<INT8>(y.w, s0, inv));
+          }
+        }
+        reinterpret_cast<uint4*>(codes(side) + row_of(blk, row) * Sh::kRow)[x % Sh::kUnits] = y;
+      }
     }
     __syncthreads();  // shared memory is free again
   }
@@ -374,24 +380,26 @@ extern "C" zg_status zg_kv_evict(const zg_kv_cache* cache, const int32_t* table,
   uint32_t* status = nullptr;
   if ((st = get_status_ptr(&status)) != ZG_OK) return st;
   const int bhs = B * cache->heads;
-  const EvictArgs a = {{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes), cache->k_scale,
-                        cache->v_scale, cache->n_blocks, cache->heads, cache->block_tokens, max_blocks, table, status},
-                       length, weights, new_length, kept, B, w_tokens, keep, recent};
-  cudaStream_t sm = static_cast<cudaStream_t>(stream);
-  // as many CTAs a head as hold its weights four a thread, and as fit the SMs at once
+  EvictArgs a = {{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes), cache->k_scale,
+                  cache->v_scale, cache->n_blocks, cache->heads, cache->block_tokens, max_blocks, table, status},
+                 length, weights, new_length, kept, w_tokens, keep, recent, 0, 0};
+  // as many CTAs a head as hold its weights four a thread (or its kept rows in a batch), and as fit the SMs at once
   int ranks = 1;
-  while (ranks < kMostRanks && tokens > (int64_t)ranks * 4 * kSelThreads && bhs * ranks * 2 <= sm_count()) ranks *= 2;
-  cudaError_t err = launch_clusters(k_evict_select, dim3(bhs * ranks), ranks, kSelThreads, 0, sm, a);
-  // a batch for all rows where the cluster allows it
-  ranks = 1;
-  while (ranks < kMostRanks && keep > ranks * kRows) ranks *= 2;
+  while (ranks < kMostRanks && (tokens > (int64_t)ranks * 4 * kThreads || keep > ranks * 512) && bhs * ranks * 2 <= sm_count())
+    ranks *= 2;
+  cudaError_t err = cudaSuccess;
   for_dim(cache->dim, [&](auto dv) {
     for_format(cache->format, [&](auto fv) {
-      using Sh = MoveShape<decltype(dv)::value, decltype(fv)::value>;
-      auto kern = k_evict_move<decltype(dv)::value, decltype(fv)::value>;
-      if (err == cudaSuccess && Sh::kSmem > 40 * 1024)
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
-      if (err == cudaSuccess) err = launch_clusters(kern, dim3(ranks, 2, bhs), ranks, kMoveThreads, Sh::kSmem, sm, a);
+      using Sh = EvictShape<decltype(dv)::value, decltype(fv)::value>;
+      auto kern = k_evict<decltype(dv)::value, decltype(fv)::value>;
+      const int64_t share = (keep + ranks - 1) / ranks;
+      a.rows = (int)std::min<int64_t>(Sh::kRows, (share + 127) / 128 * 128);
+      const int64_t per = (tokens + ranks * kThreads - 1) / (ranks * kThreads) + 1;  // weights a thread
+      a.held = (int)std::min<int64_t>(per, kMostSmem / (4 * kThreads));
+      const int smem = std::max(a.held * 4 * kThreads, a.rows * 2 * Sh::kRow);
+      a.held = smem / (4 * kThreads);
+      err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (err == cudaSuccess) err = launch_clusters(kern, dim3(bhs * ranks), ranks, kThreads, smem, static_cast<cudaStream_t>(stream), a);
     });
   });
   return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache eviction launch");

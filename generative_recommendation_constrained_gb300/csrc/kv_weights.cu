@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
       }
       const float had = reinterpret_cast<const float*>(at + Sh::kCodes + Sh::kScales)[lane];
       const int first = key0 + step * kKeys + warp * 32;
-      float sum[2][2] = {};  // keys g and g + 8 of both tiles
+      uint64_t sum2[2][2] = {};  // keys g and g + 8 of both tiles, even and odd rows
 #pragma unroll 1
       for (int n8 = 0; n8 < groups; ++n8) {
         float z[2][4] = {};
@@ -229,22 +229,34 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
         const float4 p = par[n8 * 4 + c];
         const int2 v = sees[n8 * 4 + c];
         const bool masked = __any_sync(0xFFFFFFFFu, min(v.x, v.y) < first + 32);
+        const uint64_t less = pair(-p.y, -p.w);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float f0 = p.x * ks[n], f1 = p.z * ks[n];
-          float e[4] = {exp2_fast(fmaf(z[n][0], f0, -p.y)), exp2_fast(fmaf(z[n][1], f1, -p.w)),
-                        exp2_fast(fmaf(z[n][2], f0, -p.y)), exp2_fast(fmaf(z[n][3], f1, -p.w))};
-          if (masked) {
-            const int key = first + 16 * n + g;
-            if (key >= v.x) e[0] = 0.f;
-            if (key >= v.y) e[1] = 0.f;
-            if (key + 8 >= v.x) e[2] = 0.f;
-            if (key + 8 >= v.y) e[3] = 0.f;
+          const uint64_t f = mul2(pair(p.x, p.z), pair(ks[n], ks[n]));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float e0, e1;
+            unpair(fma2(pair(z[n][2 * i], z[n][2 * i + 1]), f, less), e0, e1);
+            e0 = exp2_fast(e0);
+            e1 = exp2_fast(e1);
+            if (masked) {
+              const int key = first + 16 * n + 8 * i + g;
+              if (key >= v.x) e0 = 0.f;
+              if (key >= v.y) e1 = 0.f;
+            }
+            sum2[n][i] = add2(sum2[n][i], pair(e0, e1));
           }
-          sum[n][0] += e[0] + e[1];
-          sum[n][1] += e[2] + e[3];
         }
       }
+      float sum[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float odd;
+          unpair(sum2[n][i], sum[n][i], odd);
+          sum[n][i] += odd;
+        }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -319,8 +331,9 @@ extern "C" zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* tabl
   a.scale = scale * 1.4426950408889634f;
   a.decay = decay;
   const int64_t units = (tokens + kKeys - 1) / kKeys, M = (int64_t)R * a.G;
-  // several steps a CTA, so that its queries and block numbers are brought in once for them, where steps are many
-  a.steps = (int)std::max<int64_t>(1, std::min<int64_t>(kMostSteps, units * B * cache->heads / (sm_count() * 16)));
+  // several steps a CTA, so that its queries and block numbers are brought in once for them, where steps are many: of
+  // few rows as many as leave 16 CTAs an SM, of many, which take longer to bring in, 4
+  a.steps = (int)std::max<int64_t>(1, std::min<int64_t>(kMostSteps, units * B * cache->heads / (sm_count() * (M > 16 ? 4 : 16))));
   cudaError_t err = cudaSuccess;
   for_dim(cache->dim, [&](auto dv) {
     constexpr int D = decltype(dv)::value;
