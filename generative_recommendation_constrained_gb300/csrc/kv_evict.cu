@@ -28,6 +28,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+static_assert(2 * kThreads == kBins, "two bins a thread");
+constexpr int kHists = 6;
+constexpr int kStrip = 128;              // tokens that a warp looks at at once, four a lane
 constexpr int kMostRanks = 8;            // CTAs of a cluster, at most
 constexpr int kMostSmem = 128 * 1024;    // weights of a CTA, then rows of a batch
 
@@ -37,12 +40,15 @@ struct EvictArgs {
   float* w;
   int32_t *new_length, *kept;
   int32_t w_tokens, keep, recent;
-  int32_t held, rows;  // weights a thread keeps in shared memory; rows of a CTA's share of a batch, whole blocks
+  int32_t bt_log2;     // of a block's tokens
+  int32_t smem;        // bytes before the histograms
+  int32_t held, rows;  // strips that a warp keeps in shared memory; rows of a CTA's share of a batch, whole blocks
 };
 
-// Larger numbers for larger weights; NaN below everything, both zeros the same.
+// Larger numbers for larger weights; NaN (1) below everything, both zeros the
+// same; 0 stands for no token.
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) return 0;
+  if (x != x) return 1;
   const uint32_t u = __float_as_uint(x + 0.f);  // -0 + 0 = 0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
@@ -53,6 +59,13 @@ __device__ __forceinline__ int held(const EvictArgs& a, int b, bool report) {
   if (report) atomicOr(a.c.status, kStatusCache);
   return min(max(n, 0), most);
 }
+
+// The scale bytes of a row, as wide as they are aligned.
+template <int D>
+struct ScaleBytes {
+  using type = std::conditional_t<D == 128, uint2, std::conditional_t<D == 64, uint32_t, uint16_t>>;
+  static constexpr int kCount = Row4<D>::kScales / sizeof(type);
+};
 
 template <int D, int FMT>
 struct EvictShape {
@@ -76,17 +89,21 @@ __device__ __forceinline__ uint32_t code_again(uint32_t w, float s0, float inv) 
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ EvictArgs a) {
   using Sh = EvictShape<D, FMT>;
+  using Bytes = typename ScaleBytes<D>::type;
+  constexpr int kBytes = ScaleBytes<D>::kCount;
   constexpr bool INT8 = FMT == ZG_KV_INT8;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(8) uint32_t hist[3][kBins];  // a pass each, so that none is written while another CTA reads it
+  // a histogram a pass, so that none is written while another CTA reads it; of the first, in which most weights fall into
+  // few bins, one for every fourth lane, of which hist[0] is the sum
+  uint32_t(*hist)[kBins] = reinterpret_cast<uint32_t(*)[kBins]>(smem + a.smem);
   __shared__ uint32_t sums[kWarps], found[3][3];
   __shared__ int mine[2];  // of this CTA's tokens: above the last weight, equal to it
   __shared__ int warp_above[kWarps], warp_equal[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.x / ranks, b = bh / a.c.heads, h = bh % a.c.heads;
-  for (int i = tid; i < 3 * kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < kHists * kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
   auto all = [&]() {  // every thread of the cluster
     if (ranks > 1) cl.sync();
     else __syncthreads();
@@ -105,34 +122,55 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
 
   if (want > 0) {
     // ------------------------------------------------------------- select
-    // this warp's tokens, 32 side by side at a time; a thread's own lie kThreads apart in shared memory
-    uint32_t* mem = reinterpret_cast<uint32_t*>(smem) + tid;
-    const int per = ((m + ranks * kWarps - 1) / (ranks * kWarps) + 31) / 32 * 32;
+    // this warp's tokens, whole strips of them, and its place in shared memory
+    uint32_t* mem = reinterpret_cast<uint32_t*>(smem) + warp * a.held * kStrip;
+    const int per = ((m + ranks * kWarps - 1) / (ranks * kWarps) + kStrip - 1) / kStrip * kStrip;
     const int64_t from = (int64_t)(rank * kWarps + warp) * per;
     const int lo = (int)min((int64_t)m, from), hi = (int)min((int64_t)m, from + per);
-#pragma unroll 8
-    for (int j = 0; j < min(a.held, (hi - lo + 31) / 32); ++j) {
-      const int i = lo + 32 * j + lane;
-      mem[j * kThreads] = i < hi ? order_key(w[i]) : 0;
-    }
-    // f(key, whether it is one, token) for each of the warp's tokens in order, a lane a token, whole warps
-    auto each = [&](auto&& f) {
-#pragma unroll 4
-      for (int j = 0; j < (hi - lo + 31) / 32; ++j) {
-        const int i = lo + 32 * j + lane;
-        f(j < a.held ? mem[j * kThreads] : i < hi ? order_key(w[i]) : 0, i < hi, i);
+    const int strips = (hi - lo + kStrip - 1) / kStrip;
+    auto key_at = [&](int i) -> uint32_t { return i < hi ? order_key(w[i]) : 0; };
+    // they come in sixteen a lane at a time, and are counted by their first bits at once
+    __syncthreads();  // the histograms are zero
+    uint32_t* counts = hist[lane & 3 ? 2 + (lane & 3) : 0];
+    for (int j0 = lane; j0 < (hi - lo); j0 += 16 * 32) {
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = j0 + 32 * k < hi - lo ? w[lo + j0 + 32 * k] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int j = j0 + 32 * k;
+        const uint32_t u = j < hi - lo ? order_key(x[k]) : 0;
+        if (u && j < a.held * kStrip) mem[j] = u;
+        if (u) atomicAdd(&counts[u >> (32 - 11)], 1u);
       }
+    }
+    for (int j = hi - lo + lane; j < min(a.held, strips) * kStrip; j += 32) mem[j] = 0;  // no tokens
+    __syncwarp();
+    // a lane's four neighbours of a strip
+    auto strip = [&](int s) -> uint4 {
+      if (s < a.held) return reinterpret_cast<const uint4*>(mem)[s * 32 + lane];
+      const int i = lo + s * kStrip + 4 * lane;
+      return make_uint4(key_at(i), key_at(i + 1), key_at(i + 2), key_at(i + 3));
     };
     uint32_t key = 0;  // what is known of the last kept weight
     int above = 0;     // weights above what is known of it
     int left = 32;     // bits not known yet
-    __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass < 2 ? 11 : 10, shift = left - bits, bins = 1 << bits;
-      each([&](uint32_t x, bool is, int) {
-        if (is && (pass == 0 || x >> left == key >> left)) atomicAdd(&hist[pass][(x >> shift) & (bins - 1)], 1u);
-      });
+      if (pass == 0) {
+        __syncthreads();
+        for (int i = tid; i < kBins; i += kThreads) hist[0][i] += hist[3][i] + hist[4][i] + hist[5][i];
+      } else {
+#pragma unroll 2
+        for (int s = 0; s < strips; ++s) {
+          const uint4 x4 = strip(s);
+          const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (x[k] >> left == key >> left) atomicAdd(&hist[pass][(x[k] >> shift) & (bins - 1)], 1u);
+        }
+      }
       all();
       // two bins a thread, the largest first; the bin in which the count passes what is wanted
       uint32_t t[2] = {};
@@ -183,10 +221,12 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
     }
     // kept before this warp's tokens: all above the last weight, and of those equal to it the first ones
     int na = 0, ne = 0;
-    each([&](uint32_t x, bool is, int) {
-      na += is && x > key;
-      ne += is && x == key;
-    });
+#pragma unroll 2
+    for (int s = 0; s < strips; ++s) {
+      const uint4 x = strip(s);
+      na += (x.x > key) + (x.y > key) + (x.z > key) + (x.w > key);
+      ne += (x.x == key) + (x.y == key) + (x.z == key) + (x.w == key);
+    }
     na = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)na);
     ne = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)ne);
     if (lane == 0) warp_above[warp] = na, warp_equal[warp] = ne;
@@ -207,27 +247,39 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
     over = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)over);
     equal = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)equal);
     const int ties = want - above;  // kept of those equal
-    each([&](uint32_t x, bool is, int i) {
-      const uint32_t ba = __ballot_sync(0xFFFFFFFFu, is && x > key), be = __ballot_sync(0xFFFFFFFFu, is && x == key),
-                     below = (1u << lane) - 1;
-      const int my_over = over + __popc(ba & below), my_equal = equal + __popc(be & below);
-      if (is && (x > key || (x == key && my_equal < ties))) kept[my_over + min(my_equal, ties)] = i;
-      over += __popc(ba);
-      equal += __popc(be);
-    });
+    const uint32_t below = (1u << lane) - 1;
+    for (int s = 0; s < strips; ++s) {
+      const uint4 x4 = strip(s);
+      const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+      int my_over = over, my_equal = equal;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t ba = __ballot_sync(0xFFFFFFFFu, x[k] > key), be = __ballot_sync(0xFFFFFFFFu, x[k] == key);
+        my_over += __popc(ba & below);
+        my_equal += __popc(be & below);
+        over += __popc(ba);
+        equal += __popc(be);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (x[k] > key || (x[k] == key && my_equal < ties)) kept[my_over + min(my_equal, ties)] = lo + s * kStrip + 4 * lane + k;
+        my_over += x[k] > key;
+        my_equal += x[k] == key;
+      }
+    }
   }
   all();  // the kept numbers are there; nobody reads another's shared memory from here on
 
   // ----------------------------------------------------------------- move
   __shared__ float row_scale[2][Sh::k4 ? 1 : Sh::kRows], new_scale[2][Sh::k4 ? 1 : Sh::kRows / 16];
-  const int bt = a.c.bt;
+  const int bt = a.c.bt, sh = a.bt_log2;
   const int32_t* table = a.c.table + (int64_t)b * a.c.max_blocks;
   auto good = [&](int blk) { return blk >= 0 && blk < a.c.n_blocks; };
-  auto row_of = [&](int blk, int token) -> int64_t { return ((int64_t)blk * a.c.heads + h) * bt + token % bt; };
+  auto row_of = [&](int blk, int token) -> int64_t { return (((int64_t)blk * a.c.heads + h) << sh) + (token & (bt - 1)); };
   auto codes = [&](int side) { return side ? a.c.vc : a.c.kc; };
   auto scales = [&](int side) { return side ? a.c.vs : a.c.ks; };
   auto bytes = [&](int side, int blk, int token) {
-    return reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(scales(side)) + row_of(blk, token) * Sh::kScales);
+    return reinterpret_cast<Bytes*>(reinterpret_cast<uint8_t*>(scales(side)) + row_of(blk, token) * Sh::kScales);
   };
   for (int64_t first = 0; first < a.keep; first += (int64_t)ranks * a.rows) {
     const int64_t r0 = first + (int64_t)rank * a.rows;
@@ -242,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
         from[k] = x < units ? __ldcg(kept + base + x / Sh::kUnits) : -1;
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) blk[k] = from[k] >= 0 ? table[from[k] / bt] : -1;
+      for (int k = 0; k < 4; ++k) blk[k] = from[k] >= 0 ? table[from[k] >> sh] : -1;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int x = x0 + k * kThreads;
@@ -262,19 +314,19 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
     }
     // what is small of a row stays with its thread
     float weight = 0.f;
-    uint16_t u[2][Sh::k4 ? Sh::kScales / 2 : 1];
+    Bytes u[2][Sh::k4 ? kBytes : 1];
     int to_blk = -1;
     if (tid < count) {
-      to_blk = table[(base + tid) / bt];
-      const int from = __ldcg(kept + base + tid), blk = table[from / bt];
+      to_blk = table[(base + tid) >> sh];
+      const int from = __ldcg(kept + base + tid), blk = table[from >> sh];
       if (!good(blk) || !good(to_blk)) atomicOr(a.c.status, kStatusCache);
       weight = __ldcg(w + from);
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
         if constexpr (Sh::k4) {
-          const uint16_t* p = bytes(side, good(blk) ? blk : 0, from);
+          const Bytes* p = bytes(side, good(blk) ? blk : 0, from);
 #pragma unroll
-          for (int j = 0; j < Sh::kScales / 2; ++j) u[side][j] = good(blk) ? p[j] : (uint16_t)0;
+          for (int j = 0; j < kBytes; ++j) u[side][j] = good(blk) ? p[j] : Bytes{};
         } else {
           row_scale[side][tid] = good(blk) ? scales(side)[(int64_t)blk * a.c.heads + h] : 0.f;
         }
@@ -282,12 +334,12 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
     }
     if constexpr (!Sh::k4) {  // the new scales of the rows' blocks
       __syncthreads();
-      for (int j = warp; j * bt < count; j += kWarps) {
+      for (int j = warp; j << sh < count; j += kWarps) {
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
           float s = 0.f;
           for (int r = lane; r < bt; r += 32)
-            if (j * bt + r < count) s = fmaxf(s, row_scale[side][j * bt + r]);
+            if ((j << sh) + r < count) s = fmaxf(s, row_scale[side][(j << sh) + r]);
 #pragma unroll
           for (int o = 16; o; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
           if (lane == 0) new_scale[side][j] = s;
@@ -303,24 +355,24 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
           if constexpr (Sh::k4) {
-            uint16_t* p = bytes(side, to_blk, row);
+            Bytes* p = bytes(side, to_blk, row);
 #pragma unroll
-            for (int j = 0; j < Sh::kScales / 2; ++j) p[j] = u[side][j];
-          } else if (row % bt == 0) {
-            scales(side)[(int64_t)to_blk * a.c.heads + h] = new_scale[side][tid / bt];
+            for (int j = 0; j < kBytes; ++j) p[j] = u[side][j];
+          } else if ((row & (bt - 1)) == 0) {
+            scales(side)[(int64_t)to_blk * a.c.heads + h] = new_scale[side][tid >> sh];
           }
         }
       }
     }
 #pragma unroll 2
     for (int x = tid; x < units; x += kThreads) {
-      const int i = x / Sh::kUnits, row = base + i, blk = table[row / bt];
+      const int i = x / Sh::kUnits, row = base + i, blk = table[row >> sh];
       if (!good(blk)) continue;  // recorded above
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
         uint4 y = reinterpret_cast<const uint4*>(smem)[side * a.rows * Sh::kUnits + x];
         if constexpr (!Sh::k4) {
-          const float s0 = row_scale[side][i], s1 = new_scale[side][i / bt];
+          const float s0 = row_scale[side][i], s1 = new_scale[side][i >> sh];
           if (s0 != s1) {
             const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
             y = make_uint4(code_again<INT8>(y.x, s0, inv), code_again<INT8>(y.y, s0, inv), code_again<INT8>(y.z, s0, inv),
@@ -382,7 +434,8 @@ extern "C" zg_status zg_kv_evict(const zg_kv_cache* cache, const int32_t* table,
   const int bhs = B * cache->heads;
   EvictArgs a = {{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes), cache->k_scale,
                   cache->v_scale, cache->n_blocks, cache->heads, cache->block_tokens, max_blocks, table, status},
-                 length, weights, new_length, kept, w_tokens, keep, recent, 0, 0};
+                 length, weights, new_length, kept, w_tokens, keep, recent, 0, 0, 0, 0};
+  while (1 << a.bt_log2 < cache->block_tokens) ++a.bt_log2;
   // as many CTAs a head as hold its weights four a thread (or its kept rows in a batch), and as fit the SMs at once
   int ranks = 1;
   while (ranks < kMostRanks && (tokens > (int64_t)ranks * 4 * kThreads || keep > ranks * 512) && bhs * ranks * 2 <= sm_count())
@@ -394,12 +447,14 @@ extern "C" zg_status zg_kv_evict(const zg_kv_cache* cache, const int32_t* table,
       auto kern = k_evict<decltype(dv)::value, decltype(fv)::value>;
       const int64_t share = (keep + ranks - 1) / ranks;
       a.rows = (int)std::min<int64_t>(Sh::kRows, (share + 127) / 128 * 128);
-      const int64_t per = (tokens + ranks * kThreads - 1) / (ranks * kThreads) + 1;  // weights a thread
-      a.held = (int)std::min<int64_t>(per, kMostSmem / (4 * kThreads));
-      const int smem = std::max(a.held * 4 * kThreads, a.rows * 2 * Sh::kRow);
-      a.held = smem / (4 * kThreads);
-      err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (err == cudaSuccess) err = launch_clusters(kern, dim3(bhs * ranks), ranks, kThreads, smem, static_cast<cudaStream_t>(stream), a);
+      constexpr int kStripBytes = 4 * kStrip * kWarps;
+      const int64_t strips = (tokens + ranks * kWarps * kStrip - 1) / (ranks * kWarps * kStrip);  // a warp
+      const int smem = std::max((int)std::min<int64_t>(strips * kStripBytes, kMostSmem), a.rows * 2 * Sh::kRow);
+      a.held = smem / kStripBytes;
+      a.smem = smem;
+      const int with = smem + kHists * kBins * 4;
+      err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, with);
+      if (err == cudaSuccess) err = launch_clusters(kern, dim3(bhs * ranks), ranks, kThreads, with, static_cast<cudaStream_t>(stream), a);
     });
   });
   return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache eviction launch");
