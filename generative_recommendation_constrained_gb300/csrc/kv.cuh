@@ -433,10 +433,14 @@ inline int head_chunk(int64_t tokens, int heads, int lanes) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(heads, all / room));
 }
 
-// 4-bit codes (kv_cache4.cu); `chunk` heads a lane group, `nchunk` such chunks a token (a token and side)
+// 4-bit codes (kv_cache4.cu).  The write has CTAs of its own for what is turned (`chunk` heads a lane group, `nchunk`
+// such chunks a token) and for what is only coded, of which a token has append4_plain() units; the read `chunk` heads a
+// lane group, `nchunk` such chunks a (token, side).
+int append4_plain(int heads, bool turned);
 cudaError_t launch_append4(const CacheView& c, int dim, const NormRopeArgs* nr, const zg_rows* k, const zg_rows* v,
                            const zg_rows* q, const zg_rows* q_out, int32_t Hq, const int32_t* start, const int32_t* n_new,
-                           int32_t B, int32_t T, int chunk, int nchunk, cudaStream_t st);
+                           int32_t B, int32_t T, int64_t turn_ctas, int64_t plain_ctas, int chunk, int nchunk,
+                           cudaStream_t st);
 cudaError_t launch_read4(const CacheView& c, int dim, const zg_rows* k_out, const zg_rows* v_out, const int32_t* start,
                          const int32_t* n, int32_t B, int32_t T, int chunk, int nchunk, cudaStream_t st);
 

@@ -526,14 +526,16 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
   if (cache->format == ZG_KV_E2M1) {
     uint32_t* status = nullptr;
     const int64_t tokens = (int64_t)B * T;
-    const int heads = Hq + 2 * cache->heads;
+    const int heads = nr ? Hq + cache->heads : 0;  // turned on the way
     if (tokens > kMostRows) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^40 tokens");
-    const int chunk = head_chunk(tokens, heads, lanes), nchunk = (heads + chunk - 1) / chunk;
-    const int64_t ctas = (tokens * nchunk * lanes + 255) / 256;
-    if (ctas > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^31 CTAs");
+    const int chunk = heads ? head_chunk(tokens, heads, lanes) : 1, nchunk = (heads + chunk - 1) / chunk;
+    const int64_t turn = (tokens * nchunk * lanes + 255) / 256;
+    const int64_t plain = (tokens * append4_plain(cache->heads, nr != nullptr) * lanes + 255) / 256;
+    if (turn + plain > 0x7FFFFFFF) return fail(ZG_ERR_UNSUPPORTED, "zg_kv_append: more than 2^31 CTAs");
     if ((st = get_status_ptr(&status)) != ZG_OK) return st;
     const cudaError_t err = launch_append4(view(cache, table, max_blocks, status), cache->dim, nr ? &na : nullptr, k, v, q,
-                                           q_out, Hq, start, n_new, B, T, chunk, nchunk, static_cast<cudaStream_t>(stream));
+                                           q_out, Hq, start, n_new, B, T, turn, plain, chunk, nchunk,
+                                           static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache append launch");
   }
   const int64_t tokens = (int64_t)B * T, jmax = ((int64_t)T + bt - 2) / bt + 1;

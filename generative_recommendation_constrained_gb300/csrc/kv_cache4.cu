@@ -86,91 +86,61 @@ struct Append4Args {
   Rows<T> k, v, q, qo;
   const int32_t *start, *n_new;
   int32_t B, T_, Hq, chunk, nchunk, has_nr;
+  int32_t turn_ctas, side0, sides, nplain, wide;  // CTAs of what is turned; sides that are not, chunks of kAtOnce heads
   NormRopeArgs nr;
 };
 
-// Where a lane group's codes and scale bytes go: its lane's word and byte of a
-// row, `step` to the next head.
-struct To4 {
-  uint8_t *codes, *scales;
-  int64_t codes_step, scales_step;
+// x / d and x % d, in 32 bits where they fit (a 64-bit division is some hundred instructions).
+struct Quot {
+  int64_t q, r;
 };
-
-// `n` heads of one token to codes, kAhead of them in flight as in turn_heads.
-// With TURN each is normalised and rotated first; a lane then holds parts of
-// two places (m), and the elements go through `row`, the group's place in
-// shared memory, to lanes that hold eight neighbours.
-template <typename T, int D, bool INTER, bool TURN>
-__device__ __forceinline__ void code_heads(const NormRopeArgs& a, const LaneMap& m, const Turn& t, int l, const T* from,
-                                           int64_t from_step, To4 to, int n, int most, T* ring, int step, float* row,
-                                           bool& bad) {
-  from += m.e0;
-  const int d = m.e1 - m.e0;
-  auto fetch = [&](int i) {
-    if (i < n) {
-      T* s = ring + (i % kAhead) * 2 * step;
-      copy4_async(s, from);
-      copy4_async(s + step, from + d);
-    }
-    from += from_step;
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-#pragma unroll
-  for (int i = 0; i < kAhead - 1; ++i) fetch(i);
-  for (int i = 0; i < most; ++i) {
-    fetch(i + kAhead - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-    float x[8] = {};
-    if (i < n) {
-      const T* s = ring + (i % kAhead) * 2 * step;
-      load4(s, x);
-      load4(s + step, x + 4);
-    }
-    if constexpr (TURN) {
-      norm_rotate<D, INTER>(a, t, x);
-      if (!INTER && a.rot) {
-        if (m.used) {
-          store4(row + m.e0, x);
-          store4(row + m.e1, x + 4);
-        }
-        __syncwarp();
-        if (m.used) {
-          load4(row + 8 * l, x);
-          load4(row + 8 * l + 4, x + 4);
-        }
-        __syncwarp();
-      }
-    }
-    uint32_t u;
-    bool odd = false;
-    const uint32_t w = codes8(x, u, odd);
-    if (i < n) {
-      bad |= odd;
-      *reinterpret_cast<uint32_t*>(to.codes) = w;
-      if (!(l & 1)) *to.scales = (uint8_t)u;
-    }
-    to.codes += to.codes_step;
-    to.scales += to.scales_step;
-  }
+__device__ __forceinline__ Quot divide(int64_t x, int64_t d) {
+  if (((x | d) >> 32) == 0) return {(uint32_t)x / (uint32_t)d, (uint32_t)x % (uint32_t)d};
+  return {x / d, x % d};
 }
 
-// One group of lanes a (token, chunk of heads), as in the norm and rotation
-// alone; heads 0 .. Hq - 1 are the queries, then the keys, then the values.
+constexpr int kAtOnce = 4;  // heads that a lane group codes at once
+
+// Eight neighbouring elements of a lane; `wide`: aligned to 16 bytes.
+__device__ __forceinline__ void load8(const float* p, bool, float* x) {
+  load4(p, x);
+  load4(p + 4, x + 4);
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool wide, float* x) {
+  uint4 w;
+  if (wide) {
+    w = *reinterpret_cast<const uint4*>(p);
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 4);
+    w = make_uint4(a.x, a.y, b.x, b.y);
+  }
+  load4(reinterpret_cast<const T*>(&w.x), x);
+  load4(reinterpret_cast<const T*>(&w.z), x + 4);
+}
+
+// CTAs before turn_ctas: one group of lanes a (token, chunk of heads), as in
+// the norm and rotation alone, heads 0 .. Hq - 1 the queries, then the keys;
+// a lane holds parts of two places of a head, so the turned keys go through
+// shared memory to lanes that hold eight neighbours.  The others: what is only
+// coded, a group of lanes a (token, side, four heads), all in flight at once.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(256) k_kv_append4(const __grid_constant__ Append4Args<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
   __shared__ __align__(16) T ring[kAhead * 2 * 256 * 4];
   __shared__ __align__(16) float turned[256 * 8];
   after_predecessor();
-  const int l = threadIdx.x % GS;
-  const int64_t g = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS;
-  const int64_t token = g / a.nchunk;
-  const bool live = token < (int64_t)a.B * a.T_;
-  const int b = live ? (int)(token / a.T_) : 0, t = live ? (int)(token % a.T_) : 0;
-  const int Hk = a.c.heads, h0 = (int)(g % a.nchunk) * a.chunk, h1 = min(h0 + a.chunk, a.Hq + 2 * Hk);
+  const int l = threadIdx.x % GS, Hk = a.c.heads;
+  const bool turns = (int)blockIdx.x < a.turn_ctas;
+  const int64_t tokens = (int64_t)a.B * a.T_;
+  const int64_t g = ((int64_t)(blockIdx.x - (turns ? 0 : a.turn_ctas)) * blockDim.x + threadIdx.x) / GS;
+  // what is turned has its angles once a token; what is not has neighbouring tokens side by side
+  const Quot of = divide(g, turns ? a.nchunk : tokens);
+  const int64_t token = turns ? of.q : of.r, part = turns ? of.r : of.q;
+  const bool live = turns ? token < tokens : part < a.sides * a.nplain;
+  const Quot bt = divide(live ? token : 0, a.T_);
+  const int b = (int)bt.q, t = (int)bt.r;
   const int start = a.start[b], n = a.n_new ? a.n_new[b] : a.T_;
-  T* mine = ring + threadIdx.x * 4;
-
   int blk = -1, row = 0;
   if (start < 0 || n < 0 || n > a.T_ || (int64_t)start + n > (int64_t)a.c.max_blocks * a.c.bt) {
     if (l == 0 && live) atomicOr(a.c.status, kStatusCache);
@@ -183,37 +153,102 @@ __global__ void __launch_bounds__(256) k_kv_append4(const __grid_constant__ Appe
       blk = -1;
     }
   }
+  const bool writes = live && blk >= 0 && l < HeadLanes<D>::kUsed;
+  bool bad = false;
+  // this lane's word and scale byte of a row, and the way to the next head's
+  auto word = [&](int side, int h) -> uint32_t* {
+    return reinterpret_cast<uint32_t*>((side ? a.c.vc : a.c.kc) + (((int64_t)max(blk, 0) * Hk + h) * a.c.bt + row) * Row4<D>::kCodes) + l;
+  };
+  auto byte = [&](int side, int h) -> uint8_t* {
+    return reinterpret_cast<uint8_t*>(side ? a.c.vs : a.c.ks) + (((int64_t)max(blk, 0) * Hk + h) * a.c.bt + row) * Row4<D>::kScales + l / 2;
+  };
+  const int64_t words = (int64_t)a.c.bt * Row4<D>::kCodes / 4, bytes = (int64_t)a.c.bt * Row4<D>::kScales;
+
+  if (!turns) {
+    const int side = a.side0 + (int)(part / a.nplain), h0 = (int)(part % a.nplain) * kAtOnce;
+    const Rows<T>& src = side ? a.v : a.k;
+    const T* from = src.at(b, t, h0) + 8 * l;
+    float x[kAtOnce][8] = {};
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (writes && h0 + i < Hk) load8(from + i * src.sh, a.wide, x[i]);
+    uint32_t* w = word(side, h0);
+    uint8_t* s = byte(side, h0);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      uint32_t u;
+      const uint32_t c = codes8(x[i], u, bad);
+      if (writes && h0 + i < Hk) {
+        w[i * words] = c;
+        if (!(l & 1)) s[i * bytes] = (uint8_t)u;
+      }
+    }
+    if (bad) atomicOr(a.c.status, kStatusNonFinite);
+    return;
+  }
+
+  T* mine = ring + threadIdx.x * 4;
+  const int h0 = (int)part * a.chunk, h1 = min(h0 + a.chunk, a.Hq + (a.has_nr ? Hk : 0));
   const LaneMap m = lane_map<D, INTER>(a.nr, l);
-  const bool on = live && m.used, writes = on && blk >= 0;
   float sn[4], cs[4];
   lane_angles(a.nr, m, l, (int)((uint32_t)start + (uint32_t)t), sn, cs);
   if (a.Hq) {
     const Turn tq = turn_of(sn, cs, lane_gain<INTER>(a.nr.q_gain, m));
     turn_heads<T, D, INTER>(a.nr, m, tq, a.q.at(b, t, h0), a.q.sh, a.qo.at(b, t, h0), a.qo.sh,
-                            on ? min(h1, a.Hq) - h0 : 0, min(a.chunk, a.Hq), mine, 256 * 4);
+                            live && m.used ? min(h1, a.Hq) - h0 : 0, min(a.chunk, a.Hq), mine, 256 * 4);
   }
-  // the first of this chunk's keys (values), and where a row's codes go
-  auto to = [&](uint8_t* codes, float* scales, int h) -> To4 {
-    const int64_t at = ((int64_t)max(blk, 0) * Hk + h) * a.c.bt + row;
-    return {codes + at * Row4<D>::kCodes + 4 * l, reinterpret_cast<uint8_t*>(scales) + at * Row4<D>::kScales + l / 2,
-            (int64_t)a.c.bt * Row4<D>::kCodes, (int64_t)a.c.bt * Row4<D>::kScales};
-  };
-  bool bad = false;
+  // the keys, kAhead of them in flight as in turn_heads
+  const Turn tk = turn_of(sn, cs, lane_gain<INTER>(a.nr.k_gain, m));
+  const int k0 = max(h0 - a.Hq, 0), count = writes ? h1 - a.Hq - k0 : 0;
   float* place = turned + threadIdx.x / GS * (GS * 8);
-  const int most = min(a.chunk, Hk), k0 = max(h0 - a.Hq, 0), k1 = min(h1 - a.Hq, Hk);
-  const int v0 = max(h0 - a.Hq - Hk, 0), v1 = h1 - a.Hq - Hk;
-  const LaneMap plain = {8 * l, 8 * l + 4, m.used, false};
-  const int nk = writes ? k1 - k0 : 0, nv = writes ? v1 - v0 : 0;
-  if (a.has_nr) {
-    const Turn tk = turn_of(sn, cs, lane_gain<INTER>(a.nr.k_gain, m));
-    code_heads<T, D, INTER, true>(a.nr, m, tk, l, a.k.at(b, t, k0), a.k.sh, to(a.c.kc, a.c.ks, k0), nk, most, mine, 256 * 4,
-                                  place, bad);
-  } else {
-    code_heads<T, D, INTER, false>(a.nr, plain, Turn{}, l, a.k.at(b, t, k0), a.k.sh, to(a.c.kc, a.c.ks, k0), nk, most, mine,
-                                   256 * 4, place, bad);
+  const T* from = a.k.at(b, t, k0) + m.e0;
+  const int d = m.e1 - m.e0;
+  uint32_t* w = word(0, k0);
+  uint8_t* s = byte(0, k0);
+  auto fetch = [&](int i) {
+    if (i < count) {
+      T* to = mine + (i % kAhead) * 2 * 256 * 4;
+      copy4_async(to, from);
+      copy4_async(to + 256 * 4, from + d);
+    }
+    from += a.k.sh;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) fetch(i);
+  for (int i = 0; i < min(a.chunk, Hk); ++i) {
+    fetch(i + kAhead - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    float x[8] = {};
+    if (i < count) {
+      const T* at = mine + (i % kAhead) * 2 * 256 * 4;
+      load4(at, x);
+      load4(at + 256 * 4, x + 4);
+    }
+    norm_rotate<D, INTER>(a.nr, tk, x);
+    if (!INTER && a.nr.rot) {
+      if (m.used) {
+        store4(place + m.e0, x);
+        store4(place + m.e1, x + 4);
+      }
+      __syncwarp();
+      if (m.used) {
+        load4(place + 8 * l, x);
+        load4(place + 8 * l + 4, x + 4);
+      }
+      __syncwarp();
+    }
+    uint32_t u;
+    bool odd = false;
+    const uint32_t c = codes8(x, u, odd);
+    if (i < count) {
+      bad |= odd;
+      *w = c;
+      if (!(l & 1)) *s = (uint8_t)u;
+    }
+    w += words;
+    s += bytes;
   }
-  code_heads<T, D, INTER, false>(a.nr, plain, Turn{}, l, a.v.at(b, t, v0), a.v.sh, to(a.c.vc, a.c.vs, v0), nv, most, mine,
-                                 256 * 4, place, bad);
   if (bad) atomicOr(a.c.status, kStatusNonFinite);
 }
 
@@ -292,20 +327,26 @@ __global__ void __launch_bounds__(256) k_kv_read4(const __grid_constant__ Read4A
 
 cudaError_t launch_append4(const CacheView& c, int dim, const NormRopeArgs* nr, const zg_rows* k, const zg_rows* v,
                            const zg_rows* q, const zg_rows* q_out, int32_t Hq, const int32_t* start, const int32_t* n_new,
-                           int32_t B, int32_t T, int chunk, int nchunk, cudaStream_t st) {
+                           int32_t B, int32_t T, int64_t turn_ctas, int64_t plain_ctas, int chunk, int nchunk,
+                           cudaStream_t st) {
   cudaError_t err = cudaSuccess;
-  const int64_t ctas = ((int64_t)B * T * nchunk * group_lanes(dim) + 255) / 256;
+  auto wide = [&](const zg_rows* r) {
+    return reinterpret_cast<uintptr_t>(r->data) % 16 == 0 && (r->stride_b | r->stride_t | r->stride_h) % 8 == 0;
+  };
   for_type(k->dtype, [&](auto e) {
     using E = typename decltype(e)::type;
     const Append4Args<E> a = {c, rows_of<E>(k), rows_of<E>(v), rows_of<E>(q), rows_of<E>(q_out), start, n_new, B, T, Hq,
-                              chunk, nchunk, nr != nullptr, nr ? *nr : NormRopeArgs{}};
+                              chunk, nchunk, nr != nullptr, (int32_t)turn_ctas, nr ? 1 : 0, nr ? 1 : 2,
+                              (c.heads + kAtOnce - 1) / kAtOnce, wide(k) && wide(v), nr ? *nr : NormRopeArgs{}};
     for_dim(dim, [&](auto dv) {
       auto kern = a.nr.inter ? k_kv_append4<E, decltype(dv)::value, true> : k_kv_append4<E, decltype(dv)::value, false>;
-      err = launch_early(kern, ctas, 256, 0, st, a);
+      err = launch_early(kern, turn_ctas + plain_ctas, 256, 0, st, a);
     });
   });
   return err;
 }
+
+int append4_plain(int heads, bool turned) { return (heads + kAtOnce - 1) / kAtOnce * (turned ? 1 : 2); }
 
 cudaError_t launch_read4(const CacheView& c, int dim, const zg_rows* k_out, const zg_rows* v_out, const int32_t* start,
                          const int32_t* n, int32_t B, int32_t T, int chunk, int nchunk, cudaStream_t st) {

@@ -3,16 +3,19 @@
 //
 //   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j)
 //
-// One CTA takes up to 256 query rows (token, query head of the group) of one
-// sequence and key head, as two tiles of 128, through 128 keys a step:
-//   warp 9      brings keys and values in by TMA, as they lie in memory;
-//   warp 8      issues S = Q K^T and O += P V (tcgen05, one thread);
-//   warps 0-7   one thread a row: scores out of tensor memory, running
+// One CTA takes up to 128 query rows (token, query head of the group) of one
+// sequence and key head through 128 keys a step:
+//   one warp    brings keys and values in by TMA, as they lie in memory;
+//   one warp    issues S = Q K^T and O += P V (tcgen05, one thread);
+//   four warps  one thread a row: scores out of tensor memory, running
 //               maximum, p = exp2, rounded to the rows' type back to tensor
 //               memory, in halves of 64 keys so that the product starts early;
-//   warps 10-11 look over the values of tiles that some row does not see whole.
-// Tensor memory holds S and O of both tiles; up to 64 dims P has a place of
-// its own, beyond it lies over S.  The rows of a group's heads share the keys.
+//   two warps   look over the values of tiles that some row does not see whole.
+// Two CTAs share an SM, each with half of its tensor memory, and fill one
+// another's waits, beginnings and ends (one CTA with two tiles an SM: 8 x 4,000
+// rows of 8 heads over 2 take 181 us against 164 at 64 dims, 239 against 228 at
+// 128).  Up to 64 dims P has columns of its own, beyond it lies over S.  The
+// rows of a group's heads share the keys.
 //
 // A weight of 0 times an infinity or a NaN would be a NaN, so values that a row
 // does not see must not meet it: rows of the tile behind the sequence are made
@@ -31,23 +34,24 @@
 namespace zg {
 namespace {
 
-constexpr int kThreads = 384, kNK = 128, kItem = 256;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarps = 2;
-// Registers a thread: 168 at launch, 384 threads; 256 x 224 + 128 x 56 = 384 x 168.
-constexpr int kSoftRegs = 224, kOtherRegs = 56;
+constexpr int kNK = 128, kItem = 128;  // keys a step, query rows a CTA
+constexpr int kMmaWarp = 4, kLoadWarp = 5, kFixWarps = 2, kThreads = 256;
+// Registers a thread: 128 at launch, 256 threads; 128 x 200 + 128 x 56 = 256 x 128.
+constexpr int kSoftRegs = 200, kOtherRegs = 56;
 constexpr uint32_t kSpin = 1u << 20;
-constexpr int kEdges = 4;  // tiles of an item that not all its rows see whole: two at most
+constexpr uint32_t kColumns = 256;  // of tensor memory
+constexpr int kEdges = 4;           // tiles of an item that not all its rows see whole: two at most
 
 template <int D>
 struct PromptShape {
   static constexpr bool kApart = D <= 64;       // P beside S
   static constexpr int kSub = (D + 63) / 64;    // 64-dim subtiles (128-byte rows)
   static constexpr int kTile = kSub * 128 * 128;
-  static constexpr int kRing = kApart ? 8 : 5;  // entries, each the keys or values of a step
-  static constexpr size_t kSmem = (2 + kRing) * kTile + 1024;
-  static constexpr uint32_t kS = 0, kP = kApart ? 256 : 0, kPStep = kApart ? 64 : kNK, kO = 512 - 2 * D;
-  static_assert((kApart ? 256 + 128 : 256) <= kO, "S, P and O fit");
-  static_assert(kSmem <= 225 * 1024, "with the barriers inside 227 KiB");
+  static constexpr int kRing = kApart ? 5 : 2;  // entries, each the keys or values of a step
+  static constexpr size_t kSmem = (1 + kRing) * kTile + 1024;
+  static constexpr uint32_t kP = kApart ? kNK : 0, kO = kColumns - D;  // S in front
+  static_assert((kApart ? kNK + 64 : kNK) <= kO, "S, P and O fit");
+  static_assert(kSmem <= 111 * 1024, "with the barriers inside 227 KiB an SM");
   // Ring entries in the order of their use.  Apart: keys 0, keys 1, values 0, keys 2, values 1, ..., one entry for
   // the keys behind the last step empty.  Else: keys 0, values 0, keys 1, ...
   static __device__ __forceinline__ int entries(int steps) { return kApart && steps ? 2 * steps + 1 : 2 * steps; }
@@ -94,7 +98,7 @@ __device__ __forceinline__ Seq seq_of(const PromptArgs& a, int b, bool report) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     k_prompt(const __grid_constant__ PromptArgs a, const Rows<T> q, const Rows<T> k, const Rows<T> v, const Rows<T> out,
              const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, uint32_t spin) {
   using Sh = PromptShape<D>;
@@ -102,14 +106,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kBf16 = std::is_same<T, __half>::value ? 0u : 1u;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sq = smem;                  // two query tiles
-  uint8_t* ring = sq + 2 * Sh::kTile;  // keys and values
-  // The barriers of a query tile have one phase a step, and none is passed twice before all who wait for it have seen
+  uint8_t* sq = smem;               // the query tile
+  uint8_t* ring = sq + Sh::kTile;  // keys and values
+  // The barriers of the scores have one phase a step, and none is passed twice before all who wait for it have seen
   // it; the fixing warps pass every entry of the ring too, so that none of its barriers leaves them behind.
   __shared__ uint64_t full[kRing], empty[kRing];
-  __shared__ uint64_t q_full, s_full[2], s_free[2], p_full[2][2], o_done[2], fixed[kEdges], drained;
+  __shared__ uint64_t q_full, s_full, s_free, p_full[2], o_done, fixed[kEdges], drained;
   __shared__ uint32_t s_bad[kEdges][4];  // keys of an edge tile whose values are not finite
-  __shared__ int s_count[34];
   __shared__ int2 s_item;  // sequence, tile of rows
   __shared__ uint32_t tmem_base;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -119,108 +122,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&full[i], 1);
       bar_init(&empty[i], 1 + kFixWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&s_full[i], 1);
-      bar_init(&s_free[i], 4);
-      bar_init(&p_full[i][0], 4);
-      bar_init(&p_full[i][1], 4);
-      bar_init(&o_done[i], 1);
-    }
+    bar_init(&s_full, 1);
+    bar_init(&s_free, 4);
+    bar_init(&p_full[0], 4);
+    bar_init(&p_full[1], 4);
+    bar_init(&o_done, 1);
     for (int i = 0; i < kEdges; ++i) bar_init(&fixed[i], kFixWarps);
-    bar_init(&q_full, 8);
+    bar_init(&q_full, 4);
     bar_init(&drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x < 34) s_count[threadIdx.x] = 0;
-  if (threadIdx.x == 0) s_item = make_int2(-1, 0);
-  __syncthreads();
   after_predecessor();
+  if (warp == kMmaWarp) {  // only now: a CTA of the predecessor that waits for tensor memory must not wait for this one
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                 "r"(kColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
 
   // CTAs start in the order of their numbers: those with the most keys before them first.  Item p is the (p - F(m +
   // 1))-th of the sequences with more than m tiles, where F(x) counts the tiles of numbers x and on, and m is the
-  // largest with F(m) > p.
+  // largest with F(m) > p.  One warp looks for it, among the tile counts of all sequences in shared memory (of the
+  // first kCounts; it counts those behind anew each time).
   const int p = blockIdx.x / a.Hk, h = blockIdx.x % a.Hk;
-  {
-    auto tiles_of = [&](int b, bool report) -> int {
-      const Seq s = seq_of(a, b, report);
-      return (int)(((int64_t)s.n * a.G + kItem - 1) / kItem);
-    };
-    const int mine = (int)threadIdx.x < a.B ? tiles_of(threadIdx.x, blockIdx.x == 0) : 0;
-    auto each = [&](auto&& f) {  // tiles of this thread's sequences
-      if ((int)threadIdx.x < a.B) f((int)threadIdx.x, mine);
-      for (int b = threadIdx.x + kThreads; b < a.B; b += kThreads) f(b, tiles_of(b, false));
-    };
-    int slot = 0;
-    auto count = [&](int x) -> int {
+  constexpr int kCounts = Sh::kTile / 4;
+  int* s_tiles = reinterpret_cast<int*>(sq);
+  auto tiles_of = [&](int b, bool report) -> int {
+    const Seq s = seq_of(a, b, report);
+    return (int)(((int64_t)s.n * a.G + kItem - 1) / kItem);
+  };
+  for (int b = threadIdx.x; b < a.B; b += kThreads)
+    if (b < kCounts || blockIdx.x == 0) {
+      const int t = tiles_of(b, blockIdx.x == 0);
+      if (b < kCounts) s_tiles[b] = t;
+    }
+  __syncthreads();
+  if (warp == 0) {
+    auto tiles = [&](int b) { return b < kCounts ? s_tiles[b] : tiles_of(b, false); };
+    auto count = [&](int x) -> int {  // F(x)
       int c = 0;
-      each([&](int, int t) { c += max(0, t - x); });
-      c = __reduce_add_sync(0xFFFFFFFFu, c);
-      if (lane == 0 && c) atomicAdd(&s_count[slot], c);
-      __syncthreads();
-      return s_count[slot++];
+      for (int b = lane; b < a.B; b += 32) c += max(0, tiles(b) - x);
+      return __reduce_add_sync(0xFFFFFFFFu, c);
     };
-    int most = 0;
-    each([&](int, int t) { most = max(most, t); });
+    int most = 0, all = 0;
+    for (int b = lane; b < a.B; b += 32) {
+      most = max(most, tiles(b));
+      all += tiles(b);
+    }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
-    if (lane == 0) atomicMax(&s_count[33], most);
-    __syncthreads();
-    int lo = 0, hi = s_count[33];  // F(lo) > p if any, F(hi) <= p
-    int f_hi = 0;
-    if (count(0) > p) {
+    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    if (lane == 0) s_item = make_int2(-1, 0);
+    __syncwarp();
+    if (all > p) {
+      int lo = 0, hi = most, f_hi = 0;  // F(lo) > p >= F(hi)
       while (hi - lo > 1) {
         const int mid = lo + (hi - lo) / 2, f = count(mid);
         if (f > p) lo = mid;
         else hi = mid, f_hi = f;
       }
-      // the sequence: in blocks of kThreads, by their number of sequences with more than `lo` tiles
-      int rank = p - f_hi;
-      __shared__ int s_warp[kThreads / 32];
-      for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        const bool has = b < a.B && (b0 ? tiles_of(b, false) : mine) > lo;
-        const uint32_t bal = __ballot_sync(0xFFFFFFFFu, has);
-        if (lane == 0) s_warp[warp] = __popc(bal);
-        __syncthreads();
-        int before = 0, all = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-          if (w < warp) before += s_warp[w];
-          all += s_warp[w];
-        }
-        if (has && before + __popc(bal & ((1u << lane) - 1)) == rank) s_item = make_int2(b, lo);
-        __syncthreads();
-        if (rank < all) break;
-        rank -= all;
+      int rank = p - f_hi;  // among the sequences with more than `lo` tiles
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const uint32_t has = __ballot_sync(0xFFFFFFFFu, b0 + lane < a.B && tiles(b0 + lane) > lo);
+        if (((has >> lane) & 1) && __popc(has & ((1u << lane) - 1)) == rank) s_item = make_int2(b0 + lane, lo);
+        rank -= __popc(has);
+        if (rank < 0) break;
       }
     }
-  }
-  const int b = s_item.x, m = s_item.y;
-  if (b < 0) return;  // fewer items than CTAs
-  const Seq s = seq_of(a, b, false);
-  const int row0 = m * kItem, mine = min(s.n * a.G - row0, kItem);  // query rows of this item
-  auto sees = [&](int row) -> int { return a.causal ? row / a.G + 1 : s.n; };
-  // steps of each tile; the second sees no less than the first
-  int steps2[2];
-  for (int i = 0; i < 2; ++i) {
-    const int last = min(mine, 128 * (i + 1)) - 1;
-    steps2[i] = mine > 128 * i ? (sees(row0 + last) + kNK - 1) / kNK : 0;
-  }
-  const int steps = __shfl_sync(0xFFFFFFFFu, max(steps2[0], steps2[1]), 0);
-  const int steps0 = __shfl_sync(0xFFFFFFFFu, steps2[0], 0), steps1 = __shfl_sync(0xFFFFFFFFu, steps2[1], 0);
-  const int edge = sees(row0) / kNK;  // the first tile that not all rows see whole
-
-  if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
   auto give_up = [&]() { atomicOr(a.status, kStatusTimeout); };
+  const int b = s_item.x, m = s_item.y;
+  const Seq s = b < 0 ? Seq{0, 0} : seq_of(a, b, false);  // fewer items than CTAs: nothing to do
+  const int row0 = m * kItem, mine = min((int)min((int64_t)s.n * a.G, (int64_t)0x7FFFFFFF) - row0, kItem);  // query rows
+  auto sees = [&](int row) -> int { return a.causal ? row / a.G + 1 : s.n; };
+  const int steps = __shfl_sync(0xFFFFFFFFu, mine > 0 ? (sees(row0 + mine - 1) + kNK - 1) / kNK : 0, 0);
+  const int edge = sees(row0) / kNK;  // the first tile that not all rows see whole
 
-  if (warp >= 8) {
+  if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kMmaWarp) {
       // ----------------------------------------------------------- products
@@ -228,63 +209,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_s = (1u << 4) | types | ((uint32_t)(kNK >> 3) << 17) | ((128u >> 4) << 24);
       const uint32_t id_o = (1u << 4) | types | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
       const uint64_t q0 = desc_k(smem_u32(sq)), k0 = desc_k(smem_u32(ring)), v0 = desc_mn(smem_u32(ring), kNK * 128);
-      // an entry is there for the first tile that uses it, and free behind the last
-      auto first_of = [&](int t) { return t < steps0 ? 0 : 1; };
-      auto last_of = [&](int t) { return t < steps1 ? 1 : 0; };
-      auto scores = [&](int t, int i) -> bool {
+      auto scores = [&](int t) -> bool {
         const int n = Sh::keys(t), ws = n % kRing;
-        if (i == first_of(t) && !spin_wait(&full[ws], (n / kRing) & 1, spin)) return false;
+        if (!spin_wait(&full[ws], (n / kRing) & 1, spin)) return false;
         // apart: every warp has the last scores in registers; else the product that reads P in their place is over
-        if (t > 0 && !spin_wait(Sh::kApart ? &s_free[i] : &o_done[i], (t - 1) & 1, spin)) return false;
+        if (t > 0 && !spin_wait(Sh::kApart ? &s_free : &o_done, (t - 1) & 1, spin)) return false;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t kd = k0 + ws * (Sh::kTile >> 4), qd = q0 + i * (Sh::kTile >> 4);
+        const uint64_t kd = k0 + ws * (Sh::kTile >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             const uint32_t off = (c / 4) * (128 * 128 >> 4) + (c % 4) * 2;
-            mma_ss(tmem + Sh::kS + (uint32_t)(i * kNK), qd + off, kd + off, id_s, c > 0);
+            mma_ss(tmem, q0 + off, kd + off, id_s, c > 0);
           }
-          commit(&s_full[i]);
-          if (i == last_of(t)) commit(&empty[ws]);
+          commit(&s_full);
+          commit(&empty[ws]);
         }
         __syncwarp();
         return true;
       };
-      auto values = [&](int t, int i) -> bool {
+      auto values = [&](int t) -> bool {
         const int n = Sh::values(t), ws = n % kRing;
-        if (i == first_of(t)) {
-          if (!spin_wait(&full[ws], (n / kRing) & 1, spin)) return false;
-          if (t >= edge && !spin_wait(&fixed[t - edge], 0, spin)) return false;
-        }
+        if (!spin_wait(&full[ws], (n / kRing) & 1, spin)) return false;
+        if (t >= edge && !spin_wait(&fixed[t - edge], 0, spin)) return false;
         const uint64_t vd = v0 + ws * (Sh::kTile >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!spin_wait(&p_full[i][half], t & 1, spin)) return false;
+          if (!spin_wait(&p_full[half], t & 1, spin)) return false;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
 #pragma unroll
             for (int j = half * 4; j < half * 4 + 4; ++j)
-              mma_ts(tmem + Sh::kO + (uint32_t)(i * D), tmem + Sh::kP + i * Sh::kPStep + (uint32_t)(j * 8),
-                     vd + j * (2048 >> 4), id_o, (t > 0 || j > 0) ? 1u : 0u);
+              mma_ts(tmem + Sh::kO, tmem + Sh::kP + (uint32_t)(j * 8), vd + j * (2048 >> 4), id_o, (t > 0 || j > 0) ? 1u : 0u);
             if (half) {
-              commit(&o_done[i]);
-              if (i == last_of(t)) commit(&empty[ws]);
+              commit(&o_done);
+              commit(&empty[ws]);
             }
           }
           __syncwarp();
         }
         return true;
       };
-      auto in = [&](int t, int i) { return t < (i ? steps1 : steps0); };
-      bool good = spin_wait(&q_full, 0, spin);
-      for (int i = 0; i < 2 && good; ++i) good = !in(0, i) || scores(0, i);
+      bool good = spin_wait(&q_full, 0, spin) && (steps == 0 || scores(0));
       for (int t = 0; t < steps && good; ++t) {
-        if constexpr (Sh::kApart)
-          for (int i = 0; i < 2 && good; ++i) good = !in(t + 1, i) || scores(t + 1, i);
-        for (int i = 0; i < 2 && good; ++i) {
-          good = !in(t, i) || values(t, i);
-          if (!Sh::kApart && good) good = !in(t + 1, i) || scores(t + 1, i);
-        }
+        const bool more = t + 1 < steps;
+        if constexpr (Sh::kApart) good = (!more || scores(t + 1)) && values(t);
+        else good = values(t) && (!more || scores(t + 1));
       }
       if (!good && lane == 0) give_up();
       if (elect_one()) commit(&drained);
@@ -355,12 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // -------------------------------------------------------------- softmax
-    const int i = warp >> 2, r = threadIdx.x & 127;  // tile, row of the tile
-    const int ri = row0 + threadIdx.x;               // row of the sequence
+    const int r = threadIdx.x, ri = row0 + r;  // row of the tile, of the sequence
     const bool live = (int)threadIdx.x < mine;
     const int token = live ? ri / a.G : 0, qh = h * a.G + (live ? ri % a.G : 0);
     const int vis = live ? sees(ri) : 0;
-    const int turns = i ? steps1 : steps0;
     // lanes of a row when a warp moves its 32 rows: four elements each, kAt rows at a time
     constexpr int kLanes = D / 4, kSlot = D == 96 ? 32 : kLanes, kAt = 32 / kSlot;
     const int l4 = lane % kSlot, e = 4 * l4;
@@ -369,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the warp's 32 rows into its query tile: a group of lanes a row, four elements a lane; where a row is comes from
       // the lane that it belongs to
       const int64_t q_row = (int64_t)(s.first + token) * q.st + qh * q.sh;
-      uint8_t* tile = sq + i * Sh::kTile + (e / 64) * (128 * 128) + (e & 4) * 2;
+      uint8_t* tile = sq + (e / 64) * (128 * 128) + (e & 4) * 2;
       uint2 w[32 / kAt];  // every load in flight before the first is used
 #pragma unroll
       for (int c = 0; c < 32 / kAt; ++c) {
@@ -380,22 +348,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int c = 0; c < 32 / kAt; ++c) {
-        const int rr = (warp & 3) * 32 + c * kAt + lane / kSlot;  // row of the tile
+        const int rr = warp * 32 + c * kAt + lane / kSlot;  // row of the tile
         if (l4 < kLanes) *reinterpret_cast<uint2*>(tile + rr * 128 + ((((e % 64) / 8) ^ (rr & 7)) << 4)) = w[c];
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive(&q_full);
     }
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + Sh::kS + (uint32_t)(i * kNK) + lanes;
-    const uint32_t p_at = tmem + Sh::kP + i * Sh::kPStep + lanes;
-    const uint32_t o_at = tmem + Sh::kO + (uint32_t)(i * D) + lanes;
+    const uint32_t s_at = tmem + ((uint32_t)(warp * 32) << 16), p_at = s_at + Sh::kP, o_at = s_at + Sh::kO;
     const float f = a.scale;
     float mx = -INFINITY, l = 0.f;
     bool good = true;
-    for (int t = 0; t < turns; ++t) {
-      if (!warp_wait(&s_full[i], t & 1, spin)) {
+    for (int t = 0; t < steps; ++t) {
+      if (!warp_wait(&s_full, t & 1, spin)) {
         good = false;
         break;
       }
@@ -405,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (Sh::kApart) {
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) bar_arrive(&s_free[i]);
+        if (lane == 0) bar_arrive(&s_free);
       }
       float* z = reinterpret_cast<float*>(sr);
       const int left = vis - t * kNK;  // keys of this step that the row sees
@@ -441,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the product of the last step has read its probabilities, and is in the sums (with P over S the scores have
       // waited for it)
       if (Sh::kApart && t > 0) {
-        if (!warp_wait(&o_done[i], (t - 1) & 1, spin)) {
+        if (!warp_wait(&o_done, (t - 1) & 1, spin)) {
           good = false;
           break;
         }
@@ -475,26 +440,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_store_wait();
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
-          if (lane == 0) bar_arrive(&p_full[i][c >> 1]);
+          if (lane == 0) bar_arrive(&p_full[c >> 1]);
         }
       }
       float s0, s1;
       unpair(add2(sum[0], sum[1]), s0, s1);
       l += s0 + s1;
     }
-    if (good && turns > 0) good = warp_wait(&o_done[i], (turns - 1) & 1, spin);
+    if (good && steps > 0) good = warp_wait(&o_done, (steps - 1) & 1, spin);
     // what the fixing warps have left out
     bool bad = false;
     if (a.causal && good)
-      for (int t = edge; t < turns; ++t) {
+      for (int t = edge; t < steps; ++t) {
         good = good && warp_wait(&fixed[t - edge], 0, spin);
         for (int w = 0; w < 4 && good; ++w) bad |= s_bad[t - edge][w] != 0;
       }
     if (!good && lane == 0) give_up();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (good && turns > 0) {
+    if (good && steps > 0) {
       const float inv = 1.f / l;
-      uint8_t* tile = sq + i * Sh::kTile;  // every product that reads the queries is complete
+      uint8_t* tile = sq;  // every product that reads the queries is complete
 #pragma unroll
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
@@ -503,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] *= inv;
         if (bad && live) {
-          for (int t = edge; t < turns; ++t)
+          for (int t = edge; t < steps; ++t)
             for (int key = t * kNK; key < min((t + 1) * kNK, vis); ++key) {
               if (!((s_bad[t - edge][(key % kNK) / 32] >> (key % 32)) & 1)) continue;
               const T* qr = q.data + (int64_t)(s.first + token) * q.st + qh * q.sh;
@@ -527,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
 #pragma unroll 8
       for (int c = 0; c < 32 / kAt; ++c) {
-        const int rw = c * kAt + lane / kSlot, rr = (warp & 3) * 32 + rw;
+        const int rw = c * kAt + lane / kSlot, rr = warp * 32 + rw;
         const int64_t at = __shfl_sync(0xFFFFFFFFu, out_row, rw);
         if (((some >> rw) & 1) && l4 < kLanes)
           *reinterpret_cast<uint2*>(out.data + at + e) = *reinterpret_cast<const uint2*>(
@@ -540,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kColumns) : "memory");
   }
 }
 
@@ -599,7 +564,7 @@ extern "C" zg_status zg_prompt_attention(const zg_rows* q, const zg_rows* k, con
   }
   if (!starts || reinterpret_cast<uintptr_t>(starts) % 4) return bad_arg(call, "starts is NULL or not 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(lse) % 4) return bad_arg(call, "lse must be 4-byte aligned");
-  // items of 256 rows at most: a part-filled one a sequence beside the full ones
+  // items of 128 rows at most: a part-filled one a sequence beside the full ones
   const int64_t G = Hq / Hk, items = (int64_t)T * G / kItem + std::min<int64_t>(B, (int64_t)T);
   if (items * Hk > 0x7FFFFFFF || (int64_t)B > 0x7FFFFFFF - kThreads)
     return fail(ZG_ERR_UNSUPPORTED, "zg_prompt_attention: more than 2^31 CTAs");
