@@ -74,8 +74,12 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, i
 // (85 MB) 26 us, some 6 of them the chain from the lengths to the first codes.
 constexpr uint32_t kFewSpin = 1u << 20;  // polls of a wait at most
 
+// CTAs an SM.
+template <int FMT, int NT>
+constexpr int kFewResident = NT == 2 ? 2 : FMT == ZG_KV_E2M1 ? 4 : 3;
+
 template <typename T, int D, int FMT, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const __grid_constant__ AttnArgs a,
+__global__ void __launch_bounds__(kFewThreads, kFewResident<FMT, NT>) k_attn_few(const __grid_constant__ AttnArgs a,
                                                                                 const Rows<T> q, const Rows<T> out,
                                                                                 uint32_t spin) {
   using Tl = Tile16<D>;
@@ -179,35 +183,39 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       if (lane == 0) atomicOr(a.status, kStatusCache);
       return -1;
     };
-    // the tiles of step t into the warp's next slot: lanes 0-3 a copy each, (half, side)
+    // the tiles of step t into the warp's next slot: lanes 0-3 a copy each, (half, side); scale bytes by small copies of
+    // all lanes, which wait for their own (as bulk copies of 128 bytes beside those of 1,024: lifelong 91 us)
     uint8_t* mine = ring + warp * (2 * 4 * kBytes);
     auto fetch = [&](int t, int b0, int b1) {
-      if (t >= t1) return;
-      const uint32_t bar = smem_u32(&full[warp][issued & 1]);
-      const int blk = lane & 1 ? b1 : b0, key = t * 32 + (lane & 1) * 16;
-      const uint32_t bytes = ((b0 >= 0) + (b1 >= 0)) * 2 * kBytes;
-      if (lane == 0)
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-      __syncwarp();
-      if (lane < (k4 ? 8 : 4) && blk >= 0) {
-        const int64_t row = ((int64_t)blk * a.heads + h) * a.bt + (key & (a.bt - 1));
-        uint8_t* to = mine + ((issued & 1) * 4 + (lane & 3)) * kBytes;
-        const uint8_t* from = lane & 2 ? a.vc : a.kc;
-        int64_t at = row * D;
-        uint32_t n = Tl::kBytes;
-        if constexpr (k4) {  // lanes 4-7: the scale bytes
-          const bool s = lane >= 4;
-          at = row * (s ? Row4<D>::kScales : Row4<D>::kCodes);
-          n = 16 * (s ? Row4<D>::kScales : Row4<D>::kCodes);
-          if (s) from = lane & 2 ? a.vg : a.kg, to += Tl4::kCodes;
+      if (t < t1) {
+        const uint32_t bar = smem_u32(&full[warp][issued & 1]);
+        constexpr uint32_t n = k4 ? (uint32_t)Tl4::kCodes : (uint32_t)Tl::kBytes;
+        const uint32_t bytes = ((b0 >= 0) + (b1 >= 0)) * 2 * n;
+        auto row_of = [&](int half) -> int64_t {
+          return ((int64_t)(half ? b1 : b0) * a.heads + h) * a.bt + ((t * 32 + half * 16) & (a.bt - 1));
+        };
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+        __syncwarp();
+        uint8_t* slot = mine + (issued & 1) * 4 * kBytes;
+        if (lane < 4 && (lane & 1 ? b1 : b0) >= 0)
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  smem_u32(slot + lane * kBytes)),
+              "l"((lane & 2 ? a.vc : a.kc) + row_of(lane & 1) * (k4 ? Row4<D>::kCodes : D)), "r"(n), "r"(bar)
+              : "memory");
+        if constexpr (k4) {
+          constexpr int P = Row4<D>::kScales;  // pieces of 16 bytes a tile
+          const int of = lane / P, half = of & 1;
+          if (of < 4 && (half ? b1 : b0) >= 0)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             smem_u32(slot + of * kBytes + Tl4::kCodes + lane % P * 16)),
+                         "l"((of & 2 ? a.vg : a.kg) + row_of(half) * P + lane % P * 16)
+                         : "memory");
         }
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                smem_u32(to)),
-            "l"(from + at), "r"(n), "r"(bar)
-            : "memory");
+        ++issued;
       }
-      ++issued;
+      if constexpr (k4) asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto scales = [&](int blk, float& ks, float& vs) {
       ks = vs = 1.f;  // of 4-bit codes, whose scales are in the halves already
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
     scales(b0, ks[0], vs[0]);
     scales(b1, ks[1], vs[1]);
     bool ok0 = b0 >= 0, ok1 = b1 >= 0;
-    const bool small = small_scale(vs[0]);
+    const bool small = !k4 && small_scale(vs[0]);
     float last_lv = kNoScale;
     b0 = block_of(t0 + 4, 0), b1 = block_of(t0 + 4, 1);
 
@@ -291,10 +299,14 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
       const uint8_t* tiles = mine + (taken & 1) * 4 * kBytes;
       good = warp_wait(&full[warp][taken & 1], (taken >> 1) & 1, spin);
       if (!good) break;
+      if constexpr (k4) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+      }
       ++taken;
       const int key0 = t * 32;
       float z[2][NT][4], lv[2], iv[2];
-      if (last_lv == kNoScale) last_lv = scale_log2(vs[0], scale_log2(vs[1], kNoScale));
+      if (!k4 && last_lv == kNoScale) last_lv = scale_log2(vs[0], scale_log2(vs[1], kNoScale));
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -328,15 +340,19 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
             for (int n = 0; n < NT; ++n) mma_16816(z[half][n], ka, qb[n][w][0], qb[n][w][1]);
           }
         }
-        last_lv = lv[half] = scale_log2(vs[half], last_lv);
-        iv[half] = sum_weight(lv[half], small);
+        if constexpr (k4) {  // scales of 1
+          lv[half] = 0.f, iv[half] = 1.f;
+        } else {
+          last_lv = lv[half] = scale_log2(vs[half], last_lv);
+          iv[half] = sum_weight(lv[half], small);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float f = fz[n][e] * ks[half];
-            z[half][n][e] = fmaf(z[half][n][e], f, lv[half]);
-            z[half][n][2 + e] = fmaf(z[half][n][2 + e], f, lv[half]);
+            const float f = k4 ? fz[n][e] : fz[n][e] * ks[half];
+            z[half][n][e] = k4 ? z[half][n][e] * f : fmaf(z[half][n][e], f, lv[half]);
+            z[half][n][2 + e] = k4 ? z[half][n][2 + e] * f : fmaf(z[half][n][2 + e], f, lv[half]);
           }
       }
       // keys that a row does not see, and tiles that are not there
@@ -382,7 +398,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
             const float mu = mx[n][e] == -INFINITY ? 0.f : mx[n][e];
             p[e] = exp2_fast(z[half][n][e] - mu);
             p[2 + e] = exp2_fast(z[half][n][2 + e] - mu);
-            l[n][e] = fmaf(p[e] + p[2 + e], iv[half], l[n][e]);
+            l[n][e] = k4 ? l[n][e] + (p[e] + p[2 + e]) : fmaf(p[e] + p[2 + e], iv[half], l[n][e]);
           }
           pb[half][n][0] = transpose8(pack_half2(p[0], p[1]));  // (key, rows) -> (row, keys)
           pb[half][n][1] = transpose8(pack_half2(p[2], p[3]));
@@ -446,6 +462,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) k_attn_few(const
     if (!good) {  // a copy has not come: recorded; what is still on its way lands before the CTA ends
       if (lane == 0) atomicOr(a.status, kStatusTimeout);
       for (; taken < issued; ++taken) warp_wait(&full[warp][taken & 1], (taken >> 1) & 1, kFewSpin);
+      if constexpr (k4) asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncthreads();  // the sums take the ring's place
     // join the warps: accumulator tile j, element (e, row g or g + 8) is row 2c + e, dim g * D/8 + 2 j (+ 1) (4 bits: value_dim(j, g))
@@ -660,7 +677,8 @@ AttnPlan attn_plan(const zg_kv_cache* c, int max_blocks, int B, int R, int Hq) {
     p.splits = (int)((keys + p.chunk - 1) / p.chunk);
     p.slots = p.splits > 1 ? p.items * p.splits : 0;
   } else {
-    const int resident = p.tile == 16 ? 2 : 3;
+    const int resident = p.tile == 16 ? kFewResident<ZG_KV_E4M3, 2>
+                                      : c->format == ZG_KV_E2M1 ? kFewResident<ZG_KV_E2M1, 1> : kFewResident<ZG_KV_E4M3, 1>;
     p.ctas = (int)std::min<int64_t>((int64_t)sm_count() * resident, p.items * ((keys + 127) / 128));
     p.slots = p.ctas > 1 && keys > 128 ? 2 * (int64_t)p.ctas : 0;
   }

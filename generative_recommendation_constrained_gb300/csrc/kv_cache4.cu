@@ -85,7 +85,7 @@ struct Append4Args {
   CacheView c;
   Rows<T> k, v, q, qo;
   const int32_t *start, *n_new;
-  int32_t B, T_, Hq, chunk, nchunk, has_nr;
+  int32_t B, T_, Hq, chunk, nchunk;
   int32_t turn_ctas, side0, sides, nplain, wide;  // CTAs of what is turned; sides that are not, chunks of kAtOnce heads
   NormRopeArgs nr;
 };
@@ -101,29 +101,110 @@ __device__ __forceinline__ Quot divide(int64_t x, int64_t d) {
 
 constexpr int kAtOnce = 4;  // heads that a lane group codes at once
 
-// Eight neighbouring elements of a lane; `wide`: aligned to 16 bytes.
-__device__ __forceinline__ void load8(const float* p, bool, float* x) {
-  load4(p, x);
-  load4(p + 4, x + 4);
-}
+// Eight neighbouring elements of a lane as they lie in memory; `wide`: those of
+// 16 bits are aligned to 16 bytes.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool wide, float* x) {
+struct Raw8 {
   uint4 w;
-  if (wide) {
-    w = *reinterpret_cast<const uint4*>(p);
-  } else {
-    const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 4);
-    w = make_uint4(a.x, a.y, b.x, b.y);
+  __device__ __forceinline__ void load(const T* p, bool wide) {
+    if (wide) {
+      w = *reinterpret_cast<const uint4*>(p);
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 4);
+      w = make_uint4(a.x, a.y, b.x, b.y);
+    }
   }
-  load4(reinterpret_cast<const T*>(&w.x), x);
-  load4(reinterpret_cast<const T*>(&w.z), x + 4);
+  __device__ __forceinline__ void get(float* x) const {
+    load4(reinterpret_cast<const T*>(&w.x), x);
+    load4(reinterpret_cast<const T*>(&w.z), x + 4);
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, bool) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+
+// Where token t of request b goes: its block (-1: nowhere, recorded) and row.
+struct Place {
+  int blk, row;
+};
+__device__ __forceinline__ Place place_of(const CacheView& c, int b, int t, int T, int start, int n, bool live, bool report) {
+  Place p = {-1, 0};
+  if (start < 0 || n < 0 || n > T || (int64_t)start + n > (int64_t)c.max_blocks * c.bt) {
+    if (report && live) atomicOr(c.status, kStatusCache);
+  } else if (live && t < n) {
+    const uint32_t at = (uint32_t)start + t;
+    p.row = at % c.bt;
+    p.blk = c.table[(int64_t)b * c.max_blocks + at / c.bt];
+    if (p.blk < 0 || p.blk >= c.n_blocks) {
+      if (report) atomicOr(c.status, kStatusCache);
+      p.blk = -1;
+    }
+  }
+  return p;
 }
 
-// CTAs before turn_ctas: one group of lanes a (token, chunk of heads), as in
-// the norm and rotation alone, heads 0 .. Hq - 1 the queries, then the keys;
-// a lane holds parts of two places of a head, so the turned keys go through
-// shared memory to lanes that hold eight neighbours.  The others: what is only
-// coded, a group of lanes a (token, side, four heads), all in flight at once.
+// What is only coded: a group of lanes a (token, side, four heads), neighbouring
+// tokens side by side.  The rows are asked for before the place they go to is
+// known.
+template <typename T, int D>
+__device__ __forceinline__ void code_plain(const Append4Args<T>& a, int64_t g, int l) {
+  const int64_t tokens = (int64_t)a.B * a.T_;
+  const Quot of = divide(g, tokens);
+  const bool live = of.q < a.sides * a.nplain;
+  const Quot bt = divide(live ? of.r : 0, a.T_);
+  const int b = (int)bt.q, t = (int)bt.r, part = live ? (int)of.q : 0, Hk = a.c.heads;
+  const int side = a.side0 + part / a.nplain, h0 = part % a.nplain * kAtOnce;
+  const int start = a.start[b], n = a.n_new ? a.n_new[b] : a.T_;
+  const bool mine = live && t < n && l < HeadLanes<D>::kUsed;
+  const Rows<T>& src = side ? a.v : a.k;
+  const T* from = src.at(b, t, h0) + 8 * l;
+  Raw8<T> raw[kAtOnce];
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i)
+    if (mine && h0 + i < Hk) raw[i].load(from + i * src.sh, a.wide);
+  const Place to = place_of(a.c, b, t, a.T_, start, n, live, l == 0);
+  const int64_t at = ((int64_t)max(to.blk, 0) * Hk + h0) * a.c.bt + to.row;
+  uint32_t* w = reinterpret_cast<uint32_t*>((side ? a.c.vc : a.c.kc) + at * Row4<D>::kCodes) + l;
+  uint8_t* s = reinterpret_cast<uint8_t*>(side ? a.c.vs : a.c.ks) + at * Row4<D>::kScales + l / 2;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    const bool writes = mine && to.blk >= 0 && h0 + i < Hk;
+    float x[8] = {};
+    if (writes) raw[i].get(x);
+    uint32_t u;
+    const uint32_t c = codes8(x, u, bad);
+    if (writes) {
+      *w = c;
+      if (!(l & 1)) *s = (uint8_t)u;
+    }
+    w += a.c.bt * (Row4<D>::kCodes / 4);
+    s += a.c.bt * Row4<D>::kScales;
+  }
+  if (bad) atomicOr(a.c.status, kStatusNonFinite);
+}
+
+// A write of rows that are turned already, or not to be.
+template <typename T, int D>
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 4 : 5) k_kv_code4(const __grid_constant__ Append4Args<T> a) {
+  constexpr int GS = HeadLanes<D>::kGroup;
+  after_predecessor();
+  code_plain<T, D>(a, ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS, threadIdx.x % GS);
+}
+
+// A write that turns the keys.  CTAs before turn_ctas: one group of lanes a
+// (token, chunk of heads), as in the norm and rotation alone, heads 0 .. Hq - 1
+// the queries, then the keys; a lane holds parts of two places of a head, so
+// the turned keys go through shared memory to lanes that hold eight
+// neighbours.  The others code the values.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(256) k_kv_append4(const __grid_constant__ Append4Args<T> a) {
   constexpr int GS = HeadLanes<D>::kGroup;
@@ -131,64 +212,20 @@ __global__ void __launch_bounds__(256) k_kv_append4(const __grid_constant__ Appe
   __shared__ __align__(16) float turned[256 * 8];
   after_predecessor();
   const int l = threadIdx.x % GS, Hk = a.c.heads;
-  const bool turns = (int)blockIdx.x < a.turn_ctas;
-  const int64_t tokens = (int64_t)a.B * a.T_;
-  const int64_t g = ((int64_t)(blockIdx.x - (turns ? 0 : a.turn_ctas)) * blockDim.x + threadIdx.x) / GS;
-  // what is turned has its angles once a token; what is not has neighbouring tokens side by side
-  const Quot of = divide(g, turns ? a.nchunk : tokens);
-  const int64_t token = turns ? of.q : of.r, part = turns ? of.r : of.q;
-  const bool live = turns ? token < tokens : part < a.sides * a.nplain;
-  const Quot bt = divide(live ? token : 0, a.T_);
-  const int b = (int)bt.q, t = (int)bt.r;
-  const int start = a.start[b], n = a.n_new ? a.n_new[b] : a.T_;
-  int blk = -1, row = 0;
-  if (start < 0 || n < 0 || n > a.T_ || (int64_t)start + n > (int64_t)a.c.max_blocks * a.c.bt) {
-    if (l == 0 && live) atomicOr(a.c.status, kStatusCache);
-  } else if (live && t < n) {
-    const uint32_t p = (uint32_t)start + t;
-    row = p % a.c.bt;
-    blk = a.c.table[(int64_t)b * a.c.max_blocks + p / a.c.bt];
-    if (blk < 0 || blk >= a.c.n_blocks) {
-      if (l == 0) atomicOr(a.c.status, kStatusCache);
-      blk = -1;
-    }
-  }
-  const bool writes = live && blk >= 0 && l < HeadLanes<D>::kUsed;
-  bool bad = false;
-  // this lane's word and scale byte of a row, and the way to the next head's
-  auto word = [&](int side, int h) -> uint32_t* {
-    return reinterpret_cast<uint32_t*>((side ? a.c.vc : a.c.kc) + (((int64_t)max(blk, 0) * Hk + h) * a.c.bt + row) * Row4<D>::kCodes) + l;
-  };
-  auto byte = [&](int side, int h) -> uint8_t* {
-    return reinterpret_cast<uint8_t*>(side ? a.c.vs : a.c.ks) + (((int64_t)max(blk, 0) * Hk + h) * a.c.bt + row) * Row4<D>::kScales + l / 2;
-  };
-  const int64_t words = (int64_t)a.c.bt * Row4<D>::kCodes / 4, bytes = (int64_t)a.c.bt * Row4<D>::kScales;
-
-  if (!turns) {
-    const int side = a.side0 + (int)(part / a.nplain), h0 = (int)(part % a.nplain) * kAtOnce;
-    const Rows<T>& src = side ? a.v : a.k;
-    const T* from = src.at(b, t, h0) + 8 * l;
-    float x[kAtOnce][8] = {};
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-      if (writes && h0 + i < Hk) load8(from + i * src.sh, a.wide, x[i]);
-    uint32_t* w = word(side, h0);
-    uint8_t* s = byte(side, h0);
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      uint32_t u;
-      const uint32_t c = codes8(x[i], u, bad);
-      if (writes && h0 + i < Hk) {
-        w[i * words] = c;
-        if (!(l & 1)) s[i * bytes] = (uint8_t)u;
-      }
-    }
-    if (bad) atomicOr(a.c.status, kStatusNonFinite);
+  if ((int)blockIdx.x >= a.turn_ctas) {
+    code_plain<T, D>(a, ((int64_t)(blockIdx.x - a.turn_ctas) * blockDim.x + threadIdx.x) / GS, l);
     return;
   }
-
+  const Quot of = divide(((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GS, a.nchunk);
+  const bool live = of.q < (int64_t)a.B * a.T_;
+  const Quot bt = divide(live ? of.q : 0, a.T_);
+  const int b = (int)bt.q, t = (int)bt.r, part = (int)of.r;
+  const int start = a.start[b], n = a.n_new ? a.n_new[b] : a.T_;
+  const Place to = place_of(a.c, b, t, a.T_, start, n, live, l == 0);
+  const bool writes = live && to.blk >= 0 && l < HeadLanes<D>::kUsed;
+  bool bad = false;
   T* mine = ring + threadIdx.x * 4;
-  const int h0 = (int)part * a.chunk, h1 = min(h0 + a.chunk, a.Hq + (a.has_nr ? Hk : 0));
+  const int h0 = part * a.chunk, h1 = min(h0 + a.chunk, a.Hq + Hk);
   const LaneMap m = lane_map<D, INTER>(a.nr, l);
   float sn[4], cs[4];
   lane_angles(a.nr, m, l, (int)((uint32_t)start + (uint32_t)t), sn, cs);
@@ -203,13 +240,14 @@ __global__ void __launch_bounds__(256) k_kv_append4(const __grid_constant__ Appe
   float* place = turned + threadIdx.x / GS * (GS * 8);
   const T* from = a.k.at(b, t, k0) + m.e0;
   const int d = m.e1 - m.e0;
-  uint32_t* w = word(0, k0);
-  uint8_t* s = byte(0, k0);
+  const int64_t at = ((int64_t)max(to.blk, 0) * Hk + k0) * a.c.bt + to.row;
+  uint32_t* w = reinterpret_cast<uint32_t*>(a.c.kc + at * Row4<D>::kCodes) + l;
+  uint8_t* s = reinterpret_cast<uint8_t*>(a.c.ks) + at * Row4<D>::kScales + l / 2;
   auto fetch = [&](int i) {
     if (i < count) {
-      T* to = mine + (i % kAhead) * 2 * 256 * 4;
-      copy4_async(to, from);
-      copy4_async(to + 256 * 4, from + d);
+      T* held = mine + (i % kAhead) * 2 * 256 * 4;
+      copy4_async(held, from);
+      copy4_async(held + 256 * 4, from + d);
     }
     from += a.k.sh;
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -221,9 +259,9 @@ __global__ void __launch_bounds__(256) k_kv_append4(const __grid_constant__ Appe
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
     float x[8] = {};
     if (i < count) {
-      const T* at = mine + (i % kAhead) * 2 * 256 * 4;
-      load4(at, x);
-      load4(at + 256 * 4, x + 4);
+      const T* held = mine + (i % kAhead) * 2 * 256 * 4;
+      load4(held, x);
+      load4(held + 256 * 4, x + 4);
     }
     norm_rotate<D, INTER>(a.nr, tk, x);
     if (!INTER && a.nr.rot) {
@@ -246,8 +284,8 @@ __global__ void __launch_bounds__(256) k_kv_append4(const __grid_constant__ Appe
       *w = c;
       if (!(l & 1)) *s = (uint8_t)u;
     }
-    w += words;
-    s += bytes;
+    w += a.c.bt * (Row4<D>::kCodes / 4);
+    s += a.c.bt * Row4<D>::kScales;
   }
   if (bad) atomicOr(a.c.status, kStatusNonFinite);
 }
@@ -336,10 +374,11 @@ cudaError_t launch_append4(const CacheView& c, int dim, const NormRopeArgs* nr, 
   for_type(k->dtype, [&](auto e) {
     using E = typename decltype(e)::type;
     const Append4Args<E> a = {c, rows_of<E>(k), rows_of<E>(v), rows_of<E>(q), rows_of<E>(q_out), start, n_new, B, T, Hq,
-                              chunk, nchunk, nr != nullptr, (int32_t)turn_ctas, nr ? 1 : 0, nr ? 1 : 2,
+                              chunk, nchunk, (int32_t)turn_ctas, nr ? 1 : 0, nr ? 1 : 2,
                               (c.heads + kAtOnce - 1) / kAtOnce, wide(k) && wide(v), nr ? *nr : NormRopeArgs{}};
     for_dim(dim, [&](auto dv) {
-      auto kern = a.nr.inter ? k_kv_append4<E, decltype(dv)::value, true> : k_kv_append4<E, decltype(dv)::value, false>;
+      constexpr int D = decltype(dv)::value;
+      auto kern = !nr ? k_kv_code4<E, D> : a.nr.inter ? k_kv_append4<E, D, true> : k_kv_append4<E, D, false>;
       err = launch_early(kern, turn_ctas + plain_ctas, 256, 0, st, a);
     });
   });

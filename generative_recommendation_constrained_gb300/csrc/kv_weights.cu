@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
       const float had = reinterpret_cast<const float*>(at + Sh::kCodes + Sh::kScales)[lane];
       const int first = key0 + step * kKeys + warp * 32;
       uint64_t sum2[2][2] = {};  // keys g and g + 8 of both tiles, even and odd rows
-#pragma unroll 1
+#pragma unroll 2
       for (int n8 = 0; n8 < groups; ++n8) {
         float z[2][4] = {};
 #pragma unroll
