@@ -219,17 +219,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint4 w = *reinterpret_cast<const uint4*>(codes + 128 * i * 16);
             uint32_t u = *reinterpret_cast<const uint16_t*>(scales + r * Row4<D>::kScales + 2 * c);
             if (r >= held) u = 0;  // behind the history: not defined, may be NaN
-            const uint32_t s0 = scale_twice(u & 0xFF), s1 = scale_twice(u >> 8);
+            const bool second = c >= 2;
+            const uint32_t s0 = scale_twice(second ? u >> 8 : u & 0xFF), s1 = scale_twice(second ? u & 0xFF : u >> 8);
             uint4 h[4];
-            e2m1_half8(w.x, s0, &h[0].x);
-            e2m1_half8(w.y, s0, &h[1].x);
-            e2m1_half8(w.z, s1, &h[2].x);
-            e2m1_half8(w.w, s1, &h[3].x);
+            e2m1_half8(second ? w.z : w.x, s0, &h[0].x);
+            e2m1_half8(second ? w.w : w.y, s0, &h[1].x);
+            e2m1_half8(second ? w.x : w.z, s1, &h[2].x);
+            e2m1_half8(second ? w.y : w.w, s1, &h[3].x);
             uint8_t* at = to + (c / 2) * (kNK * 128) + r * 128;
-            const bool swap2 = c >= 2;
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-              *reinterpret_cast<uint4*>(at + (((j + (swap2 ? p ^ 2 : p)) ^ (r & 7)) << 4)) = swap2 ? h[p ^ 2] : h[p];
+            for (int p = 0; p < 4; ++p) *reinterpret_cast<uint4*>(at + (((j + (second ? p ^ 2 : p)) ^ (r & 7)) << 4)) = h[p];
           }
         } else {
 #pragma unroll

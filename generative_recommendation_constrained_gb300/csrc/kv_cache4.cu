@@ -38,40 +38,52 @@ __device__ __forceinline__ uint32_t scale_byte(float top) {
   return min((b >> 20) - (112u << 3), 226u);  // 10240
 }
 
+// 1 / s rounded once, s the value of a scale byte: one step of Newton's from
+// the approximation, which for each of those 226 numbers gives the nearest
+// from any start within a unit in the last place.
+__device__ __forceinline__ float scale_reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return fmaf(fmaf(-s, r, 1.f), r, r);
+}
+
+// Largest |.| of three, NaN if one is.
+__device__ __forceinline__ float abs_max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Eight elements of a lane to codes; two neighbouring lanes share a scale.
 // Every lane of the warp takes part.  NaN -> 0, an infinity -> +-6 of what the
 // finite elements give; `bad` is set.
 __device__ __forceinline__ uint32_t codes8(float* x, uint32_t& u, bool& bad) {
-  float top = 0.f, all = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    top = fmaxf(top, fabsf(x[i]));
-    all += x[i];
-  }
-  const bool odd = !(fabsf(all) <= FLT_MAX);  // a NaN or an infinity (or a sum past the range)
+  float top = abs_max3(abs_max3(x[0], x[1], x[2]), abs_max3(x[3], x[4], x[5]), abs_max3(x[6], x[7], x[7]));
+  const bool odd = !(top <= FLT_MAX);  // a NaN or an infinity
   if (odd) {
+    bad = true;
     top = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (fabsf(x[i]) <= FLT_MAX) {
-        top = fmaxf(top, fabsf(x[i]));
-      } else {
-        bad = true;
-        if (isnan(x[i])) x[i] = 0.f;
-      }
+      if (fabsf(x[i]) <= FLT_MAX) top = fmaxf(top, fabsf(x[i]));
+      else if (isnan(x[i])) x[i] = 0.f;
     }
   }
   top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
   u = scale_byte(top);
-  const float s = scale_value(u), r = u ? __frcp_rn(s) : 0.f;
+  const float s = scale_value(u), r = u ? scale_reciprocal(s) : 0.f;
   if (odd) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (isinf(x[i])) x[i] = copysignf(8.f * s, x[i]);
   }
+  const uint64_t r2 = pair(r, r), s2 = pair(-s, -s);
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], s, r);
+  for (int i = 0; i < 8; i += 2) {  // quotient() of two
+    const uint64_t a = pair(x[i], x[i + 1]), y = mul2(a, r2);
+    unpair(fma2(fma2(y, s2, a), r2, y), q[i], q[i + 1]);
+  }
   uint32_t w;
   asm("{\n .reg .b8 b0, b1, b2, b3;\n cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
       " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n mov.b32 %0, {b0, b1, b2, b3};\n}"
@@ -174,6 +186,7 @@ __device__ __forceinline__ void code_plain(const Append4Args<T>& a, int64_t g, i
   const int64_t at = ((int64_t)max(to.blk, 0) * Hk + h0) * a.c.bt + to.row;
   uint32_t* w = reinterpret_cast<uint32_t*>((side ? a.c.vc : a.c.kc) + at * Row4<D>::kCodes) + l;
   uint8_t* s = reinterpret_cast<uint8_t*>(side ? a.c.vs : a.c.ks) + at * Row4<D>::kScales + l / 2;
+  if (!__any_sync(0xFFFFFFFFu, mine && to.blk >= 0)) return;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kAtOnce; ++i) {

@@ -159,11 +159,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   if (warp == 0) {
     auto tiles = [&](int b) { return b < kCounts ? s_tiles[b] : tiles_of(b, false); };
-    auto count = [&](int x) -> int {  // F(x)
-      int c = 0;
-      for (int b = lane; b < a.B; b += 32) c += max(0, tiles(b) - x);
-      return __reduce_add_sync(0xFFFFFFFFu, c);
-    };
     int most = 0, all = 0;
     for (int b = lane; b < a.B; b += 32) {
       most = max(most, tiles(b));
@@ -175,10 +170,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     if (all > p) {
       int lo = 0, hi = most, f_hi = 0;  // F(lo) > p >= F(hi)
-      while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2, f = count(mid);
-        if (f > p) lo = mid;
-        else hi = mid, f_hi = f;
+      while (hi - lo > 1) {             // 31 places between at a time, a lane each
+        const int step = (hi - lo + 31) / 32, x = min(lo + (lane + 1) * step, hi);
+        int f = 0;
+#pragma unroll 8
+        for (int b = 0; b < a.B; ++b) f += max(0, tiles(b) - x);
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, f > p));  // the first ones: F falls
+        const int at = __shfl_sync(0xFFFFFFFFu, f, min(n, 31));
+        lo = min(lo + n * step, hi);
+        if (n < 32) hi = min(lo + step, hi), f_hi = at;
       }
       int rank = p - f_hi;  // among the sequences with more than `lo` tiles
       for (int b0 = 0; b0 < a.B; b0 += 32) {
