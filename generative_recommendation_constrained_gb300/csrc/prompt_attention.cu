@@ -142,51 +142,52 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // CTAs start in the order of their numbers: those with the most keys before them first.  Item p is the (p - F(m +
   // 1))-th of the sequences with more than m tiles, where F(x) counts the tiles of numbers x and on, and m is the
-  // largest with F(m) > p.  One warp looks for it, among the tile counts of all sequences in shared memory (of the
-  // first kCounts; it counts those behind anew each time).
+  // largest with F(m) > p.  One warp looks for it.
   const int p = blockIdx.x / a.Hk, h = blockIdx.x % a.Hk;
-  constexpr int kCounts = Sh::kTile / 4;
-  int* s_tiles = reinterpret_cast<int*>(sq);
+  constexpr int kHeld = 4;
   auto tiles_of = [&](int b, bool report) -> int {
     const Seq s = seq_of(a, b, report);
     return (int)(((int64_t)s.n * a.G + kItem - 1) / kItem);
   };
-  for (int b = threadIdx.x; b < a.B; b += kThreads)
-    if (b < kCounts || blockIdx.x == 0) {
-      const int t = tiles_of(b, blockIdx.x == 0);
-      if (b < kCounts) s_tiles[b] = t;
-    }
-  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.B; b += kThreads) tiles_of(b, true);
   if (warp == 0) {
-    auto tiles = [&](int b) { return b < kCounts ? s_tiles[b] : tiles_of(b, false); };
-    int most = 0, all = 0;
-    for (int b = lane; b < a.B; b += 32) {
-      most = max(most, tiles(b));
-      all += tiles(b);
-    }
-    most = __reduce_max_sync(0xFFFFFFFFu, most);
-    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    int held[kHeld];  // of sequences lane, lane + 32, ...; those behind are counted anew each time
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) held[j] = lane + 32 * j < a.B ? tiles_of(lane + 32 * j, false) : 0;
+    auto count = [&](int x) -> int {  // F(x)
+      int c = 0;
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) c += max(0, held[j] - x);
+#pragma unroll 1
+      for (int b = lane + 32 * kHeld; b < a.B; b += 32) c += max(0, tiles_of(b, false) - x);
+      return __reduce_add_sync(0xFFFFFFFFu, c);
+    };
     if (lane == 0) s_item = make_int2(-1, 0);
     __syncwarp();
-    if (all > p) {
-      int lo = 0, hi = most, f_hi = 0;  // F(lo) > p >= F(hi)
-      while (hi - lo > 1) {             // 31 places between at a time, a lane each
-        const int step = (hi - lo + 31) / 32, x = min(lo + (lane + 1) * step, hi);
-        int f = 0;
-#pragma unroll 8
-        for (int b = 0; b < a.B; ++b) f += max(0, tiles(b) - x);
-        const int n = __popc(__ballot_sync(0xFFFFFFFFu, f > p));  // the first ones: F falls
-        const int at = __shfl_sync(0xFFFFFFFFu, f, min(n, 31));
-        lo = min(lo + n * step, hi);
-        if (n < 32) hi = min(lo + step, hi), f_hi = at;
+    if (count(0) > p) {
+      // F(lo) > p >= F(hi); a sequence has fewer tiles than the whole, rounded up
+      int lo = 0, hi = (int)(((int64_t)a.T_ * a.G + kItem - 1) / kItem), f_hi = 0;
+      int most = 0;
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) most = max(most, held[j]);
+      if (a.B <= 32 * kHeld) hi = __reduce_max_sync(0xFFFFFFFFu, most);
+#pragma unroll 1
+      while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2, f = count(mid);
+        if (f > p) lo = mid;
+        else hi = mid, f_hi = f;
       }
       int rank = p - f_hi;  // among the sequences with more than `lo` tiles
-      for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const uint32_t has = __ballot_sync(0xFFFFFFFFu, b0 + lane < a.B && tiles(b0 + lane) > lo);
+      auto look = [&](int b0, int tiles) {
+        const uint32_t has = __ballot_sync(0xFFFFFFFFu, tiles > lo);
         if (((has >> lane) & 1) && __popc(has & ((1u << lane) - 1)) == rank) s_item = make_int2(b0 + lane, lo);
         rank -= __popc(has);
-        if (rank < 0) break;
-      }
+      };
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) look(32 * j, held[j]);
+#pragma unroll 1
+      for (int b0 = 32 * kHeld; b0 < a.B && rank >= 0; b0 += 32) look(b0, b0 + lane < a.B ? tiles_of(b0 + lane, false) : 0);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
