@@ -3,15 +3,19 @@
 Every user has a history of item events.  One attention layer with random
 weights stands for the model that makes the decoder's request vectors:
 
-  1. the histories are written into an 8-bit block cache in one call (keys
-     normalised per head and rotated by position on the way);
+  1. the histories, packed one behind the other, are taken in by prompt
+     attention (the states that a deeper layer would go on with), and written
+     into a block cache of 8 or 4 bits in one call (keys normalised per head and
+     rotated by position on the way);
+     with --keep, histories that are longer are cut to that many events a head:
+     those that their own last events attend to most, and the last ones;
   2. a new event of every user is appended, and its query attends to the whole
-     history: the result is the request vector u;
+     (kept) history: the result is the request vector u;
   3. zg_decode searches the catalogue with beams, constrained to real items;
   4. the returned items attend to the history they were made from, all beams of
      a user at once over the one cache, and are re-scored by it.
 
-    python examples/history_decode.py [--users 64] [--events 500] [--fmt int8]
+    python examples/history_decode.py [--users 64] [--events 500] [--fmt e2m1] [--keep 200]
 
 The weights are random: the numbers show the path, not quality.
 """
@@ -28,9 +32,11 @@ import torch
 
 import generative_recommendation_constrained_gb300 as zg
 import synth
-from generative_recommendation_constrained_gb300.device import CacheAttention, Decoder, DeviceModel, KVCache, NormRope
+from generative_recommendation_constrained_gb300.device import (CacheAttention, CacheEviction, Decoder, DeviceModel, KVCache,
+                                                                NormRope, PromptAttention)
 
 HEADS, KV_HEADS, DIM, BLOCK = 8, 2, 64, 32
+WINDOW = 16          # last events whose attention says which others stay
 
 
 class HistoryLayer:
@@ -56,7 +62,8 @@ def main(argv=None) -> dict:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--users", type=int, default=64)
     ap.add_argument("--events", type=int, default=500, help="events of the longest history")
-    ap.add_argument("--fmt", choices=("e4m3", "int8"), default="e4m3")
+    ap.add_argument("--fmt", choices=("e4m3", "int8", "e2m1"), default="e4m3")
+    ap.add_argument("--keep", type=int, default=0, help="events a head that stay of a longer history (0: all)")
     ap.add_argument("--seed", type=int, default=1)
     a = ap.parse_args(argv)
 
@@ -89,14 +96,35 @@ def main(argv=None) -> dict:
     decoder = Decoder(index, None, dm, B, cfg.beam, cfg.topk)
 
     # 1. the histories
-    _, k, v = layer.project(embed(events))
+    q, k, v = layer.project(embed(events))
+    at = torch.arange(T, device="cuda", dtype=torch.int32)
+    b, t = (at[None] < held[:, None]).nonzero(as_tuple=True)
+    starts = torch.cat([zero[:1], held.cumsum(0)]).to(torch.int32)
+    pq, pk = layer.turn(q[b, t][None], k[b, t][None], at[t][None])
+    packed = pq[0], pk[0], v[b, t]
+    states, _ = PromptAttention(HEADS, KV_HEADS, DIM)(*packed, starts)
     cache.append(k, v, table, zero, held, norm_rope=layer.turn)
+    kept, weights = held, None
+    if a.keep:
+        # the last events look back over their history, causally
+        rows = held.clamp(max=WINDOW)
+        last = (held[:, None] - rows[:, None] + torch.arange(WINDOW, device="cuda", dtype=torch.int32)).clamp(max=T - 1)
+        wq = layer.turn(q.gather(1, last.long()[:, :, None, None].expand(B, WINDOW, HEADS, DIM)), None, last)[0]
+        _, lse = CacheAttention(cache, B, WINDOW, HEADS, width, causal=True, lse=True)(wq, table, held, rows)
+        weights = torch.zeros((B, KV_HEADS, width * BLOCK), device="cuda")
+        cache.add_weights(weights, wq, lse, table, held, n_rows=rows, causal=True)
+        kept, _ = CacheEviction(cache, B, width, a.keep, min(a.keep, WINDOW))(weights, table, held)
 
-    # 2. the new event: written, and its query over everything
+    # 2. the new event: written, and its query over everything that is kept.  Its position counts all events, so where
+    # some have left it is turned before it is written.
     x = embed(latest)
     q, k, v = layer.project(x)
-    q = cache.append(k, v, table, held, q=q, norm_rope=layer.turn)
-    length = held + 1
+    if a.keep:
+        q, k = layer.turn(q, k, held[:, None].contiguous())
+        cache.append(k, v, table, kept)
+    else:
+        q = cache.append(k, v, table, held, q=q, norm_rope=layer.turn)
+    length = kept + 1
     a1, _ = one(q, table, length)
     u = (x + layer.output(a1))[:, 0].contiguous()
 
@@ -106,7 +134,7 @@ def main(argv=None) -> dict:
     # 4. the found items (as events one position on) over the same history
     found = embed_sids(out_sids, dm, cfg.L)
     q, _, _ = layer.project(found)
-    pos = length[:, None].expand(B, cfg.topk).contiguous()
+    pos = (held + 1)[:, None].expand(B, cfg.topk).contiguous()
     q, _ = layer.turn(q, None, pos)
     a2, lse = beams(q, table, length)
     again = scores + (found * layer.output(a2)).sum(-1) * cfg.d ** -0.5
@@ -117,7 +145,8 @@ def main(argv=None) -> dict:
     print(f"{B} users, {int(length.sum())} events in {cache.n_blocks} blocks of {BLOCK} ({a.fmt}); "
           f"{cfg.topk} items each, re-scoring moves the first place of {int((best != 0).sum())}")
     return {"u": u, "sids": out_sids, "scores": scores, "rescored": again, "lse": lse, "length": length,
-            "table": table, "cache": cache, "layer": layer, "x": x, "items": sids, "a1": a1}
+            "table": table, "cache": cache, "layer": layer, "x": x, "items": sids, "a1": a1, "held": held, "starts": starts,
+            "states": states, "packed": packed, "weights": weights}
 
 
 def embed_sids(sids: torch.Tensor, dm: DeviceModel, L: int) -> torch.Tensor:

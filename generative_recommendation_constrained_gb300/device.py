@@ -100,8 +100,16 @@ def _rows(x: torch.Tensor | None, gpu: int):
 
 
 def _packed(x: torch.Tensor, gpu: int):
-    """zg_rows of a [T, heads, dim] tensor."""
-    return _rows(x.unsqueeze(0), gpu)
+    """zg_rows of a [T, heads, dim] tensor, as _rows."""
+    dt = _ROW_TYPES.get(x.dtype)
+    if dt is None:
+        raise ValueError(f"rows must be float32, bfloat16 or float16, not {x.dtype}")
+    st, sh, se = x.stride()
+    if se != 1 or st < 0 or sh < 0:
+        raise ValueError("the last dimension of the rows must be contiguous, and no stride negative")
+    if x.get_device() != gpu:
+        raise ValueError(f"the rows must be on the GPU, on the current device (cuda:{gpu})")
+    return _pack_rows(x.data_ptr(), dt, 0, 0, st, sh)
 
 
 def _stream(stream, gpu: int):
@@ -210,16 +218,17 @@ class PromptAttention:
         """q [T, Hq, dim], k, v [T, Hk, dim]; sequence b is rows starts[b] .. starts[b + 1] - 1 (int32 [B + 1]).  Returns
         (out, lse or None): out like q (new when None; may be q), lse [T, Hq] float32 if asked for (or given).  New tensors
         belong to `stream`, as in NormRope."""
-        T = q.shape[0]
-        if tuple(q.shape) != (T, self.Hq, self.dim) or k.shape != v.shape or tuple(k.shape) != (T, self.Hk, self.dim):
+        shape, k_shape = q.shape, k.shape                # each look at a tensor's shape costs 0.1 us
+        if (len(shape) != 3 or shape[1] != self.Hq or shape[2] != self.dim or len(k_shape) != 3 or k_shape[0] != shape[0] or
+                k_shape[1] != self.Hk or k_shape[2] != self.dim or v.shape != k_shape):
             raise ValueError("q must be [T, Hq, dim], k and v [T, Hk, dim]")
-        gpu = _current(-1, "")
+        T, gpu = shape[0], _current(-1, "")
         if starts.dim() != 1 or starts.shape[0] < 1:
             raise ValueError("starts must be [B + 1]")
         _int32(starts, starts.shape, "starts", gpu)
         if out is None:
             out = _out_like(q, stream, gpu)
-        elif out.shape != q.shape:
+        elif out.shape != shape:
             raise ValueError("out must have q's shape")
         if lse is None and self.with_lse:
             lse = _out_like(q, stream, gpu, (T, self.Hq), torch.float32)
