@@ -367,6 +367,7 @@ class CacheEviction:
 
     def __init__(self, cache: KVCache, B: int, max_blocks: int, keep: int, recent: int = 0):
         device = cache.k_codes.device
+        _current(cache.gpu, "the cache is")
         self.cache, self.B, self.max_blocks, self.keep, self.recent = cache, B, max_blocks, keep, recent
         if B < 0 or keep < 1 or not 0 <= recent <= keep:
             raise ValueError("B must be >= 0, keep >= 1 and recent in [0, keep]")
