@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* frag = reinterpret_cast<uint4*>(smem + Sh::kRing);  // [row / 8][KS / 2][lane]
   const int most = a.rows_at_once;
-  float4* par = reinterpret_cast<float4*>(frag + most / 8 * (KS / 2) * 32);  // [row / 2]: factor, log-sum-exp of both rows
+  float4* par = reinterpret_cast<float4*>(frag + most / 8 * (KS / 2) * 32);  // [row / 2]: factors of both rows, minus their log-sum-exps
   int2* sees = reinterpret_cast<int2*>(par + most / 2);                      // [row / 2]: tokens that they see
   __shared__ int s_blk[kMostSteps * kKeys / 16];  // of every 16 keys, -1: not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -154,8 +154,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
         reinterpret_cast<uint2*>(frag)[(((r >> 3) * (KS / 2) + (dw >> 1)) * 32 + (r & 7) * 4 + cc) * 2 + (dw & 1)] =
             make_uint2(pack_half2(x[0] * dn, x[1] * dn), pack_half2(x[2] * dn, x[3] * dn));
       if (r < upto && l == 0) {
-        reinterpret_cast<float2*>(par)[r] =
-            make_float2(a.scale * power_of_2(ex), vis == 0 ? INFINITY : ls * 1.4426950408889634f);
+        float* of = reinterpret_cast<float*>(par + (r >> 1)) + (r & 1);
+        of[0] = a.scale * power_of_2(ex);
+        of[2] = vis == 0 ? -INFINITY : ls * -1.4426950408889634f;
         reinterpret_cast<int*>(sees)[r] = vis;
       }
     }
@@ -213,30 +214,33 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
       }
       const float had = reinterpret_cast<const float*>(at + Sh::kCodes + Sh::kScales)[lane];
       const int first = key0 + step * kKeys + warp * 32;
+      // rows that see nothing count for nothing anyhow, so only causal ones need a mask, and only of the last keys
+      const bool masked = a.causal && first + 32 > s.len - (s.rows - 1);
+      const uint64_t ks2[2] = {pair(ks[0], ks[0]), pair(ks[1], ks[1])};
       uint64_t sum2[2][2] = {};  // keys g and g + 8 of both tiles, even and odd rows
 #pragma unroll 2
       for (int n8 = 0; n8 < groups; ++n8) {
-        float z[2][4] = {};
+        float z[2][4];
 #pragma unroll
         for (int i = 0; i < KS / 2; ++i) {
           const uint4 f = frag[(n8 * (KS / 2) + i) * 32 + lane];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            mma_16816(z[n], ka[n][2 * i], f.x, f.y);
+            if (i == 0) mma_16816_first(z[n], ka[n][0], f.x, f.y);
+            else mma_16816(z[n], ka[n][2 * i], f.x, f.y);
             mma_16816(z[n], ka[n][2 * i + 1], f.z, f.w);
           }
         }
-        const float4 p = par[n8 * 4 + c];
-        const int2 v = sees[n8 * 4 + c];
-        const bool masked = __any_sync(0xFFFFFFFFu, min(v.x, v.y) < first + 32);
-        const uint64_t less = pair(-p.y, -p.w);
+        const ulonglong2 p = reinterpret_cast<const ulonglong2*>(par)[n8 * 4 + c];
+        int2 v;
+        if (masked) v = sees[n8 * 4 + c];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const uint64_t f = mul2(pair(p.x, p.z), pair(ks[n], ks[n]));
+          const uint64_t f = k4 ? p.x : mul2(p.x, ks2[n]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float e0, e1;
-            unpair(fma2(pair(z[n][2 * i], z[n][2 * i + 1]), f, less), e0, e1);
+            unpair(fma2(pair(z[n][2 * i], z[n][2 * i + 1]), f, p.y), e0, e1);
             e0 = exp2_fast(e0);
             e1 = exp2_fast(e1);
             if (masked) {
