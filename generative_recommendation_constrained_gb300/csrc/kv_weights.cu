@@ -135,29 +135,43 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_weights(const __grid_constan
       cc = d % 64 % 32 / 8, dw = D / 64 * 4 + d % 8 / 4;
     }
     const int upto = min(most, (M - m0 + 7) / 8 * 8);
-#pragma unroll 4
-    for (int r0 = warp * kAt; r0 < upto; r0 += kWarps * kAt) {
-      const int r = r0 + lane / kSlot, m = m0 + r;
-      const bool live = m < M;
-      const int row = live ? m / a.G : 0, qh = h * a.G + (live ? m % a.G : 0);
-      float x[4] = {}, ls = -INFINITY;
-      if (live && l < kLanes) load4(q.at(b, row, qh) + d, x);
-      if (live) ls = a.lse[((int64_t)b * a.R + row) * a.Hq + qh];
-      const int vis = !live || ls == -INFINITY ? 0 : a.causal ? max(0, s.len - (s.rows - 1 - row)) : s.len;
-      if (vis == 0) x[0] = x[1] = x[2] = x[3] = 0.f;  // a row that sees nothing, whatever it holds
-      float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    constexpr int kMany = 8;  // rows of a lane in flight at once
+    for (int r0 = warp * kAt + lane / kSlot; r0 - lane / kSlot < upto; r0 += kMany * kWarps * kAt) {
+      uint4 raw[kMany];  // four elements in the first half
+      float ls[kMany];
+      int vis[kMany];
 #pragma unroll
-      for (int o = kSlot / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      const int ex = row_exponent(top);
-      const float dn = power_of_2(-ex);
-      if (r < upto && l < kLanes)
-        reinterpret_cast<uint2*>(frag)[(((r >> 3) * (KS / 2) + (dw >> 1)) * 32 + (r & 7) * 4 + cc) * 2 + (dw & 1)] =
-            make_uint2(pack_half2(x[0] * dn, x[1] * dn), pack_half2(x[2] * dn, x[3] * dn));
-      if (r < upto && l == 0) {
-        float* of = reinterpret_cast<float*>(par + (r >> 1)) + (r & 1);
-        of[0] = a.scale * power_of_2(ex);
-        of[2] = vis == 0 ? -INFINITY : ls * -1.4426950408889634f;
-        reinterpret_cast<int*>(sees)[r] = vis;
+      for (int k = 0; k < kMany; ++k) {
+        const int r = r0 + k * kWarps * kAt, m = m0 + r;
+        const bool live = r < upto && m < M;
+        const int row = live ? m / a.G : 0, qh = h * a.G + (live ? m - row * a.G : 0);
+        raw[k] = make_uint4(0, 0, 0, 0);
+        ls[k] = -INFINITY;
+        if (live && l < kLanes) *reinterpret_cast<uint2*>(&raw[k]) = *reinterpret_cast<const uint2*>(q.at(b, row, qh) + d);
+        if (live) ls[k] = a.lse[((int64_t)b * a.R + row) * a.Hq + qh];
+        vis[k] = !live ? 0 : a.causal ? max(0, s.len - (s.rows - 1 - row)) : s.len;
+      }
+#pragma unroll
+      for (int k = 0; k < kMany; ++k) {
+        const int r = r0 + k * kWarps * kAt;
+        if (r - lane / kSlot >= upto) break;  // the same for all lanes
+        if (ls[k] == -INFINITY) vis[k] = 0;
+        float x[4] = {};
+        if (vis[k] > 0) load4(reinterpret_cast<const T*>(&raw[k]), x);  // a row that sees nothing, whatever it holds: 0
+        float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+        for (int o = kSlot / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const int ex = row_exponent(top);
+        const float dn = power_of_2(-ex);
+        if (r < upto && l < kLanes)
+          reinterpret_cast<uint2*>(frag)[(((r >> 3) * (KS / 2) + (dw >> 1)) * 32 + (r & 7) * 4 + cc) * 2 + (dw & 1)] =
+              make_uint2(pack_half2(x[0] * dn, x[1] * dn), pack_half2(x[2] * dn, x[3] * dn));
+        if (r < upto && l == 0) {
+          float* of = reinterpret_cast<float*>(par + (r >> 1)) + (r & 1);
+          of[0] = a.scale * power_of_2(ex);
+          of[2] = vis[k] == 0 ? -INFINITY : ls[k] * -1.4426950408889634f;
+          reinterpret_cast<int*>(sees)[r] = vis[k];
+        }
       }
     }
   };
@@ -336,8 +350,9 @@ extern "C" zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* tabl
   a.decay = decay;
   const int64_t units = (tokens + kKeys - 1) / kKeys, M = (int64_t)R * a.G;
   // several steps a CTA, so that its queries and block numbers are brought in once for them, where steps are many: of
-  // few rows as many as leave 16 CTAs an SM, of many, which take longer to bring in, 4
-  a.steps = (int)std::max<int64_t>(1, std::min<int64_t>(kMostSteps, units * B * cache->heads / (sm_count() * (M > 16 ? 4 : 16))));
+  // few rows as many as leave 16 CTAs an SM, of many, which take longer to bring in, 6 (window of 33 rows: 34.1 us with 4,
+  // 33.6 with 6, 36.5 with 10; lifelong: 52.5 with 16, 55.3 with 12)
+  a.steps = (int)std::max<int64_t>(1, std::min<int64_t>(kMostSteps, units * B * cache->heads / (sm_count() * (M > 16 ? 6 : 16))));
   cudaError_t err = cudaSuccess;
   for_dim(cache->dim, [&](auto dv) {
     constexpr int D = decltype(dv)::value;
