@@ -565,7 +565,7 @@ ZG_API zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table,
  *     rows in no sequence are left as they are.  Starts outside that are
  *     recorded for zg_check_device_status and held inside it.
  * Products take the rows as they are and probabilities rounded to their type
- * (relative 2^-9 or 2^-11 of each); scores, sums and maxima are 32-bit.  What a
+ * (relative 2^-8 or 2^-11 of each); scores, sums and maxima are 32-bit.  What a
  * row does not see never reaches it, whatever it holds (a NaN or an infinity
  * in rows behind it, or in other sequences); a NaN in its query or in what it
  * sees gives NaN.
