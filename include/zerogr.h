@@ -587,7 +587,8 @@ ZG_API zg_status zg_prompt_attention(const zg_rows* q, const zg_rows* k, const z
  *   known: device int32 [B], the tokens whose weights exist already; those of
  *     the others, and all where decay is 0, count as 0 (NULL: all exist).
  * Sums are 32-bit, in a fixed order; a term below 2^-126 counts as 0.  Tokens of a block outside the cache
- * collect nothing (recorded).  B at most 65,535; otherwise the limits of
+ * collect nothing (recorded).  A request of n_rows 0 has its weights decayed; a
+ * call with R of 0 does nothing.  B at most 65,535; otherwise the limits of
  * zg_kv_attention; no workspace. */
 ZG_API zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,
                                const int32_t* length, const int32_t* n_rows, const int32_t* known,
