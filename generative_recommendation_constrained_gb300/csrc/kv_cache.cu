@@ -566,7 +566,10 @@ zg_status zg_kv_append(const zg_kv_cache* cache, const zg_norm_rope* nr, const z
       auto kern = cache->format == ZG_KV_INT8
                       ? (na.inter ? k_kv_append<E, D, true, true> : k_kv_append<E, D, true, false>)
                       : (na.inter ? k_kv_append<E, D, false, true> : k_kv_append<E, D, false, false>);
-      if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      // the limit is the kernel's, not the call's: the most that any call asks for (of 16 groups a CTA, block_tokens being
+      // 128 at most), so that calls of several threads agree
+      constexpr int kMostSmem = 2 * kPasses * 16 * HeadLanes<D>::kGroup * 8 * (int)sizeof(E);
+      if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
       if (err == cudaSuccess) err = launch_early(kern, kv + qc, threads, smem, static_cast<cudaStream_t>(stream), a);
     });
   });

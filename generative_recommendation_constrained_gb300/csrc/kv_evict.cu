@@ -459,9 +459,12 @@ extern "C" zg_status zg_kv_evict(const zg_kv_cache* cache, const int32_t* table,
       const int smem = std::max((int)std::min<int64_t>(strips * kStripBytes, kMostSmem), a.rows * 2 * Sh::kRow);
       a.held = smem / kStripBytes;
       a.smem = smem;
-      const int with = smem + kHists * kBins * 4;
-      err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, with);
-      if (err == cudaSuccess) err = launch_clusters(kern, dim3(bhs * ranks), ranks, kThreads, with, static_cast<cudaStream_t>(stream), a);
+      // the limit is the kernel's, not the call's: the most that any call asks for, so that calls of several threads agree
+      constexpr int kHistBytes = kHists * kBins * 4;
+      static_assert(Sh::kRows * 2 * Sh::kRow <= kMostSmem, "a batch of rows fits too");
+      err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem + kHistBytes);
+      if (err == cudaSuccess)
+        err = launch_clusters(kern, dim3(bhs * ranks), ranks, kThreads, smem + kHistBytes, static_cast<cudaStream_t>(stream), a);
     });
   });
   return err == cudaSuccess ? ZG_OK : cuda_fail(err, "cache eviction launch");

@@ -371,7 +371,9 @@ extern "C" zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* tabl
         constexpr int FMT = decltype(fv)::value;
         auto kern = k_kv_weights<E, D, FMT>;
         const int smem = WeightShape<D, FMT>::kRing + a.rows_at_once * kRowBytes;
-        if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        // the limit is the kernel's, not the call's: the most that any call asks for, so that calls of several threads agree
+        constexpr int kMostSmem = WeightShape<D, FMT>::kRing + kRowsAtOnce * kRowBytes;
+        if (smem > 40 * 1024) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (err == cudaSuccess)
           err = launch_early(kern, dim3((unsigned)((units + a.steps - 1) / a.steps), cache->heads, B), 32 * kWarps, smem,
                              static_cast<cudaStream_t>(stream), a, rows_of<E>(q));
