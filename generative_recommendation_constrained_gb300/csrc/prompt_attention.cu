@@ -477,19 +477,22 @@ __global__ void __launch_bounds__(kThreads, 2)
         float* x = reinterpret_cast<float*>(o);
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] *= inv;
-        if (bad && live) {
-          for (int t = edge; t < steps; ++t)
-            for (int key = t * kNK; key < min((t + 1) * kNK, vis); ++key) {
-              if (!((s_bad[t - edge][(key % kNK) / 32] >> (key % 32)) & 1)) continue;
-              const T* qr = q.data + (int64_t)(s.first + token) * q.st + qh * q.sh;
-              const T* kr = k.data + (int64_t)(s.first + key) * k.st + h * k.sh;
-              const T* vr = v.data + (int64_t)(s.first + key) * v.st + h * v.sh + d;
-              float z = 0.f;
-              for (int c = 0; c < D; ++c) z = fmaf((float)qr[c], (float)kr[c], z);
-              const float pw = exp2_fast(fmaf(z, f, -mx)) * inv;
+        if (bad) {  // of all lanes or none
+          if (live) {
+            for (int t = edge; t < steps; ++t)
+              for (int key = t * kNK; key < min((t + 1) * kNK, vis); ++key) {
+                if (!((s_bad[t - edge][(key % kNK) / 32] >> (key % 32)) & 1)) continue;
+                const T* qr = q.data + (int64_t)(s.first + token) * q.st + qh * q.sh;
+                const T* kr = k.data + (int64_t)(s.first + key) * k.st + h * k.sh;
+                const T* vr = v.data + (int64_t)(s.first + key) * v.st + h * v.sh + d;
+                float z = 0.f;
+                for (int c = 0; c < D; ++c) z = fmaf((float)qr[c], (float)kr[c], z);
+                const float pw = exp2_fast(fmaf(z, f, -mx)) * inv;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = fmaf(pw, (float)vr[j], x[j]);
-            }
+                for (int j = 0; j < 32; ++j) x[j] = fmaf(pw, (float)vr[j], x[j]);
+              }
+          }
+          __syncwarp();  // lanes see different numbers of keys, and the next load of tensor memory takes the whole warp
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 8)
