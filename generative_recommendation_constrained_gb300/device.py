@@ -371,17 +371,20 @@ class CacheEviction:
         self.cache, self.B, self.max_blocks, self.keep, self.recent = cache, B, max_blocks, keep, recent
         if B < 0 or keep < 1 or not 0 <= recent <= keep:
             raise ValueError("B must be >= 0, keep >= 1 and recent in [0, keep]")
-        self.length = torch.empty((B,), dtype=torch.int32, device=device)
+        self._lengths = [torch.empty((B,), dtype=torch.int32, device=device) for _ in range(2)]
+        self.length = self._lengths[0]
         self.kept = torch.empty((B, cache.heads, keep), dtype=torch.int32, device=device)
 
     def __call__(self, weights, table, length, stream: int | None = None):
         """Shortens the histories of more than `keep` of the length[b] tokens, in place, and their weights [B, heads,
         tokens] with them; returns (the new lengths [B], the places that the kept tokens had [B, heads, keep], -1 behind
-        them), this object's own buffers."""
+        them), this object's own buffers.  The lengths that one call returns may be the next one's `length`: there are two
+        buffers of them, and the one that is not given is written."""
         gpu = _current(self.cache.gpu, "the cache is")
         _int32(table, (self.B, self.max_blocks), "table", gpu)
         _int32(length, (self.B,), "length", gpu)
         tokens = _weights_of(weights, self.B, self.cache, self.max_blocks, gpu)
+        self.length = self._lengths[length.data_ptr() == self._lengths[0].data_ptr()]
         Z.zg_kv_evict(self.cache.struct, table, self.max_blocks, length, weights, tokens, self.keep, self.recent,
                       self.length, self.kept, self.B, _stream(stream, gpu))
         return self.length, self.kept

@@ -56,3 +56,31 @@ def test_weights_beyond_shared_memory(zg, dev, fmt):  # noqa: F811
     w = some_weights(B, 1, width * bt, 5, levels=1)
     w[3, 0, 30000:] *= 2                     # many of the kept ones, and of the equal ones, lie behind
     check_evict(zg, dev, c, fmt, table, length, w, keep, 5)
+
+
+def test_lengths_handed_back(zg, dev):  # noqa: F811
+    """A loop that adds to the returned lengths in place and hands them to the next eviction, as one that keeps copies."""
+    def loop(own):
+        B, width, bt = 3, 12, 16
+        c = dev.KVCache(B * width, bt, 2, 64, "e2m1")
+        c.k_codes.zero_(), c.v_codes.zero_(), c.k_scale.zero_(), c.v_scale.zero_()
+        table = torch.arange(B * width, dtype=torch.int32, device="cuda").view(B, width)
+        e = dev.CacheEviction(c, B, width, 40, 4)
+        length, w = ints([0, 7, 33]), some_weights(B, 2, width * bt, 9)
+        g = torch.Generator(device="cuda").manual_seed(1)
+        x = torch.randn((6, 2, B, 30, 2, 64), generator=g, device="cuda").bfloat16()
+        seen = []
+        for k, v in x:
+            c.append(k, v, table, length)
+            length += 30
+            new, kept = e(w, table, length)
+            length = new if own else new.clone()
+            seen += [length.clone(), kept.clone()]
+        return [c.k_codes, c.v_codes, c.k_scale, c.v_scale, w, *seen]
+
+    got, want = loop(True), loop(False)
+    torch.cuda.synchronize()
+    zg.zg_check_device_status(0)
+    assert got[-2].tolist() == [40] * 3
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
