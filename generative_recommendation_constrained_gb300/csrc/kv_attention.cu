@@ -73,8 +73,8 @@ __device__ __forceinline__ int request_units(const AttnArgs& a, const Seen& s, i
 // them here (6.3 TB/s) and the rest the join; 64 requests of up to 4,096 tokens
 // (85 MB) 26 us, some 6 of them the chain from the lengths to the first codes.
 // 4-bit codes: 90 us and 25 us; there the kernel is bound by its instructions,
-// 400 a tile of 16 keys and values (of which 64 convert and 64 scale), at 2.3 a
-// cycle and SM.
+// 400 a tile of 16 keys and values (of which 64 convert and 64 scale), in chains:
+// 2.6 a cycle and SM, and no warp ready in 35 % of cycles.
 constexpr uint32_t kFewSpin = 1u << 20;  // polls of a wait at most
 
 // CTAs an SM (4-bit codes, lifelong: 94 us with three, 91 with four).
@@ -660,6 +660,11 @@ struct AttnPlan {
 //                                128 dims: 26.8/37.7  36.9/37.1  40.4/37.1  59.7/37.2
 //    4 requests of 30,000 tokens, 64 dims: 31.0/55.7  45.3/55.6  47.4/55.6  53.4/55.9
 //                                128 dims: 41.1/59.7  61.1/59.8  63.7/59.7  70.8/60.2
+// In 4 bits:
+//   32 requests of  2,000 tokens, 64 dims: 22.2/38.2  31.9/38.2  32.8/37.9  46.4/38.0
+//                                128 dims: 28.4/40.8  39.1/40.8  41.4/40.8  58.9/41.0
+//    4 requests of 30,000 tokens, 64 dims: 29.4/64.0  43.9/64.0  44.5/64.1  61.5/65.6
+//                                128 dims: 38.0/66.8  56.0/66.8  57.2/67.2  79.7/69.2
 inline int few_rows(int dim) { return dim <= 64 ? 32 : 24; }
 
 // Few rows: as many CTAs as are resident, or one for each unit that the

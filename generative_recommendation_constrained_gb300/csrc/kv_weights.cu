@@ -9,11 +9,14 @@
 // nothing is added atomically, and what is not defined behind a history stays
 // with keys that are not written.
 // Measured: one token over 8 histories of up to 131,072 tokens (16 heads over 4
-// of 128, 4 bits, 201 MB with the weights) 53 us, 3.8 TB/s, bound by the
-// instructions of decoding and softmax; with keys read into registers
-// one step ahead 119 us.  33 rows back over 16 histories of up to 8,190 tokens
-// (16 heads over 4 of 64, e4m3) 34 us: queries brought in (38 us with a row in
-// flight at a time), issue, CTAs unevenly on the SMs.
+// of 128, 4 bits, 201 MB with the weights) 53 us, 3.8 TB/s, bound by chains of
+// dependent instructions (decoding, products, softmax) in 16 warps an SM: 60 %
+// of issue slots are busy, in the others no warp is ready; with keys read into
+// registers one step ahead 119 us.  33 rows back over 16 histories of up to
+// 8,190 tokens (16 heads over 4 of 64, e4m3) 34 us: every CTA brings all queries
+// in for its few steps (38 us with a row in flight at a time), CTAs unevenly on
+// the SMs.  A CTA's share of keys follows the table's width, not the lengths:
+// behind tables 16 times as wide the two take 73 and 66 us.
 #include <cmath>
 
 #include "kv_attn.cuh"
@@ -362,7 +365,8 @@ extern "C" zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* tabl
   cudaError_t err = cudaSuccess;
   for_dim(cache->dim, [&](auto dv) {
     constexpr int D = decltype(dv)::value;
-    // query rows in shared memory at once: all, or as many as leave an SM two CTAs
+    // query rows in shared memory at once: all, or as many as leave an SM two CTAs (one of 128 dims in 8 bits, whose ring
+    // is the largest, from some 170 rows on)
     constexpr int kRowBytes = 2 * D + 12, kRowsAtOnce = 60 * 1024 / kRowBytes / 8 * 8;
     a.rows_at_once = (int)std::min<int64_t>((M + 7) / 8 * 8, kRowsAtOnce);
     auto typed = [&](auto ev) {

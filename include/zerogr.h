@@ -568,7 +568,8 @@ ZG_API zg_status zg_kv_attention(const zg_kv_cache* cache, const int32_t* table,
  * (relative 2^-8 or 2^-11 of each); scores, sums and maxima are 32-bit.  What a
  * row does not see never reaches it, whatever it holds (a NaN or an infinity
  * in rows behind it, or in other sequences); a NaN in its query or in what it
- * sees gives NaN.
+ * sees gives NaN, an infinite value that it sees an infinity or a NaN.  Each
+ * row of values that is not finite costs a causal call time.
  * dim 32, 64, 96 or 128; Hq a multiple of Hk, at most 1024; T * Hq below 2^31;
  * no workspace. */
 ZG_API zg_status zg_prompt_attention(const zg_rows* q, const zg_rows* k, const zg_rows* v, const zg_rows* out,
@@ -599,18 +600,20 @@ ZG_API zg_status zg_kv_weights(const zg_kv_cache* cache, const int32_t* table, i
  * head for itself: the last `recent` tokens stay, and of the others the keep -
  * recent of largest weight (equal ones: the earlier; a NaN counts as below
  * every number).  They move to the places 0 .. keep - 1 in their order, with
- * their weights, in place; shorter histories stay as they are, and so does
- * what lies in places from keep on.
- *   new_length: device int32 [B], min(length, keep) (not length itself).
+ * their weights, in place; shorter histories stay as they are, and so do the
+ * codes (and 4-bit scales) and weights in places from keep on.
+ *   new_length: device int32 [B], min(length, keep); not length itself, which
+ *     is read while it is written.
  *   kept: device int32 [B][heads][keep], the places that the kept tokens had,
  *     -1 behind them.
  * In 8 bits a block's new scale is the largest of its kept rows' old ones,
- * and rows of a smaller one are coded again as an append does it; in 4 bits
- * nothing is rounded.  Keys keep the rotation of the position that they were
- * written at: from then on a token's place is not its position, so later keys
- * and queries are turned by zg_qk_norm_rope at positions of the caller's, and
- * appended without a norm_rope.  Blocks of one request must be its own.  Rows
- * from a block outside the cache become zeros (recorded).
+ * also where rows from keep on lie behind them, and rows of a smaller one are
+ * coded again as an append does it; in 4 bits nothing is rounded.
+ * Keys keep the rotation of the position that they were written at: from then
+ * on a token's place is not its position, so later keys and queries are turned
+ * by zg_qk_norm_rope at positions of the caller's, and appended without a
+ * norm_rope.  Blocks of one request must be its own.  Rows from a block
+ * outside the cache become zeros (recorded).
  * B * heads at most 65,535; keep from 1 to 2^30; recent from 0 to keep; no
  * workspace. */
 ZG_API zg_status zg_kv_evict(const zg_kv_cache* cache, const int32_t* table, int32_t max_blocks,
